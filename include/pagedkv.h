@@ -265,6 +265,124 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
                                  void *workspace, size_t workspace_bytes,
                                  pkv_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* A tree of drafted tokens: attention, verification, commit.               */
+/* ------------------------------------------------------------------------ */
+/*
+ * Speculative decoding ("LLM推理优化实战" §4) with a TREE of drafted tokens per
+ * sequence instead of a chain.  The tree's nodes are appended to the cache in
+ * index order (paged_kv_append, slots in order), so node i of sequence b sits
+ * at position start_b + i, start_b = context_lens[b] - n_b; n_b is
+ * tree_lens[b], or q_len for every sequence when tree_lens is NULL (a padded
+ * batch: q_len is the widest tree; n_b = 0 is a padding sequence).  Node 0 is
+ * the last confirmed token, every node comes after its parent, and
+ *   tree_mask  uint64 per node, device, 8-byte aligned: [B][q_len]
+ *              (mask_per_seq = 1) or [q_len], one tree for every sequence
+ *              (mask_per_seq = 0); bit j of node i's mask: node i sees node j.
+ * A node's mask normally names its ancestors and itself; bits at or past n_b
+ * are ignored.  The three calls share this description:
+ *   paged_tree_attention -> (the model's next layers) -> paged_tree_verify
+ *   -> paged_tree_commit on each layer's cache, pkv_bm_truncate on the host.
+ * A tree_lens[b] outside [0, q_len] is clamped (the attention also sets
+ * PKV_FLAG_BAD_LEN).
+ */
+/*
+ * Attention of the tree's query rows over the paged cache:
+ *   out[b][i][hq] = softmax_t( scale * q[b][i][hq] . K_t ) . V_t over
+ *     t < start_b, and t = start_b + j for the nodes j in node i's mask.
+ * Any mask is allowed (also one that leaves its own node out); a row that sees
+ * nothing gives 0.  Rows i >= n_b of out are left as they were.
+ *
+ *   q, out     [B][q_len][Hq][D], q_len 1 .. PKV_MAX_Q_LEN
+ *   window     0 (none) or W >= 1: node i stands at position start_b + d - 1,
+ *              d = max(1, nodes in its mask) its depth, and sees the cached
+ *              positions t >= start_b + d - W; the nodes it sees are the
+ *              mask's.  Blocks no row reaches may be -1 in block_table.
+ *   scale      > 0 (PKV_EINVAL otherwise)
+ *   workspace  paged_tree_workspace_bytes(...) bytes, 256-byte aligned, as for
+ *              paged_decode_attention (status: paged_decode_status)
+ * Types, layouts, block_table, context_lens and errors as for
+ * paged_decode_attention_multi.
+ */
+int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D,
+                               int cache_dtype, int q_dtype, size_t *bytes_out);
+int paged_tree_attention(void *out, const void *q, int q_dtype,
+                         const void *k_cache, const void *v_cache, int cache_dtype,
+                         const float *k_scale, const float *v_scale,
+                         const int32_t *block_table, int max_blocks_per_seq,
+                         const int32_t *context_lens,
+                         const uint64_t *tree_mask, int mask_per_seq, const int32_t *tree_lens,
+                         int B, int q_len, int window, int Hq, int Hkv, int D,
+                         int64_t num_blocks, float scale,
+                         void *workspace, size_t workspace_bytes,
+                         pkv_stream_t stream);
+
+/*
+ * Which drafted tokens the target model accepts, and the token that follows.
+ * Node i's parent is the highest node below i in its mask; its children are
+ * tried in index order, starting at node 0.  p_v is the target's distribution
+ * after node v (row b * q_len + v of target_probs), q_v the draft's, from which
+ * v's children were drawn.
+ *  - draft_probs and uniforms given: sampled drafts.  Child c of v, after j
+ *    refusals at v, is accepted iff u_c q_v(c) z_j < w_j(c) with
+ *      w_j(t) = max(p_v(t) - a_j q_v(t), 0), z_j = sum_t w_j(t),
+ *      a_0 = 0, z_0 = 1, a_(j+1) = a_j + z_j
+ *    (speculative sampling: each refusal leaves the normalised residual
+ *    max(r - q, 0)), so that the tokens are distributed as the target's.
+ *  - draft_probs NULL, uniforms given: deterministic drafts (each node's most
+ *    likely continuations).  Child c is accepted iff
+ *    u_c (1 - sum of p_v over the distinct tokens refused) < p_v(c); a token
+ *    already refused at v counts 0.  w is p_v with the refused tokens at 0.
+ *  - uniforms NULL (then draft_probs is NULL too, else PKV_EINVAL): greedy.
+ *    Child c is accepted iff its token is p_v's largest (the lowest id of
+ *    equals); target_probs may hold logits.
+ * next_token[b]: with v the last accepted node, the smallest t whose
+ * w(0) + .. + w(t) exceeds u_0 * sum(w) (u_0 is node 0's number, used for this
+ * alone); greedy: p_v's largest.  -1 if w has no weight at all, or for a row
+ * of NaN.
+ *
+ *   path        [B][q_len] int32: the accepted nodes, node 0 first, then -1
+ *   path_len    [B] int32: how many (>= 1; 0 for n_b = 0)
+ *   next_token  [B] int64 (-1 for n_b = 0)
+ *   draft_tokens [B][q_len] int64; node 0's plays no part; an id outside
+ *               [0, V) is never accepted
+ *   target_probs, draft_probs  rows of V values of prob_dtype (F32, F16 or
+ *               BF16), ld_target / ld_draft elements apart (>= V), row
+ *               b * q_len + i; probabilities are >= 0 and sum to 1
+ *   uniforms    [B][q_len] fp32 in [0, 1)
+ * Sums are kept to ~48 bits, so a draw agrees with one made in double
+ * precision.  Needs no workspace; V <= 2^30.
+ */
+int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token,
+                      const int64_t *draft_tokens,
+                      const uint64_t *tree_mask, int mask_per_seq, const int32_t *tree_lens,
+                      const void *target_probs, int64_t ld_target,
+                      const void *draft_probs, int64_t ld_draft, int prob_dtype,
+                      const float *uniforms, int B, int q_len, int V,
+                      pkv_stream_t stream);
+
+/*
+ * Moves the accepted path's K / V rows together, in place: for k = 0 ..
+ * path_len[b] - 1 the row of position start_b + path[b][k] becomes that of
+ * position start_b + k (all kv heads, K and V).  Call it on each layer's cache
+ * with the path of paged_tree_verify; positions past the path keep their
+ * rejected rows until they are written again.  path[b][k] is in [k, n_b) as
+ * paged_tree_verify writes it; an entry that is not moves nothing, nor does one
+ * whose block id is outside [0, num_blocks).  The tree's blocks must not be
+ * shared with another sequence (pkv_bm_append_slots sees to that).
+ * FP8 caches: a row that stays in its block keeps its bytes; one that changes
+ * blocks is stored as e4m3_rne_sat( fp32( decode(q) * s_src ) / s_dst ) with the
+ * destination block's scale, which stays as it is.
+ *   new_lens   [B] int32 or NULL: receives start_b + path_len[b]
+ */
+int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype,
+                      const float *k_scale, const float *v_scale,
+                      const int32_t *path, const int32_t *path_len,
+                      const int32_t *block_table, int max_blocks_per_seq,
+                      const int32_t *context_lens, const int32_t *tree_lens,
+                      int32_t *new_lens, int B, int q_len, int Hkv, int D,
+                      int64_t num_blocks, pkv_stream_t stream);
+
 /*
  * Paged prefill attention on the tensor cores (tcgen05): sequence b's
  * n_b = q_start[b+1] - q_start[b] new tokens — its prompt, or a chunk of it
@@ -538,6 +656,15 @@ int pkv_bm_free(pkv_block_manager *bm, int64_t seq);
  * unknown id. */
 int pkv_bm_release_window(pkv_block_manager *bm, int64_t seq, int64_t window,
                           int64_t *released_out);
+
+/* Shortens a sequence to its first num_tokens tokens (the rejected nodes of a
+ * tree, after paged_tree_commit): blocks past ceil(num_tokens / 16) are
+ * released (refcount - 1, back to the free list at 0, the last block first).
+ * Do not go below the count a sliding window's pkv_bm_release_window was
+ * called at: a shorter sequence's window reaches further back.  PKV_ERANGE if
+ * the sequence is shorter, PKV_EINVAL for num_tokens < 0, PKV_ENOTFOUND for an
+ * unknown id; nothing changes then. */
+int pkv_bm_truncate(pkv_block_manager *bm, int64_t seq, int64_t num_tokens);
 
 /*
  * Reserves the slot of one new token for each of the n sequences seqs[i]:

@@ -15,6 +15,7 @@ __all__ = [
     "PagedKVError", "paged_kv_append", "paged_decode_workspace_bytes",
     "paged_decode_attention", "paged_prefill_attention", "paged_decode_status", "paged_decode_merge",
     "paged_decode_attention_static", "paged_decode_static_status",
+    "paged_tree_workspace_bytes", "paged_tree_attention", "paged_tree_verify", "paged_tree_commit",
     "paged_kv_copy_blocks", "pkv_copy", "pkv_status_string", "pkv_version", "pkv_set_route",
     "pkv_get_route", "pkv_test_stall_next", "BlockManager", "Prepared",
     "DTYPE_CODES", "LIB_PATH", "lib",
@@ -50,6 +51,13 @@ _sig("paged_decode_attention_multi", _i32, _P, _P, _i32, _P, _P, _i32, _P, _P, _
      _i32, _i32, _i32, _i32, _i32, _i32, _i64, ctypes.c_float, _i32, _P, _sz, _P)
 _sig("paged_prefill_attention", _i32, _P, _P, _i32, _P, _P, _i32, _P, _i32, _P, _P,
      _i32, _i32, _i32, _i32, _i32, _i64, ctypes.c_float, _i32, _P, _P)
+_sig("paged_tree_workspace_bytes", _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz))
+_sig("paged_tree_attention", _i32, _P, _P, _i32, _P, _P, _i32, _P, _P, _P, _i32, _P, _P, _i32, _P,
+     _i32, _i32, _i32, _i32, _i32, _i32, _i64, ctypes.c_float, _P, _sz, _P)
+_sig("paged_tree_verify", _i32, _P, _P, _P, _P, _P, _i32, _P, _P, _i64, _P, _i64, _i32, _P,
+     _i32, _i32, _i32, _P)
+_sig("paged_tree_commit", _i32, _P, _P, _i32, _P, _P, _P, _P, _P, _i32, _P, _P, _P,
+     _i32, _i32, _i32, _i32, _i64, _P)
 _sig("paged_decode_status", _i32, _P, _sz, _P, ctypes.POINTER(_i32))
 _sig("paged_decode_attention_static", _i32, _P, _P, _i32, _P, _P, _i32, _P, _P, _P, _i32, _P,
      _i32, _i32, _i32, _i32, _i64, ctypes.c_float, _i32, _P)
@@ -70,6 +78,7 @@ _sig("pkv_bm_adopt", _i32, _P, _i64, _P, _i32, _i64)
 _sig("pkv_bm_fork", _i32, _P, _i64, _i64)
 _sig("pkv_bm_free", _i32, _P, _i64)
 _sig("pkv_bm_release_window", _i32, _P, _i64, _i64, ctypes.POINTER(_i64))
+_sig("pkv_bm_truncate", _i32, _P, _i64, _i64)
 _sig("pkv_bm_append_slots", _i32, _P, _P, _i32, _P, _P, ctypes.POINTER(_i32))
 _sig("pkv_bm_export", _i32, _P, _P, _i32, _P, _i32, _P)
 _sig("pkv_bm_num_free", _i64, _P)
@@ -305,6 +314,184 @@ def paged_prefill_attention(out, q, k_cache, v_cache, block_table, context_lens,
         _dev(status, "status", torch.int32), _stream(stream)), "paged_prefill_attention")
 
 
+def _shape(t, name, *want):
+    """`t` has one of the shapes `want`."""
+    if tuple(t.shape) not in want:
+        raise ValueError(f"{name} must have shape {' or '.join(map(str, want))}, got {tuple(t.shape)}")
+
+
+def _one_device(device, **tensors):
+    """Every tensor given lives on `device`, which must be the current one (the
+    stream and the launch are the current device's)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if device.type == "cuda" and device.index != _torch().cuda.current_device():
+        raise ValueError(f"the tensors are on {device}: make it the current device (torch.cuda.device)")
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a cache's four tensors against one another; (num_blocks, Hkv, D)."""
+    if k_cache.dim() != 4 or k_cache.shape[2] != 16:
+        raise ValueError(f"k_cache must be [num_blocks, Hkv, 16, D], got {tuple(k_cache.shape)}")
+    nb, Hkv, _, D = k_cache.shape
+    _shape(v_cache, "v_cache", tuple(k_cache.shape))
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache is {v_cache.dtype}, k_cache {k_cache.dtype}")
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is not None:
+            _shape(s, name, (nb, Hkv))
+    return nb, Hkv, D
+
+
+def _tree_mask(tree_mask, B, n):
+    """(pointer, mask_per_seq) of an int64 [n] or [B, n] mask."""
+    _shape(tree_mask, "tree_mask", (n,), (B, n))
+    return _dev(tree_mask, "tree_mask", _torch().int64), int(tree_mask.dim() == 2)
+
+
+def paged_tree_workspace_bytes(B, q_len, Hq, Hkv, D, cache_dtype, q_dtype):
+    """Workspace size for paged_tree_attention on the current device.  dtypes
+    are torch dtypes or C codes."""
+    conv = lambda d: d if isinstance(d, int) else _code(_torch().empty(0, dtype=d))
+    out = _sz(0)
+    _check(_L.paged_tree_workspace_bytes(B, q_len, Hq, Hkv, D, conv(cache_dtype), conv(q_dtype),
+                                         ctypes.byref(out)), "paged_tree_workspace_bytes")
+    return out.value
+
+
+def paged_tree_attention(out, q, k_cache, v_cache, block_table, context_lens, tree_mask, scale,
+                         tree_lens=None, k_scale=None, v_scale=None, window=0, workspace=None,
+                         stream=None, prepare=False):
+    """Attention of a tree of drafted tokens over the paged cache.
+
+    q, out [B, q_len, Hq, D]: row i is the tree's node i, the cache's position
+    context_lens[b] - n_b + i; it sees the positions before the tree and the
+    nodes in its mask.  tree_mask int64 [B, q_len], or [q_len] for one tree
+    shared by all sequences; tree_lens int32 [B]: n_b (None: q_len each; rows
+    past n_b of out are left as they were).  workspace: a uint8 CUDA tensor of
+    paged_tree_workspace_bytes(...) bytes, allocated here (by torch) when None;
+    returned for paged_decode_status.  prepare=True returns the call as a
+    Prepared object instead of issuing it."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, q_len, Hq, D], got {tuple(q.shape)}")
+    B, n, Hq, D = q.shape
+    _shape(out, "out", (B, n, Hq, D))
+    if out.dtype != q.dtype:
+        raise TypeError(f"out is {out.dtype}, q {q.dtype}")
+    num_blocks, Hkv, Dc = _cache(k_cache, v_cache, k_scale, v_scale)
+    if Dc != D:
+        raise ValueError(f"q has head dim {D}, the cache {Dc}")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
+    _shape(context_lens, "context_lens", (B,))
+    if tree_lens is not None:
+        _shape(tree_lens, "tree_lens", (B,))
+    mask, per_seq = _tree_mask(tree_mask, B, n)
+    if workspace is None:
+        size = paged_tree_workspace_bytes(B, n, Hq, Hkv, D, _code(k_cache), _code(q))
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    _one_device(q.device, out=out if out.is_cuda else None, k_cache=k_cache, v_cache=v_cache,
+                block_table=block_table, context_lens=context_lens, tree_mask=tree_mask,
+                tree_lens=tree_lens, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
+    args = (_out(out), _dev(q, "q"), _code(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _code(k_cache), _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
+            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+            _dev(context_lens, "context_lens", torch.int32), mask, per_seq,
+            _dev(tree_lens, "tree_lens", torch.int32), B, n, int(window), Hq, Hkv, D, num_blocks, float(scale),
+            _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream))
+    if prepare:
+        return Prepared(_L.paged_tree_attention, args, "paged_tree_attention")
+    _check(_L.paged_tree_attention(*args), "paged_tree_attention")
+    return workspace
+
+
+def _rows(t, name, B, n):
+    """(pointer, row distance, V) of [B, n, V] rows, a fixed number of elements
+    apart (a slice of a wider vocabulary is such a tensor)."""
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != n:
+        raise ValueError(f"{name} must be [{B}, {n}, V], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    V = t.shape[2]
+    sb, sn, sv = t.stride()
+    ld = sn if n > 1 else (sb if B > 1 else V)
+    if (V > 1 and sv != 1) or ld < V or (B > 1 and n > 1 and sb != n * sn):
+        raise ValueError(f"{name} must have contiguous rows a fixed distance apart, got strides {t.stride()}")
+    return t.data_ptr(), ld, V
+
+
+def paged_tree_verify(path, path_len, next_token, draft_tokens, tree_mask, target_probs,
+                      draft_probs=None, uniforms=None, tree_lens=None, stream=None, prepare=False):
+    """Accepts a path of the tree's drafted tokens from the target's
+    probabilities (see include/pagedkv.h for the rule) and draws the next token.
+
+    Writes path int32 [B, n] (accepted nodes, then -1), path_len int32 [B] and
+    next_token int64 [B].  draft_tokens int64 [B, n]; target_probs, draft_probs
+    [B, n, V] fp32 / fp16 / bf16 of one type, rows a fixed distance apart;
+    uniforms fp32 [B, n].  With draft_probs: sampled drafts; without: each
+    node's deterministic continuations; without uniforms too: greedy."""
+    torch = _torch()
+    if draft_tokens.dim() != 2:
+        raise ValueError(f"draft_tokens must be [B, n], got {tuple(draft_tokens.shape)}")
+    B, n = draft_tokens.shape
+    _shape(path, "path", (B, n))
+    _shape(path_len, "path_len", (B,))
+    _shape(next_token, "next_token", (B,))
+    if tree_lens is not None:
+        _shape(tree_lens, "tree_lens", (B,))
+    if uniforms is not None:
+        _shape(uniforms, "uniforms", (B, n))
+    mask, per_seq = _tree_mask(tree_mask, B, n)
+    target, ld_t, V = _rows(target_probs, "target_probs", B, n)
+    draft, ld_d = None, 0
+    if draft_probs is not None:
+        draft, ld_d, Vd = _rows(draft_probs, "draft_probs", B, n)
+        if Vd != V or draft_probs.dtype != target_probs.dtype:
+            raise ValueError("draft_probs must have target_probs' vocabulary and type")
+    _one_device(target_probs.device, path=path, path_len=path_len, next_token=next_token,
+                draft_tokens=draft_tokens, tree_mask=tree_mask, draft_probs=draft_probs,
+                uniforms=uniforms, tree_lens=tree_lens)
+    args = (_dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32),
+            _dev(next_token, "next_token", torch.int64), _dev(draft_tokens, "draft_tokens", torch.int64),
+            mask, per_seq, _dev(tree_lens, "tree_lens", torch.int32), target, ld_t, draft, ld_d,
+            _code(target_probs), _dev(uniforms, "uniforms", torch.float32), B, n, V, _stream(stream))
+    if prepare:
+        return Prepared(_L.paged_tree_verify, args, "paged_tree_verify")
+    _check(_L.paged_tree_verify(*args), "paged_tree_verify")
+
+
+def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_lens, k_scale=None,
+                      v_scale=None, tree_lens=None, new_lens=None, stream=None, prepare=False):
+    """Moves the accepted path's K/V rows together in the paged cache, in
+    place: position context_lens[b] - n_b + k takes the row of node path[b, k].
+    new_lens (optional int32 [B]) receives the lengths that remain."""
+    torch = _torch()
+    num_blocks, Hkv, D = _cache(k_cache, v_cache, k_scale, v_scale)
+    if path.dim() != 2:
+        raise ValueError(f"path must be [B, n], got {tuple(path.shape)}")
+    B, n = path.shape
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
+    for t, name in ((path_len, "path_len"), (context_lens, "context_lens"), (tree_lens, "tree_lens"),
+                    (new_lens, "new_lens")):
+        if t is not None:
+            _shape(t, name, (B,))
+    _one_device(k_cache.device, v_cache=v_cache, path=path, path_len=path_len, block_table=block_table,
+                context_lens=context_lens, tree_lens=tree_lens, new_lens=new_lens, k_scale=k_scale,
+                v_scale=v_scale)
+    args = (_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _code(k_cache),
+            _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
+            _dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32),
+            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+            _dev(context_lens, "context_lens", torch.int32), _dev(tree_lens, "tree_lens", torch.int32),
+            _dev(new_lens, "new_lens", torch.int32), B, n, Hkv, D, num_blocks, _stream(stream))
+    if prepare:
+        return Prepared(_L.paged_tree_commit, args, "paged_tree_commit")
+    _check(_L.paged_tree_commit(*args), "paged_tree_commit")
+
+
 def paged_decode_status(workspace, stream=None):
     """Synchronises the stream; returns the PKV_FLAG_* bits the last decode
     recorded in `workspace` (raises on a timeout or range flag)."""
@@ -423,6 +610,10 @@ class BlockManager:
         _check(_L.pkv_bm_release_window(self._h, seq, window, ctypes.byref(n)),
                "release_outside_window")
         return n.value
+
+    def truncate(self, seq, num_tokens):
+        """Shortens seq to its first num_tokens tokens (rejected drafts)."""
+        _check(_L.pkv_bm_truncate(self._h, seq, num_tokens), "truncate")
 
     def append_slots(self, seqs):
         """One new token per sequence: (slots list, [(src, dst), ...]) or None on OOM."""

@@ -16,6 +16,7 @@
 #include "pagedkv.h"
 #include "mq_decode.h"
 #include "prefill.h"
+#include "tree.h"
 
 namespace pkv {
 
@@ -71,6 +72,8 @@ Registry &registry() {
     r.n += register_decode_f16(r.k + r.n);
     r.n += register_decode_fp8(r.k + r.n);
     r.n += register_decode_f32(r.k + r.n);
+    r.n += register_decode_tree(r.k + r.n);
+    r.n += register_decode_tree_fp8(r.k + r.n);
   });
   return r;
 }
@@ -264,7 +267,7 @@ struct Choice {
 // also compiles alternative shapes and lets PKV_PATH=mma|simt,
 // PKV_DECODE_WARPS, PKV_DECODE_STAGES and PKV_DECODE_GC=8 in the environment
 // pick among them.
-int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c) {
+int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c, bool tree) {
 #ifdef PKV_SWEEP_SHAPES
   static const int force = [] {
     const char *v = std::getenv("PKV_PATH");
@@ -303,7 +306,8 @@ int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c) {
     }
     for (int i = 0; i < r.n; ++i) {
       const DecodeKernel &k = r.k[i];
-      if (k.mma == (mma ? 1 : 0) && k.cache_dtype == cache_dtype && k.q_dtype == q_dtype && k.D == D && k.GC == GC) {
+      if (k.mma == (mma ? 1 : 0) && k.cache_dtype == cache_dtype && k.q_dtype == q_dtype && k.D == D && k.GC == GC &&
+          k.tree == (tree ? 1 : 0)) {
         if (first < 0) first = i;
         if ((want_warps == 0 || k.warps == want_warps) && (want_stages == 0 || k.stages == want_stages)) {
           first = i;
@@ -339,8 +343,8 @@ int validate_decode_shapes(int q_dtype, int cache_dtype, int B, int q_len, int H
 
 // Resolves the kernel and the partition count for a call.
 int plan_call(int cache_dtype, int q_dtype, int B, int q_len, int Hq, int Hkv, int D, int num_splits, Choice *c,
-              int *P) {
-  int rc = choose_kernel(cache_dtype, q_dtype, D, q_len * (Hq / Hkv), c);
+              int *P, bool tree = false) {
+  int rc = choose_kernel(cache_dtype, q_dtype, D, q_len * (Hq / Hkv), c, tree);
   if (rc != PKV_OK) return rc;
   if (num_splits < 0) return PKV_EINVAL;
   if (num_splits > 0) {
@@ -505,6 +509,100 @@ static cudaError_t launch_prefill_auto(const PrefillParams &p, int cache_dtype, 
   return tiles ? launch_prefill_tiles(p, cache_dtype, tmK, tmV, s) : launch_prefill(p, cache_dtype, tmK, tmV, s);
 }
 
+// The decode kernel (8- or 16-row units, one partition per warp) and its
+// split-KV merge: single-token decode, and several new tokens per sequence on
+// the unit route, causal or (tree) under per-node masks.
+struct TreeArgs {
+  const uint64_t *mask;
+  const int32_t *lens;
+  int mask_stride;
+};
+static int run_units(const Choice &c, int P, void *out, const void *q, int q_dtype, const void *k_cache,
+                     const void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
+                     const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens, int B, int q_len,
+                     int window, int Hq, int Hkv, int D, int64_t num_blocks, float scale, void *workspace,
+                     pkv_stream_t stream, const TreeArgs *tree) {
+  const WsLayout L = ws_layout(B, P, D, c.GC);
+  int rc = PKV_OK;
+  const DecodeKernel &k = registry().k[c.ki];
+  int ctas = 0, sms = 0;
+  rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
+  if (rc != PKV_OK) return rc;
+
+  CUtensorMap tmK, tmV;
+  rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
+  if (rc != PKV_OK) return rc;
+  rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
+  if (rc != PKV_OK) return rc;
+
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.out = out;
+  p.q = q;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.hdr = reinterpret_cast<WsHeader *>(ws + L.hdr);
+  p.prefix = reinterpret_cast<int32_t *>(ws + L.prefix);
+  p.starts = reinterpret_cast<int4 *>(ws + L.starts);
+  p.part_o = reinterpret_cast<float *>(ws + L.part_o);
+  p.part_lse = reinterpret_cast<float *>(ws + L.part_lse);
+  p.cta_flags = reinterpret_cast<int32_t *>(ws + L.cta_flags);
+  p.num_blocks = num_blocks;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.G = Hq / Hkv;
+  p.GC = c.GC;
+  p.NC = c.NC;
+  p.HU = Hkv * c.NC;
+  p.q_len = q_len;
+  p.R = q_len * p.G;
+  // a window of 2^30 positions or more covers any context this call accepts
+  p.window = window < (1 << 30) ? window : 0;
+  p.wlen = p.window > 0 ? p.window : (1 << 30);
+  p.P = P;
+  p.max_blocks = max_blocks_per_seq;
+  p.out_dtype = q_dtype;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  if (tree) {
+    p.tree_mask = tree->mask;
+    p.tree_lens = tree->lens;
+    p.mask_stride = tree->mask_stride;
+  }
+  take_stall(p, PKV_STALL_DECODE);
+
+  p.inline_plan = B + 1 <= kInlinePrefix ? 1 : 0;
+  p.n_ctas = (P + k.warps - 1) / k.warps;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool pdl = s != nullptr;  // programmatic launch on explicit streams only
+  cudaError_t e = cudaSuccess;
+  if (!p.inline_plan) {
+    e = launch_plan(p, s);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_ctas);
+  cfg.blockDim = dim3(k.warps * 32);
+  cfg.dynamicSmemBytes = k.smem_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  void *args[3] = {&p, &tmK, &tmV};
+  e = cudaLaunchKernelExC(&cfg, k.fn, args);
+  if (e != cudaSuccess) return cuda_status(e);
+  e = launch_splitk_merge(p, s, pdl);
+  return cuda_status(e);
+}
+
 int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache,
                                  int cache_dtype, const float *k_scale, const float *v_scale,
                                  const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
@@ -632,78 +730,121 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
       return cuda_status(launch_prefill_auto(pp, cache_dtype, tmK, tmV, s));
     }
   }
-  const DecodeKernel &k = registry().k[c.ki];
-  int ctas = 0, sms = 0;
-  rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
-  if (rc != PKV_OK) return rc;
+  return run_units(c, P, out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
+                   max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, D, num_blocks, scale, workspace, stream,
+                   nullptr);
+}
 
-  CUtensorMap tmK, tmV;
-  rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
+int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cache_dtype, int q_dtype,
+                               size_t *bytes_out) {
+  if (!bytes_out) return PKV_EINVAL;
+  int rc = validate_decode_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, 1, 1);
   if (rc != PKV_OK) return rc;
-  rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
+  Choice c;
+  int P = 0;
+  rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
   if (rc != PKV_OK) return rc;
+  *bytes_out = ws_layout(B, P, D, c.GC).total;
+  return PKV_OK;
+}
 
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  DecodeParams p;
+int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                         int cache_dtype, const float *k_scale, const float *v_scale, const int32_t *block_table,
+                         int max_blocks_per_seq, const int32_t *context_lens, const uint64_t *tree_mask,
+                         int mask_per_seq, const int32_t *tree_lens, int B, int q_len, int window, int Hq, int Hkv,
+                         int D, int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                         pkv_stream_t stream) {
+  int rc = validate_decode_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks_per_seq);
+  if (rc != PKV_OK) return rc;
+  if (window < 0 || (mask_per_seq != 0 && mask_per_seq != 1)) return PKV_EINVAL;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return PKV_EINVAL;
+  if (B == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens || !tree_mask) return PKV_EINVAL;
+  if (cache_dtype == PKV_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_EINVAL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return PKV_EINVAL;
+  Choice c;
+  int P = 0;
+  rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
+  if (rc != PKV_OK) return rc;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < ws_layout(B, P, D, c.GC).total)
+    return PKV_EWORKSPACE;
+  const TreeArgs tree{tree_mask, tree_lens, mask_per_seq ? q_len : 0};
+  return run_units(c, P, out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
+                   max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, D, num_blocks, scale, workspace, stream,
+                   &tree);
+}
+
+int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token, const int64_t *draft_tokens,
+                      const uint64_t *tree_mask, int mask_per_seq, const int32_t *tree_lens, const void *target_probs,
+                      int64_t ld_target, const void *draft_probs, int64_t ld_draft, int prob_dtype,
+                      const float *uniforms, int B, int q_len, int V, pkv_stream_t stream) {
+  if (B < 0 || V <= 0 || q_len < 1 || q_len > PKV_MAX_Q_LEN) return PKV_EINVAL;
+  if (prob_dtype != PKV_F32 && prob_dtype != PKV_F16 && prob_dtype != PKV_BF16)
+    return esize_of(prob_dtype) == 0 ? PKV_EINVAL : PKV_EUNSUPPORTED;
+  if (mask_per_seq != 0 && mask_per_seq != 1) return PKV_EINVAL;
+  if (V > (1 << 30) || B > (1 << 24)) return PKV_EUNSUPPORTED;
+  if (ld_target < V || (draft_probs && ld_draft < V) || (draft_probs && !uniforms)) return PKV_EINVAL;
+  if (B == 0) return PKV_OK;
+  if (!path || !path_len || !next_token || !draft_tokens || !tree_mask || !target_probs) return PKV_EINVAL;
+  const uintptr_t es = (uintptr_t)esize_of(prob_dtype);
+  if (reinterpret_cast<uintptr_t>(target_probs) % es != 0 || reinterpret_cast<uintptr_t>(draft_probs) % es != 0 ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)
+    return PKV_EINVAL;
+  VerifyParams p;
   std::memset(&p, 0, sizeof(p));
-  p.out = out;
-  p.q = q;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
+  p.path = path;
+  p.path_len = path_len;
+  p.next_token = next_token;
+  p.tokens = draft_tokens;
+  p.mask = tree_mask;
+  p.lens = tree_lens;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.u = uniforms;
+  p.ld_target = ld_target;
+  p.ld_draft = ld_draft;
+  p.n = q_len;
+  p.mask_stride = mask_per_seq ? q_len : 0;
+  p.V = V;
+  return cuda_status(launch_tree_verify(p, prob_dtype, B, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
+                      const int32_t *path, const int32_t *path_len, const int32_t *block_table,
+                      int max_blocks_per_seq, const int32_t *context_lens, const int32_t *tree_lens,
+                      int32_t *new_lens, int B, int q_len, int Hkv, int D, int64_t num_blocks, pkv_stream_t stream) {
+  if (B < 0 || Hkv <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0) return PKV_EINVAL;
+  if (q_len < 1 || q_len > PKV_MAX_Q_LEN) return PKV_EINVAL;
+  if (esize_of(cache_dtype) == 0) return PKV_EINVAL;
+  if (D != 64 && D != 128) return PKV_EUNSUPPORTED;
+  if (max_blocks_per_seq > (1 << 26) || (double)B * Hkv >= 1073741000.0) return PKV_EUNSUPPORTED;
+  if (B == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !path || !path_len || !block_table || !context_lens) return PKV_EINVAL;
+  if (cache_dtype == PKV_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_EINVAL;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_EINVAL;
+  CommitParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.k_cache = static_cast<uint8_t *>(k_cache);
+  p.v_cache = static_cast<uint8_t *>(v_cache);
+  if (cache_dtype == PKV_FP8_E4M3) {
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+  }
+  p.path = path;
+  p.path_len = path_len;
   p.block_table = block_table;
   p.context_lens = context_lens;
-  p.hdr = reinterpret_cast<WsHeader *>(ws + L.hdr);
-  p.prefix = reinterpret_cast<int32_t *>(ws + L.prefix);
-  p.starts = reinterpret_cast<int4 *>(ws + L.starts);
-  p.part_o = reinterpret_cast<float *>(ws + L.part_o);
-  p.part_lse = reinterpret_cast<float *>(ws + L.part_lse);
-  p.cta_flags = reinterpret_cast<int32_t *>(ws + L.cta_flags);
+  p.tree_lens = tree_lens;
+  p.new_lens = new_lens;
   p.num_blocks = num_blocks;
   p.B = B;
-  p.Hq = Hq;
+  p.n = q_len;
   p.Hkv = Hkv;
-  p.D = D;
-  p.G = Hq / Hkv;
-  p.GC = c.GC;
-  p.NC = c.NC;
-  p.HU = Hkv * c.NC;
-  p.q_len = q_len;
-  p.R = q_len * p.G;
-  // a window of 2^30 positions or more covers any context this call accepts
-  p.window = window < (1 << 30) ? window : 0;
-  p.wlen = p.window > 0 ? p.window : (1 << 30);
-  p.P = P;
   p.max_blocks = max_blocks_per_seq;
-  p.out_dtype = q_dtype;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  take_stall(p, PKV_STALL_DECODE);
-
-  p.inline_plan = B + 1 <= kInlinePrefix ? 1 : 0;
-  p.n_ctas = (P + k.warps - 1) / k.warps;
-
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool pdl = s != nullptr;  // programmatic launch on explicit streams only
-  cudaError_t e = cudaSuccess;
-  if (!p.inline_plan) {
-    e = launch_plan(p, s);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
-
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_ctas);
-  cfg.blockDim = dim3(k.warps * 32);
-  cfg.dynamicSmemBytes = k.smem_bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  void *args[3] = {&p, &tmK, &tmV};
-  e = cudaLaunchKernelExC(&cfg, k.fn, args);
-  if (e != cudaSuccess) return cuda_status(e);
-  e = launch_splitk_merge(p, s, pdl);
-  return cuda_status(e);
+  p.row_bytes = D * esize_of(cache_dtype);
+  return cuda_status(launch_tree_commit(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int paged_prefill_attention(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache,

@@ -139,6 +139,29 @@ int pkv_bm_release_window(pkv_block_manager *bm, int64_t seq, int64_t window, in
   return PKV_OK;
 }
 
+int pkv_bm_truncate(pkv_block_manager *bm, int64_t seq, int64_t num_tokens) {
+  if (!bm || num_tokens < 0) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq);
+  if (it == bm->seqs.end()) return PKV_ENOTFOUND;
+  pkv_block_manager::Seq &s = it->second;
+  if (num_tokens > s.tokens) return PKV_ERANGE;
+  try {
+    bm->compact();
+    // the free list never holds more than num_blocks entries (compacted above)
+    bm->free_list.reserve((size_t)bm->num_blocks);
+  } catch (...) {
+    return PKV_EOOM;
+  }
+  const size_t keep = (size_t)blocks_for(num_tokens);
+  while (s.table.size() > keep) {  // last block first: the next append takes the earliest one again
+    const int32_t blk = s.table.back();
+    s.table.pop_back();
+    if (blk >= 0 && --bm->refcount[blk] == 0) bm->free_list.push_back(blk);
+  }
+  s.tokens = num_tokens;
+  return PKV_OK;
+}
+
 int pkv_bm_append_slots(pkv_block_manager *bm, const int64_t *seqs, int n, int64_t *slot_out, int32_t *cow_pairs_out,
                         int *n_cow_out) {
   if (!bm || n < 0 || (n > 0 && (!seqs || !slot_out || !cow_pairs_out)) || !n_cow_out) return PKV_EINVAL;

@@ -54,12 +54,17 @@ namespace pkv {
 // rescale per 32 tokens) and one producer step — an fp8 block carries half a
 // 16-bit block's bytes for the same per-block instructions, which made the
 // one-block fp8 kernel issue-bound.
-template <class CacheT, class QT, int D_, int GC_, bool MMA_, int WARPS_, int BUDGET_, int BPS_ = 1>
+// TREE_: the new tokens form a tree (paged_tree_attention): besides the cached
+// positions before the tree, row r sees the tree's nodes that its node's
+// 64-bit mask names.  Blocks wholly before the tree (and inside every row's
+// window) need no mask at all; only a context's last few blocks take the
+// per-position test.
+template <class CacheT, class QT, int D_, int GC_, bool MMA_, int WARPS_, int BUDGET_, int BPS_ = 1, bool TREE_ = false>
 struct DecodeCfg {
   using Cache = CacheT;
   using Q = QT;
   static constexpr int D = D_, GC = GC_, WARPS = WARPS_, BPS = BPS_;
-  static constexpr bool MMA = MMA_;
+  static constexpr bool MMA = MMA_, TREE = TREE_;
   static constexpr bool FP8 = CacheT::kBytes == 1;
   static constexpr int ROWB = D * CacheT::kBytes;           // bytes per token row
   static constexpr int TILE = kBlock * ROWB;                // bytes per (block, head) tile
@@ -103,7 +108,8 @@ __device__ __forceinline__ void load_seq(Producer &pr, const DecodeParams &p) {
   const int ctx = clamped_len(p, __ldg(p.context_lens + pr.b));
   pr.ctx = ctx;
   pr.n = (ctx + kBlock - 1) / kBlock;
-  pr.j0 = first_block(p, ctx);
+  if (p.tree_lens != nullptr && seq_rows(p, pr.b) == 0) pr.n = 0;  // no query rows: nothing to stream
+  pr.j0 = first_block(p, pr.b, ctx);
 }
 
 // Block-table entry (and, for fp8, the block's K / V scales) of block jj of
@@ -261,11 +267,50 @@ __device__ __forceinline__ int row_back(const DecodeParams &p, int r) {
   return max(0, p.q_len - 1 - r / p.G);
 }
 
+// Rows of kv head chunk r0 .. r0 + GC - 1 of sequence b that exist (<= 0: none).
+template <class Cfg>
+__device__ __forceinline__ int unit_rows(const DecodeParams &p, int b, int r0) {
+  return min(Cfg::GC, (Cfg::TREE ? seq_rows(p, b) * p.G : p.R) - r0);
+}
+
+// What one row sees of a tree sequence: cached positions [lo, start), then
+// node j at position start + j iff bit j of mask.
+struct TreeRow {
+  uint64_t mask;
+  int lo;
+};
+// Row r of sequence b (ctx: its clamped length, n: its nodes); a row past the
+// sequence's nodes sees nothing.  With a window W a node at depth d (the nodes
+// its mask names, itself among them) stands at position start + d - 1 and sees
+// [start + d - W, start).
+__device__ __forceinline__ TreeRow tree_row(const DecodeParams &p, int b, int ctx, int n, int r) {
+  TreeRow t;
+  const int i = r / p.G;
+  t.mask = i < n ? __ldg(p.tree_mask + (size_t)b * p.mask_stride + i) & (~0ull >> (64 - n)) : 0ull;
+  t.lo = i < n ? (p.window > 0 ? ctx - n + max(1, __popcll(t.mask)) - p.window : 0) : INT32_MAX;
+  return t;
+}
+__device__ __forceinline__ bool tree_sees(const TreeRow &r, int start, int pos) {
+  const int t = pos - start;
+  return t < 0 ? pos >= r.lo : (t < 64 && ((r.mask >> t) & 1));
+}
+
 // ---------------------------------------------------------------------------
 // MMA path state and steps.
 // ---------------------------------------------------------------------------
+// The rows' views of a tree sequence (empty for other kernels).
+template <int NH, bool TREE>
+struct MmaTree {};
+template <int NH>
+struct MmaTree<NH, true> {
+  TreeRow row[NH][2];  // of score columns 8 nh + 2 tig, 8 nh + 2 tig + 1
+  int start, lo_hi;    // the tree's first position; no row's view starts after lo_hi
+  // every row sees positions [pos, pos + count)
+  __device__ __forceinline__ bool all_see(int pos, int count) const { return pos + count <= start && pos >= lo_hi; }
+};
+
 template <class Cfg>
-struct MmaState {
+struct MmaState : MmaTree<(Cfg::GC >= 8 ? Cfg::GC / 8 : 1), Cfg::TREE> {
   static constexpr int KS = Cfg::D / 16;  // k-steps of q.K
   static constexpr int MT = Cfg::D / 16;  // m-tiles of V^T
   static constexpr int NH = Cfg::GC >= 8 ? Cfg::GC / 8 : 1;  // 8-row column groups of a unit
@@ -281,7 +326,16 @@ __device__ __forceinline__ void mma_begin(MmaState<Cfg> &st, const DecodeParams 
                                           int lane) {
   const int gid = lane >> 2, tig = lane & 3;
   const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
-  const int gc = min(Cfg::GC, p.R - r0);
+  const int gc = unit_rows<Cfg>(p, m.b, r0);
+  if constexpr (Cfg::TREE) {
+    const int ctx = m.j * kBlock + m.rem, n = seq_rows(p, m.b);
+    st.start = ctx - n;
+    st.lo_hi = p.window > 0 ? st.start + p.q_len - p.window : 0;
+#pragma unroll
+    for (int nh = 0; nh < MmaState<Cfg>::NH; ++nh)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) st.row[nh][c] = tree_row(p, m.b, ctx, n, r0 + 8 * nh + 2 * tig + c);
+  }
   st.bk_lo = row_back(p, r0 + Cfg::GC - 1);  // row_back does not grow with the row
   st.bk_hi = row_back(p, r0);
 #pragma unroll
@@ -409,10 +463,20 @@ __device__ __forceinline__ void mma_compute(MmaState<Cfg> &st, const MmaFrags<Cf
   // ---- online softmax over the block (log2 domain) ----
   const float sc = p.scale_log2 * m.ks;
   float x0 = s[0] * sc, x1 = s[1] * sc, x2 = s[2] * sc, x3 = s[3] * sc;
-  if ((uint32_t)(gid - base0) >= wl) x0 = -INFINITY;
-  if ((uint32_t)(gid - base1) >= wl) x1 = -INFINITY;
-  if ((uint32_t)(gid + 8 - base0) >= wl) x2 = -INFINITY;
-  if ((uint32_t)(gid + 8 - base1) >= wl) x3 = -INFINITY;
+  if constexpr (Cfg::TREE) {
+    const int pos = m.j * kBlock;
+    if (!st.all_see(pos, kBlock)) {
+      if (!tree_sees(st.row[0][0], st.start, pos + gid)) x0 = -INFINITY;
+      if (!tree_sees(st.row[0][1], st.start, pos + gid)) x1 = -INFINITY;
+      if (!tree_sees(st.row[0][0], st.start, pos + gid + 8)) x2 = -INFINITY;
+      if (!tree_sees(st.row[0][1], st.start, pos + gid + 8)) x3 = -INFINITY;
+    }
+  } else {
+    if ((uint32_t)(gid - base0) >= wl) x0 = -INFINITY;
+    if ((uint32_t)(gid - base1) >= wl) x1 = -INFINITY;
+    if ((uint32_t)(gid + 8 - base0) >= wl) x2 = -INFINITY;
+    if ((uint32_t)(gid + 8 - base1) >= wl) x3 = -INFINITY;
+  }
   float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
   // the running maxima change only when some lane holds a larger score;
   // otherwise the exchange and the rescale (by exactly 1) are skipped
@@ -604,7 +668,20 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
     if (two) {
       y0 = t[nh][0] * sc1; y1 = t[nh][1] * sc1; y2 = t[nh][2] * sc1; y3 = t[nh][3] * sc1;
     }
-    if (!full) {
+    if constexpr (Cfg::TREE) {
+      const int pos = m.j * kBlock;
+      if (!st.all_see(pos, two ? 2 * kBlock : kBlock)) {
+        const TreeRow &ra = st.row[nh][0], &rb = st.row[nh][1];
+        if (!tree_sees(ra, st.start, pos + gid)) x0 = -INFINITY;
+        if (!tree_sees(rb, st.start, pos + gid)) x1 = -INFINITY;
+        if (!tree_sees(ra, st.start, pos + gid + 8)) x2 = -INFINITY;
+        if (!tree_sees(rb, st.start, pos + gid + 8)) x3 = -INFINITY;
+        if (!tree_sees(ra, st.start, pos + gid + 16)) y0 = -INFINITY;
+        if (!tree_sees(rb, st.start, pos + gid + 16)) y1 = -INFINITY;
+        if (!tree_sees(ra, st.start, pos + gid + 24)) y2 = -INFINITY;
+        if (!tree_sees(rb, st.start, pos + gid + 24)) y3 = -INFINITY;
+      }
+    } else if (!full) {
       // token rows r of a block visible to score column c: base_c <= r < base_c + W
       // (see mma_compute); the second block's base is 16 lower
       const int base0 = rem0 - st.back[nh][0] - p.wlen, base1 = rem0 - st.back[nh][1] - p.wlen;
@@ -674,7 +751,7 @@ __device__ __forceinline__ void mma_finish(MmaState<Cfg> &st, const DecodeParams
                                            int w, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
   const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
-  const int gc = min(Cfg::GC, p.R - r0);
+  const int gc = unit_rows<Cfg>(p, m.b, r0);
   const bool complete = m.flags & kComplete;
   // partials: [worker][slot][GC rows][D]
   const size_t base = ((size_t)w * 2 + ((m.flags & kWFirst) ? 0 : 1)) * Cfg::GC;
@@ -728,6 +805,8 @@ struct SimtState {
   float acc[Cfg::GC][DPL];
   float m[Cfg::GC], l[Cfg::GC];
   int back[Cfg::GC];
+  TreeRow row[Cfg::TREE ? Cfg::GC : 1];
+  int start;
 };
 
 // 16 bytes of cache elements -> floats
@@ -796,7 +875,7 @@ template <class Cfg>
 __device__ __forceinline__ void simt_begin(SimtState<Cfg> &st, const DecodeParams &p, const StageMeta &m,
                                            float *qbuf, int lane) {
   const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
-  const int gc = min(Cfg::GC, p.R - r0);
+  const int gc = unit_rows<Cfg>(p, m.b, r0);
   __syncwarp();
   for (int idx = lane; idx < Cfg::GC * Cfg::D; idx += 32) {
     const int g = idx / Cfg::D, d = idx % Cfg::D;
@@ -806,6 +885,11 @@ __device__ __forceinline__ void simt_begin(SimtState<Cfg> &st, const DecodeParam
 #pragma unroll
   for (int g = 0; g < Cfg::GC; ++g) {
     st.back[g] = row_back(p, r0 + g);
+    if constexpr (Cfg::TREE) {
+      const int ctx = m.j * kBlock + m.rem, n = seq_rows(p, m.b);
+      st.start = ctx - n;
+      st.row[g] = tree_row(p, m.b, ctx, n, r0 + g);
+    }
     st.m[g] = -INFINITY;
     st.l[g] = 0.f;
 #pragma unroll
@@ -826,7 +910,7 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
   const int nvalid = m.nvalid;
   int vis = 0;  // rows visible to some column: p.V skips the rest
 #pragma unroll
-  for (int g = 0; g < GC; ++g) vis = max(vis, min(nvalid, m.rem - st.back[g]));
+  for (int g = 0; g < GC; ++g) vis = Cfg::TREE ? nvalid : max(vis, min(nvalid, m.rem - st.back[g]));
 
   // scores: lane (t, half) dots token t with half of q, then the halves add
   float part[GC];
@@ -853,7 +937,10 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
 #pragma unroll
   for (int g = 0; g < GC; ++g) {
     float x = part[g] + __shfl_xor_sync(kFull, part[g], 16);
-    x = ((uint32_t)(t - (m.rem - st.back[g] - p.wlen)) < (uint32_t)p.wlen) ? x * sc : -INFINITY;
+    if constexpr (Cfg::TREE)
+      x = tree_sees(st.row[g], st.start, m.j * kBlock + t) ? x * sc : -INFINITY;
+    else
+      x = ((uint32_t)(t - (m.rem - st.back[g] - p.wlen)) < (uint32_t)p.wlen) ? x * sc : -INFINITY;
     float bm = x;
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, off));
@@ -889,7 +976,7 @@ __device__ __forceinline__ void simt_finish(SimtState<Cfg> &st, const DecodePara
                                             int w, int lane) {
   constexpr int DPL = SimtState<Cfg>::DPL;
   const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
-  const int gc = min(Cfg::GC, p.R - r0);
+  const int gc = unit_rows<Cfg>(p, m.b, r0);
   if (m.flags & kComplete) {
 #pragma unroll
     for (int g = 0; g < Cfg::GC; ++g) {
@@ -921,8 +1008,8 @@ __device__ __forceinline__ void simt_finish(SimtState<Cfg> &st, const DecodePara
 // needed; CTA 0 also stores it for the merge kernel.  Lengths are clamped to
 // [0, 16 * max_blocks] and flagged.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int clamp_len(const DecodeParams &p, int ctx, int *flags) {
-  if (ctx < 0 || ctx > p.max_blocks * kBlock) *flags |= PKV_FLAG_BAD_LEN;
+__device__ __forceinline__ int clamp_len(const DecodeParams &p, int b, int ctx, int *flags) {
+  *flags |= len_flags(p, b, ctx);
   return clamped_len(p, ctx);
 }
 
@@ -933,7 +1020,7 @@ __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_pr
   const int b0 = tid * k;
   int sum = 0, flags = 0;
   for (int i = 0; i < k; ++i)
-    if (b0 + i < p.B) sum += seq_items(p, clamp_len(p, __ldg(p.context_lens + b0 + i), &flags));
+    if (b0 + i < p.B) sum += seq_items(p, b0 + i, clamp_len(p, b0 + i, __ldg(p.context_lens + b0 + i), &flags));
   int x = sum;  // inclusive scan within the warp
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -959,7 +1046,7 @@ __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_pr
     const int b = b0 + i;
     if (b < p.B) {
       s_prefix[b] = run;
-      run += seq_items(p, clamp_len(p, __ldg(p.context_lens + b), &unused));
+      run += seq_items(p, b, clamp_len(p, b, __ldg(p.context_lens + b), &unused));
       if (b == p.B - 1) s_prefix[p.B] = run;
     }
   }
@@ -986,7 +1073,7 @@ __device__ __forceinline__ int4 locate(const DecodeParams &p, const int32_t *pre
   }
   const int n = pre[lo + 1] - pre[lo];
   const int64_t rr = s - (int64_t)p.HU * pre[lo];
-  const int j0 = first_block(p, clamped_len(p, __ldg(p.context_lens + lo)));
+  const int j0 = first_block(p, lo, clamped_len(p, __ldg(p.context_lens + lo)));
   return make_int4((int)s, lo, (int)(rr / n), j0 + (int)(rr % n));
 }
 
@@ -1159,6 +1246,7 @@ DecodeKernel decode_entry() {
   k.warps = Cfg::WARPS;
   k.stages = Cfg::STAGES;
   k.smem_bytes = Cfg::SMEM;
+  k.tree = Cfg::TREE ? 1 : 0;
   return k;
 }
 

@@ -1,0 +1,21 @@
+// decode_tree.cu — decode-attention kernel variants for a tree of drafted
+// tokens (paged_tree_attention) on bf16, f16 and fp32 caches: the pipeline
+// shapes of decode_bf16.cu / decode_f16.cu / decode_f32.cu with the tree's masks.
+#include "decode.cuh"
+
+namespace pkv {
+
+int register_decode_tree(DecodeKernel *out) {
+  int n = 0;
+  out[n++] = decode_entry<DecodeCfg<BF16, BF16, 128, 8, true, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<BF16, BF16, 64, 8, true, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F16, F16, 128, 8, true, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F16, F16, 64, 8, true, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F32, F32, 128, 2, false, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F32, F32, 64, 2, false, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F32, F32, 128, 1, false, kWarps, kBudget, 1, true>>();
+  out[n++] = decode_entry<DecodeCfg<F32, F32, 64, 1, false, kWarps, kBudget, 1, true>>();
+  return n;
+}
+
+}  // namespace pkv

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "pagedkv.h"
+
 namespace pkv {
 
 constexpr int kBlock = 16;      // tokens per physical block (PKV_BLOCK_SIZE)
@@ -74,6 +76,11 @@ struct DecodeParams {
   uint64_t stall_ns;    // failure-path test hook (pkv_test_stall_next): 0 = off
   int inline_plan;      // 1: the decode kernel computes prefix and partition starts itself
   int n_ctas;           // decode grid size
+  // tree of drafted tokens (paged_tree_attention; null otherwise): node i of
+  // sequence b sees node j iff bit j of tree_mask[b * mask_stride + i] is set
+  const uint64_t *tree_mask;
+  const int32_t *tree_lens;  // [B] nodes of each sequence (<= q_len), or null: q_len
+  int mask_stride;           // q_len, or 0: one tree for every sequence
 };
 
 #ifdef __CUDACC__
@@ -81,15 +88,30 @@ struct DecodeParams {
 __device__ __forceinline__ int clamped_len(const DecodeParams &p, int ctx) {
   return ctx < 0 ? 0 : (ctx > p.max_blocks * kBlock ? p.max_blocks * kBlock : ctx);
 }
-// First block any row of a sequence of (clamped) length ctx can see: with a
-// window, row 0's window starts at ctx - (q_len - 1) - W.
-__device__ __forceinline__ int first_block(const DecodeParams &p, int ctx) {
-  const int lo = p.window > 0 ? ctx - (p.q_len - 1) - p.window : 0;
+// New tokens of sequence b: q_len, or its tree's node count (clamped to [0, q_len]).
+__device__ __forceinline__ int seq_rows(const DecodeParams &p, int b) {
+  return p.tree_lens == nullptr ? p.q_len : min(max(__ldg(p.tree_lens + b), 0), p.q_len);
+}
+// First block any row of sequence b, of (clamped) length ctx, can see: with a
+// window, row 0's window starts at ctx - (n - 1) - W, n its new tokens (tree
+// nodes of depth 1 see as far back).
+__device__ __forceinline__ int first_block(const DecodeParams &p, int b, int ctx) {
+  const int lo = p.window > 0 ? ctx - (seq_rows(p, b) - 1) - p.window : 0;
   return lo > 0 ? lo / kBlock : 0;
 }
-// Work items (blocks streamed per unit) of a sequence of (clamped) length ctx.
-__device__ __forceinline__ int seq_items(const DecodeParams &p, int ctx) {
-  return (ctx + kBlock - 1) / kBlock - first_block(p, ctx);
+// Work items (blocks streamed per unit) of sequence b of (clamped) length ctx.
+__device__ __forceinline__ int seq_items(const DecodeParams &p, int b, int ctx) {
+  if (p.tree_lens != nullptr && seq_rows(p, b) == 0) return 0;
+  return (ctx + kBlock - 1) / kBlock - first_block(p, b, ctx);
+}
+// PKV_FLAG_BAD_LEN if sequence b's length or tree size is out of range (both are clamped).
+__device__ __forceinline__ int len_flags(const DecodeParams &p, int b, int ctx) {
+  bool bad = ctx < 0 || ctx > p.max_blocks * kBlock;
+  if (p.tree_lens != nullptr) {
+    const int n = __ldg(p.tree_lens + b);
+    bad |= n < 0 || n > p.q_len;
+  }
+  return bad ? PKV_FLAG_BAD_LEN : 0;
 }
 // Partitions that receive work: P, or one per work item when the call has
 // fewer items than partitions (a small step: more partitions would only add
@@ -116,12 +138,15 @@ struct DecodeKernel {
   int cache_dtype, q_dtype, D, GC;
   int warps, stages;
   size_t smem_bytes;
+  int tree;             // 1 = masks from a tree of drafted tokens
 };
 // Appends the variants a translation unit compiled; returns how many.
 int register_decode_bf16(DecodeKernel *out);
 int register_decode_f16(DecodeKernel *out);
 int register_decode_fp8(DecodeKernel *out);
 int register_decode_f32(DecodeKernel *out);
+int register_decode_tree(DecodeKernel *out);
+int register_decode_tree_fp8(DecodeKernel *out);
 
 // Paged prefill (tcgen05): each sequence's new tokens attend causally.
 struct PrefillParams {

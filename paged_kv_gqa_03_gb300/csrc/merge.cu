@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeParams p) {
     int n = 0;
     if (b < p.B) {
       const int ctx = p.context_lens[b];
-      if (ctx < 0 || ctx > p.max_blocks * kBlock) flags |= PKV_FLAG_BAD_LEN;
-      n = seq_items(p, clamped_len(p, ctx));
+      flags |= len_flags(p, b, ctx);
+      n = seq_items(p, b, clamped_len(p, ctx));
     }
     int x = n;  // inclusive scan within the warp
 #pragma unroll
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeParams p) {
       }
       const int n = pre[lo + 1] - pre[lo];
       const int64_t rr = s - (int64_t)p.HU * pre[lo];
-      const int j0 = first_block(p, clamped_len(p, p.context_lens[lo]));
+      const int j0 = first_block(p, lo, clamped_len(p, p.context_lens[lo]));
       r = make_int4((int)s, lo, (int)(rr / n), j0 + (int)(rr % n));
     }
     p.starts[w] = r;
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(512) splitk_merge_kernel(const DecodeParams p)
   const int u = blockIdx.x;
   const int b = u / p.HU, hu = u % p.HU;
   const int h = hu / p.NC, r0 = (hu % p.NC) * p.GC;
-  const int gc = min(p.GC, p.R - r0);
+  const int gc = min(p.GC, (p.tree_lens ? seq_rows(p, b) * p.G : p.R) - r0);
+  if (gc <= 0) return;  // (tree) rows past the sequence's nodes are left as they were
   const int D = p.D;
   const int pb = p.prefix[b];
   const int n = p.prefix[b + 1] - pb;

@@ -1,0 +1,196 @@
+"""paged_tree_attention against its definition in 64 bits, through the binding:
+types, head layouts, tree shapes, lengths, masks, windows, and the calls around
+it (streams, graphs, status)."""
+import numpy as np
+import pytest
+import torch
+
+from tree_reference import Inputs, check_attention, masks_of, to_i64
+
+pytestmark = pytest.mark.gpu
+
+
+def _pkv():
+    import paged_kv_gqa_03_gb300 as pkv
+    return pkv
+
+
+def _call(x, window=0, mask=None, fill=7.0, lens=True, **kw):
+    pkv, dev = _pkv(), "cuda"
+    out = torch.full(x.q.shape, fill, dtype=x.q.dtype, device=dev)
+    up = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    ws = pkv.paged_tree_attention(
+        out, x.q.to(dev), x.kc.to(dev), x.vc.to(dev), torch.from_numpy(x.table).to(dev),
+        torch.tensor(x.ctx, dtype=torch.int32, device=dev), up(x.mask if mask is None else mask), x.scale,
+        tree_lens=torch.tensor(x.nodes, dtype=torch.int32, device=dev) if lens else None,
+        k_scale=up(x.ks), v_scale=up(x.vs), window=window, **kw)
+    return out, ws
+
+
+def _run(x, window=0, **kw):
+    out, ws = _call(x, window, **kw)
+    rc, flags = _pkv().paged_decode_status(ws)
+    assert (rc, flags) == (0, 0)
+    check_attention(out, x, window, untouched=7.0)
+    return out
+
+
+TYPES = [("bf16", "bf16"), ("f16", "f16"), ("fp8_e4m3", "bf16"), ("fp8_e4m3", "f16"), ("f32", "f32")]
+
+
+@pytest.mark.parametrize("dtype,q_dtype", TYPES, ids=["-".join(t) for t in TYPES])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (6, 2, 64), (4, 4, 128), (14, 2, 128)])
+@pytest.mark.parametrize("n", [1, 5, 17])
+def test_types_and_heads(dtype, q_dtype, Hq, Hkv, D, n):
+    """Contexts of the tree alone, inside one block, ending at and inside tiles."""
+    _run(Inputs(11 + n, [n, n + 1, 16 + n, 128, 150 + n, 300], n, Hq, Hkv, D, dtype, q_dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8_e4m3", "f32"])
+@pytest.mark.parametrize("n,kind", [(64, "random"), (64, "star"), (33, "chain"), (2, "random")])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 128), (3, 1, 64)])
+def test_tree_sizes(dtype, n, kind, Hq, Hkv, D):
+    """The widest trees (R = 512 and 192 rows per kv head), every tile boundary inside them."""
+    _run(Inputs(5, [64, 100, 128 + 64, 129 + 63, 257, 700], n, Hq, Hkv, D, dtype, kind=kind))
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 12), ("bf16", 16, 1, 128, 40), ("f16", 4, 2, 64, 9),
+                                              ("fp8_e4m3", 8, 2, 128, 21), ("f32", 4, 2, 64, 7)])
+def test_ragged_trees_leave_the_other_rows(dtype, Hq, Hkv, D, n):
+    nodes = [0, 1, n, n // 2, 3, n]
+    # (a context shorter than its tree: the positions before 0 do not exist)
+    _run(Inputs(2, [2, 0, n - 1, 200, 1, 515], n, Hq, Hkv, D, dtype, nodes=nodes))
+    _run(Inputs(3, [90, 1, n, 200, 131, 515], n, Hq, Hkv, D, dtype, nodes=nodes))
+    _run(Inputs(4, [90, 1, n, 200, 131, 515], n, Hq, Hkv, D, dtype, nodes=nodes, shared=True))
+
+
+def test_all_sequences_empty():
+    x = Inputs(9, [40, 0, 3], 4, 8, 2, 128, "bf16", nodes=[0, 0, 0])
+    _run(x)
+
+
+@pytest.mark.parametrize("dtype,Hq,D,n", [("bf16", 8, 128, 6), ("bf16", 8, 128, 30), ("f16", 8, 64, 6),
+                                          ("fp8_e4m3", 8, 128, 6), ("f32", 8, 64, 6)])
+def test_masks_that_are_no_tree(dtype, Hq, D, n):
+    """Rows that see nothing (an empty mask on a context that is the tree
+    alone) give 0; rows without their own node; a node that sees later ones;
+    bits past the nodes are ignored."""
+    x = Inputs(21, [n, n, 140, 256 + n], n, Hq, 1, D, dtype)
+    rng = np.random.default_rng(2)
+    x.masks = [[0] * n, [int(v) for v in rng.integers(0, 1 << n, n)], [0] * n,
+               [int(v) | (0xABCD << n) & ((1 << 64) - 1) for v in rng.integers(0, 1 << n, n)]]
+    x.mask = torch.stack([to_i64(m) for m in x.masks])
+    out = _run(x)
+    assert torch.all(out[0] == 0)
+
+
+def test_bit_63():
+    x = Inputs(8, [64, 300], 64, 4, 1, 128, "bf16")
+    x.masks = [[(1 << 63) | (1 << i) for i in range(64)]] * 2
+    x.mask = to_i64(x.masks[0])
+    _run(x)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 6), ("bf16", 16, 2, 128, 24), ("f16", 2, 2, 64, 5),
+                                              ("fp8_e4m3", 8, 2, 128, 6), ("f32", 4, 2, 128, 6)])
+@pytest.mark.parametrize("window", [1, 7, 16, 100, 1000, 2**31 - 1])
+def test_sliding_window(dtype, Hq, Hkv, D, n, window):
+    """Deep and shallow nodes reach back differently; blocks before every
+    row's window are -1 in the table and are not read."""
+    x = Inputs(31, [n, n + 3, 130, 260, 517], n, Hq, Hkv, D, dtype)
+    for b in range(x.B):
+        first = max(0, x.ctx[b] - n + 1 - window) // 16
+        x.table[b, :first] = -1
+    _run(x, window)
+
+
+def test_chain_is_the_causal_multi_query_decode():
+    pkv = _pkv()
+    x = Inputs(2, [40, 7, 300], 7, 8, 2, 128, "bf16", kind="chain")
+    out, _ = _call(x)
+    ref = torch.empty_like(out)
+    dev = "cuda"
+    pkv.paged_decode_attention(ref, x.q.to(dev), x.kc.to(dev), x.vc.to(dev), torch.from_numpy(x.table).to(dev),
+                               torch.tensor(x.ctx, dtype=torch.int32, device=dev), x.scale)
+    check_attention(ref, x)
+    check_attention(out, x)
+
+
+@pytest.mark.parametrize("B", [1, 3, 260, 2100])
+def test_batch_sizes(B):
+    """One sequence to more than the in-kernel plans hold."""
+    rng = np.random.default_rng(B)
+    _run(Inputs(1, [int(c) for c in rng.integers(3, 60, B)], 3, 2, 1, 128, "bf16"))
+
+
+def test_long_context_is_split_and_joined():
+    """One sequence, few rows: the context is cut over the whole GPU."""
+    for dtype, n, Hq in (("bf16", 2, 2), ("bf16", 9, 8), ("bf16", 40, 8), ("fp8_e4m3", 2, 4), ("f16", 3, 1)):
+        _run(Inputs(6, [20011], n, Hq, 1, 128, dtype, stale=False))
+
+
+def test_bad_entries_are_flagged_and_read_as_zeros():
+    pkv = _pkv()
+    for Hq in (8, 64):
+        x = Inputs(14, [200, 64], 10, Hq, 1, 128, "bf16")
+        x.table[0, 3] = x.num_blocks + 5
+        x.table[1, 0] = -4
+        out, ws = _call(x)
+        rc, flags = pkv.paged_decode_status(ws)
+        assert rc == pkv.PKV_ERANGE and flags == pkv.PKV_FLAG_BAD_BLOCK
+        assert torch.isfinite(out).all()
+        x = Inputs(14, [200, 64], 10, Hq, 1, 128, "bf16")
+        x.nodes = [10, 11]
+        out, ws = _call(x)
+        rc, flags = pkv.paged_decode_status(ws)
+        assert rc == pkv.PKV_ERANGE and flags == pkv.PKV_FLAG_BAD_LEN
+        x.nodes = [10, 10]
+        check_attention(out, x)
+
+
+def test_infinite_and_nan_values_in_hidden_places():
+    """K / V rows that no row sees may hold anything, also inside the tree."""
+    for Hq in (4, 64):
+        x = Inputs(15, [70, 133], 6, Hq, 1, 128, "bf16")
+        x.masks = [[0b000001, 0b000011, 0b000101, 0b000011, 0b000001, 0b000101]] * 2
+        x.mask = to_i64(x.masks[0])
+        for b in range(2):
+            for j in (3, 4, 5):
+                t = x.ctx[b] - 6 + j
+                x.kc[x.table[b, t // 16], :, t % 16] = float("inf")
+        _run(x)
+
+
+def test_on_a_side_stream_and_from_a_graph():
+    pkv, dev = _pkv(), "cuda"
+    for Hq, n in ((8, 5), (16, 40)):
+        x = Inputs(17, [300, 45, 128], n if n < 45 else 40, Hq, 1, 128, "bf16")
+        st = torch.cuda.Stream()
+        args = [t.to(dev) for t in (x.q, x.kc, x.vc, torch.from_numpy(x.table), torch.tensor(x.ctx, dtype=torch.int32), x.mask)]
+        out = torch.empty_like(args[0])
+        ws = torch.empty(pkv.paged_tree_workspace_bytes(x.B, x.n, Hq, 1, 128, torch.bfloat16, torch.bfloat16),
+                         dtype=torch.uint8, device=dev)
+        torch.cuda.synchronize()
+        call = pkv.paged_tree_attention(out, *args, x.scale, workspace=ws, stream=st, prepare=True)
+        call()
+        st.synchronize()
+        check_attention(out, x)
+        out.fill_(3.0)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            call()
+        args[0].copy_(torch.flip(x.q, [0]).to(dev))       # another query in the same buffer
+        x.q = torch.flip(x.q, [0])
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        check_attention(out, x)
+
+
+def test_same_inputs_same_bits():
+    for dtype, Hq, n in (("bf16", 8, 6), ("bf16", 16, 32), ("fp8_e4m3", 8, 6)):
+        x = Inputs(19, [900, 77, 2000], n, Hq, 1, 128, dtype, stale=False)
+        a, _ = _call(x)
+        b, _ = _call(x)
+        assert torch.equal(a, b)
