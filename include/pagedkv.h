@@ -548,17 +548,25 @@ int paged_kv_copy_blocks(void *k_cache, void *v_cache, int cache_dtype,
  *           (the decode kernel's 8- or 16-row units with the split-KV merge)
  *   which = PKV_ROUTE_PREFILL (the prefill kernel's schedule):
  *           PKV_ROUTE_AUTO, PKV_PREFILL_PERSISTENT, PKV_PREFILL_PER_ITEM
+ *   which = PKV_ROUTE_TREE (paged_tree_attention):
+ *           PKV_ROUTE_AUTO, PKV_TREE_TRANSPOSED (the transposed tensor-core
+ *           kernel), PKV_TREE_TILES (the split 128-row tile kernel),
+ *           PKV_TREE_UNITS (the decode kernel's units)
  * Returns PKV_EINVAL for an unknown `which` or `choice`; pkv_get_route
  * returns the current setting (or PKV_EINVAL).
  */
 #define PKV_ROUTE_MULTI_QUERY 0
 #define PKV_ROUTE_PREFILL 1
+#define PKV_ROUTE_TREE 2
 #define PKV_ROUTE_AUTO 0
 #define PKV_MQ_TRANSPOSED 1
 #define PKV_MQ_PREFILL 2
 #define PKV_MQ_UNITS 3
 #define PKV_PREFILL_PERSISTENT 1
 #define PKV_PREFILL_PER_ITEM 2
+#define PKV_TREE_TRANSPOSED 1
+#define PKV_TREE_TILES 2
+#define PKV_TREE_UNITS 3
 int pkv_set_route(int which, int choice);
 int pkv_get_route(int which);
 

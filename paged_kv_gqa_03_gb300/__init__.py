@@ -120,7 +120,8 @@ def pkv_version():
 
 # Kernel-route decisions that pkv_set_route can force (include/pagedkv.h).
 ROUTES = {"multi_query": (0, ("auto", "transposed", "prefill", "units")),
-          "prefill": (1, ("auto", "persistent", "tiles"))}
+          "prefill": (1, ("auto", "persistent", "tiles")),
+          "tree": (2, ("auto", "transposed", "tiles", "units"))}
 
 
 def pkv_set_route(which, choice):

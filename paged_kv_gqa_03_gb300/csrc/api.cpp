@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -17,6 +18,7 @@
 #include "mq_decode.h"
 #include "prefill.h"
 #include "tree.h"
+#include "tree_tiles.h"
 
 namespace pkv {
 
@@ -79,7 +81,7 @@ Registry &registry() {
 }
 
 // Route overrides set by pkv_set_route (PKV_ROUTE_AUTO = the rule of shapes).
-std::atomic<int> g_route[2];
+std::atomic<int> g_route[3];
 
 // Limit of every bounded in-kernel wait (a wait that runs out sets
 // PKV_FLAG_TIMEOUT instead of hanging).
@@ -374,6 +376,8 @@ int pkv_set_route(int which, int choice) {
     if (choice < PKV_ROUTE_AUTO || choice > PKV_MQ_UNITS) return PKV_EINVAL;
   } else if (which == PKV_ROUTE_PREFILL) {
     if (choice < PKV_ROUTE_AUTO || choice > PKV_PREFILL_PER_ITEM) return PKV_EINVAL;
+  } else if (which == PKV_ROUTE_TREE) {
+    if (choice < PKV_ROUTE_AUTO || choice > PKV_TREE_UNITS) return PKV_EINVAL;
   } else {
     return PKV_EINVAL;
   }
@@ -389,7 +393,7 @@ int pkv_test_stall_next(int which, uint64_t limit_ns) {
 }
 
 int pkv_get_route(int which) {
-  if (which != PKV_ROUTE_MULTI_QUERY && which != PKV_ROUTE_PREFILL) return PKV_EINVAL;
+  if (which != PKV_ROUTE_MULTI_QUERY && which != PKV_ROUTE_PREFILL && which != PKV_ROUTE_TREE) return PKV_EINVAL;
   return g_route[which].load(std::memory_order_relaxed);
 }
 
@@ -603,6 +607,62 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
   return cuda_status(e);
 }
 
+// The call's parameters for the kernels that share the stream-K schedule
+// (mq_walk.cuh), on a workspace laid out as M.
+static MqParams mq_params(const MqWsLayout &M, void *out, const void *q, const float *k_scale, const float *v_scale,
+                          const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens, int B,
+                          int q_len, int window, int Hq, int Hkv, int64_t num_blocks, float scale, void *workspace,
+                          const TreeArgs *tree) {
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  MqParams mp;
+  std::memset(&mp, 0, sizeof(mp));
+  mp.out = out;
+  mp.q = q;
+  mp.k_scale = k_scale;
+  mp.v_scale = v_scale;
+  mp.block_table = block_table;
+  mp.context_lens = context_lens;
+  mp.status = &reinterpret_cast<WsHeader *>(ws)->status;
+  mp.cta_flags = reinterpret_cast<int32_t *>(ws + M.cta_flags);
+  mp.prefix = reinterpret_cast<int32_t *>(ws + M.prefix);
+  mp.part_o = reinterpret_cast<float *>(ws + M.part_o);
+  mp.part_lse = reinterpret_cast<float *>(ws + M.part_lse);
+  mp.num_blocks = num_blocks;
+  mp.B = B;
+  mp.q_len = q_len;
+  mp.Hq = Hq;
+  mp.Hkv = Hkv;
+  mp.G = Hq / Hkv;
+  mp.R = q_len * mp.G;
+  mp.max_blocks = max_blocks_per_seq;
+  mp.window = window < (1 << 30) ? window : 0;
+  mp.scale_log2 = scale * 1.4426950408889634f;
+  mp.timeout_ns = kWaitLimitNs;
+  if (tree) {
+    mp.tree_mask = tree->mask;
+    mp.tree_lens = tree->lens;
+    mp.mask_stride = tree->mask_stride;
+  }
+  return mp;
+}
+
+// The transposed tensor-core kernel (head dim 128) and its merge, on the
+// workspace mq_ws_layout(B, sms) describes.
+static int run_mq(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache, int cache_dtype,
+                  const float *k_scale, const float *v_scale, const int32_t *block_table, int max_blocks_per_seq,
+                  const int32_t *context_lens, int B, int q_len, int window, int Hq, int Hkv, int64_t num_blocks,
+                  float scale, void *workspace, int sms, pkv_stream_t stream, const TreeArgs *tree) {
+  const MqWsLayout M = mq_ws_layout(B, sms);
+  CUtensorMap tmK, tmV;
+  int rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, kMqHeadDim);
+  if (rc != PKV_OK) return rc;
+  rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, kMqHeadDim);
+  if (rc != PKV_OK) return rc;
+  const MqParams mp = mq_params(M, out, q, k_scale, v_scale, block_table, max_blocks_per_seq, context_lens, B, q_len,
+                                window, Hq, Hkv, num_blocks, scale, workspace, tree);
+  return cuda_status(launch_mq_decode(mp, cache_dtype, q_dtype, tmK, tmV, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache,
                                  int cache_dtype, const float *k_scale, const float *v_scale,
                                  const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
@@ -662,40 +722,10 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
     const bool fp8_mq = fp8 && R <= kMqRowsFp8 && want_mq;
     if (!no_mq && (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16 || fp8_mq) && scale > 0.f &&
         D == kMqHeadDim && R <= kMqRows && B <= kMqMaxBatch && (R <= 32 || !prefill_fills || want_mq)) {
-      const MqWsLayout M = mq_ws_layout(B, sms);
-      if (workspace_bytes >= M.total) {
-        CUtensorMap tmK, tmV;
-        rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
-        if (rc != PKV_OK) return rc;
-        rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
-        if (rc != PKV_OK) return rc;
-        uint8_t *ws = static_cast<uint8_t *>(workspace);
-        MqParams mp;
-        std::memset(&mp, 0, sizeof(mp));
-        mp.out = out;
-        mp.q = q;
-        mp.k_scale = k_scale;
-        mp.v_scale = v_scale;
-        mp.block_table = block_table;
-        mp.context_lens = context_lens;
-        mp.status = &reinterpret_cast<WsHeader *>(ws)->status;
-        mp.cta_flags = reinterpret_cast<int32_t *>(ws + M.cta_flags);
-        mp.prefix = reinterpret_cast<int32_t *>(ws + M.prefix);
-        mp.part_o = reinterpret_cast<float *>(ws + M.part_o);
-        mp.part_lse = reinterpret_cast<float *>(ws + M.part_lse);
-        mp.num_blocks = num_blocks;
-        mp.B = B;
-        mp.q_len = q_len;
-        mp.Hq = Hq;
-        mp.Hkv = Hkv;
-        mp.G = G;
-        mp.R = R;
-        mp.max_blocks = max_blocks_per_seq;
-        mp.window = window < (1 << 30) ? window : 0;
-        mp.scale_log2 = scale * 1.4426950408889634f;
-        mp.timeout_ns = kWaitLimitNs;
-        return cuda_status(launch_mq_decode(mp, cache_dtype, q_dtype, tmK, tmV, sms, s));
-      }
+      if (workspace_bytes >= mq_ws_layout(B, sms).total)
+        return run_mq(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
+                      max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, sms,
+                      stream, nullptr);
     }
     if (!units && (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && scale > 0.f && prefill_fills) {
       CUtensorMap tmK, tmV;
@@ -735,6 +765,22 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
                    nullptr);
 }
 
+// Kernels of paged_tree_attention (PKV_TREE_*): which one a shape takes, or the
+// forced one (pkv_set_route) where it applies.
+static bool tree_mq_applies(int cache_dtype, int B, int R, int D) {
+  return (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && D == kMqHeadDim && R <= kMqRows && B <= kMqMaxBatch;
+}
+static bool tree_tiles_apply(int cache_dtype, int B) {
+  return (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && B <= kMqMaxBatch;
+}
+static int tree_route(int cache_dtype, int B, int R, int D) {
+  const int force = g_route[PKV_ROUTE_TREE].load(std::memory_order_relaxed);
+  const bool mq = tree_mq_applies(cache_dtype, B, R, D), tiles = tree_tiles_apply(cache_dtype, B);
+  if (force == PKV_TREE_UNITS || (force == PKV_TREE_TRANSPOSED && mq) || (force == PKV_TREE_TILES && tiles)) return force;
+  if (mq && R <= 32) return PKV_TREE_TRANSPOSED;
+  return tiles && R > 8 ? PKV_TREE_TILES : PKV_TREE_UNITS;
+}
+
 int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cache_dtype, int q_dtype,
                                size_t *bytes_out) {
   if (!bytes_out) return PKV_EINVAL;
@@ -744,7 +790,18 @@ int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cac
   int P = 0;
   rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
   if (rc != PKV_OK) return rc;
-  *bytes_out = ws_layout(B, P, D, c.GC).total;
+  size_t total = ws_layout(B, P, D, c.GC).total;
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc != PKV_OK) return rc;
+  const int R = q_len * (Hq / Hkv);
+  if (tree_mq_applies(cache_dtype, B, R, D)) total = std::max(total, mq_ws_layout(B, sms).total);
+  if (tree_tiles_apply(cache_dtype, B)) {
+    int RT = 0, groups = 0;
+    tree_tiles_grid(R, sms, &RT, &groups);
+    total = std::max(total, tree_tiles_ws_layout(B, D, RT, groups).total);
+  }
+  *bytes_out = total;
   return PKV_OK;
 }
 
@@ -763,14 +820,38 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   if (cache_dtype == PKV_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_EINVAL;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_EINVAL;
   if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return PKV_EINVAL;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_EWORKSPACE;
+  size_t need = 0;
+  rc = paged_tree_workspace_bytes(B, q_len, Hq, Hkv, D, cache_dtype, q_dtype, &need);
+  if (rc != PKV_OK) return rc;
+  if (workspace_bytes < need) return PKV_EWORKSPACE;
+  const TreeArgs tree{tree_mask, tree_lens, mask_per_seq ? q_len : 0};
+  const int R = q_len * (Hq / Hkv);
+  int sms = 0;
+  rc = device_sm_count(&sms);
+  if (rc != PKV_OK) return rc;
+  const int route = tree_route(cache_dtype, B, R, D);
+  if (route == PKV_TREE_TRANSPOSED)
+    return run_mq(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table, max_blocks_per_seq,
+                  context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, sms, stream, &tree);
+  if (route == PKV_TREE_TILES) {
+    CUtensorMap tmK, tmV;
+    rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
+    if (rc != PKV_OK) return rc;
+    rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
+    if (rc != PKV_OK) return rc;
+    TreeTileParams tp;
+    std::memset(&tp, 0, sizeof(tp));
+    tree_tiles_grid(R, sms, &tp.RT, &tp.groups);
+    tp.D = D;
+    tp.m = mq_params(tree_tiles_ws_layout(B, D, tp.RT, tp.groups), out, q, k_scale, v_scale, block_table,
+                     max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, &tree);
+    return cuda_status(launch_tree_tiles(tp, cache_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
+  }
   Choice c;
   int P = 0;
   rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
   if (rc != PKV_OK) return rc;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < ws_layout(B, P, D, c.GC).total)
-    return PKV_EWORKSPACE;
-  const TreeArgs tree{tree_mask, tree_lens, mask_per_seq ? q_len : 0};
   return run_units(c, P, out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
                    max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, D, num_blocks, scale, workspace, stream,
                    &tree);

@@ -39,6 +39,7 @@
 #include <math.h>
 
 #include "mq_decode.h"
+#include "mq_walk.cuh"
 #include "prefill_common.cuh"
 
 namespace pkv {
@@ -47,8 +48,12 @@ namespace pkv {
 // An fp8 cache is widened to f16 in shared memory (exact: every E4M3 value
 // is an f16 value) and the MMAs run on f16 (Q converted when staged), so
 // BF (the MMA operand type) is false for it while OUT_BF follows the query.
-template <class T, int NRH_, class QT = T>
+// TREE_: the new tokens form a tree (paged_tree_attention): positions before
+// the tree as above, then node j at position start + j for the rows whose
+// node's mask has bit j.  Tiles wholly before the tree take the unmasked path.
+template <class T, int NRH_, class QT = T, bool TREE_ = false>
 struct MqCfg {
+  static constexpr bool TREE = TREE_;
   static constexpr int D = kMqHeadDim;
   static constexpr bool FP8 = T::kBytes == 1;
   static constexpr bool BF = !FP8 && T::kCode == PKV_BF16;
@@ -127,67 +132,6 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[NRH], int lane) {
   }
   return v[0];
 }
-
-// Tile facts of one sequence: the clamped context, the first position any
-// new token's window reaches, the first K / V tile and the tile count T (per
-// kv head).  Token i sees positions [ctx - q_len + 1 + i - window, ctx - q_len
-// + 1 + i) (no lower bound without a window).
-struct MqSeq {
-  int ctx, first, j_first, T;
-  bool bad_ctx;
-};
-__device__ __forceinline__ MqSeq mq_seq(const MqParams &p, int b) {
-  MqSeq s;
-  const int raw = __ldg(p.context_lens + b);
-  const int cap = p.max_blocks * kBlock;
-  s.ctx = raw < 0 ? 0 : (raw > cap ? cap : raw);
-  s.bad_ctx = raw != s.ctx;
-  const int lim_lo = s.ctx - p.q_len + 1;  // exclusive end of token 0's positions
-  s.first = p.window > 0 ? max(0, lim_lo - p.window) : 0;
-  s.j_first = s.first / 128;
-  s.T = s.ctx > 0 ? (s.ctx - 1) / 128 - s.j_first + 1 : 0;
-  return s;
-}
-
-// A CTA's share of the stream-K order: tiles [t0, t1) of the sequence of all
-// items' tiles (item (b, h) holds tiles [prefix[b] + h * T_b, ... + T_b)).
-// One segment = the part of one item inside the range; every role walks the
-// same segments.
-struct MqSeg {
-  int b, h, j0, j1, T, ctx, first, j_first;
-  int slot;    // partial-output slot of a cut item: 0 if the segment starts the CTA's range, else 1
-  bool whole;  // the segment is the whole item (the CTA writes the output itself)
-};
-struct MqWalk {
-  int t, t0, t1, b, base;  // next tile; the range; the sequence holding tile t and its first tile
-  __device__ __forceinline__ void start(int b0, int base0, int tile0, int tile1) {
-    b = b0;
-    base = base0;
-    t = t0 = tile0;
-    t1 = tile1;
-  }
-  __device__ __forceinline__ bool next(const MqParams &p, MqSeg &sg) {
-    if (t >= t1) return false;
-    MqSeq s = mq_seq(p, b);
-    while (t >= base + s.T * p.Hkv) {  // on to the sequence holding tile t (skipping empty ones)
-      base += s.T * p.Hkv;
-      s = mq_seq(p, ++b);
-    }
-    const int off = t - base;
-    sg.b = b;
-    sg.T = s.T;
-    sg.h = off / s.T;
-    sg.j0 = off - sg.h * s.T;
-    sg.j1 = min(s.T, sg.j0 + (t1 - t));
-    sg.ctx = s.ctx;
-    sg.first = s.first;
-    sg.j_first = s.j_first;
-    sg.slot = t == t0 ? 0 : 1;
-    sg.whole = sg.j0 == 0 && sg.j1 == s.T;
-    t += sg.j1 - sg.j0;
-    return true;
-  }
-};
 
 // S^T = K . Q^T of one tile into tensor-memory columns dS (128 lanes =
 // positions, NR columns = query rows): D / 16 MMAs over the K tile (A,
@@ -317,7 +261,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t q_full[Cfg::QBUF], o_free[2], xch[2][2], xl[2], fin;
   __shared__ float red[2][2][4][32];  // partial row maxima [tile parity][half][warp quarter][row]
   __shared__ float red_l[2][4][32];   // partial row sums [half][warp quarter][row]
-  __shared__ int32_t s_wsum[8], s_b0, s_base0;  // per-warp tile sums; where the CTA's range starts
+  __shared__ MqPlan plan;
+  // (tree) which rows of a half see node t (bit e: row NRH * half + e), and the
+  // first cached position each row sees: of the segment in work, the next one
+  // (staged with its Q) and the one other warps may still be finishing
+  __shared__ uint32_t t_rows[Cfg::TREE ? 3 : 1][2][Cfg::TREE ? 64 : 1];
+  __shared__ int t_lo[Cfg::TREE ? 3 : 1][Cfg::TREE ? NR : 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_flags, k_consumed, v_consumed, k_issued, v_issued;
 
@@ -385,65 +334,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   tc::fence_after();
   const uint32_t tbase = tmem_base;
 
-  // ---- tile prefix over the sequences (256 threads, up to 8 sequences each):
-  // the total, where this CTA's range starts, and (CTA 0) the prefix for the
-  // merge kernel ----
   const int B = p.B;
-  const int per = (B + Cfg::SOFTMAX - 1) / Cfg::SOFTMAX;
-  int tk[kMqMaxBatch / Cfg::SOFTMAX];
-  int own = 0, incl = 0;
-  if (tid < Cfg::SOFTMAX) {
-    int bad = 0;
-#pragma unroll
-    for (int k = 0; k < kMqMaxBatch / Cfg::SOFTMAX; ++k) {
-      const int b = tid * per + k;
-      tk[k] = 0;
-      if (k < per && b < B) {
-        const MqSeq s = mq_seq(p, b);
-        tk[k] = s.T * p.Hkv;
-        bad |= s.bad_ctx ? 1 : 0;
-      }
-      own += tk[k];
-    }
-    incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) s_wsum[warp] = incl;
-    if (blockIdx.x == 0 && __any_sync(kFull, bad) && lane == 0) atomicOr(&cta_flags, PKV_FLAG_BAD_LEN);
-  }
-  __syncthreads();
-  int W = 0;
-#pragma unroll
-  for (int w = 0; w < Cfg::SOFTMAX / 32; ++w) W += s_wsum[w];
-  const int t0 = (int)((int64_t)W * blockIdx.x / gridDim.x);
-  const int t1 = (int)((int64_t)W * (blockIdx.x + 1) / gridDim.x);
-  if (tid == 0) {  // an empty range (t0 == W): nothing to walk
-    s_b0 = B;
-    s_base0 = W;
-    if (blockIdx.x == 0) p.prefix[B] = W;
-  }
-  __syncthreads();
-  if (tid < Cfg::SOFTMAX) {
-    int run = incl - own;
-    for (int w = 0; w < warp; ++w) run += s_wsum[w];
-#pragma unroll
-    for (int k = 0; k < kMqMaxBatch / Cfg::SOFTMAX; ++k) {
-      const int b = tid * per + k;
-      if (k < per && b < B) {
-        if (blockIdx.x == 0) p.prefix[b] = run;
-        if (run <= t0 && t0 < run + tk[k]) {  // the sequence holding the range's first tile
-          s_b0 = b;
-          s_base0 = run;
-        }
-        run += tk[k];
-      }
-    }
-  }
-  __syncthreads();
-  const int b0 = s_b0, base0 = s_base0;
+  int t0, t1, b0, base0;
+  mq_plan<Cfg::SOFTMAX>(p, (int)blockIdx.x, (int)gridDim.x, &plan, &cta_flags, &t0, &t1, &b0, &base0);
 
   if (warp == Cfg::PRODUCER || warp == Cfg::V_PRODUCER) {
     // ---------------- TMA producers: K tiles (warp 8), V tiles (warp 11) ----------------
@@ -662,12 +555,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const float c = p.scale_log2;
     // Q of segment s into buffer qb: NR rows x 16 chunks of 16 bytes, row r =
     // (new token r / G, query head r % G of kv head s.h), zeros past R
-    auto stage_q = [&](const MqSeg &s, int qb, bool async) {
+    auto stage_q = [&](const MqSeg &s, int qb, bool async, int seg) {
+      const int R = Cfg::TREE ? s.n * p.G : p.R;
+      if constexpr (Cfg::TREE) {
+        if (qd == 0) {  // one warp per half: lane e transposes row row0 + e's mask
+          uint64_t m = 0;
+          int lo = INT32_MAX;
+          const int r = row0 + lane;
+          if (lane < NRH && r < R) {
+            const int start = s.ctx - s.n;
+            m = __ldg(p.tree_mask + (size_t)s.b * p.mask_stride + r / p.G) & (~0ull >> (64 - s.n));
+            lo = p.window > 0 ? start + max(1, __popcll(m)) - p.window : 0;
+          }
+          if (lane < NRH) t_lo[seg % 3][r] = lo;
+          for (int t = 0; t < s.n; ++t) {
+            const uint32_t rows = __ballot_sync(kFull, (m >> t) & 1);
+            if (lane == (t & 31)) t_rows[seg % 3][hf][t] = rows;
+          }
+        }
+      }
       uint8_t *q0 = sQ + (size_t)qb * Cfg::Q_BYTES;
       for (int i = tid; i < NR * 16; i += Cfg::SOFTMAX) {
         const int r = i >> 4, cc = i & 15;
         const uint32_t dst = smem_u32(q0 + (cc >> 3) * Cfg::PANEL_Q + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-        if (r < p.R) {
+        if (r < R) {
           const int ii = r / p.G, gq = r - ii * p.G;
           const uint4 *src = reinterpret_cast<const uint4 *>(
               static_cast<const uint16_t *>(p.q) + (((size_t)s.b * p.q_len + ii) * p.Hq + s.h * p.G + gq) * Cfg::D) + cc;
@@ -711,7 +622,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool have = wk.next(p, sg);
     bool nhave = have && wk.next(p, nx);
     if (have) {
-      stage_q(sg, 0, false);
+      stage_q(sg, 0, false, 0);
       release_q(0, false);
     }
     bool ok = true;
@@ -727,7 +638,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // at this segment's last tile (once its last S^T has landed)
       bool staged = false;
       if (Cfg::QBUF == 2 && nhave) {
-        stage_q(nx, (si + 1) % Cfg::QBUF, true);
+        stage_q(nx, (si + 1) % Cfg::QBUF, true, si + 1);
         staged = true;
       }
 #pragma unroll
@@ -770,6 +681,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (gj + 1 < ntiles && !(ok = widen(gj + 1, false))) break;
         }
         ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
+        // (tree) orders the segment's masks, staged with its Q, before their use
+        if (Cfg::TREE && ok && j == 0) ok = warp_wait(&q_full[si % Cfg::QBUF], (uint32_t)(si / Cfg::QBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         // S^T of this thread's position and rows, masked: new token i sees the
@@ -778,13 +691,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int imin = pos - sg.ctx + p.q_len;
         const int rlo = imin > 0 ? (imin < p.q_len ? imin * p.G : p.R) : 0;
         const int rhi = p.window > 0 ? (imin + p.window >= p.q_len ? p.R : max(0, imin + p.window) * p.G) : p.R;
+        [[maybe_unused]] uint32_t rows = ~0u;  // (tree) the rows that see this position
+        if constexpr (Cfg::TREE) {
+          const int start = sg.ctx - sg.n, t = pos - start;
+          if (t >= 0) {
+            rows = t < sg.n ? t_rows[si % 3][hf][t] : 0u;
+          } else if (p.window > 0 && pos < start + p.q_len - p.window) {
+            for (int e = 0; e < NRH; ++e)
+              if (pos < t_lo[si % 3][row0 + e]) rows &= ~(1u << e);
+          }
+        }
         float s[NRH];
         auto load_s = [&]() {
           uint32_t sr[NRH];
           ld_cols<NRH>(scol, sr);
 #pragma unroll
           for (int e = 0; e < NRH; ++e) s[e] = __uint_as_float(sr[e]) * ksc;  // (fp8: the block's K scale)
-          if (!(rlo <= row0 && rhi >= row0 + NRH)) {
+          if constexpr (Cfg::TREE) {
+            if (rows != ~0u) {
+#pragma unroll
+              for (int e = 0; e < NRH; ++e)
+                if (!((rows >> e) & 1)) s[e] = -INFINITY;
+            }
+          } else if (!(rlo <= row0 && rhi >= row0 + NRH)) {
 #pragma unroll
             for (int e = 0; e < NRH; ++e)
               if (row0 + e < rlo || row0 + e >= rhi) s[e] = -INFINITY;
@@ -810,7 +739,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           mrow = reduce_scatter<NRH, true>(mx, lane);
         }
         if (Cfg::QBUF == 1 && j + 1 == n && nhave) {
-          stage_q(nx, 0, true);
+          stage_q(nx, 0, true, si + 1);
           staged = true;
         }
         if (lane < NRH) red[par][hf][qd][lane] = mrow;
@@ -939,7 +868,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int e = 0; e < NRH; ++e) {
           const int r = row0 + e;
           const float L = __shfl_sync(kFull, lt, e);
-          if (r < p.R) {
+          if (r < (Cfg::TREE ? sg.n * p.G : p.R)) {
             const int ii = r / p.G, gq = r - ii * p.G;
             const size_t idx = (((size_t)sg.b * p.q_len + ii) * p.Hq + sg.h * p.G + gq) * Cfg::D + d;
             const float v = L > 0.f ? __uint_as_float(o[e]) / L : 0.f;  // a row that sees nothing gives 0
@@ -971,11 +900,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // sequences with no tile (no visible position for any new token): zeros,
       // sequence b by CTA b mod grid
       const size_t per_seq = (size_t)p.q_len * p.Hq * Cfg::D / 8;
-      for (int b = blockIdx.x; b < B; b += gridDim.x)
-        if (mq_seq(p, b).T == 0) {
+      for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        const MqSeq s = mq_seq(p, b);
+        if (s.T == 0) {
           uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (size_t)b * per_seq * 8);
-          for (size_t i = tid; i < per_seq; i += Cfg::SOFTMAX) dst[i] = make_uint4(0, 0, 0, 0);
+          const size_t rows = Cfg::TREE ? (size_t)s.n * p.Hq * Cfg::D / 8 : per_seq;  // (tree) its nodes only
+          for (size_t i = tid; i < rows; i += Cfg::SOFTMAX) dst[i] = make_uint4(0, 0, 0, 0);
         }
+      }
     }
     if (!ok && lane == 0) {
       atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
@@ -1015,8 +947,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 
 // Finishes the items cut by range ends: block c takes the boundary between
 // CTAs c and c + 1 and, if it falls inside an item and is that item's first,
-// merges the partials of the item written by the CTAs c .. wl whose ranges
-// are not empty (a CTA whose range starts at or after the item's first tile
+// merges the partials of the item written by the CTAs c .. wl (a CTA whose range starts at or after the item's first tile
 // wrote slot 0, the one before slot 1) — weights 2^(lse - max lse), rows
 // every partial leaves empty give 0.  Block 0 also publishes the call's
 // status bits (the OR of every CTA's).
@@ -1032,8 +963,9 @@ __global__ void __launch_bounds__(256) mq_merge_kernel(const MqParams p, int P, 
   const int c = blockIdx.x;
   const int W = p.prefix[p.B];
   if (c + 1 >= P || W <= 0) return;
-  const int tcut = (int)((int64_t)W * (c + 1) / P);
-  if (tcut <= 0 || tcut >= W) return;
+  const int active = mq_active(W, P);
+  if (c + 1 >= active) return;
+  const int tcut = mq_cut(W, active, c + 1);
   int lo = 0, hi = p.B;  // the sequence holding tile tcut
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -1045,23 +977,22 @@ __global__ void __launch_bounds__(256) mq_merge_kernel(const MqParams p, int P, 
   const int h = (tcut - base) / T;
   const int a = base + h * T, e = a + T;  // the item's tiles
   if (tcut == a) return;                          // the cut falls between items
-  if ((int)((int64_t)W * c / P) > a) return;      // an earlier cut inside the item merges it
-  const int wl = (int)(((int64_t)e * P - 1) / W);  // the CTA holding the item's last tile
+  if (mq_cut(W, active, c) > a) return;           // an earlier cut inside the item merges it
+  const int wl = (int)(((int64_t)e * active - 1) / W);  // the CTA holding the item's last tile
   constexpr int D = kMqHeadDim;
-  for (int i = threadIdx.x; i < p.R * (D / 4); i += blockDim.x) {
+  const int R = (p.tree_lens != nullptr ? min(max(__ldg(p.tree_lens + b), 0), p.q_len) : p.q_len) * p.G;
+  for (int i = threadIdx.x; i < R * (D / 4); i += blockDim.x) {
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
     float M = -INFINITY;
     for (int w = c; w <= wl; ++w) {
-      const int w0 = (int)((int64_t)W * w / P);
-      if (w0 == (int)((int64_t)W * (w + 1) / P)) continue;  // an empty range (fewer tiles than CTAs)
+      const int w0 = mq_cut(W, active, w);
       M = fmaxf(M, p.part_lse[((size_t)w * 2 + (w0 >= a ? 0 : 1)) * kMqRows + r]);
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
     if (M != -INFINITY) {
       for (int w = c; w <= wl; ++w) {
-        const int w0 = (int)((int64_t)W * w / P);
-        if (w0 == (int)((int64_t)W * (w + 1) / P)) continue;
+        const int w0 = mq_cut(W, active, w);
         const size_t part = (size_t)w * 2 + (w0 >= a ? 0 : 1);
         const float l = p.part_lse[part * kMqRows + r];
         if (l == -INFINITY) continue;
@@ -1134,20 +1065,25 @@ static cudaError_t launch_mq_cfg(const MqParams &p, const CUtensorMap &tmK, cons
   return cudaLaunchKernelEx(&mc, mq_merge_kernel, p, grid, Cfg::OUT_BF ? 1 : 0);
 }
 
-template <class T, class QT = T>
+template <class T, class QT = T, bool TREE = false>
 static cudaError_t launch_mq_rows(const MqParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, int grid,
                                   cudaStream_t stream) {
-  if (p.R <= 16) return launch_mq_cfg<MqCfg<T, 8, QT>>(p, tmK, tmV, grid, stream);
-  if (p.R <= 32) return launch_mq_cfg<MqCfg<T, 16, QT>>(p, tmK, tmV, grid, stream);
+  if (p.R <= 16) return launch_mq_cfg<MqCfg<T, 8, QT, TREE>>(p, tmK, tmV, grid, stream);
+  if (p.R <= 32) return launch_mq_cfg<MqCfg<T, 16, QT, TREE>>(p, tmK, tmV, grid, stream);
   if constexpr (T::kBytes == 1)
     return cudaErrorNotSupported;  // fp8: up to 32 rows
   else
-    return launch_mq_cfg<MqCfg<T, 32, QT>>(p, tmK, tmV, grid, stream);
+    return launch_mq_cfg<MqCfg<T, 32, QT, TREE>>(p, tmK, tmV, grid, stream);
 }
 
 cudaError_t launch_mq_decode(const MqParams &p, int cache_dtype, int q_dtype, const CUtensorMap &tmK,
                              const CUtensorMap &tmV, int grid, cudaStream_t stream) {
   if (p.R < 1 || p.R > kMqRows || p.B < 1 || p.B > kMqMaxBatch || grid < 1) return cudaErrorNotSupported;
+  if (p.tree_mask != nullptr) {  // 16-bit caches
+    if (cache_dtype == PKV_BF16) return launch_mq_rows<BF16, BF16, true>(p, tmK, tmV, grid, stream);
+    if (cache_dtype == PKV_F16) return launch_mq_rows<F16, F16, true>(p, tmK, tmV, grid, stream);
+    return cudaErrorNotSupported;
+  }
   if (cache_dtype == PKV_BF16) return launch_mq_rows<BF16>(p, tmK, tmV, grid, stream);
   if (cache_dtype == PKV_F16) return launch_mq_rows<F16>(p, tmK, tmV, grid, stream);
   if (cache_dtype == PKV_FP8_E4M3 && p.R <= kMqRowsFp8) {

@@ -28,6 +28,10 @@ struct MqParams {
   int B, q_len, Hq, Hkv, G, R, max_blocks, window;
   float scale_log2;             // softmax scale * log2(e), > 0
   uint64_t timeout_ns;
+  // tree of drafted tokens (else null; see DecodeParams)
+  const uint64_t *tree_mask;
+  const int32_t *tree_lens;
+  int mask_stride;
 };
 
 // Workspace of one call: the WsHeader (status) at offset 0, then the tile

@@ -1,0 +1,624 @@
+// tree_tiles.cu — attention of a tree of drafted tokens over the paged cache on
+// the tensor cores with the query rows on the M side: kv heads with more rows
+// than the transposed kernel (mq_decode.cu) takes, and head dim 64.
+//
+// The tile pipeline is that of prefill_common.cuh (S = Q . K^T and O += P . V of
+// 128 rows x 128 positions, tcgen05, S / P / O in tensor memory, TMA rings
+// through the block table, eight softmax warps).  What differs from the
+// prefill kernels is the schedule and the mask:
+//  * a tree has at most 64 * G rows per kv head but any context, so the context
+//    is split: the K / V tiles of all (sequence, kv head) items form one
+//    sequence cut into `groups` equal ranges (stream-K, mq_walk.cuh), and the RT
+//    row tiles of an item are RT CTAs of one group that walk the same range side
+//    by side, so that each K / V tile comes from HBM once and from L2 for the
+//    other row tiles.  Items cut between groups leave normalised partials and
+//    their log-sum-exps, which tree_merge_kernel joins.
+//  * a row sees the cached positions before the tree and the nodes its 64-bit
+//    mask names.  A thread holds its row's mask in registers; a tile that
+//    touches the tree turns it into a 64-bit word over the thread's 64 columns
+//    with two shifts.  Tiles before the tree are not masked at all.
+// Warp roles, rings and bounded waits as in prefill_tiles.cu; Q of the next
+// item is copied into the one Q buffer while the current item's last tile is in
+// the softmax (its last S has been read by then).
+#include "mq_walk.cuh"
+#include "prefill_common.cuh"
+#include "tree_tiles.h"
+
+namespace pkv {
+
+template <class T, int D_>
+struct TreeCfg : PrefillCfg<T, D_> {
+  using Base = PrefillCfg<T, D_>;
+  static constexpr int STAGE_BYTES = Base::SOFTMAX / 32 * 2048;  // output staging, 2 KiB per softmax warp
+  static constexpr size_t SMEM = Base::SMEM + STAGE_BYTES;
+  static_assert(SMEM + 6144 <= 232448, "shared memory");
+};
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    tree_tile_kernel(const __grid_constant__ TreeTileParams tp, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV) {
+  const MqParams &p = tp.m;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *sQ = smem;
+  uint8_t *sK = sQ + Cfg::Q_BYTES;
+  uint8_t *sV = sK + (size_t)Cfg::KSTAGES * Cfg::KV_BYTES;
+  uint8_t *sOut = sV + (size_t)Cfg::VSTAGES * Cfg::KV_BYTES;
+  __shared__ __align__(8) uint64_t k_full[Cfg::KSTAGES], k_empty[Cfg::KSTAGES];
+  __shared__ __align__(8) uint64_t v_full[Cfg::VSTAGES], v_empty[Cfg::VSTAGES];
+  __shared__ __align__(8) uint64_t s_full[Cfg::SBUF], p_full[Cfg::SBUF], pv_done[Cfg::SBUF];
+  __shared__ __align__(8) uint64_t q_full, o_free, xl, fin;  // per item: Q staged, O read out, row sums exchanged
+  __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
+  __shared__ float red[2][2][Cfg::M];
+  __shared__ float red_l[2][Cfg::M];
+  __shared__ MqPlan plan;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag, cta_flags, k_consumed, v_consumed, k_issued, v_issued;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rt = (int)blockIdx.x % tp.RT, group = (int)blockIdx.x / tp.RT;
+  if (tid == 0) {
+#pragma unroll
+    for (int s = 0; s < Cfg::KSTAGES; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+#pragma unroll
+    for (int s = 0; s < Cfg::VSTAGES; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+#pragma unroll
+    for (int s = 0; s < Cfg::SBUF; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], Cfg::SOFTMAX / 32);
+      mbar_init(&pv_done[s], 1);
+    }
+#pragma unroll
+    for (int pr = 0; pr < Cfg::SOFTMAX / 64; ++pr) {
+      mbar_init(&xch[pr][0], 2);
+      mbar_init(&xch[pr][1], 2);
+    }
+    mbar_init(&q_full, Cfg::SOFTMAX / 32);
+    mbar_init(&o_free, Cfg::SOFTMAX / 32);
+    mbar_init(&xl, Cfg::SOFTMAX / 32);
+    mbar_init(&fin, 2);  // one commit from each issuing warp
+    fence_barrier_init();
+    abort_flag = 0;
+    cta_flags = 0;
+    k_consumed = v_consumed = k_issued = v_issued = 0;
+  }
+  if (warp == Cfg::ISSUER) tc::alloc(&tmem_base, Cfg::TMEM_COLS);
+  if (warp == Cfg::PRODUCER && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  grid_dep_wait();  // launched early behind the previous kernel: its writes are visible from here on
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = tmem_base;
+
+  int t0, t1, b0, base0;
+  mq_plan<Cfg::SOFTMAX>(p, group, tp.groups, &plan, &cta_flags, &t0, &t1, &b0, &base0);
+
+  // this CTA's next item with rows in its row tile
+  auto next_item = [&](MqWalk &wk, MqSeg &sg) -> bool {
+    while (wk.next(p, sg))
+      if (rt * Cfg::M < sg.n * p.G) return true;
+    return false;
+  };
+
+  if (warp == Cfg::PRODUCER || warp == Cfg::V_PRODUCER) {
+    // ---------------- TMA producers: K tiles (warp 8), V tiles (warp 10) ----------------
+    // lane l fetches block (l % 8) of a tile, panel l / 8; block ids are
+    // loaded three tiles ahead and first used when the tile's copies are issued
+    const int slot = lane & (Cfg::BLOCKS - 1), panel = lane / Cfg::BLOCKS;
+    MqWalk wk;
+    wk.start(b0, base0, t0, t1);
+    MqSeg cs{};
+    int cj = 0;
+    bool have = false;
+    auto step = [&]() -> bool {  // to the cursor's next tile; false past the CTA's last
+      if (have && ++cj < cs.j1) return true;
+      have = next_item(wk, cs);
+      if (have) cj = cs.j0;
+      return have;
+    };
+    int bad = 0;
+    struct Pend {
+      int id, h;
+      bool none;
+    };
+    auto fetch = [&]() -> Pend {
+      Pend f;
+      const int lb = (cs.j_first + cj) * Cfg::BLOCKS + slot;
+      const int nblk = (cs.ctx + kBlock - 1) / kBlock;
+      f.h = cs.h;
+      f.none = lb >= nblk || (lb + 1) * kBlock <= cs.first;
+      f.id = f.none ? 0 : __ldg(p.block_table + (size_t)cs.b * p.max_blocks + lb);
+      return f;
+    };
+    // the box row of a fetched block; the box past the tensor (zeros) for none or a bad id
+    auto row_of = [&](const Pend &f) -> int64_t {
+      if (f.none) return p.num_blocks * p.Hkv;
+      const bool good = f.id >= 0 && (int64_t)f.id < p.num_blocks;
+      bad |= good ? 0 : 1;
+      return good ? (int64_t)f.id * p.Hkv + f.h : p.num_blocks * p.Hkv;
+    };
+    const bool vw = warp == Cfg::V_PRODUCER;
+    uint8_t *ring = vw ? sV : sK;
+    uint64_t *full = vw ? v_full : k_full, *empty = vw ? v_empty : k_empty;
+    const int stages = vw ? Cfg::VSTAGES : Cfg::KSTAGES;
+    const CUtensorMap *tm = vw ? &tmV : &tmK;
+    int *issued = vw ? &v_issued : &k_issued;
+    bool ok = true;
+    const Pend nil{0, 0, true};
+    bool h0 = step();
+    Pend f0 = h0 ? fetch() : nil;
+    bool h1 = h0 && step();
+    Pend f1 = h1 ? fetch() : nil;
+    bool h2 = h1 && step();
+    Pend f2 = h2 ? fetch() : nil;
+    for (int g = 0; h0; ++g) {
+      const bool h3 = h2 && step();
+      const Pend f3 = h3 ? fetch() : nil;
+      const int64_t trow = row_of(f0);
+      const int s = g % stages;
+      if (g >= stages) ok = warp_wait(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
+      if (!ok || __any_sync(kFull, *(volatile int *)&abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], Cfg::KV_BYTES);
+      __syncwarp();
+      if (lane < Cfg::LOADS)
+        tma_load_2d(ring + (size_t)s * Cfg::KV_BYTES + panel * Cfg::PANEL_KV + slot * 2048, tm, panel * 64,
+                    (int)(trow * kBlock), &full[s]);
+      if (lane == 0) *issued = g + 1;
+      h0 = h1;
+      f0 = f1;
+      h1 = h2;
+      f1 = f2;
+      h2 = h3;
+      f2 = f3;
+    }
+    if (__any_sync(kFull, bad) && lane == 0) atomicOr(&cta_flags, PKV_FLAG_BAD_BLOCK);
+    if (!ok && lane == 0) {
+      atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+      abort_flag = 1;
+    }
+  } else if (warp == Cfg::ISSUER) {
+    // ---------------- S issue: in tile order as K lands ----------------
+    bool ok = true;
+    MqWalk wk;
+    wk.start(b0, base0, t0, t1);
+    MqSeg sg{};
+    int g = 0;
+    for (int si = 0; ok && next_item(wk, sg); ++si) {
+      ok = warp_wait(&q_full, (uint32_t)si & 1u, p.timeout_ns);
+      for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+        const int ks = g % Cfg::KSTAGES, sb = g % Cfg::SBUF;
+        ok = warp_wait(&k_full[ks], (uint32_t)(g / Cfg::KSTAGES) & 1u, p.timeout_ns);
+        // S overwrites the buffer whose P . V of tile g - SBUF read P from it
+        if (ok && g >= Cfg::SBUF)
+          ok = warp_wait(&pv_done[sb], (uint32_t)((g / Cfg::SBUF) - 1) & 1u, p.timeout_ns);
+        if (!ok) break;
+        if (lane == 0) k_consumed = g + 1;
+        tc::fence_after();
+        if (lane == 0) {
+          mma_s_tile<Cfg>(tbase + (uint32_t)(sb * Cfg::N), smem_u32(sQ), smem_u32(sK + (size_t)ks * Cfg::KV_BYTES));
+          tc::commit(&s_full[sb]);
+          tc::commit(&k_empty[ks]);
+        }
+        __syncwarp();
+        if (__any_sync(kFull, *(volatile int *)&abort_flag)) ok = false;
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+      abort_flag = 1;
+    }
+  } else if (warp == Cfg::PV_ISSUER) {
+    // ---------------- P . V issue; an item's first waits until O was read out ----------------
+    bool ok = true;
+    MqWalk wk;
+    wk.start(b0, base0, t0, t1);
+    MqSeg sg{};
+    int g = 0;
+    for (int si = 0; ok && next_item(wk, sg); ++si) {
+      if (si > 0) ok = warp_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
+      const int nblk = (sg.ctx + kBlock - 1) / kBlock;
+      for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+        const int vs = g % Cfg::VSTAGES, sb = g % Cfg::SBUF;
+        ok = warp_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
+        if (ok) ok = warp_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
+        if (!ok) break;
+        if (lane == 0) v_consumed = g + 1;
+        uint8_t *vt = sV + (size_t)vs * Cfg::KV_BYTES;
+        const int kv0 = (sg.j_first + j) * Cfg::N;  // first position of the tile
+        zero_v_rows<Cfg>(vt, sg.ctx - kv0, min(nblk * kBlock - kv0, Cfg::N), lane);
+        __syncwarp();
+        tc::fence_after();
+        if (lane == 0) {
+          mma_pv_tile<Cfg>(tbase + Cfg::COL_O, tbase + (uint32_t)(sb * Cfg::N), smem_u32(vt), j > sg.j0);
+          tc::commit(&pv_done[sb]);
+          tc::commit(&v_empty[vs]);
+        }
+        __syncwarp();
+        if (__any_sync(kFull, *(volatile int *)&abort_flag)) ok = false;
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+      abort_flag = 1;
+    }
+  } else {
+    // ---------------- softmax + epilogue: thread (row, half) ----------------
+    constexpr int SC = Cfg::N / 2;  // S columns of a thread (its half of the row)
+    constexpr int OC = Cfg::D / 2;  // O columns of a thread
+    const int row = tid & (Cfg::M - 1), half = tid / Cfg::M;
+    const int r = rt * Cfg::M + row, node = r / p.G, gq = r - node * p.G;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float c = p.scale_log2;
+    // half of this row of an item's Q (zeros for a row past the nodes)
+    auto stage_q = [&](const MqSeg &s) {
+      const bool live = node < s.n;
+      const uint16_t *src = static_cast<const uint16_t *>(p.q) +
+                            (((size_t)s.b * p.q_len + (live ? node : 0)) * p.Hq + s.h * p.G + gq) * Cfg::D;
+#pragma unroll
+      for (int k = 0; k < Cfg::D / 16; ++k) {
+        const int ch = half * (Cfg::D / 16) + k;
+        const uint32_t dst = smem_u32(sQ + (ch >> 3) * Cfg::PANEL_Q + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+        if (live)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + ch * 8) : "memory");
+        else
+          sts128(dst, make_uint4(0, 0, 0, 0));
+      }
+    };
+    auto release_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+    };
+    MqWalk wk;
+    wk.start(b0, base0, t0, t1);
+    MqSeg sg{}, nx{};
+    bool have = next_item(wk, sg);
+    bool nhave = have && next_item(wk, nx);
+    if (have) {
+      stage_q(sg);
+      release_q();
+    }
+    bool ok = true;
+    int g = 0, si = 0;
+    while (have && ok) {
+      const int n = sg.j1 - sg.j0;
+      // what this row sees: [lo, start), then node t at start + t iff bit t of mask
+      const bool live = node < sg.n;
+      const int start = sg.ctx - sg.n;
+      uint64_t mask = 0;
+      int lo = INT32_MAX;
+      if (live) {
+        mask = __ldg(p.tree_mask + (size_t)sg.b * p.mask_stride + node) & (~0ull >> (64 - sg.n));
+        lo = p.window > 0 ? start + max(1, __popcll(mask)) - p.window : 0;
+      }
+      const int lo_all = p.window > 0 ? start + p.q_len - p.window : 0;  // no row's lo is above it
+      float m_run = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int gj = g + j, sb = gj % Cfg::SBUF, par = gj & 1;
+        ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
+        if (!ok) break;
+        tc::fence_after();
+        // the item's last S has read Q: the next item's may come in
+        if (j + 1 == n && nhave) stage_q(nx);
+        const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);
+        uint32_t s[SC];
+        const int kvh = (sg.j_first + sg.j0 + j) * Cfg::N + half * SC;  // first position of this half
+#pragma unroll
+        for (int q = 0; q < SC / 32; ++q)
+          tc::ld32(scol + (uint32_t)(q * 32), *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
+        if (kvh + SC > start || kvh < lo_all) {  // (warp-uniform) the tree or a window's edge is in these columns
+          const int c0 = start - kvh;            // the tree's first column
+          uint64_t sees = c0 >= SC ? ~0ull : (c0 > 0 ? ~(~0ull << c0) | mask << c0 : (c0 > -64 ? mask >> -c0 : 0ull));
+          const int cl = lo - kvh;               // the first cached column this row sees
+          if (cl > 0) {
+            const uint64_t past = ~0ull << min(cl, 63), hidden = cl > 63 ? ~0ull : ~past;
+            // (the tree's nodes are the mask's alone)
+            sees &= ~(c0 >= SC ? hidden : (c0 > 0 ? hidden & ~(~0ull << c0) : 0ull));
+          }
+          const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
+#pragma unroll
+          for (int e = 0; e < SC; ++e)
+            if (!(((e < 32 ? s0 : s1) >> (e & 31)) & 1)) s[e] = 0xff800000u;  // -inf
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < SC; e += 2) mx = fmax3(mx, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        // the row max over both halves (double-buffered exchange, bounded wait)
+        red[par][half][row] = mx;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xch[warp & 3][par]);
+        ok = warp_wait(&xch[warp & 3][par], (uint32_t)(gj >> 1) & 1u, p.timeout_ns);
+        if (!ok) break;
+        mx = fmaxf(mx, red[par][half ^ 1][row]);
+        const float m_new = fmaxf(m_run, mx * c);
+        // warps w and w + 4 hold the same rows and the same m_new: same decision
+        const bool rescale = __any_sync(kFull, m_new > m_run + 8.f);
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);
+          m_run = m_new;
+        }
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        const uint64_t cmu = f2_pack(c, c), nmu = f2_pack(-mu, -mu);
+        uint64_t sum2 = f2_pack(0.f, 0.f);
+        uint32_t w[SC / 2], wl[Cfg::BF ? SC / 2 : 1];
+#pragma unroll
+        for (int e = 0; e < SC / 2; ++e) {
+          uint32_t lo_;
+          p_pair<Cfg::BF>(s[2 * e], s[2 * e + 1], cmu, nmu, sum2, w[e], lo_);
+          if constexpr (Cfg::BF) wl[e] = lo_;
+        }
+        const float2 sp = f2_unpack(sum2);
+        if (rescale && j > 0) {  // O must hold P . V of the item's previous tile before it is scaled
+          ok = warp_wait(&pv_done[(gj - 1) % Cfg::SBUF], (uint32_t)((gj - 1) / Cfg::SBUF) & 1u, p.timeout_ns);
+          if (!ok) break;
+          tc::fence_after();
+          scale_o<Cfg>(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), alpha);
+        }
+        l = l * alpha + (sp.x + sp.y);
+        // P (bf16: high parts and residuals; f16: f16 pairs) over this thread's own (already read) S columns
+        tc::st32(scol, w);
+        if constexpr (Cfg::BF) tc::st32(scol + 32, wl);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+      }
+      if (!ok) break;
+      if (nhave) release_q();
+      // ---- epilogue of the item: O / l, or a normalised partial and its lse ----
+      const int gl = g + n - 1;
+      ok = warp_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
+      if (ok) {
+        red_l[half][row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xl);
+        ok = warp_wait(&xl, (uint32_t)si & 1u, p.timeout_ns);
+      }
+      if (!ok) break;
+      tc::fence_after();
+      const float lt = l + red_l[half ^ 1][row];
+      const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees nothing gives 0
+      uint32_t o[OC / 32][32];
+#pragma unroll
+      for (int q = 0; q < OC / 32; ++q)
+        tc::ld32(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC + q * 32), o[q]);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free);
+      if (sg.whole) {
+        uint4 *dst = live ? reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
+                                                      (((size_t)sg.b * p.q_len + node) * p.Hq + sg.h * p.G + gq) * Cfg::D +
+                                                      half * OC)
+                          : nullptr;
+        store_rows_staged<Cfg>(o, inv, dst, sOut + (size_t)(warp * 2048), lane);
+      } else if (live) {
+        const size_t part = ((size_t)blockIdx.x * 2 + sg.slot) * Cfg::M + row;
+        float4 *po = reinterpret_cast<float4 *>(p.part_o + part * Cfg::D + half * OC);
+#pragma unroll
+        for (int q = 0; q < OC / 32; ++q)
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            po[q * 8 + v] = make_float4(__uint_as_float(o[q][4 * v]) * inv, __uint_as_float(o[q][4 * v + 1]) * inv,
+                                        __uint_as_float(o[q][4 * v + 2]) * inv, __uint_as_float(o[q][4 * v + 3]) * inv);
+        if (half == 0) p.part_lse[part] = lt > 0.f ? m_run + log2f(lt) : -INFINITY;
+      }
+      g += n;
+      ++si;
+      sg = nx;
+      have = nhave;
+      nhave = have && next_item(wk, nx);
+    }
+    if (ok) {  // sequences with rows but no tile (an empty context): zeros, sequence b by CTA b mod grid
+      for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const MqSeq s = mq_seq(p, b);
+        if (s.T == 0) {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (size_t)b * p.q_len * p.Hq * Cfg::D);
+          for (size_t i = tid; i < (size_t)s.n * p.Hq * Cfg::D / 8; i += Cfg::SOFTMAX) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+      abort_flag = 1;
+    }
+  }
+
+  // ---------------- drain, then free tensor memory ----------------
+  tc::fence_before();
+  __syncthreads();
+  if (warp == Cfg::ISSUER || warp == Cfg::PV_ISSUER) {
+    if (lane == 0) tc::commit(&fin);  // completes once every MMA either warp issued has
+    __syncwarp();
+    if (!mbar_wait_bounded(&fin, 0, p.timeout_ns) && lane == 0) atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+  } else if (warp == Cfg::PRODUCER && lane == 0) {  // copies issued but never consumed (abort only)
+    for (int j = k_consumed; j < k_issued; ++j)
+      mbar_wait_bounded(&k_full[j % Cfg::KSTAGES], (uint32_t)(j / Cfg::KSTAGES) & 1u, p.timeout_ns);
+    for (int j = v_consumed; j < v_issued; ++j)
+      mbar_wait_bounded(&v_full[j % Cfg::VSTAGES], (uint32_t)(j / Cfg::VSTAGES) & 1u, p.timeout_ns);
+  } else if (tid < Cfg::SOFTMAX) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a Q copy left in flight by an abort
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == Cfg::ISSUER) tc::dealloc(tbase, Cfg::TMEM_COLS);
+  if (tid == 0) p.cta_flags[blockIdx.x] = cta_flags;
+  grid_dep_launch();
+}
+
+// Finishes the items cut between groups: block (x, y) takes row tile x % RT,
+// rows 16 y .. 16 y + 15 of it, of the boundary between groups c = x / RT and
+// c + 1; if that falls inside an item and is the item's first, the partials of
+// groups c .. (the item's last) are merged with weights 2^(lse - max lse) (rows
+// every partial leaves empty give 0).  Block (0, 0) publishes the status bits.
+constexpr int kMergeRows = 16;
+
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeTileParams tp, int n_ctas, int out_bf16) {
+  const MqParams &p = tp.m;
+  grid_dep_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+    int f = 0;
+    for (int c = threadIdx.x; c < n_ctas; c += 32) f |= p.cta_flags[c];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) f |= __shfl_xor_sync(kFull, f, off);
+    if (threadIdx.x == 0) *p.status = f;
+  }
+  const int W = p.prefix[p.B];
+  const int active = mq_active(W, tp.groups);
+  const int c = (int)blockIdx.x / tp.RT, rt = (int)blockIdx.x % tp.RT;
+  if (W <= 0 || c + 1 >= active) return;
+  const int tcut = mq_cut(W, active, c + 1);
+  int lo = 0, hi = p.B;  // the sequence holding tile tcut
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.prefix[mid] <= tcut) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = lo, base = p.prefix[b];
+  const int T = (p.prefix[b + 1] - base) / p.Hkv;
+  const int h = (tcut - base) / T;
+  const int a = base + h * T, e = a + T;                // the item's tiles
+  if (tcut == a) return;                                // the cut falls between items
+  if (mq_cut(W, active, c) > a) return;                 // an earlier cut inside the item merges it
+  const int wl = (int)(((int64_t)e * active - 1) / W);  // the group holding the item's last tile
+  const int R = (p.tree_lens != nullptr ? min(max(__ldg(p.tree_lens + b), 0), p.q_len) : p.q_len) * p.G;
+  const int D = tp.D, row0 = (int)blockIdx.y * kMergeRows;
+  // partial of group w: slot 0 if its range starts inside the item, else 1
+  auto part_of = [&](int w) {
+    return (((size_t)w * tp.RT + rt) * 2 + (mq_cut(W, active, w) >= a ? 0 : 1)) * kTreeTileRows;
+  };
+  for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += blockDim.x) {
+    const int row = row0 + i / (D / 4), d = 4 * (i % (D / 4));
+    const int r = rt * kTreeTileRows + row;
+    if (r >= R) continue;
+    // up to kBatch partials' loads in flight together, joined to a running max and sum
+    constexpr int kBatch = 8;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, den = 0.f;
+    for (int w0 = c; w0 <= wl; w0 += kBatch) {
+      float4 o[kBatch];
+      float l[kBatch];
+      float cm = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        l[t] = -INFINITY;
+        o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w0 + t <= wl) {
+          const size_t part = part_of(w0 + t) + row;
+          l[t] = p.part_lse[part];
+          o[t] = *reinterpret_cast<const float4 *>(p.part_o + part * D + d);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
+      if (cm == -INFINITY) continue;
+      const float mn = fmaxf(M, cm), rescale = exp2f(M - mn);
+      acc.x *= rescale; acc.y *= rescale; acc.z *= rescale; acc.w *= rescale;
+      den *= rescale;
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        const float wt = l[t] == -INFINITY ? 0.f : exp2f(l[t] - mn);
+        acc.x = fmaf(wt, o[t].x, acc.x);
+        acc.y = fmaf(wt, o[t].y, acc.y);
+        acc.z = fmaf(wt, o[t].z, acc.z);
+        acc.w = fmaf(wt, o[t].w, acc.w);
+        den += wt;
+      }
+      M = mn;
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const int node = r / p.G, gq = r - node * p.G;
+    const size_t idx = (((size_t)b * p.q_len + node) * p.Hq + h * p.G + gq) * D + d;
+    const uint2 v = out_bf16 ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
+                             : make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + idx) = v;
+  }
+}
+
+void tree_tiles_grid(int R, int sms, int *RT, int *groups) {
+  *RT = (R + kTreeTileRows - 1) / kTreeTileRows;
+  *groups = *RT >= sms ? 1 : sms / *RT;
+}
+
+static inline size_t tt_align(size_t x) { return (x + 255) / 256 * 256; }
+
+MqWsLayout tree_tiles_ws_layout(int B, int D, int RT, int groups) {
+  const size_t grid = (size_t)RT * groups;
+  MqWsLayout L;
+  size_t o = tt_align(sizeof(WsHeader));
+  L.prefix = o;
+  o = tt_align(o + sizeof(int32_t) * (size_t)(B + 1));
+  L.cta_flags = o;
+  o = tt_align(o + sizeof(int32_t) * grid);
+  L.part_o = o;
+  o = tt_align(o + sizeof(float) * grid * 2 * kTreeTileRows * D);
+  L.part_lse = o;
+  o = tt_align(o + sizeof(float) * grid * 2 * kTreeTileRows);
+  L.total = o;
+  return L;
+}
+
+template <class Cfg>
+static cudaError_t launch_tiles_cfg(const TreeTileParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                    cudaStream_t stream) {
+  static int configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(tree_tile_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    configured[dev] = 1;
+  }
+  const int grid = p.RT * p.groups;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = stream != nullptr ? 1 : 0;  // early launch on explicit streams only
+  e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<Cfg>, p, tmK, tmV);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t mc = {};
+  mc.gridDim = dim3((unsigned)(p.groups > 1 ? (p.groups - 1) * p.RT : 1), kTreeTileRows / kMergeRows);
+  mc.blockDim = dim3(256);
+  mc.stream = stream;
+  mc.attrs = attr;
+  mc.numAttrs = cfg.numAttrs;
+  return cudaLaunchKernelEx(&mc, tree_merge_kernel, p, grid, Cfg::BF ? 1 : 0);
+}
+
+cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                              cudaStream_t stream) {
+  if (p.m.B < 1 || p.m.B > kMqMaxBatch || p.RT < 1 || p.groups < 1) return cudaErrorNotSupported;
+  if (cache_dtype == PKV_BF16) {
+    if (p.D == 128) return launch_tiles_cfg<TreeCfg<BF16, 128>>(p, tmK, tmV, stream);
+    if (p.D == 64) return launch_tiles_cfg<TreeCfg<BF16, 64>>(p, tmK, tmV, stream);
+  } else if (cache_dtype == PKV_F16) {
+    if (p.D == 128) return launch_tiles_cfg<TreeCfg<F16, 128>>(p, tmK, tmV, stream);
+    if (p.D == 64) return launch_tiles_cfg<TreeCfg<F16, 64>>(p, tmK, tmV, stream);
+  }
+  return cudaErrorNotSupported;
+}
+
+}  // namespace pkv

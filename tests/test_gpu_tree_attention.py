@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_helpers import routes
 from tree_reference import Inputs, check_attention, masks_of, to_i64
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +195,19 @@ def test_same_inputs_same_bits():
         a, _ = _call(x)
         b, _ = _call(x)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("route", ["transposed", "tiles", "units"])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 3), ("bf16", 8, 2, 128, 16), ("f16", 6, 2, 128, 13),
+                                              ("bf16", 2, 2, 64, 2), ("f16", 5, 1, 64, 33), ("bf16", 16, 1, 128, 64),
+                                              ("bf16", 12, 4, 128, 1)])
+def test_every_kernel_on_the_same_inputs(route, dtype, Hq, Hkv, D, n):
+    """Each kernel where it applies (pkv_set_route), one tree size each side of
+    its row tiles; windows, ragged trees, an empty context."""
+    with routes(tree=route):
+        ctx = [0, n, 127 + n, 128, 129 + n, 700, 2049]
+        ctx = [max(c, n) if c else 0 for c in ctx]
+        _run(Inputs(40, ctx, n, Hq, Hkv, D, dtype, nodes=[0, n, n, max(1, n - 1), n, n, 1]))
+        _run(Inputs(41, ctx[1:], n, Hq, Hkv, D, dtype), window=130)
+        _run(Inputs(42, [5000], n, Hq, Hkv, D, dtype, stale=False))
+        _run(Inputs(43, [n + 3] * 170, n, Hq, Hkv, D, dtype))
