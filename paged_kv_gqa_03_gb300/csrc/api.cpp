@@ -799,7 +799,7 @@ int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cac
   if (tree_tiles_apply(cache_dtype, B)) {
     int RT = 0, groups = 0;
     tree_tiles_grid(R, sms, &RT, &groups);
-    total = std::max(total, tree_tiles_ws_layout(B, D, RT, groups).total);
+    total = std::max(total, tree_tiles_ws_layout(D, RT, groups).total);
   }
   *bytes_out = total;
   return PKV_OK;
@@ -844,8 +844,9 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
     std::memset(&tp, 0, sizeof(tp));
     tree_tiles_grid(R, sms, &tp.RT, &tp.groups);
     tp.D = D;
-    tp.m = mq_params(tree_tiles_ws_layout(B, D, tp.RT, tp.groups), out, q, k_scale, v_scale, block_table,
+    tp.m = mq_params(tree_tiles_ws_layout(D, tp.RT, tp.groups), out, q, k_scale, v_scale, block_table,
                      max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, &tree);
+    tp.cuts = reinterpret_cast<TreeCut *>(tp.m.prefix);
     return cuda_status(launch_tree_tiles(tp, cache_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
   }
   Choice c;

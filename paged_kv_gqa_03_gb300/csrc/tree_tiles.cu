@@ -34,6 +34,98 @@ struct TreeCfg : PrefillCfg<T, D_> {
   static_assert(SMEM + 6144 <= 232448, "shared memory");
 };
 
+// A cut of the schedule that falls within this many tiles of an item's end is
+// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
+// and the item needs no partials and no merge.
+constexpr int kSnapTiles = 4;
+
+// What group g's range is, for the merge kernel: its first tile, and the item
+// that tile cuts ([a, e) its tiles), e = 0 if the range starts at an item's end.
+struct TreeCut {
+  int t0, b, h, a, e;
+};
+
+// The schedule of one CTA: range [t0, t1) of the tiles, starting in sequence b0
+// whose first tile is base0.
+struct TreeRange {
+  int t0, t1, b0, base0;
+};
+// Block-wide; `find` is shared memory for the scan: the sequences holding the
+// range's ends.
+struct TreeFind {
+  int32_t wsum[8], b[2], base[2];
+};
+template <int THREADS>
+__device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int groups, TreeFind *find, int *cta_flags) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = p.B, per = (B + THREADS - 1) / THREADS;
+  int tk[kMqMaxBatch / THREADS];
+  int own = 0, incl = 0;
+  if (tid < THREADS) {
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
+      const int b = tid * per + k;
+      tk[k] = 0;
+      if (k < per && b < B) {
+        const MqSeq s = mq_seq(p, b);
+        tk[k] = s.T * p.Hkv;
+        bad |= s.bad_ctx ? 1 : 0;
+      }
+      own += tk[k];
+    }
+    incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) find->wsum[warp] = incl;
+    if (blockIdx.x == 0 && __any_sync(kFull, bad) && lane == 0) atomicOr(cta_flags, PKV_FLAG_BAD_LEN);
+  }
+  __syncthreads();
+  int W = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before = W;
+    W += find->wsum[w];
+  }
+  const int active = mq_active(W, groups);
+  TreeRange r;
+  r.t0 = mq_cut(W, active, group);
+  r.t1 = mq_cut(W, active, group + 1);
+  if (tid < THREADS) {
+    int run = before + incl - own;
+#pragma unroll
+    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
+      const int b = tid * per + k;
+      if (run <= r.t0 && r.t0 < run + tk[k]) {
+        find->b[0] = b;
+        find->base[0] = run;
+      }
+      if (run <= r.t1 && r.t1 < run + tk[k]) {
+        find->b[1] = b;
+        find->base[1] = run;
+      }
+      run += tk[k];
+    }
+  }
+  __syncthreads();
+  auto snap = [&](int t, int b, int base) -> int {
+    const int T = mq_seq(p, b).T, d = (t - base) % T;
+    return d <= kSnapTiles ? t - d : (T - d <= kSnapTiles ? t + T - d : t);
+  };
+  r.b0 = B;
+  r.base0 = W;
+  if (r.t0 < W) {  // (else an empty range)
+    r.b0 = find->b[0];
+    r.base0 = find->base[0];
+    r.t0 = snap(r.t0, r.b0, r.base0);
+  }
+  if (r.t1 < W) r.t1 = snap(r.t1, find->b[1], find->base[1]);
+  return r;
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tree_tile_kernel(const __grid_constant__ TreeTileParams tp, const __grid_constant__ CUtensorMap tmK,
@@ -52,7 +144,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
   __shared__ float red[2][2][Cfg::M];
   __shared__ float red_l[2][Cfg::M];
-  __shared__ MqPlan plan;
+  __shared__ TreeFind find;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_flags, k_consumed, v_consumed, k_issued, v_issued;
 
@@ -100,8 +192,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   tc::fence_after();
   const uint32_t tbase = tmem_base;
 
-  int t0, t1, b0, base0;
-  mq_plan<Cfg::SOFTMAX>(p, group, tp.groups, &plan, &cta_flags, &t0, &t1, &b0, &base0);
+  grid_dep_launch();  // the merge kernel's blocks may take the SMs as CTAs leave (it waits for this grid's end)
+  const TreeRange rg = tree_plan<Cfg::SOFTMAX>(p, group, tp.groups, &find, &cta_flags);
 
   // this CTA's next item with rows in its row tile
   auto next_item = [&](MqWalk &wk, MqSeg &sg) -> bool {
@@ -116,7 +208,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // loaded three tiles ahead and first used when the tile's copies are issued
     const int slot = lane & (Cfg::BLOCKS - 1), panel = lane / Cfg::BLOCKS;
     MqWalk wk;
-    wk.start(b0, base0, t0, t1);
+    wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg cs{};
     int cj = 0;
     bool have = false;
@@ -193,7 +285,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ---------------- S issue: in tile order as K lands ----------------
     bool ok = true;
     MqWalk wk;
-    wk.start(b0, base0, t0, t1);
+    wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg sg{};
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
@@ -224,7 +316,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ---------------- P . V issue; an item's first waits until O was read out ----------------
     bool ok = true;
     MqWalk wk;
-    wk.start(b0, base0, t0, t1);
+    wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg sg{};
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
@@ -284,14 +376,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (lane == 0) mbar_arrive(&q_full);
     };
     MqWalk wk;
-    wk.start(b0, base0, t0, t1);
+    wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg sg{}, nx{};
     bool have = next_item(wk, sg);
-    bool nhave = have && next_item(wk, nx);
-    if (have) {
-      stage_q(sg);
-      release_q();
+    if (have) stage_q(sg);
+    if (rt == 0 && tid == 0) {  // (rt 0 has rows in every item with any)
+      TreeCut cut{rg.t0, 0, 0, 0, 0};
+      if (have && sg.j0 > 0) cut = TreeCut{rg.t0, sg.b, sg.h, rg.t0 - sg.j0, rg.t0 - sg.j0 + sg.T};
+      tp.cuts[group] = cut;
     }
+    bool nhave = have && next_item(wk, nx);
+    if (have) release_q();
     bool ok = true;
     int g = 0, si = 0;
     while (have && ok) {
@@ -407,15 +502,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                           : nullptr;
         store_rows_staged<Cfg>(o, inv, dst, sOut + (size_t)(warp * 2048), lane);
       } else if (live) {
-        const size_t part = ((size_t)blockIdx.x * 2 + sg.slot) * Cfg::M + row;
-        float4 *po = reinterpret_cast<float4 *>(p.part_o + part * Cfg::D + half * OC);
+        // partials lie as [D / 4][128 rows] groups of four: a warp's rows side by side
+        const size_t part = ((size_t)blockIdx.x * 2 + sg.slot) * Cfg::M;
+        float4 *po = reinterpret_cast<float4 *>(p.part_o + part * Cfg::D) + (size_t)(half * (OC / 4)) * Cfg::M + row;
 #pragma unroll
         for (int q = 0; q < OC / 32; ++q)
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            po[q * 8 + v] = make_float4(__uint_as_float(o[q][4 * v]) * inv, __uint_as_float(o[q][4 * v + 1]) * inv,
+            po[(size_t)(q * 8 + v) * Cfg::M] = make_float4(__uint_as_float(o[q][4 * v]) * inv, __uint_as_float(o[q][4 * v + 1]) * inv,
                                         __uint_as_float(o[q][4 * v + 2]) * inv, __uint_as_float(o[q][4 * v + 3]) * inv);
-        if (half == 0) p.part_lse[part] = lt > 0.f ? m_run + log2f(lt) : -INFINITY;
+        if (half == 0) p.part_lse[part + row] = lt > 0.f ? m_run + log2f(lt) : -INFINITY;
       }
       g += n;
       ++si;
@@ -458,96 +554,95 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   tc::fence_after();
   if (warp == Cfg::ISSUER) tc::dealloc(tbase, Cfg::TMEM_COLS);
   if (tid == 0) p.cta_flags[blockIdx.x] = cta_flags;
-  grid_dep_launch();
 }
 
-// Finishes the items cut between groups: block (x, y) takes row tile x % RT,
-// rows 16 y .. 16 y + 15 of it, of the boundary between groups c = x / RT and
-// c + 1; if that falls inside an item and is the item's first, the partials of
-// groups c .. (the item's last) are merged with weights 2^(lse - max lse) (rows
-// every partial leaves empty give 0).  Block (0, 0) publishes the status bits.
-constexpr int kMergeRows = 16;
-
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeTileParams tp, int n_ctas, int out_bf16) {
+// Finishes the items cut between groups: block (x, y) takes row tile x % RT and
+// the y-th 16 head-dim elements of the item that group c = x / RT + 1's range
+// starts inside, if c's is the item's first cut: the partials of groups
+// c - 1 .. (the item's last) are joined with weights 2^(lse - max lse) (rows
+// every partial leaves empty give 0).  Thread (row, 8 elements).  Block (0, 0)
+// publishes the status bits.
+__global__ void __launch_bounds__(2 * kTreeTileRows)
+    tree_merge_kernel(const __grid_constant__ TreeTileParams tp, int n_ctas, int out_bf16) {
   const MqParams &p = tp.m;
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31;
   grid_dep_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32) {
     int f = 0;
-    for (int c = threadIdx.x; c < n_ctas; c += 32) f |= p.cta_flags[c];
+    for (int c = tid; c < n_ctas; c += 32) f |= p.cta_flags[c];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) f |= __shfl_xor_sync(kFull, f, off);
-    if (threadIdx.x == 0) *p.status = f;
+    if (tid == 0) *p.status = f;
   }
-  const int W = p.prefix[p.B];
-  const int active = mq_active(W, tp.groups);
-  const int c = (int)blockIdx.x / tp.RT, rt = (int)blockIdx.x % tp.RT;
-  if (W <= 0 || c + 1 >= active) return;
-  const int tcut = mq_cut(W, active, c + 1);
-  int lo = 0, hi = p.B;  // the sequence holding tile tcut
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.prefix[mid] <= tcut) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo, base = p.prefix[b];
-  const int T = (p.prefix[b + 1] - base) / p.Hkv;
-  const int h = (tcut - base) / T;
-  const int a = base + h * T, e = a + T;                // the item's tiles
-  if (tcut == a) return;                                // the cut falls between items
-  if (mq_cut(W, active, c) > a) return;                 // an earlier cut inside the item merges it
-  const int wl = (int)(((int64_t)e * active - 1) / W);  // the group holding the item's last tile
-  const int R = (p.tree_lens != nullptr ? min(max(__ldg(p.tree_lens + b), 0), p.q_len) : p.q_len) * p.G;
-  const int D = tp.D, row0 = (int)blockIdx.y * kMergeRows;
-  // partial of group w: slot 0 if its range starts inside the item, else 1
-  auto part_of = [&](int w) {
-    return (((size_t)w * tp.RT + rt) * 2 + (mq_cut(W, active, w) >= a ? 0 : 1)) * kTreeTileRows;
-  };
-  for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += blockDim.x) {
-    const int row = row0 + i / (D / 4), d = 4 * (i % (D / 4));
-    const int r = rt * kTreeTileRows + row;
-    if (r >= R) continue;
-    // up to kBatch partials' loads in flight together, joined to a running max and sum
-    constexpr int kBatch = 8;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, den = 0.f;
-    for (int w0 = c; w0 <= wl; w0 += kBatch) {
-      float4 o[kBatch];
-      float l[kBatch];
-      float cm = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < kBatch; ++t) {
-        l[t] = -INFINITY;
-        o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w0 + t <= wl) {
-          const size_t part = part_of(w0 + t) + row;
-          l[t] = p.part_lse[part];
-          o[t] = *reinterpret_cast<const float4 *>(p.part_o + part * D + d);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
-      if (cm == -INFINITY) continue;
-      const float mn = fmaxf(M, cm), rescale = exp2f(M - mn);
-      acc.x *= rescale; acc.y *= rescale; acc.z *= rescale; acc.w *= rescale;
-      den *= rescale;
-#pragma unroll
-      for (int t = 0; t < kBatch; ++t) {
-        const float wt = l[t] == -INFINITY ? 0.f : exp2f(l[t] - mn);
-        acc.x = fmaf(wt, o[t].x, acc.x);
-        acc.y = fmaf(wt, o[t].y, acc.y);
-        acc.z = fmaf(wt, o[t].z, acc.z);
-        acc.w = fmaf(wt, o[t].w, acc.w);
-        den += wt;
-      }
-      M = mn;
+  const int c = (int)blockIdx.x / tp.RT + 1, rt = (int)blockIdx.x % tp.RT;
+  if (c >= tp.groups) return;
+  const TreeCut cut = tp.cuts[c];
+  const int first = tp.cuts[c - 1].t0;
+  if (cut.e == 0 || first > cut.a) return;  // no item cut here, or an earlier cut merges it
+  if (tid < 32) {  // the last group whose range starts inside the item
+    int last = c;
+    for (int w = c; w < tp.groups; w += 32) {
+      const bool in = w + lane < tp.groups && tp.cuts[w + lane].t0 < cut.e;
+      const unsigned m = __ballot_sync(kFull, in);
+      if (m == 0) break;
+      last = w + 31 - __clz(m);
+      if (m != kFull) break;
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    const int node = r / p.G, gq = r - node * p.G;
-    const size_t idx = (((size_t)b * p.q_len + node) * p.Hq + h * p.G + gq) * D + d;
-    const uint2 v = out_bf16 ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
-                             : make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + idx) = v;
+    if (lane == 0) s_last = last;
   }
+  const int n = p.tree_lens != nullptr ? min(max(__ldg(p.tree_lens + cut.b), 0), p.q_len) : p.q_len;
+  __syncthreads();
+  const int last = s_last;
+  const int row = tid & (kTreeTileRows - 1), r = rt * kTreeTileRows + row;
+  if (r >= n * p.G) return;
+  const int D = tp.D, d8 = (int)blockIdx.y * 2 + tid / kTreeTileRows;  // elements 8 d8 .. 8 d8 + 7
+  constexpr int kBatch = 4;  // partials whose loads are in flight together
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float M = -INFINITY, den = 0.f;
+  for (int w0 = c - 1; w0 <= last; w0 += kBatch) {
+    float4 x[kBatch], y[kBatch];
+    float l[kBatch], cm = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      l[t] = -INFINITY;
+      x[t] = y[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int w = w0 + t;
+      if (w <= last) {
+        // the item's part of group w: slot 0 if w's range starts in the item, else (c - 1, unless the item is its first) 1
+        const int slot = w >= c || first == cut.a ? 0 : 1;
+        const size_t part = (((size_t)w * tp.RT + rt) * 2 + slot) * kTreeTileRows;
+        l[t] = p.part_lse[part + row];
+        const float4 *po = reinterpret_cast<const float4 *>(p.part_o + part * D) + (size_t)(2 * d8) * kTreeTileRows + row;
+        x[t] = po[0];
+        y[t] = po[kTreeTileRows];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
+    if (cm == -INFINITY) continue;
+    const float mn = fmaxf(M, cm), rescale = exp2f(M - mn);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= rescale;
+    den *= rescale;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const float wt = l[t] == -INFINITY ? 0.f : exp2f(l[t] - mn);
+      const float v[8] = {x[t].x, x[t].y, x[t].z, x[t].w, y[t].x, y[t].y, y[t].z, y[t].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wt, v[e], acc[e]);
+      den += wt;
+    }
+    M = mn;
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int node = r / p.G, gq = r - node * p.G;
+  const size_t idx = (((size_t)cut.b * p.q_len + node) * p.Hq + cut.h * p.G + gq) * D + 8 * d8;
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o[e] = out_bf16 ? pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + idx) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 void tree_tiles_grid(int R, int sms, int *RT, int *groups) {
@@ -557,12 +652,12 @@ void tree_tiles_grid(int R, int sms, int *RT, int *groups) {
 
 static inline size_t tt_align(size_t x) { return (x + 255) / 256 * 256; }
 
-MqWsLayout tree_tiles_ws_layout(int B, int D, int RT, int groups) {
+MqWsLayout tree_tiles_ws_layout(int D, int RT, int groups) {
   const size_t grid = (size_t)RT * groups;
   MqWsLayout L;
   size_t o = tt_align(sizeof(WsHeader));
-  L.prefix = o;
-  o = tt_align(o + sizeof(int32_t) * (size_t)(B + 1));
+  L.prefix = o;  // the groups' cuts
+  o = tt_align(o + sizeof(TreeCut) * (size_t)groups);
   L.cta_flags = o;
   o = tt_align(o + sizeof(int32_t) * grid);
   L.part_o = o;
@@ -596,15 +691,15 @@ static cudaError_t launch_tiles_cfg(const TreeTileParams &p, const CUtensorMap &
   cfg.dynamicSmemBytes = Cfg::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = stream != nullptr ? 1 : 0;  // early launch on explicit streams only
+  cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<Cfg>, p, tmK, tmV);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mc = {};
-  mc.gridDim = dim3((unsigned)(p.groups > 1 ? (p.groups - 1) * p.RT : 1), kTreeTileRows / kMergeRows);
-  mc.blockDim = dim3(256);
+  mc.gridDim = dim3((unsigned)(p.groups > 1 ? (p.groups - 1) * p.RT : 1), (unsigned)(p.D / 16));
+  mc.blockDim = dim3(2 * kTreeTileRows);
   mc.stream = stream;
   mc.attrs = attr;
-  mc.numAttrs = cfg.numAttrs;
+  mc.numAttrs = 1;
   return cudaLaunchKernelEx(&mc, tree_merge_kernel, p, grid, Cfg::BF ? 1 : 0);
 }
 
