@@ -148,9 +148,15 @@ def pkv_get_route(which):
     return names[_L.pkv_get_route(idx)]
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _dtype_codes():
@@ -195,9 +201,12 @@ def _out(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """The raw stream: the current one of `device` (None: the current device)
+    when none is given."""
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -315,40 +324,55 @@ def paged_prefill_attention(out, q, k_cache, v_cache, block_table, context_lens,
         _dev(status, "status", torch.int32), _stream(stream)), "paged_prefill_attention")
 
 
-def _shape(t, name, *want):
-    """`t` has one of the shapes `want`."""
-    if tuple(t.shape) not in want:
-        raise ValueError(f"{name} must have shape {' or '.join(map(str, want))}, got {tuple(t.shape)}")
+def _arg(t, name, dtype, shape, device):
+    """The pointer of a contiguous tensor of this type and shape on CUDA device
+    `device` (an index).  One test on the way through; what is wrong is looked
+    for only when it fails."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _dev(t, name)   # a CUDA tensor, contiguous
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
-def _one_device(device, **tensors):
-    """Every tensor given lives on `device`, which must be the current one (the
-    stream and the launch are the current device's)."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if device.type == "cuda" and device.index != _torch().cuda.current_device():
-        raise ValueError(f"the tensors are on {device}: make it the current device (torch.cuda.device)")
+def _device_of(t, name):
+    """The CUDA device a call runs on, from one of its tensors: it must be the
+    current device, whose stream and context the call uses."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if d != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{d}: make it the current device (torch.cuda.device)")
+    return d
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a cache's four tensors against one another; (num_blocks, Hkv, D)."""
-    if k_cache.dim() != 4 or k_cache.shape[2] != 16:
-        raise ValueError(f"k_cache must be [num_blocks, Hkv, 16, D], got {tuple(k_cache.shape)}")
-    nb, Hkv, _, D = k_cache.shape
-    _shape(v_cache, "v_cache", tuple(k_cache.shape))
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError(f"v_cache is {v_cache.dtype}, k_cache {k_cache.dtype}")
-    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if s is not None:
-            _shape(s, name, (nb, Hkv))
-    return nb, Hkv, D
+def _cache(k_cache, v_cache, k_scale, v_scale, device):
+    """Checks a cache's tensors; (k, v, k scale, v scale pointers, num_blocks, Hkv, D)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != 16:
+        raise ValueError(f"k_cache must be [num_blocks, Hkv, 16, D], got {tuple(shape)}")
+    dtype, f32, sc = k_cache.dtype, _torch().float32, shape[:2]
+    return (_arg(k_cache, "k_cache", dtype, shape, device), _arg(v_cache, "v_cache", dtype, shape, device),
+            None if k_scale is None else _arg(k_scale, "k_scale", f32, sc, device),
+            None if v_scale is None else _arg(v_scale, "v_scale", f32, sc, device), shape[0], shape[1], shape[3])
 
 
-def _tree_mask(tree_mask, B, n):
+def _table(block_table, B, device):
+    """(pointer, max_blocks) of an int32 [B, max_blocks] table."""
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
+    mb = block_table.shape[1]
+    return _arg(block_table, "block_table", _torch().int32, (B, mb), device), mb
+
+
+def _tree_mask(tree_mask, B, n, device):
     """(pointer, mask_per_seq) of an int64 [n] or [B, n] mask."""
-    _shape(tree_mask, "tree_mask", (n,), (B, n))
-    return _dev(tree_mask, "tree_mask", _torch().int64), int(tree_mask.dim() == 2)
+    if tree_mask.dim() == 1:
+        return _arg(tree_mask, "tree_mask", _torch().int64, (n,), device), 0
+    return _arg(tree_mask, "tree_mask", _torch().int64, (B, n), device), 1
 
 
 def paged_tree_workspace_bytes(B, q_len, Hq, Hkv, D, cache_dtype, q_dtype):
@@ -375,52 +399,54 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_table, context_lens, tr
     returned for paged_decode_status.  prepare=True returns the call as a
     Prepared object instead of issuing it."""
     torch = _torch()
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, q_len, Hq, D], got {tuple(q.shape)}")
-    B, n, Hq, D = q.shape
-    _shape(out, "out", (B, n, Hq, D))
-    if out.dtype != q.dtype:
-        raise TypeError(f"out is {out.dtype}, q {q.dtype}")
-    num_blocks, Hkv, Dc = _cache(k_cache, v_cache, k_scale, v_scale)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [B, q_len, Hq, D], got {tuple(shape)}")
+    B, n, Hq, D = shape
+    dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
+    k, v, ks, vs, num_blocks, Hkv, Dc = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if Dc != D:
         raise ValueError(f"q has head dim {D}, the cache {Dc}")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
-    _shape(context_lens, "context_lens", (B,))
-    if tree_lens is not None:
-        _shape(tree_lens, "tree_lens", (B,))
-    mask, per_seq = _tree_mask(tree_mask, B, n)
+    table, max_blocks = _table(block_table, B, dev)
+    mask, per_seq = _tree_mask(tree_mask, B, n, dev)
+    if out.is_cuda:
+        o = _arg(out, "out", dtype, shape, dev)
+    else:   # pinned host memory, as for the other calls that write an output
+        o = _out(out)
+        if out.shape != shape or out.dtype is not dtype:
+            raise ValueError(f"out must be {dtype} of shape {tuple(shape)}")
+    qc, kc = _code(q), _code(k_cache)
     if workspace is None:
-        size = paged_tree_workspace_bytes(B, n, Hq, Hkv, D, _code(k_cache), _code(q))
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    _one_device(q.device, out=out if out.is_cuda else None, k_cache=k_cache, v_cache=v_cache,
-                block_table=block_table, context_lens=context_lens, tree_mask=tree_mask,
-                tree_lens=tree_lens, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
-    args = (_out(out), _dev(q, "q"), _code(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _code(k_cache), _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
-            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-            _dev(context_lens, "context_lens", torch.int32), mask, per_seq,
-            _dev(tree_lens, "tree_lens", torch.int32), B, n, int(window), Hq, Hkv, D, num_blocks, float(scale),
-            _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace = torch.empty(paged_tree_workspace_bytes(B, n, Hq, Hkv, D, kc, qc), dtype=torch.uint8, device=q.device)
+    args = (o, _arg(q, "q", dtype, shape, dev), qc, k, v, kc, ks, vs, table, max_blocks,
+            _arg(context_lens, "context_lens", i32, (B,), dev), mask, per_seq,
+            None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, (B,), dev), B, n, int(window), Hq, Hkv, D,
+            num_blocks, float(scale), _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+            workspace.nbytes, _stream(stream, dev))
     if prepare:
         return Prepared(_L.paged_tree_attention, args, "paged_tree_attention")
-    _check(_L.paged_tree_attention(*args), "paged_tree_attention")
+    rc = _L.paged_tree_attention(*args)
+    if rc != PKV_OK:
+        raise PagedKVError(rc, "paged_tree_attention")
     return workspace
 
 
-def _rows(t, name, B, n):
-    """(pointer, row distance, V) of [B, n, V] rows, a fixed number of elements
+def _rows(t, name, dtype, B, n, V, device):
+    """(pointer, row distance) of [B, n, V] rows a fixed number of elements
     apart (a slice of a wider vocabulary is such a tensor)."""
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != n:
-        raise ValueError(f"{name} must be [{B}, {n}, V], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    V = t.shape[2]
+    if t.shape != (B, n, V):
+        raise ValueError(f"{name} must be [{B}, {n}, {V}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, is on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), V
     sb, sn, sv = t.stride()
     ld = sn if n > 1 else (sb if B > 1 else V)
     if (V > 1 and sv != 1) or ld < V or (B > 1 and n > 1 and sb != n * sn):
         raise ValueError(f"{name} must have contiguous rows a fixed distance apart, got strides {t.stride()}")
-    return t.data_ptr(), ld, V
+    return t.data_ptr(), ld
 
 
 def paged_tree_verify(path, path_len, next_token, draft_tokens, tree_mask, target_probs,
@@ -434,33 +460,28 @@ def paged_tree_verify(path, path_len, next_token, draft_tokens, tree_mask, targe
     uniforms fp32 [B, n].  With draft_probs: sampled drafts; without: each
     node's deterministic continuations; without uniforms too: greedy."""
     torch = _torch()
-    if draft_tokens.dim() != 2:
-        raise ValueError(f"draft_tokens must be [B, n], got {tuple(draft_tokens.shape)}")
-    B, n = draft_tokens.shape
-    _shape(path, "path", (B, n))
-    _shape(path_len, "path_len", (B,))
-    _shape(next_token, "next_token", (B,))
-    if tree_lens is not None:
-        _shape(tree_lens, "tree_lens", (B,))
-    if uniforms is not None:
-        _shape(uniforms, "uniforms", (B, n))
-    mask, per_seq = _tree_mask(tree_mask, B, n)
-    target, ld_t, V = _rows(target_probs, "target_probs", B, n)
-    draft, ld_d = None, 0
-    if draft_probs is not None:
-        draft, ld_d, Vd = _rows(draft_probs, "draft_probs", B, n)
-        if Vd != V or draft_probs.dtype != target_probs.dtype:
-            raise ValueError("draft_probs must have target_probs' vocabulary and type")
-    _one_device(target_probs.device, path=path, path_len=path_len, next_token=next_token,
-                draft_tokens=draft_tokens, tree_mask=tree_mask, draft_probs=draft_probs,
-                uniforms=uniforms, tree_lens=tree_lens)
-    args = (_dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32),
-            _dev(next_token, "next_token", torch.int64), _dev(draft_tokens, "draft_tokens", torch.int64),
-            mask, per_seq, _dev(tree_lens, "tree_lens", torch.int32), target, ld_t, draft, ld_d,
-            _code(target_probs), _dev(uniforms, "uniforms", torch.float32), B, n, V, _stream(stream))
+    i32, i64 = torch.int32, torch.int64
+    shape = draft_tokens.shape
+    if len(shape) != 2:
+        raise ValueError(f"draft_tokens must be [B, n], got {tuple(shape)}")
+    B, n = shape
+    if target_probs.dim() != 3:
+        raise ValueError(f"target_probs must be [{B}, {n}, V], got {tuple(target_probs.shape)}")
+    dev, V, dtype = _device_of(target_probs, "target_probs"), target_probs.shape[2], target_probs.dtype
+    mask, per_seq = _tree_mask(tree_mask, B, n, dev)
+    target, ld_t = _rows(target_probs, "target_probs", dtype, B, n, V, dev)
+    draft, ld_d = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", dtype, B, n, V, dev)
+    args = (_arg(path, "path", i32, shape, dev), _arg(path_len, "path_len", i32, (B,), dev),
+            _arg(next_token, "next_token", i64, (B,), dev), _arg(draft_tokens, "draft_tokens", i64, shape, dev),
+            mask, per_seq, None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, (B,), dev), target, ld_t,
+            draft, ld_d, _code(target_probs),
+            None if uniforms is None else _arg(uniforms, "uniforms", torch.float32, shape, dev), B, n, V,
+            _stream(stream, dev))
     if prepare:
         return Prepared(_L.paged_tree_verify, args, "paged_tree_verify")
-    _check(_L.paged_tree_verify(*args), "paged_tree_verify")
+    rc = _L.paged_tree_verify(*args)
+    if rc != PKV_OK:
+        raise PagedKVError(rc, "paged_tree_verify")
 
 
 def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_lens, k_scale=None,
@@ -468,29 +489,25 @@ def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_len
     """Moves the accepted path's K/V rows together in the paged cache, in
     place: position context_lens[b] - n_b + k takes the row of node path[b, k].
     new_lens (optional int32 [B]) receives the lengths that remain."""
-    torch = _torch()
-    num_blocks, Hkv, D = _cache(k_cache, v_cache, k_scale, v_scale)
-    if path.dim() != 2:
-        raise ValueError(f"path must be [B, n], got {tuple(path.shape)}")
-    B, n = path.shape
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [B, max_blocks], got {tuple(block_table.shape)}")
-    for t, name in ((path_len, "path_len"), (context_lens, "context_lens"), (tree_lens, "tree_lens"),
-                    (new_lens, "new_lens")):
-        if t is not None:
-            _shape(t, name, (B,))
-    _one_device(k_cache.device, v_cache=v_cache, path=path, path_len=path_len, block_table=block_table,
-                context_lens=context_lens, tree_lens=tree_lens, new_lens=new_lens, k_scale=k_scale,
-                v_scale=v_scale)
-    args = (_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _code(k_cache),
-            _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
-            _dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32),
-            _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-            _dev(context_lens, "context_lens", torch.int32), _dev(tree_lens, "tree_lens", torch.int32),
-            _dev(new_lens, "new_lens", torch.int32), B, n, Hkv, D, num_blocks, _stream(stream))
+    i32 = _torch().int32
+    shape = path.shape
+    if len(shape) != 2:
+        raise ValueError(f"path must be [B, n], got {tuple(shape)}")
+    B, n = shape
+    dev, one = _device_of(k_cache, "k_cache"), (B,)
+    k, v, ks, vs, num_blocks, Hkv, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    table, max_blocks = _table(block_table, B, dev)
+    args = (k, v, _code(k_cache), ks, vs, _arg(path, "path", i32, shape, dev),
+            _arg(path_len, "path_len", i32, one, dev), table, max_blocks,
+            _arg(context_lens, "context_lens", i32, one, dev),
+            None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, one, dev),
+            None if new_lens is None else _arg(new_lens, "new_lens", i32, one, dev), B, n, Hkv, D, num_blocks,
+            _stream(stream, dev))
     if prepare:
         return Prepared(_L.paged_tree_commit, args, "paged_tree_commit")
-    _check(_L.paged_tree_commit(*args), "paged_tree_commit")
+    rc = _L.paged_tree_commit(*args)
+    if rc != PKV_OK:
+        raise PagedKVError(rc, "paged_tree_commit")
 
 
 def paged_decode_status(workspace, stream=None):

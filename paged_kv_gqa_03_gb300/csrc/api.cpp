@@ -821,19 +821,17 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_EINVAL;
   if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return PKV_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_EWORKSPACE;
-  size_t need = 0;
-  rc = paged_tree_workspace_bytes(B, q_len, Hq, Hkv, D, cache_dtype, q_dtype, &need);
-  if (rc != PKV_OK) return rc;
-  if (workspace_bytes < need) return PKV_EWORKSPACE;
   const TreeArgs tree{tree_mask, tree_lens, mask_per_seq ? q_len : 0};
   const int R = q_len * (Hq / Hkv);
   int sms = 0;
   rc = device_sm_count(&sms);
   if (rc != PKV_OK) return rc;
   const int route = tree_route(cache_dtype, B, R, D);
-  if (route == PKV_TREE_TRANSPOSED)
+  if (route == PKV_TREE_TRANSPOSED) {
+    if (workspace_bytes < mq_ws_layout(B, sms).total) return PKV_EWORKSPACE;
     return run_mq(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table, max_blocks_per_seq,
                   context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, sms, stream, &tree);
+  }
   if (route == PKV_TREE_TILES) {
     CUtensorMap tmK, tmV;
     rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
@@ -844,7 +842,9 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
     std::memset(&tp, 0, sizeof(tp));
     tree_tiles_grid(R, sms, &tp.RT, &tp.groups);
     tp.D = D;
-    tp.m = mq_params(tree_tiles_ws_layout(D, tp.RT, tp.groups), out, q, k_scale, v_scale, block_table,
+    const MqWsLayout M = tree_tiles_ws_layout(D, tp.RT, tp.groups);
+    if (workspace_bytes < M.total) return PKV_EWORKSPACE;
+    tp.m = mq_params(M, out, q, k_scale, v_scale, block_table,
                      max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, &tree);
     tp.cuts = reinterpret_cast<TreeCut *>(tp.m.prefix);
     return cuda_status(launch_tree_tiles(tp, cache_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
@@ -853,6 +853,7 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   int P = 0;
   rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
   if (rc != PKV_OK) return rc;
+  if (workspace_bytes < ws_layout(B, P, D, c.GC).total) return PKV_EWORKSPACE;
   return run_units(c, P, out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
                    max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, D, num_blocks, scale, workspace, stream,
                    &tree);
@@ -890,7 +891,10 @@ int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token, con
   p.n = q_len;
   p.mask_stride = mask_per_seq ? q_len : 0;
   p.V = V;
-  return cuda_status(launch_tree_verify(p, prob_dtype, B, reinterpret_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  const int rc = device_sm_count(&sms);
+  if (rc != PKV_OK) return rc;
+  return cuda_status(launch_tree_verify(p, prob_dtype, B, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,

@@ -17,7 +17,7 @@ struct VerifyParams {
   int64_t ld_target, ld_draft;  // elements between rows
   int n, mask_stride, V;
 };
-cudaError_t launch_tree_verify(const VerifyParams &p, int dtype, int B, cudaStream_t stream);
+cudaError_t launch_tree_verify(const VerifyParams &p, int dtype, int B, int sms, cudaStream_t stream);
 
 struct CommitParams {
   uint8_t *k_cache, *v_cache;

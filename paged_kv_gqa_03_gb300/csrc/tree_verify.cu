@@ -15,18 +15,23 @@
 //
 // What bounds it.  Only refusals and the final draw read whole rows (p and q,
 // V values each); accepted drafts need two numbers each, gathered for all
-// nodes at once.  So the kernel is a few dependent latencies plus one or two
-// row passes: a cluster of CTAs serves one sequence, each CTA a contiguous
-// slice of the vocabulary, each warp a contiguous part of it.  CTA 0's first
-// warp walks; it hands the others one command at a time through distributed
-// shared memory, so that no CTA ever decides on its own how many cluster
-// barriers there are.
+// nodes at once.  So the kernel is a few dependent latencies plus one row pass
+// per refusal: a cluster of 8 CTAs serves one sequence, each CTA a contiguous
+// slice of the vocabulary, each warp a contiguous part of it.  CTA 0 gathers
+// what the walk needs and hands it to the others through distributed shared
+// memory; from then on every CTA walks by itself on the same numbers (the row
+// sums, exchanged the same way, included), so that one cluster barrier per
+// pass is all they share, and all of them reach the same ones whatever
+// happens to the inputs meanwhile.  The CTA whose slice holds the drawn token
+// finds it.
 //
 // Exactness.  A draw compares partial sums of up to V terms with u times the
 // total; sums in 32 bits would move such a border by ~1e-7, and with it one
-// token in some thousands.  The terms and sums are therefore kept as
-// unevaluated pairs of floats (Knuth's two-sum, Dekker's product by fma,
-// ~48 bits): the fp64 pipe of this GPU is far too narrow for V terms.
+// token in some thousands.  The fp64 pipe of this GPU is far too narrow for V
+// terms, so the sums and the walk's scalars are unevaluated pairs of floats
+// (Knuth's two-sum, products by fma, ~46 bits), and the sum of max(p - a q, 0)
+// is sum p - a sum q over the terms that are positive: 19 operations a term, about
+// two thirds of the time the terms take to arrive from HBM.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -40,9 +45,9 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kTree = PKV_MAX_Q_LEN;
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8;  // CTAs per sequence
 
-// An unevaluated sum h + l of two floats.
+// An unevaluated sum h + l of two floats, |l| <= ulp(h) / 2.
 struct F2 {
   float h, l;
 };
@@ -50,13 +55,45 @@ __device__ __forceinline__ F2 two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ F2 f2_plus(F2 a, F2 b) {
-  const F2 s = two_sum(a.h, b.h);
-  const float e = __fadd_rn(s.l, __fadd_rn(a.l, b.l));
-  const float h = __fadd_rn(s.h, e);
-  return {h, __fsub_rn(e, __fsub_rn(h, s.h))};
+__device__ __forceinline__ F2 renorm(float h, float l) {  // |h| >= |l|, or h = 0
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
 }
-__device__ __forceinline__ double f2_double(F2 a) { return (double)a.h + (double)a.l; }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  const F2 s = two_sum(a.h, b.h), t = two_sum(a.l, b.l);
+  const F2 r = renorm(s.h, __fadd_rn(s.l, t.h));
+  return renorm(r.h, __fadd_rn(r.l, t.l));
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) { return a + F2{-b.h, -b.l}; }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  const float m = __fmul_rn(a.h, b.h);
+  float e = __fmaf_rn(a.h, b.h, -m);
+  e = __fmaf_rn(a.h, b.l, e);
+  e = __fmaf_rn(a.l, b.h, e);
+  return renorm(m, e);
+}
+__device__ __forceinline__ bool less(F2 a, F2 b) { return (b - a).h > 0.f; }
+
+// A running sum hi + lo of floats.
+struct Split {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const F2 r = two_sum(hi, x);
+    hi = r.h;
+    lo = __fadd_rn(lo, r.l);
+  }
+  __device__ __forceinline__ void add(Split o) {
+    const F2 r = two_sum(hi, o.hi);
+    hi = r.h;
+    lo = __fadd_rn(__fadd_rn(lo, o.lo), r.l);
+  }
+  __device__ __forceinline__ F2 value() const { return renorm(hi, lo); }
+};
+// Sums over the terms p - a q that are positive.
+struct Sums {
+  Split p, q;
+  __device__ __forceinline__ F2 value(F2 a) const { return p.value() - a * q.value(); }
+};
 
 enum : int { kExit = 0, kSum = 1, kArgmax = 2 };
 
@@ -65,18 +102,30 @@ struct Cmd {
   F2 a;  // residual coefficient of the draft row
 };
 
-// max(p - a q, 0)
-__device__ __forceinline__ F2 residual(float p, float q, F2 a) {
-  const float m = __fmul_rn(a.h, q);
-  const float ml = __fmaf_rn(a.l, q, __fmaf_rn(a.h, q, -m));
-  F2 d = two_sum(p, -m);
-  d.l = __fsub_rn(d.l, ml);
-  return __fadd_rn(d.h, d.l) > 0.f ? d : F2{0.f, 0.f};  // (a NaN gives 0)
+// What the walk of one sequence needs; the same in every CTA of its cluster.
+struct Walk {
+  uint64_t kids[kTree];  // a node's children
+  uint64_t again;        // (deterministic drafts) nodes whose token an earlier sibling has
+  uint64_t ok;           // nodes accepted if tried: all of them (deterministic drafts), or a node's first child
+  float p[kTree], q[kTree], u[kTree];  // target's and draft's probability of the node's token; its number
+  int tok[kTree];        // -1: outside the vocabulary
+  int n, pad[3];
+};
+static_assert(sizeof(Walk) % 16 == 0, "copied in 16-byte words");
+
+// p - a q where it is positive, rounded to fp32: its sign is exact to 2^-48 of p.
+// (A NaN is not positive.)
+__device__ __forceinline__ bool positive(float p, float q, F2 a) {
+  return __fmaf_rn(-a.l, q, __fmaf_rn(-a.h, q, p)) > 0.f;
 }
 
+// Four elements per lane of the 128 that start at `t`: neighbours (vec: one
+// aligned 4-element load) or 32 apart.  Elements at or past `end` are 0.
+__device__ __forceinline__ int index4(int t, int lane, int e, bool vec) { return vec ? t + 4 * lane + e : t + lane + 32 * e; }
 template <class T>
-__device__ __forceinline__ void load4(const void *row, int64_t i, bool vec, int64_t end, float (&x)[4]) {
-  if (vec) {  // 4 elements, aligned, inside the row
+__device__ __forceinline__ void load4(const void *row, int t, int lane, bool vec, int end, float (&x)[4]) {
+  if (vec && t + 4 * lane + 4 <= end) {
+    const int i = t + 4 * lane;
     if constexpr (T::kBytes == 4) {
       const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i);
       x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
@@ -87,17 +136,19 @@ __device__ __forceinline__ void load4(const void *row, int64_t i, bool vec, int6
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = i + e < end ? load_scalar(T{}, row, (size_t)(i + e)) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const int i = index4(t, lane, e, vec);
+      x[e] = i < end ? load_scalar(T{}, row, (size_t)i) : 0.f;
+    }
   }
 }
 
 }  // namespace
 
-// The nodes, as bits, that are children of `node` with a token in [lo, hi)
-// (warp-wide).
-__device__ __forceinline__ uint64_t lost_in(const int *parent, const int *tok, int node, int lo, int hi, int lane) {
-  const bool l0 = parent[lane] == node && tok[lane] >= lo && tok[lane] < hi;
-  const bool l1 = parent[lane + 32] == node && tok[lane + 32] >= lo && tok[lane + 32] < hi;
+// The nodes of `kids`, as bits, whose token is in [lo, hi) (warp-wide).
+__device__ __forceinline__ uint64_t lost_in(const Walk &w, uint64_t kids, int lo, int hi, int lane) {
+  const bool l0 = ((kids >> lane) & 1) && w.tok[lane] >= lo && w.tok[lane] < hi;
+  const bool l1 = ((kids >> (lane + 32)) & 1) && w.tok[lane + 32] >= lo && w.tok[lane + 32] < hi;
   return (uint64_t)__ballot_sync(kFull, l0) | (uint64_t)__ballot_sync(kFull, l1) << 32;
 }
 
@@ -110,140 +161,181 @@ __device__ __forceinline__ void warp_part(int V, int w, int total, int *lo, int 
 }
 
 template <class T, int THREADS>
-__global__ void __launch_bounds__(THREADS) tree_verify_kernel(const __grid_constant__ VerifyParams p) {
-  constexpr int WARPS = THREADS / 32;
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(const __grid_constant__ VerifyParams p) {
+  constexpr int WARPS = THREADS / 32, C = kCluster;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
+  const int rank = (int)cluster.block_rank();
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ __align__(16) Walk walk;
   __shared__ Cmd cmd;
-  __shared__ int s_parent[kTree];
-  __shared__ int s_tok[kTree];  // -1: outside the vocabulary
-  __shared__ float s_p[kTree], s_q[kTree], s_u[kTree];
   __shared__ int s_path[kTree];
-  // (leader) each warp's sum, or argmax
-  __shared__ double s_sum[kMaxCluster * WARPS];
-  __shared__ float s_best[kMaxCluster * WARPS];
-  __shared__ int s_at[kMaxCluster * WARPS];
-  __shared__ F2 s_scan[WARPS];
-  // (leader) the final draw: the warp part, the first element past the border, the last with any weight
-  __shared__ int s_hit, s_node, s_first, s_last;
-  __shared__ double s_base, s_thr;
-  __shared__ F2 s_a;
+  // every warp's result of a pass, of the whole cluster; alternating between passes
+  __shared__ __align__(16) float4 s_part[2][C * WARPS];
+  __shared__ float4 s_scan[WARPS];
+  __shared__ F2 s_base, s_thr;
+  __shared__ Cmd s_draw;  // the last row pass
+  __shared__ int s_hit, s_first, s_last;  // the final draw: the part, the first element past the border, the last with weight
+  cluster.barrier_arrive();  // (shared memory of the others is written only after all of them run)
   grid_dep_wait();
 
-  const int n = p.lens ? min(max(p.lens[b], 0), p.n) : p.n;
   const bool draft = p.draft != nullptr, greedy = p.u == nullptr;
   auto row = [&](const void *base, int64_t ld, int node) {
     return static_cast<const void *>(static_cast<const uint8_t *>(base) + ((int64_t)b * p.n + node) * ld * T::kBytes);
   };
-  if (tid < kTree) {
+  if (rank == 0) {
+    if (tid < kTree) walk.kids[tid] = 0;
+    if (tid == kTree) walk.again = walk.ok = 0;
+    __syncthreads();
     int up = -1, tok = -1;
-    if (tid < n) {
-      const uint64_t below = p.mask[(int64_t)b * p.mask_stride + tid] & ((1ull << tid) - 1);
-      up = below ? 63 - __clzll(below) : -1;
-      const int64_t t = p.tokens[(int64_t)b * p.n + tid];
-      tok = t >= 0 && t < p.V ? (int)t : -1;
-    }
-    s_parent[tid] = up;
-    s_tok[tid] = tok;
-    if (rank == 0) {
+    if (tid < kTree) {
+      const int n = p.lens ? min(max(p.lens[b], 0), p.n) : p.n;
+      if (tid < n) {
+        const uint64_t below = p.mask[(int64_t)b * p.mask_stride + tid] & ((1ull << tid) - 1);
+        const int64_t t = p.tokens[(int64_t)b * p.n + tid];
+        up = below ? 63 - __clzll(below) : -1;
+        tok = t >= 0 && t < p.V ? (int)t : -1;
+      }
       const bool ask = up >= 0 && tok >= 0 && !greedy;
-      s_p[tid] = ask ? load_scalar(T{}, row(p.target, p.ld_target, up), (size_t)tok) : 0.f;
-      s_q[tid] = ask && draft ? load_scalar(T{}, row(p.draft, p.ld_draft, up), (size_t)tok) : 1.f;
-      s_u[tid] = !greedy && tid < n ? p.u[(int64_t)b * p.n + tid] : 0.f;
+      walk.p[tid] = ask ? load_scalar(T{}, row(p.target, p.ld_target, up), (size_t)tok) : 0.f;
+      walk.q[tid] = ask && draft ? load_scalar(T{}, row(p.draft, p.ld_draft, up), (size_t)tok) : 1.f;
+      walk.u[tid] = !greedy && tid < n ? p.u[(int64_t)b * p.n + tid] : 0.f;
+      walk.tok[tid] = tok;
+      if (up >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&walk.kids[up]), 1ull << tid);
+      if (tid == 0) walk.n = n;
     }
+    __syncthreads();
+    if (!greedy && !draft) {
+      if (up >= 0) {
+        bool again = false;
+        for (uint64_t k = walk.kids[up] & ((1ull << tid) - 1); k; k &= k - 1) again |= walk.tok[__ffsll((long long)k) - 1] == tok;
+        if (again) atomicOr(reinterpret_cast<unsigned long long *>(&walk.again), 1ull << tid);
+      }
+      __syncthreads();
+    }
+    if (!greedy && up >= 0) {  // u q z < w (see the top of the file), as far as it is known without a row sum
+      bool ok = tok >= 0;
+      const F2 u{walk.u[tid], 0.f};
+      if (draft) {
+        ok &= less(u * F2{walk.q[tid], 0.f}, F2{walk.p[tid], 0.f});
+      } else {
+        F2 left{1.f, 0.f};
+        for (uint64_t k = walk.kids[up] & ((1ull << tid) - 1) & ~walk.again; k; k &= k - 1)
+          left = left - F2{walk.p[__ffsll((long long)k) - 1], 0.f};
+        ok &= less(u * left, F2{(walk.again >> tid) & 1 ? 0.f : walk.p[tid], 0.f});
+      }
+      if (ok) atomicOr(reinterpret_cast<unsigned long long *>(&walk.ok), 1ull << tid);
+    }
+    __syncthreads();
+    cluster.barrier_wait();
+    constexpr int WORDS = (int)(sizeof(Walk) / 16);
+    const uint4 *src = reinterpret_cast<const uint4 *>(&walk);
+    for (int i = tid; i < WORDS * (C - 1); i += THREADS)
+      reinterpret_cast<uint4 *>(cluster.map_shared_rank(&walk, 1 + i / WORDS))[i % WORDS] = src[i % WORDS];
+  } else {
+    cluster.barrier_wait();
   }
-  cluster.sync();  // (every CTA of the cluster is running before its shared memory is written)
+  cluster.sync();
 
-  // ---- the walk's state (first warp of the leader; every lane the same) ----
-  int cur = 0, i = 1, len = 1, best = -1;
-  double a = 0.0, z = 1.0, left = 1.0;
-  bool summed = false, done = false;
+  // ---- the walk (first warp of every CTA; every lane the same) ----
+  const int n = walk.n;
+  int cur = 0, len = 1, best = -1;
+  uint64_t kids = walk.kids[0];  // cur's children not tried yet
+  F2 a{0.f, 0.f}, z{1.f, 0.f};
+  int last_pass = 0;  // its sums are the final draw's
+  bool summed = false, seen = false, first = true;
   auto take = [&](int node) {
     cur = node;
+    kids = walk.kids[node];
     if (lane == 0) s_path[len] = node;
     ++len;
-    a = 0.0;
-    z = left = 1.0;
-    summed = false;
+    a = F2{0.f, 0.f};
+    z = F2{1.f, 0.f};
+    summed = seen = false;
+    first = true;
   };
   // runs to the next row pass, or to the end (kExit)
   auto advance = [&]() -> Cmd {
     Cmd c{kExit, 0, {0.f, 0.f}};
+    if (n == 0) return c;
     if (greedy) {
-      if (best >= 0) {  // cur's most likely token is known: its child, if drafted
-        int found = -1;
-        for (; i < n && found < 0; ++i)
-          if (s_parent[i] == cur && s_tok[i] == best) found = i;
-        if (found < 0) return c;
-        take(found);
-        best = -1;
-      } else if (done) {
-        return c;
+      if (seen) {  // cur's most likely token is known: is it drafted?
+        const bool m0 = ((kids >> lane) & 1) && walk.tok[lane] == best, m1 = ((kids >> (lane + 32)) & 1) && walk.tok[lane + 32] == best;
+        const uint64_t m = (uint64_t)__ballot_sync(kFull, m0) | (uint64_t)__ballot_sync(kFull, m1) << 32;
+        if (best < 0 || m == 0) return c;
+        take(__ffsll((long long)m) - 1);
       }
-      done = true;
       c.op = kArgmax;
       c.node = cur;
       return c;
     }
-    bool ask = false;
-    for (; i < n && !ask; ++i) {
-      if (s_parent[i] != cur) continue;
-      bool ok;
-      if (draft) {
-        const double qc = s_q[i], w = (double)s_p[i] - a * qc;
-        ok = s_tok[i] >= 0 && (double)s_u[i] * qc * z < (w > 0.0 ? w : 0.0);
-      } else {
-        bool again = false;  // a token one of its siblings already lost
-        for (int k = 1; k < i; ++k) again |= s_parent[k] == cur && s_tok[k] == s_tok[i];
-        const double pc = again ? 0.0 : (double)s_p[i];
-        ok = s_tok[i] >= 0 && (double)s_u[i] * left < pc;
-        if (!ok) left -= pc;
+    if (!draft) {
+      for (uint64_t m; (m = kids & walk.ok) != 0;) take(__ffsll((long long)m) - 1);
+    } else {
+      bool ask = false;
+      while (kids != 0 && !ask) {
+        const int i = __ffsll((long long)kids) - 1;
+        kids &= kids - 1;
+        bool ok;
+        if (first) {
+          ok = (walk.ok >> i) & 1;
+        } else {
+          const F2 q{walk.q[i], 0.f}, w = F2{walk.p[i], 0.f} - a * q;
+          ok = walk.tok[i] >= 0 && w.h > 0.f && less(F2{walk.u[i], 0.f} * q * z, w);
+        }
+        first = false;
+        if (ok) {
+          take(i);
+        } else {
+          a = a + z;
+          ask = true;
+        }
       }
-      if (ok) {
-        take(i);
-      } else if (draft) {
-        a += z;
-        ask = true;
-      }
+      if (ask) summed = false;
     }
-    if (!ask && summed) return c;  // the last pass was the last node's residual
+    if (summed) return c;  // the last pass was the last node's residual
     c.op = kSum;
     c.node = cur;
-    c.a.h = (float)a;
-    c.a.l = (float)(a - (double)c.a.h);
+    c.a = a;
     return c;
   };
 
-  for (;;) {
-    if (rank == 0 && warp == 0) {
-      const Cmd c = n > 0 ? advance() : Cmd{kExit, 0, {0.f, 0.f}};
-      __syncwarp();
-      if (lane < C) *cluster.map_shared_rank(&cmd, lane) = c;
+  const int me = rank * WARPS + warp;
+  int lo, hi;  // this warp's part of the vocabulary
+  warp_part(p.V, me, C * WARPS, &lo, &hi);
+  constexpr uintptr_t kAlign = 4 * T::kBytes;
+  constexpr int U = 4;  // loads in flight per row
+  for (int pass = 0;; ++pass) {
+    if (warp == 0) {
+      const Cmd c = advance();
+      if (lane == 0) {
+        cmd = c;
+        if (c.op != kExit) s_draw = c;
+      }
     }
-    cluster.sync();
+    __syncthreads();
     const Cmd c = cmd;
     if (c.op == kExit) break;
-    const int W = C * WARPS, me = rank * WARPS + warp;
-    int lo, hi;
-    warp_part(p.V, me, W, &lo, &hi);
+    const int par = pass & 1;
     const void *pr = row(p.target, p.ld_target, c.node);
     const void *qr = draft ? row(p.draft, p.ld_draft, c.node) : nullptr;
-    constexpr uintptr_t kAlign = 4 * T::kBytes;
-    const bool vec = reinterpret_cast<uintptr_t>(pr) % kAlign == 0 &&
-                     (qr == nullptr || reinterpret_cast<uintptr_t>(qr) % kAlign == 0);
+    const bool vec = reinterpret_cast<uintptr_t>(pr) % kAlign == 0 && reinterpret_cast<uintptr_t>(qr) % kAlign == 0;
     if (c.op == kArgmax) {
       float m = -INFINITY;
       int at = INT32_MAX;
-      for (int t = lo + 4 * lane; t < hi; t += 128) {
-        float x[4];
-        load4<T>(pr, t, vec && t + 4 <= hi, hi, x);
+      for (int t = lo; t < hi; t += 128 * U) {
+        float x[U][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (t + e < hi && (x[e] > m || (x[e] == m && at == INT32_MAX))) {
-            m = x[e];
-            at = t + e;
+        for (int k = 0; k < U; ++k) load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // (a lane's indexes grow: the first of equals stays)
+            const int i = index4(t + 128 * k, lane, e, vec);
+            if (i < hi && (x[k][e] > m || (x[k][e] == m && at == INT32_MAX))) {
+              m = x[k][e];
+              at = i;
+            }
           }
       }
 #pragma unroll
@@ -255,50 +347,72 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const __grid_const
           at = oa;
         }
       }
-      if (lane == 0) {
-        *cluster.map_shared_rank(&s_best[me], 0) = m;
-        *cluster.map_shared_rank(&s_at[me], 0) = at;
-      }
+      if (lane < C) *cluster.map_shared_rank(&s_part[par][me], lane) = make_float4(m, __int_as_float(at), 0.f, 0.f);
     } else {
-      // (deterministic drafts) which of this node's children's tokens, all
-      // refused, lie in this warp's part: their weight is 0
-      const uint64_t lost = draft ? 0 : lost_in(s_parent, s_tok, c.node, lo, hi, lane);
-      F2 s{0.f, 0.f};
-      for (int t = lo + 4 * lane; t < hi; t += 128) {
-        float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-        load4<T>(pr, t, vec && t + 4 <= hi, hi, x);
-        if (draft) load4<T>(qr, t, vec && t + 4 <= hi, hi, y);
-        for (uint64_t l = lost; l; l &= l - 1) {
-          const int off = s_tok[__ffsll((long long)l) - 1] - t;
+      // (deterministic drafts) this node's children's tokens in this warp's
+      // part, all refused: their weight is 0
+      const uint64_t lost = draft ? 0 : lost_in(walk, walk.kids[c.node], lo, hi, lane);
+      Sums s{{0.f, 0.f}, {0.f, 0.f}};
+      if (c.a.h == 0.f) {  // no refusal of a sampled draft: the weights are p, and q is not read
+        for (int t = lo; t < hi; t += 128 * U) {
+          float x[U][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (off == e) x[e] = 0.f;
+          for (int k = 0; k < U; ++k) load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
+          for (uint64_t l = lost; l; l &= l - 1) {
+            const int tok = walk.tok[__ffsll((long long)l) - 1];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (index4(t + 128 * k, lane, e, vec) == tok) x[k][e] = 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            if (t + 128 * k < hi) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s.p.add(x[k][e] > 0.f ? x[k][e] : 0.f);
+            }
         }
+      } else {
+        for (int t = lo; t < hi; t += 128 * U) {
+          float x[U][4], y[U][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const F2 w = residual(x[e], y[e], c.a);
-          const F2 r = two_sum(s.h, w.h);
-          s.h = r.h;
-          s.l = __fadd_rn(s.l, __fadd_rn(r.l, w.l));
+          for (int k = 0; k < U; ++k) {
+            load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
+            load4<T>(qr, t + 128 * k, lane, vec, hi, y[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            if (t + 128 * k < hi) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const bool pos = positive(x[k][e], y[k][e], c.a);
+                s.p.add(pos ? x[k][e] : 0.f);
+                s.q.add(pos ? y[k][e] : 0.f);
+              }
+            }
         }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const F2 other{__shfl_xor_sync(kFull, s.h, o), __shfl_xor_sync(kFull, s.l, o)};
-        s = f2_plus(s, other);
+        s.p.add(Split{__shfl_xor_sync(kFull, s.p.hi, o), __shfl_xor_sync(kFull, s.p.lo, o)});
+        s.q.add(Split{__shfl_xor_sync(kFull, s.q.hi, o), __shfl_xor_sync(kFull, s.q.lo, o)});
       }
-      if (lane == 0) *cluster.map_shared_rank(&s_sum[me], 0) = f2_double(s);
+      if (lane < C) *cluster.map_shared_rank(&s_part[par][me], lane) = make_float4(s.p.hi, s.p.lo, s.q.hi, s.q.lo);
     }
     cluster.sync();
-    if (rank == 0 && warp == 0) {  // the pass's result, summed in a fixed order
+    if (warp == 0) {  // every warp's results joined in a fixed order
       if (c.op == kArgmax) {
         float m = -INFINITY;
         int at = INT32_MAX;
-        for (int k = lane; k < W; k += 32)
-          if (s_best[k] > m || (s_best[k] == m && s_at[k] < at)) {
-            m = s_best[k];
-            at = s_at[k];
+        for (int k = lane; k < C * WARPS; k += 32) {
+          const float om = s_part[par][k].x;
+          const int oa = __float_as_int(s_part[par][k].y);
+          if (om > m || (om == m && oa < at)) {
+            m = om;
+            at = oa;
           }
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const float om = __shfl_xor_sync(kFull, m, o);
@@ -309,128 +423,167 @@ __global__ void __launch_bounds__(THREADS) tree_verify_kernel(const __grid_const
           }
         }
         best = at < p.V ? at : -1;  // -1: a row of NaN
+        seen = true;
       } else {
-        double part = 0.0;
-        for (int k = lane; k < W; k += 32) part += s_sum[k];
+        Sums s{{0.f, 0.f}, {0.f, 0.f}};
+        for (int k = lane; k < C * WARPS; k += 32) {
+          const float4 v = s_part[par][k];
+          s.p.add(Split{v.x, v.y});
+          s.q.add(Split{v.z, v.w});
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
-        z = part;
+        for (int o = 16; o > 0; o >>= 1) {
+          s.p.add(Split{__shfl_xor_sync(kFull, s.p.hi, o), __shfl_xor_sync(kFull, s.p.lo, o)});
+          s.q.add(Split{__shfl_xor_sync(kFull, s.q.hi, o), __shfl_xor_sync(kFull, s.q.lo, o)});
+        }
+        z = s.value(c.a);
+        if (z.h < 0.f) z = F2{0.f, 0.f};
         summed = true;
+        last_pass = pass;
       }
     }
   }
-  if (rank != 0) return;
 
-  // ---- the leader: the token after the walk, and the outputs ----
-  int token = -1;
-  if (n > 0 && !greedy) {
-    if (warp == 0) {  // the warp part in which the partial sums pass u_0 times the total
-      const int W = C * WARPS, per = (W + 31) / 32;
-      const double thr = (double)s_u[0] * z;
-      double own = 0.0;
-      for (int k = lane * per; k < min(W, (lane + 1) * per); ++k) own += s_sum[k];
-      double incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += up;
-      }
-      // (rounding, or u_0 >= 1: the last part with any weight)
-      const unsigned past = __ballot_sync(kFull, own > 0.0 && incl > thr), any = __ballot_sync(kFull, own > 0.0);
-      const int who = past ? __ffs(past) - 1 : 31 - __clz(any);  // -1: no weight at all
-      if (lane == 0) {
-        s_hit = -1;
-        s_node = cur;
-        s_a = F2{(float)a, (float)(a - (double)(float)a)};
-        s_thr = thr;
-        s_first = INT32_MAX;
-        s_last = -1;
-      }
-      __syncwarp();
-      if (lane == who) {
-        double run = incl - own;
-        for (int k = lane * per; k < min(W, (lane + 1) * per); ++k) {
-          if (s_sum[k] > 0.0) {
-            s_hit = k;
-            s_base = run;
-            if (run + s_sum[k] > thr) break;
-          }
-          run += s_sum[k];
-        }
-      }
-    }
-    __syncthreads();
-    if (s_hit >= 0) {
-      int lo, hi;
-      warp_part(p.V, s_hit, C * WARPS, &lo, &hi);
-      const int node = s_node;
-      const F2 ca = s_a;
-      const double base = s_base, thr = s_thr;
-      const void *pr = row(p.target, p.ld_target, node);
-      const void *qr = draft ? row(p.draft, p.ld_draft, node) : nullptr;
-      const uint64_t lost = draft ? 0 : lost_in(s_parent, s_tok, node, lo, hi, lane);
-      const int per = (hi - lo + THREADS - 1) / THREADS;  // elements of a thread, consecutive
-      const int t0 = min(hi, lo + tid * per), t1 = min(hi, t0 + per);
-      auto weight = [&](int t) -> F2 {
-        float x = load_scalar(T{}, pr, (size_t)t);
-        for (uint64_t l = lost; l; l &= l - 1)
-          if (s_tok[__ffsll((long long)l) - 1] == t) x = 0.f;
-        return residual(x, draft ? load_scalar(T{}, qr, (size_t)t) : 0.f, ca);
-      };
-      F2 mine{0.f, 0.f};
-      for (int t = t0; t < t1; ++t) {
-        const F2 w = weight(t);
-        if (__fadd_rn(w.h, w.l) > 0.f) atomicMax(&s_last, t);
-        mine = f2_plus(mine, w);
-      }
-      F2 incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const F2 up{__shfl_up_sync(kFull, incl.h, o), __shfl_up_sync(kFull, incl.l, o)};
-        if (lane >= o) incl = f2_plus(up, incl);
-      }
-      if (lane == 31) s_scan[warp] = incl;
-      __syncthreads();
-      F2 run{0.f, 0.f};  // the weights before this thread's
-      for (int k = 0; k < warp; ++k) run = f2_plus(run, s_scan[k]);
-      const F2 ex{__shfl_up_sync(kFull, incl.h, 1), __shfl_up_sync(kFull, incl.l, 1)};
-      if (lane > 0) run = f2_plus(run, ex);
-      if (base + f2_double(f2_plus(run, mine)) > thr) {
-        for (int t = t0; t < t1; ++t) {
-          const F2 w = weight(t);
-          run = f2_plus(run, w);
-          if (__fadd_rn(w.h, w.l) > 0.f && base + f2_double(run) > thr) {
-            atomicMin(&s_first, t);
-            break;
-          }
-        }
-      }
-      __syncthreads();
-      token = s_first != INT32_MAX ? s_first : s_last;
-    }
-  } else if (n > 0) {
-    token = best;  // (the leader's first warp holds it)
-  }
-  if (warp == 0) {
+  // ---- the outputs (leader) and the token after the walk ----
+  if (rank == 0 && warp == 0) {
     const int m = n > 0 ? len : 0;
+    __syncwarp();
     for (int k = lane; k < p.n; k += 32) p.path[(int64_t)b * p.n + k] = k >= m ? -1 : (k == 0 ? 0 : s_path[k]);
     if (lane == 0) {
       p.path_len[b] = m;
-      p.next_token[b] = token;
+      if (n == 0 || greedy) p.next_token[b] = n > 0 ? best : -1;
     }
   }
+  if (n == 0 || greedy) return;
+  const Cmd last = s_draw;
+  if (warp == 0) {
+    // the part (warp of the cluster) in which the sums pass the border u_0 z; by
+    // rounding, or for u_0 >= 1, none may: then the last part with any weight
+    constexpr int PER = C * WARPS / 32;  // consecutive parts of a lane
+    const float4 *part = s_part[last_pass & 1];
+    const F2 thr = F2{walk.u[0], 0.f} * z;
+    auto sums = [&](int k) { return Sums{{part[k].x, part[k].y}, {part[k].z, part[k].w}}; };
+    Sums own{{0.f, 0.f}, {0.f, 0.f}};
+    bool any = false;
+    for (int k = lane * PER; k < (lane + 1) * PER; ++k) {
+      const Sums v = sums(k);
+      any |= v.value(last.a).h > 0.f;
+      own.p.add(v.p);
+      own.q.add(v.q);
+    }
+    Sums incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Split up{__shfl_up_sync(kFull, incl.p.hi, o), __shfl_up_sync(kFull, incl.p.lo, o)};
+      const Split uq{__shfl_up_sync(kFull, incl.q.hi, o), __shfl_up_sync(kFull, incl.q.lo, o)};
+      if (lane >= o) {
+        incl.p.add(up);
+        incl.q.add(uq);
+      }
+    }
+    const unsigned past = __ballot_sync(kFull, any && less(thr, incl.value(last.a))), some = __ballot_sync(kFull, any);
+    const int who = past ? __ffs(past) - 1 : 31 - __clz(some);  // -1: no weight at all
+    if (lane == 0) {
+      s_hit = -1;
+      s_first = INT32_MAX;
+      s_last = -1;
+      if (who < 0 && rank == 0) p.next_token[b] = -1;
+    }
+    __syncwarp();
+    if (lane == who) {
+      Sums run = incl;  // the sums before this lane's parts
+      run.p.add(Split{-own.p.hi, -own.p.lo});
+      run.q.add(Split{-own.q.hi, -own.q.lo});
+      int hit = -1;
+      F2 base{0.f, 0.f};
+      for (int k = lane * PER; k < (lane + 1) * PER; ++k) {
+        const Sums v = sums(k);
+        const F2 before = run.value(last.a);
+        run.p.add(v.p);
+        run.q.add(v.q);
+        if (v.value(last.a).h > 0.f) {
+          hit = k;
+          base = before;
+          if (less(thr, run.value(last.a))) break;
+        }
+      }
+      if (hit / WARPS == rank) {  // this CTA holds the token
+        s_hit = hit;
+        s_base = base;
+        s_thr = thr;
+      }
+    }
+  }
+  __syncthreads();
+  if (s_hit < 0) return;
+  warp_part(p.V, s_hit, C * WARPS, &lo, &hi);
+  const F2 base = s_base, thr = s_thr;
+  const void *pr = row(p.target, p.ld_target, last.node);
+  const void *qr = last.a.h != 0.f ? row(p.draft, p.ld_draft, last.node) : nullptr;
+  const uint64_t lost = draft ? 0 : lost_in(walk, walk.kids[last.node], lo, hi, lane);
+  // each thread a run of consecutive elements: their sums, the sums before
+  // them, and in the thread that passes the border the element that does
+  const int per = (hi - lo + THREADS - 1) / THREADS;
+  const int t0 = min(hi, lo + tid * per), t1 = min(hi, t0 + per);
+  auto add = [&](Sums &s, int t) -> bool {
+    float x = load_scalar(T{}, pr, (size_t)t);
+    const float y = qr ? load_scalar(T{}, qr, (size_t)t) : 0.f;
+    for (uint64_t l = lost; l; l &= l - 1)
+      if (walk.tok[__ffsll((long long)l) - 1] == t) x = 0.f;
+    const bool pos = positive(x, y, last.a);
+    if (pos) {
+      s.p.add(x);
+      s.q.add(y);
+    }
+    return pos;
+  };
+  Sums mine{{0.f, 0.f}, {0.f, 0.f}};
+  for (int t = t0; t < t1; ++t)
+    if (add(mine, t)) atomicMax(&s_last, t);
+  Sums incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Split up{__shfl_up_sync(kFull, incl.p.hi, o), __shfl_up_sync(kFull, incl.p.lo, o)};
+    const Split uq{__shfl_up_sync(kFull, incl.q.hi, o), __shfl_up_sync(kFull, incl.q.lo, o)};
+    if (lane >= o) {
+      incl.p.add(up);
+      incl.q.add(uq);
+    }
+  }
+  if (lane == 31) s_scan[warp] = make_float4(incl.p.hi, incl.p.lo, incl.q.hi, incl.q.lo);
+  Sums run{{__shfl_up_sync(kFull, incl.p.hi, 1), __shfl_up_sync(kFull, incl.p.lo, 1)},
+           {__shfl_up_sync(kFull, incl.q.hi, 1), __shfl_up_sync(kFull, incl.q.lo, 1)}};
+  if (lane == 0) run = Sums{{0.f, 0.f}, {0.f, 0.f}};
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) {
+    run.p.add(Split{s_scan[k].x, s_scan[k].y});
+    run.q.add(Split{s_scan[k].z, s_scan[k].w});
+  }
+  auto past = [&](const Sums &s) { return less(thr, base + s.value(last.a)); };
+  Sums after = run;
+  after.p.add(mine.p);
+  after.q.add(mine.q);
+  if (t0 < t1 && past(after)) {
+    for (int t = t0; t < t1; ++t)
+      if (add(run, t) && past(run)) {
+        atomicMin(&s_first, t);
+        break;
+      }
+  }
+  __syncthreads();
+  if (tid == 0) p.next_token[b] = s_first != INT32_MAX ? s_first : s_last;
 }
 
 template <class T, int THREADS>
 static cudaError_t launch_verify_t(const VerifyParams &p, int B, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kMaxCluster;
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)B * kMaxCluster);
+  cfg.gridDim = dim3((unsigned)B * kCluster);
   cfg.blockDim = dim3(THREADS);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -438,10 +591,17 @@ static cudaError_t launch_verify_t(const VerifyParams &p, int B, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, tree_verify_kernel<T, THREADS>, p);
 }
 
-cudaError_t launch_tree_verify(const VerifyParams &p, int dtype, int B, cudaStream_t stream) {
-  if (dtype == PKV_F32) return launch_verify_t<F32, 256>(p, B, stream);
-  if (dtype == PKV_F16) return launch_verify_t<F16, 256>(p, B, stream);
-  if (dtype == PKV_BF16) return launch_verify_t<BF16, 256>(p, B, stream);
+// Threads per CTA: 512 while two CTAs per SM hold the batch's clusters side by
+// side (a GPC has room for few clusters at one CTA per SM), else 256, four to an SM.
+template <class T>
+static cudaError_t launch_verify(const VerifyParams &p, int B, int sms, cudaStream_t stream) {
+  return B * kCluster <= 2 * sms ? launch_verify_t<T, 512>(p, B, stream) : launch_verify_t<T, 256>(p, B, stream);
+}
+
+cudaError_t launch_tree_verify(const VerifyParams &p, int dtype, int B, int sms, cudaStream_t stream) {
+  if (dtype == PKV_F32) return launch_verify<F32>(p, B, sms, stream);
+  if (dtype == PKV_F16) return launch_verify<F16>(p, B, sms, stream);
+  if (dtype == PKV_BF16) return launch_verify<BF16>(p, B, sms, stream);
   return cudaErrorNotSupported;
 }
 

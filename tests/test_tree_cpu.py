@@ -80,59 +80,114 @@ def test_commit_refusals():
     assert call(B=0) == pkv.PKV_OK
 
 
-def test_binding_refusals():
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on device 0: the binding's checks run
+    without a GPU (the C call behind them is replaced)."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def _gpu(x):
+    return x.as_subclass(OnGpu) if isinstance(x, torch.Tensor) else x
+
+
+def _recorded(monkeypatch, pkv):
+    """Replaces the C calls and what asks for a GPU; the list of calls made."""
+    made = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: made.append((name, a)) or 0
+    monkeypatch.setattr(pkv, "_L", Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_stream", lambda s, d=None: 0)
+    return made
+
+
+def test_binding_refusals(monkeypatch):
     """Shapes, types, strides and places are checked before the call."""
     pkv = _pkv()
     x = Inputs(1, [40, 33], 4, 4, 2, 64, "bf16")
+    made = _recorded(monkeypatch, pkv)
     table, lens = torch.from_numpy(x.table), torch.tensor(x.ctx, dtype=torch.int32)
-    ws = torch.empty(256, dtype=torch.uint8)
-    good = dict(out=torch.empty_like(x.q), q=x.q, k_cache=x.kc, v_cache=x.vc, block_table=table, context_lens=lens,
-                tree_mask=x.mask, scale=0.1, workspace=ws)
+    ones = torch.ones(x.num_blocks, 2)
 
     def refused(fn, base, exc, **kw):
+        before = len(made)
         with pytest.raises(exc):
-            fn(**{**base, **kw})
+            fn(**{k: _gpu(v) for k, v in {**base, **kw}.items()})
+        assert len(made) == before
+        for name, v in kw.items():   # the same call is fine otherwise
+            assert name in base or name in ("tree_lens", "k_scale", "uniforms", "draft_probs", "new_lens"), name
+    good = dict(out=torch.empty_like(x.q), q=x.q, k_cache=x.kc, v_cache=x.vc, block_table=table, context_lens=lens,
+                tree_mask=x.mask, scale=0.1, workspace=torch.empty(256, dtype=torch.uint8))
     f = pkv.paged_tree_attention
-    for kw in (dict(), dict(q=x.q[0]), dict(out=x.q[:, :3]), dict(v_cache=x.vc[:1]), dict(k_cache=x.kc[:, :, :8]),
+    f(**{k: _gpu(v) for k, v in good.items()})
+    assert made[-1][0] == "paged_tree_attention" and made[-1][1][12] == 1       # one mask per sequence
+    f(**{k: _gpu(v) for k, v in {**good, "tree_mask": x.mask[0].contiguous()}.items()})
+    assert made[-1][1][12] == 0
+    wide = torch.zeros(2, 4, 4, 128, dtype=torch.bfloat16)
+    for kw in (dict(q=x.q[0]), dict(out=x.q[:, :3]), dict(v_cache=x.vc[:1]), dict(k_cache=x.kc[:, :, :8]),
                dict(block_table=table[0]), dict(block_table=table[:1]), dict(context_lens=lens[:1]),
                dict(tree_mask=x.mask[:, :3]), dict(tree_mask=x.mask[:1]), dict(tree_lens=lens[:1]),
-               dict(k_scale=torch.ones(3, 3)), dict(q=torch.zeros(2, 4, 4, 128, dtype=torch.bfloat16),
-                                                    out=torch.zeros(2, 4, 4, 128, dtype=torch.bfloat16))):
-        refused(f, good, ValueError, **kw)   # dict(): right shapes, but not on a GPU
-    refused(f, good, TypeError, out=x.q.float())
-    refused(f, good, TypeError, v_cache=x.vc.half())
+               dict(k_scale=ones[:, :1]), dict(q=wide, out=wide), dict(q=x.q.transpose(1, 2).contiguous().transpose(1, 2)),
+               dict(tree_mask=torch.stack([x.mask, x.mask], 1)[:, 0])):
+        refused(f, good, ValueError, **kw)
+    for kw in (dict(out=x.q.float()), dict(v_cache=x.vc.half()), dict(tree_mask=x.mask.int()), dict(context_lens=lens.long()),
+               dict(block_table=table.long()), dict(tree_lens=lens.long()), dict(k_scale=ones.double())):
+        refused(f, good, TypeError, **kw)
+    for name in ("q", "k_cache", "v_cache", "block_table", "context_lens", "tree_mask", "workspace", "out"):
+        with pytest.raises(ValueError):   # one tensor on the host
+            f(**{k: v if k == name else _gpu(v) for k, v in good.items()})
     B, n, V = 2, 4, 50
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     good = dict(path=i32(B, n), path_len=i32(B), next_token=torch.zeros(B, dtype=torch.int64),
                 draft_tokens=torch.zeros(B, n, dtype=torch.int64), tree_mask=x.mask, target_probs=torch.zeros(B, n, V))
     f = pkv.paged_tree_verify
-    for kw in (dict(), dict(path=i32(B, 3)), dict(path_len=i32(3)), dict(next_token=i32(3)), dict(draft_tokens=i32(8)),
-               dict(uniforms=torch.zeros(B)), dict(target_probs=torch.zeros(B, V)), dict(tree_lens=lens[:1]),
-               dict(draft_probs=torch.zeros(B, n, V + 1))):
+    f(**{k: _gpu(v) for k, v in good.items()})
+    for kw in (dict(path=i32(B, 3)), dict(path_len=i32(3)), dict(next_token=torch.zeros(3, dtype=torch.int64)),
+               dict(draft_tokens=torch.zeros(8, dtype=torch.int64)), dict(uniforms=torch.zeros(B)),
+               dict(target_probs=torch.zeros(B, V)), dict(tree_lens=lens[:1]), dict(draft_probs=torch.zeros(B, n, V + 1)),
+               dict(target_probs=torch.zeros(B, n, 2 * V)[..., ::2])):
         refused(f, good, ValueError, **kw)
+    for kw in (dict(draft_tokens=i32(B, n)), dict(next_token=i32(B)), dict(uniforms=torch.zeros(B, n).double()),
+               dict(draft_probs=torch.zeros(B, n, V).half()), dict(path=i32(B, n).long())):
+        refused(f, good, TypeError, **kw)
     good = dict(k_cache=x.kc, v_cache=x.vc, path=i32(B, n), path_len=i32(B), block_table=table, context_lens=lens)
     f = pkv.paged_tree_commit
-    for kw in (dict(), dict(path=i32(8)), dict(path_len=i32(1)), dict(block_table=table[:1]), dict(new_lens=i32(3)),
+    f(**{k: _gpu(v) for k, v in good.items()})
+    for kw in (dict(path=i32(8)), dict(path_len=i32(1)), dict(block_table=table[:1]), dict(new_lens=i32(3)),
                dict(tree_lens=i32(1)), dict(k_cache=x.kc[0])):
         refused(f, good, ValueError, **kw)
+    refused(f, good, TypeError, new_lens=torch.zeros(B, dtype=torch.int64))
+
+
+def test_other_device_is_refused(monkeypatch):
+    pkv = _pkv()
+    x = Inputs(1, [40, 33], 4, 4, 2, 64, "bf16")
+    made = _recorded(monkeypatch, pkv)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    path = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="current device"):
+        pkv.paged_tree_commit(*(_gpu(t) for t in (x.kc, x.vc, path, path[:, 0], torch.from_numpy(x.table), path[:, 0])))
+    assert made == []
 
 
 def test_row_strides_of_probabilities():
     """_rows takes rows a fixed distance apart and nothing else."""
     pkv = _pkv()
-
-    class OnGpu(torch.Tensor):
-        is_cuda = True
-    as_gpu = lambda t: t.as_subclass(OnGpu)  # noqa: E731
+    rows = lambda t: pkv._rows(_gpu(t), "t", t.dtype, *t.shape, 0)  # noqa: E731
     t = torch.zeros(3, 5, 40)
-    assert pkv._rows(as_gpu(t), "t", 3, 5)[1:] == (40, 40)
-    assert pkv._rows(as_gpu(t[..., :33]), "t", 3, 5)[1:] == (40, 33)
-    assert pkv._rows(as_gpu(t[:, :1, :33]), "t", 3, 1)[1:] == (200, 33)
-    assert pkv._rows(as_gpu(t[:1]), "t", 1, 5)[1:] == (40, 40)
+    assert rows(t)[1] == 40
+    assert rows(t[..., :33])[1] == 40
+    assert rows(t[:, :1, :33])[1] == 200
+    assert rows(t[:1])[1] == 40
     for bad in (t[:, :4], t.transpose(0, 1).contiguous().transpose(0, 1), t[..., ::2], t[:, ::2], t[:1].expand(3, 5, 40),
                 t[:, :1].expand(3, 5, 40)):
         with pytest.raises(ValueError):
-            pkv._rows(as_gpu(bad), "t", bad.shape[0], bad.shape[1])
+            rows(bad)
 
 
 # ---------------------------------------------------------------------------
