@@ -180,7 +180,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Tensor map over a [num_blocks][Hkv][16][D] cache as 2-D rows of 128 bytes
 // wide boxes with the 128-byte swizzle; one box is 16 token rows x 128 bytes
 // (or 8 lines of two 64-byte tokens).
-int encode_cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_blocks, int Hkv, int D) {
+// rows64: 64-byte rows as 16 x 64-byte boxes with the 64-byte swizzle instead (the
+// K-major operand layout of an 8-bit tile of head dim 64).
+int encode_cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_blocks, int Hkv, int D, bool rows64) {
   auto fn = encode_fn();
   if (!fn) return cuda_status(cudaErrorNotSupported);
   const int es = esize_of(dtype);
@@ -188,11 +190,11 @@ int encode_cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_
   cuuint64_t dims[2], strides[1];
   cuuint32_t box[2], estr[2] = {1, 1};
   const cuuint64_t tiles = (cuuint64_t)num_blocks * Hkv;
-  if (rowb >= 128) {
+  if (rowb >= 128 || rows64) {
     dims[0] = (cuuint64_t)D;
     dims[1] = tiles * kBlock;
     strides[0] = (cuuint64_t)rowb;
-    box[0] = 128 / es;
+    box[0] = rows64 ? D : 128 / es;
     box[1] = kBlock;
   } else {
     dims[0] = 128 / es;
@@ -205,7 +207,7 @@ int encode_cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_
                                  : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUresult r = fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  rows64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cuda_status(cudaErrorInvalidValue);
   return PKV_OK;
@@ -220,8 +222,10 @@ struct MapKey {
   const void *base;
   int64_t num_blocks;
   int dtype, Hkv, D;
+  bool rows64;
   bool operator==(const MapKey &o) const {
-    return base == o.base && num_blocks == o.num_blocks && dtype == o.dtype && Hkv == o.Hkv && D == o.D;
+    return base == o.base && num_blocks == o.num_blocks && dtype == o.dtype && Hkv == o.Hkv && D == o.D &&
+           rows64 == o.rows64;
   }
 };
 struct MapCache {
@@ -233,8 +237,8 @@ struct MapCache {
 };
 MapCache g_maps;
 
-int cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_blocks, int Hkv, int D) {
-  const MapKey k{base, num_blocks, dtype, Hkv, D};
+int cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_blocks, int Hkv, int D, bool rows64 = false) {
+  const MapKey k{base, num_blocks, dtype, Hkv, D, rows64};
   {
     std::lock_guard<std::mutex> lock(g_maps.mu);
     for (int i = 0; i < g_maps.used; ++i)
@@ -243,7 +247,7 @@ int cache_map(CUtensorMap *map, const void *base, int dtype, int64_t num_blocks,
         return PKV_OK;
       }
   }
-  const int rc = encode_cache_map(map, base, dtype, num_blocks, Hkv, D);
+  const int rc = encode_cache_map(map, base, dtype, num_blocks, Hkv, D, rows64);
   if (rc != PKV_OK) return rc;
   std::lock_guard<std::mutex> lock(g_maps.mu);
   const int slot = g_maps.used < MapCache::kEntries ? g_maps.used++ : g_maps.next;
@@ -771,7 +775,7 @@ static bool tree_mq_applies(int cache_dtype, int B, int R, int D) {
   return (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && D == kMqHeadDim && R <= kMqRows && B <= kMqMaxBatch;
 }
 static bool tree_tiles_apply(int cache_dtype, int B) {
-  return (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && B <= kMqMaxBatch;
+  return cache_dtype != PKV_F32 && B <= kMqMaxBatch;
 }
 static int tree_route(int cache_dtype, int B, int R, int D) {
   const int force = g_route[PKV_ROUTE_TREE].load(std::memory_order_relaxed);
@@ -834,7 +838,7 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   }
   if (route == PKV_TREE_TILES) {
     CUtensorMap tmK, tmV;
-    rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
+    rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D, cache_dtype == PKV_FP8_E4M3 && D == 64);
     if (rc != PKV_OK) return rc;
     rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
     if (rc != PKV_OK) return rc;
@@ -847,7 +851,7 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
     tp.m = mq_params(M, out, q, k_scale, v_scale, block_table,
                      max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, &tree);
     tp.cuts = reinterpret_cast<TreeCut *>(tp.m.prefix);
-    return cuda_status(launch_tree_tiles(tp, cache_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_tree_tiles(tp, cache_dtype, q_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
   }
   Choice c;
   int P = 0;

@@ -789,8 +789,9 @@ __device__ __forceinline__ void mma_finish(MmaState<Cfg> &st, const DecodeParams
           if (hB < gc) oB[d] = st.acc[nh][mt][2 * r + 1] * inv1;
         }
       if (gid == 0) {
-        if (hA < gc) p.part_lse[base + hA] = st.m[nh][0] + log2f(l0);
-        if (hB < gc) p.part_lse[base + hB] = st.m[nh][1] + log2f(l1);
+        // (tree: a sum that is NaN gives +inf, and the merge NaN)
+        if (hA < gc) p.part_lse[base + hA] = Cfg::TREE && l0 != l0 ? INFINITY : st.m[nh][0] + log2f(l0);
+        if (hB < gc) p.part_lse[base + hB] = Cfg::TREE && l1 != l1 ? INFINITY : st.m[nh][1] + log2f(l1);
       }
     }
   }
@@ -996,7 +997,7 @@ __device__ __forceinline__ void simt_finish(SimtState<Cfg> &st, const DecodePara
       float *o = p.part_o + (base + g) * Cfg::D + lane * DPL;
 #pragma unroll
       for (int e = 0; e < DPL; ++e) o[e] = st.acc[g][e] * inv;
-      if (lane == 0) p.part_lse[base + g] = st.m[g] + log2f(st.l[g]);
+      if (lane == 0) p.part_lse[base + g] = Cfg::TREE && st.l[g] != st.l[g] ? INFINITY : st.m[g] + log2f(st.l[g]);
     }
   }
 }

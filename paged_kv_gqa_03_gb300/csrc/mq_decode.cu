@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (r < (Cfg::TREE ? sg.n * p.G : p.R)) {
             const int ii = r / p.G, gq = r - ii * p.G;
             const size_t idx = (((size_t)sg.b * p.q_len + ii) * p.Hq + sg.h * p.G + gq) * Cfg::D + d;
-            const float v = L > 0.f ? __uint_as_float(o[e]) / L : 0.f;  // a row that sees nothing gives 0
+            // a row that sees nothing gives 0 (tree: and a NaN stays one)
+            const float v = (Cfg::TREE ? L != 0.f : L > 0.f) ? __uint_as_float(o[e]) / L : 0.f;
             if constexpr (Cfg::OUT_BF)
               store_scalar(BF16{}, p.out, idx, v);
             else
@@ -885,7 +886,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < NRH; ++e) {
           const float L = __shfl_sync(kFull, lt, e);
-          po[(size_t)(row0 + e) * Cfg::D + d] = L > 0.f ? __uint_as_float(o[e]) / L : 0.f;
+          po[(size_t)(row0 + e) * Cfg::D + d] = (Cfg::TREE ? L != 0.f : L > 0.f) ? __uint_as_float(o[e]) / L : 0.f;
+          if (Cfg::TREE && lane == e && L != L) mine = INFINITY;  // the merge gives NaN
           if (lane == e && L > 0.f) mine = (m_run[e] == -INFINITY ? 0.f : m_run[e]) + log2f(L);
         }
         if (qd == 0 && lane < NRH) p.part_lse[part * kMqRows + row0 + lane] = mine;

@@ -20,9 +20,8 @@
 // Warp roles, rings and bounded waits as in prefill_tiles.cu; Q of the next
 // item is copied into the one Q buffer while the current item's last tile is in
 // the softmax (its last S has been read by then).
-#include "mq_walk.cuh"
 #include "prefill_common.cuh"
-#include "tree_tiles.h"
+#include "tree_tiles.cuh"
 
 namespace pkv {
 
@@ -33,98 +32,6 @@ struct TreeCfg : PrefillCfg<T, D_> {
   static constexpr size_t SMEM = Base::SMEM + STAGE_BYTES;
   static_assert(SMEM + 6144 <= 232448, "shared memory");
 };
-
-// A cut of the schedule that falls within this many tiles of an item's end is
-// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
-// and the item needs no partials and no merge.
-constexpr int kSnapTiles = 4;
-
-// What group g's range is, for the merge kernel: its first tile, and the item
-// that tile cuts ([a, e) its tiles), e = 0 if the range starts at an item's end.
-struct TreeCut {
-  int t0, b, h, a, e;
-};
-
-// The schedule of one CTA: range [t0, t1) of the tiles, starting in sequence b0
-// whose first tile is base0.
-struct TreeRange {
-  int t0, t1, b0, base0;
-};
-// Block-wide; `find` is shared memory for the scan: the sequences holding the
-// range's ends.
-struct TreeFind {
-  int32_t wsum[8], b[2], base[2];
-};
-template <int THREADS>
-__device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int groups, TreeFind *find, int *cta_flags) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = p.B, per = (B + THREADS - 1) / THREADS;
-  int tk[kMqMaxBatch / THREADS];
-  int own = 0, incl = 0;
-  if (tid < THREADS) {
-    int bad = 0;
-#pragma unroll
-    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
-      const int b = tid * per + k;
-      tk[k] = 0;
-      if (k < per && b < B) {
-        const MqSeq s = mq_seq(p, b);
-        tk[k] = s.T * p.Hkv;
-        bad |= s.bad_ctx ? 1 : 0;
-      }
-      own += tk[k];
-    }
-    incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) find->wsum[warp] = incl;
-    if (blockIdx.x == 0 && __any_sync(kFull, bad) && lane == 0) atomicOr(cta_flags, PKV_FLAG_BAD_LEN);
-  }
-  __syncthreads();
-  int W = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = W;
-    W += find->wsum[w];
-  }
-  const int active = mq_active(W, groups);
-  TreeRange r;
-  r.t0 = mq_cut(W, active, group);
-  r.t1 = mq_cut(W, active, group + 1);
-  if (tid < THREADS) {
-    int run = before + incl - own;
-#pragma unroll
-    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
-      const int b = tid * per + k;
-      if (run <= r.t0 && r.t0 < run + tk[k]) {
-        find->b[0] = b;
-        find->base[0] = run;
-      }
-      if (run <= r.t1 && r.t1 < run + tk[k]) {
-        find->b[1] = b;
-        find->base[1] = run;
-      }
-      run += tk[k];
-    }
-  }
-  __syncthreads();
-  auto snap = [&](int t, int b, int base) -> int {
-    const int T = mq_seq(p, b).T, d = (t - base) % T;
-    return d <= kSnapTiles ? t - d : (T - d <= kSnapTiles ? t + T - d : t);
-  };
-  r.b0 = B;
-  r.base0 = W;
-  if (r.t0 < W) {  // (else an empty range)
-    r.b0 = find->b[0];
-    r.base0 = find->base[0];
-    r.t0 = snap(r.t0, r.b0, r.base0);
-  }
-  if (r.t1 < W) r.t1 = snap(r.t1, find->b[1], find->base[1]);
-  return r;
-}
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -416,14 +323,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int q = 0; q < SC / 32; ++q)
           tc::ld32(scol + (uint32_t)(q * 32), *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
         if (kvh + SC > start || kvh < lo_all) {  // (warp-uniform) the tree or a window's edge is in these columns
-          const int c0 = start - kvh;            // the tree's first column
-          uint64_t sees = c0 >= SC ? ~0ull : (c0 > 0 ? ~(~0ull << c0) | mask << c0 : (c0 > -64 ? mask >> -c0 : 0ull));
-          const int cl = lo - kvh;               // the first cached column this row sees
-          if (cl > 0) {
-            const uint64_t past = ~0ull << min(cl, 63), hidden = cl > 63 ? ~0ull : ~past;
-            // (the tree's nodes are the mask's alone)
-            sees &= ~(c0 >= SC ? hidden : (c0 > 0 ? hidden & ~(~0ull << c0) : 0ull));
-          }
+          const uint64_t sees = tree_columns(mask, start, lo, kvh);
           const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
 #pragma unroll
           for (int e = 0; e < SC; ++e)
@@ -487,7 +387,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (!ok) break;
       tc::fence_after();
       const float lt = l + red_l[half ^ 1][row];
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees nothing gives 0
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing gives 0 (and a NaN stays one)
       uint32_t o[OC / 32][32];
 #pragma unroll
       for (int q = 0; q < OC / 32; ++q)
@@ -511,7 +411,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           for (int v = 0; v < 8; ++v)
             po[(size_t)(q * 8 + v) * Cfg::M] = make_float4(__uint_as_float(o[q][4 * v]) * inv, __uint_as_float(o[q][4 * v + 1]) * inv,
                                         __uint_as_float(o[q][4 * v + 2]) * inv, __uint_as_float(o[q][4 * v + 3]) * inv);
-        if (half == 0) p.part_lse[part + row] = lt > 0.f ? m_run + log2f(lt) : -INFINITY;
+        if (half == 0) p.part_lse[part + row] = partial_lse(m_run, lt);
       }
       g += n;
       ++si;
@@ -645,6 +545,19 @@ __global__ void __launch_bounds__(2 * kTreeTileRows)
   *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + idx) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+cudaError_t launch_tree_merge(const TreeTileParams &p, int grid, int out_bf16, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t mc = {};
+  mc.gridDim = dim3((unsigned)(p.groups > 1 ? (p.groups - 1) * p.RT : 1), (unsigned)(p.D / 16));
+  mc.blockDim = dim3(2 * kTreeTileRows);
+  mc.stream = stream;
+  mc.attrs = attr;
+  mc.numAttrs = 1;
+  return cudaLaunchKernelEx(&mc, tree_merge_kernel, p, grid, out_bf16);
+}
+
 void tree_tiles_grid(int R, int sms, int *RT, int *groups) {
   *RT = (R + kTreeTileRows - 1) / kTreeTileRows;
   *groups = *RT >= sms ? 1 : sms / *RT;
@@ -694,16 +607,10 @@ static cudaError_t launch_tiles_cfg(const TreeTileParams &p, const CUtensorMap &
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<Cfg>, p, tmK, tmV);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t mc = {};
-  mc.gridDim = dim3((unsigned)(p.groups > 1 ? (p.groups - 1) * p.RT : 1), (unsigned)(p.D / 16));
-  mc.blockDim = dim3(2 * kTreeTileRows);
-  mc.stream = stream;
-  mc.attrs = attr;
-  mc.numAttrs = 1;
-  return cudaLaunchKernelEx(&mc, tree_merge_kernel, p, grid, Cfg::BF ? 1 : 0);
+  return launch_tree_merge(p, grid, Cfg::BF ? 1 : 0, stream);
 }
 
-cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
+cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, int q_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
                               cudaStream_t stream) {
   if (p.m.B < 1 || p.m.B > kMqMaxBatch || p.RT < 1 || p.groups < 1) return cudaErrorNotSupported;
   if (cache_dtype == PKV_BF16) {
@@ -712,6 +619,8 @@ cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, const CU
   } else if (cache_dtype == PKV_F16) {
     if (p.D == 128) return launch_tiles_cfg<TreeCfg<F16, 128>>(p, tmK, tmV, stream);
     if (p.D == 64) return launch_tiles_cfg<TreeCfg<F16, 64>>(p, tmK, tmV, stream);
+  } else if (cache_dtype == PKV_FP8_E4M3) {
+    return launch_tree_tiles_fp8(p, q_dtype, tmK, tmV, stream);
   }
   return cudaErrorNotSupported;
 }

@@ -1,0 +1,124 @@
+// tree_tiles.cuh — the schedule and the masks shared by the row-tile kernels for
+// a tree of drafted tokens (tree_tiles.cu: 16-bit caches, tree_tiles_fp8.cu).
+#pragma once
+
+#include "mq_walk.cuh"
+#include "tree_tiles.h"
+
+namespace pkv {
+
+// A cut of the schedule that falls within this many tiles of an item's end is
+// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
+// and the item needs no partials and no merge.
+constexpr int kSnapTiles = 4;
+
+// What group g's range is, for the merge kernel: its first tile, and the item
+// that tile cuts ([a, e) its tiles), e = 0 if the range starts at an item's end.
+struct TreeCut {
+  int t0, b, h, a, e;
+};
+
+// The schedule of one CTA: range [t0, t1) of the tiles, starting in sequence b0
+// whose first tile is base0.
+struct TreeRange {
+  int t0, t1, b0, base0;
+};
+// Block-wide; `find` is shared memory for the scan: the sequences holding the
+// range's ends.
+struct TreeFind {
+  int32_t wsum[8], b[2], base[2];
+};
+template <int THREADS>
+__device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int groups, TreeFind *find, int *cta_flags) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = p.B, per = (B + THREADS - 1) / THREADS;
+  int tk[kMqMaxBatch / THREADS];
+  int own = 0, incl = 0;
+  if (tid < THREADS) {
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
+      const int b = tid * per + k;
+      tk[k] = 0;
+      if (k < per && b < B) {
+        const MqSeq s = mq_seq(p, b);
+        tk[k] = s.T * p.Hkv;
+        bad |= s.bad_ctx ? 1 : 0;
+      }
+      own += tk[k];
+    }
+    incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) find->wsum[warp] = incl;
+    if (blockIdx.x == 0 && __any_sync(kFull, bad) && lane == 0) atomicOr(cta_flags, PKV_FLAG_BAD_LEN);
+  }
+  __syncthreads();
+  int W = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before = W;
+    W += find->wsum[w];
+  }
+  const int active = mq_active(W, groups);
+  TreeRange r;
+  r.t0 = mq_cut(W, active, group);
+  r.t1 = mq_cut(W, active, group + 1);
+  if (tid < THREADS) {
+    int run = before + incl - own;
+#pragma unroll
+    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
+      const int b = tid * per + k;
+      if (run <= r.t0 && r.t0 < run + tk[k]) {
+        find->b[0] = b;
+        find->base[0] = run;
+      }
+      if (run <= r.t1 && r.t1 < run + tk[k]) {
+        find->b[1] = b;
+        find->base[1] = run;
+      }
+      run += tk[k];
+    }
+  }
+  __syncthreads();
+  auto snap = [&](int t, int b, int base) -> int {
+    const int T = mq_seq(p, b).T, d = (t - base) % T;
+    return d <= kSnapTiles ? t - d : (T - d <= kSnapTiles ? t + T - d : t);
+  };
+  r.b0 = B;
+  r.base0 = W;
+  if (r.t0 < W) {  // (else an empty range)
+    r.b0 = find->b[0];
+    r.base0 = find->base[0];
+    r.t0 = snap(r.t0, r.b0, r.base0);
+  }
+  if (r.t1 < W) r.t1 = snap(r.t1, find->b[1], find->base[1]);
+  return r;
+}
+
+// Which of the 64 cache positions from `pos` on a row sees, as bits: the cached
+// ones in [lo, start), then node t at start + t iff bit t of mask.
+__device__ __forceinline__ uint64_t tree_columns(uint64_t mask, int start, int lo, int pos) {
+  const int c0 = start - pos;  // the tree's first column
+  uint64_t sees = c0 >= 64 ? ~0ull : (c0 > 0 ? ~(~0ull << c0) | mask << c0 : (c0 > -64 ? mask >> -c0 : 0ull));
+  const int cl = lo - pos;     // the first cached column this row sees
+  if (cl > 0) {
+    const uint64_t hidden = cl >= 64 ? ~0ull : ~(~0ull << cl);
+    sees &= ~(c0 >= 64 ? hidden : (c0 > 0 ? hidden & ~(~0ull << c0) : 0ull));  // (the nodes are the mask's alone)
+  }
+  return sees;
+}
+
+// Log-sum-exp (log2) of a partial with running max m and sum l: -inf where the row
+// sees nothing, +inf for a sum that is NaN, so that the merge gives NaN.
+__device__ __forceinline__ float partial_lse(float m, float l) {
+  return l > 0.f ? m + log2f(l) : (l == 0.f ? -INFINITY : INFINITY);
+}
+
+// The schedule's launch (tree_tiles.cu): joins the items cut between groups.
+cudaError_t launch_tree_merge(const TreeTileParams &p, int grid, int out_bf16, cudaStream_t stream);
+
+}  // namespace pkv

@@ -1,5 +1,6 @@
-// tree_tiles.h — host side of the row-tile tensor-core kernel for a tree of
-// drafted tokens (tree_tiles.cu): 16-bit caches, any number of query rows.
+// tree_tiles.h — host side of the row-tile tensor-core kernels for a tree of
+// drafted tokens (tree_tiles.cu, tree_tiles_fp8.cu): 16-bit and fp8 caches, any
+// number of query rows.
 #pragma once
 
 #include "mq_decode.h"
@@ -21,7 +22,9 @@ struct TreeTileParams {
 void tree_tiles_grid(int R, int sms, int *RT, int *groups);
 // Workspace: the WsHeader at offset 0, then the fields (as MqWsLayout).
 MqWsLayout tree_tiles_ws_layout(int D, int RT, int groups);
-cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
-                              cudaStream_t stream);
+cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, int q_dtype, const CUtensorMap &tmK,
+                              const CUtensorMap &tmV, cudaStream_t stream);
+cudaError_t launch_tree_tiles_fp8(const TreeTileParams &p, int q_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                  cudaStream_t stream);
 
 }  // namespace pkv

@@ -200,7 +200,8 @@ def test_same_inputs_same_bits():
 @pytest.mark.parametrize("route", ["transposed", "tiles", "units"])
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 3), ("bf16", 8, 2, 128, 16), ("f16", 6, 2, 128, 13),
                                               ("bf16", 2, 2, 64, 2), ("f16", 5, 1, 64, 33), ("bf16", 16, 1, 128, 64),
-                                              ("bf16", 12, 4, 128, 1)])
+                                              ("bf16", 12, 4, 128, 1), ("fp8_e4m3", 8, 2, 128, 9), ("fp8_e4m3", 6, 2, 64, 5),
+                                              ("fp8_e4m3", 16, 1, 128, 64), ("fp8_e4m3", 3, 1, 64, 1)])
 def test_every_kernel_on_the_same_inputs(route, dtype, Hq, Hkv, D, n):
     """Each kernel where it applies (pkv_set_route), one tree size each side of
     its row tiles; windows, ragged trees, an empty context."""
@@ -211,3 +212,101 @@ def test_every_kernel_on_the_same_inputs(route, dtype, Hq, Hkv, D, n):
         _run(Inputs(41, ctx[1:], n, Hq, Hkv, D, dtype), window=130)
         _run(Inputs(42, [5000], n, Hq, Hkv, D, dtype, stale=False))
         _run(Inputs(43, [n + 3] * 170, n, Hq, Hkv, D, dtype))
+
+
+def _rescaled(x, k, v):
+    """The same stored bytes under other block scales."""
+    x.ks, x.vs = (x.ks * k).contiguous(), (x.vs * v).contiguous()
+    return x
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("D,q_dtype", [(128, "bf16"), (64, "f16")])
+def test_fp8_scales_of_all_sizes(route, D, q_dtype):
+    """Block scales that differ by orders of magnitude between blocks and from
+    1 (tiles: also values far below f16's normal range)."""
+    with routes(tree=route):
+        for seed, spread, level in ((1, 0.0, 1.0), (2, 3.0, 1.0), (3, 1.0, 2.0 ** 6)) + (((4, 2.0, 2.0 ** -12),) if route == "tiles" else ()):
+            x = Inputs(50 + seed, [9, 130, 400, 1000], 9, 8, 2, D, "fp8_e4m3", q_dtype)
+            g = torch.Generator().manual_seed(seed)
+            f = lambda: torch.exp2(spread * torch.randn(x.vs.shape, generator=g))  # noqa: E731
+            _run(_rescaled(x, torch.exp2(0.3 * spread * torch.randn(x.ks.shape, generator=g)), level * f()))
+
+
+def test_fp8_zero_and_negative_scales():
+    """A block may hold nothing (scale 0) or be stored with negative scales:
+    the literal products."""
+    for D in (128, 64):
+        x = Inputs(61, [140, 400, 33], 12, 8, 2, D, "fp8_e4m3")
+        x.ks[x.table[0, 1]] = 0.0
+        x.vs[x.table[0, 2]] = 0.0
+        x.vs[x.table[1, 5]] *= -1.0
+        x.ks[x.table[1, 6]] *= -1.0
+        x.vs[x.table[2, 0], 1] = 0.0
+        _run(x)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("route", ["tiles", "units"])
+def test_fp8_every_byte_value(route, D):
+    """Blocks whose values run over all the numbers of the type, subnormal ones
+    among them, one range of magnitudes per sequence; a NaN byte that a row
+    sees is a NaN in its output, and in no other row's."""
+    with routes(tree=route):
+        x = Inputs(70, [16 * 3 + 12, 200, 77], 12, 2, 1, D, "fp8_e4m3", stale=False)
+        g = torch.Generator().manual_seed(1)
+        for b, (lo, hi) in enumerate(((0, 8), (0, 127), (100, 127))):
+            for c in (x.kc, x.vc):
+                raw = c.view(torch.uint8)
+                for blk in x.table[b][x.table[b] >= 0].tolist():
+                    raw[blk] = (torch.randint(lo, hi, raw[blk].shape, generator=g) | (torch.randint(0, 2, raw[blk].shape, generator=g) << 7)).to(torch.uint8)
+        x.ks = torch.full_like(x.ks, 1.0 / 64)
+        _run(x)
+        # sequence 1's node 5: its V row holds a NaN at element 3
+        t = x.ctx[1] - 12 + 5
+        x.masks[1] = [m & ~(1 << 5) | ((1 << 5) if i in (5, 7) else 0) for i, m in enumerate(x.masks[1])]
+        x.mask = torch.stack([to_i64(m) for m in x.masks])
+        x.kc.view(torch.uint8)[x.table[1, t // 16], 0, t % 16, 3] = 0x7F
+        out, _ = _call(x)
+        bad = torch.isnan(out[1].float()).any(-1).any(-1).cpu()
+        assert bad.tolist() == [i in (5, 7) for i in range(12)]
+        assert torch.isfinite(out[0].float()).all() and torch.isfinite(out[2].float()).all()
+
+
+@pytest.mark.parametrize("dtype,Hq,D,n", [("bf16", 2, 128, 3), ("bf16", 8, 128, 20), ("f16", 8, 64, 20), ("fp8_e4m3", 2, 128, 3),
+                                          ("fp8_e4m3", 8, 128, 20), ("f32", 2, 64, 3)])
+def test_a_nan_that_is_seen_is_not_lost(dtype, Hq, D, n):
+    """One query row of NaN over a context that is split between CTAs: NaN in
+    its output and in no other; the same for a K row that every node sees."""
+    x = Inputs(80, [9000, 300], n, Hq, 1, D, dtype, stale=False)
+    q = x.q.clone()
+    x.q[0, 1, Hq - 1, 5] = float("nan")
+    x.q[1, 0, 0, 0] = float("inf")
+    out, _ = _call(x)
+    bad = torch.isnan(out.float()).all(-1).cpu()
+    assert bad[0, 1, Hq - 1] and bad[1, 0, 0] and int(bad.sum()) == 2
+    assert int(torch.isnan(out.float()).any(-1).sum()) == 2
+    x.q = q
+    blk = x.table[0, 100]
+    if dtype == "fp8_e4m3":
+        x.kc.view(torch.uint8)[blk, 0, 7, 0] = 0xFF
+    else:
+        x.kc[blk, 0, 7, 0] = float("nan")
+    out, _ = _call(x)
+    assert torch.isnan(out[0].float()).all() and torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("D,q_dtype", [(128, "bf16"), (64, "bf16"), (128, "f16"), (64, "f16")])
+def test_fp8_queries_of_all_sizes(D, q_dtype):
+    """The tile kernel splits a query row into E4M3 parts under a scale of the
+    row: rows whose elements differ by orders of magnitude, tiny and huge rows."""
+    with routes(tree="tiles"):
+        x = Inputs(90, [40, 300], 20, 8, 1, D, "fp8_e4m3", q_dtype)
+        g = torch.Generator().manual_seed(3)
+        mag = torch.exp2(3.0 * torch.randn(x.q.shape, generator=g))
+        x.q = (x.q.float() * mag).to(x.q.dtype)
+        x.q[0, 3] *= 2.0 ** -10
+        x.q[0, 4] *= 2.0 ** 5
+        x.q[1, 2] = 0
+        x.scale /= 40
+        _run(x)
