@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const int n = sg.j1 - sg.j0;
       // what this row sees: [lo, start), then node t at start + t iff bit t of mask
       const bool live = node < sg.n;
+      const bool dead = rt * Cfg::M + (warp & 3) * 32 >= sg.n * p.G;  // no live row in this warp (nor in the one that shares its rows)
       const int start = sg.ctx - sg.n;
       uint64_t mask = 0;
       int lo = INT32_MAX;
@@ -316,19 +317,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         tc::fence_after();
         // the item's last S has read Q: the next item's may come in
         if (j + 1 == n && nhave) stage_q(nx);
+        if (dead) {  // (rows past the nodes: their P and O are never looked at)
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[sb]);
+          continue;
+        }
         const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);
-        uint32_t s[SC];
         const int kvh = (sg.j_first + sg.j0 + j) * Cfg::N + half * SC;  // first position of this half
+        if (kvh + SC > start || kvh < lo_all)  // (warp-uniform) the tree or a window's edge is in these columns
+          fix_scores(scol, tree_columns(mask, start, lo, kvh), nullptr, 0);
+        uint32_t s[SC];
 #pragma unroll
         for (int q = 0; q < SC / 32; ++q)
           tc::ld32(scol + (uint32_t)(q * 32), *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
-        if (kvh + SC > start || kvh < lo_all) {  // (warp-uniform) the tree or a window's edge is in these columns
-          const uint64_t sees = tree_columns(mask, start, lo, kvh);
-          const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
-#pragma unroll
-          for (int e = 0; e < SC; ++e)
-            if (!(((e < 32 ? s0 : s1) >> (e & 31)) & 1)) s[e] = 0xff800000u;  // -inf
-        }
         float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < SC; e += 2) mx = fmax3(mx, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           ok = warp_wait(&pv_done[(gj - 1) % Cfg::SBUF], (uint32_t)((gj - 1) / Cfg::SBUF) & 1u, p.timeout_ns);
           if (!ok) break;
           tc::fence_after();
-          scale_o<Cfg>(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), alpha);
+          rescale_o(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), alpha, OC);
         }
         l = l * alpha + (sp.x + sp.y);
         // P (bf16: high parts and residuals; f16: f16 pairs) over this thread's own (already read) S columns

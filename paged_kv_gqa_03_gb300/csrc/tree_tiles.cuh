@@ -112,6 +112,56 @@ __device__ __forceinline__ uint64_t tree_columns(uint64_t mask, int start, int l
   return sees;
 }
 
+// What a softmax warp does to its 64 columns of a tile's S, P or its half of O only
+// now and then, each in a function of its own on tensor memory: the tile loop
+// itself stays a short run of instructions (inline, these rare parts cost every tile
+// instruction-cache misses).  All are warp-wide.
+//
+// Hides the columns of S whose bit of `sees` is 0; `k`, where given, holds the block
+// scales {k_b, v_b} of literal products: S of such blocks is multiplied by k_b.
+static __device__ __noinline__ void fix_scores(uint32_t scol, uint64_t sees, const float2 *raw, uint32_t literal) {
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {  // 8 columns
+    uint32_t s[8];
+    tc::ld8(scol + (uint32_t)(q * 8), s);
+    const float k = (literal >> (q >> 1)) & 1 ? raw[q >> 1].x : 1.f;
+    const uint32_t bits = (uint32_t)(sees >> (q * 8));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      s[e] = (bits >> e) & 1 ? __float_as_uint(__uint_as_float(s[e]) * k) : 0xff800000u;  // hidden: -inf
+    tc::st8(scol + (uint32_t)(q * 8), s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7]);
+  }
+  tc::wait_st();
+}
+// Multiplies the packed f16 weights (32 columns at pcol) of literal blocks by v_b.
+static __device__ __noinline__ void fix_weights(uint32_t pcol, const float2 *raw, uint32_t literal) {
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    if (!((literal >> b) & 1)) continue;
+    uint32_t w[8];
+    tc::ld8(pcol + (uint32_t)(b * 8), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 x = unpack2(F16{}, w[e]);
+      w[e] = pack_f16x2(x.x * raw[b].y, x.y * raw[b].y);
+    }
+    tc::st8(pcol + (uint32_t)(b * 8), w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+  }
+  tc::wait_st();
+}
+// Multiplies `cols` columns of O at ta by alpha.
+static __device__ __noinline__ void rescale_o(uint32_t ta, float alpha, int cols) {
+#pragma unroll 1
+  for (int q = 0; q < cols; q += 8) {
+    uint32_t o[8];
+    tc::ld8(ta + (uint32_t)q, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tc::st8(ta + (uint32_t)q, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+  }
+  tc::wait_st();
+}
+
 // Log-sum-exp (log2) of a partial with running max m and sum l: -inf where the row
 // sees nothing, +inf for a sum that is NaN, so that the merge gives NaN.
 __device__ __forceinline__ float partial_lse(float m, float l) {

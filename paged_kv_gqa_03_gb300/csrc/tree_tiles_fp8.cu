@@ -48,6 +48,7 @@ struct TreeFp8Cfg : PrefillCfg<F16, D_> {
   static constexpr int ISSUER = Base::SOFTMAX / 32 + 1, PV_ISSUER = Base::SOFTMAX / 32 + 2,
                        V_PRODUCER = Base::SOFTMAX / 32 + 3, WIDEN = Base::SOFTMAX / 32 + 4;
   static constexpr int WIDENERS = 128;
+  static constexpr int SCALES = 8;  // tiles whose block scales are kept: more than can be between K's copy and the softmax
   static constexpr int THREADS = Base::SOFTMAX + 256;
   // registers per thread: 128 at launch; the softmax warpgroups take what the others leave
   static constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
@@ -126,6 +127,57 @@ __device__ __forceinline__ void widen_tile(const uint8_t *raw, uint8_t *op, int 
   }
 }
 
+// One row of Q (D 16-bit elements at src; null: zeros), chunks ch0 .. ch1 - 1 of 16
+// elements, as E4M3 parts into row `row` of the Q tile at q0.  Returns 2^-k, the
+// row's scaling undone; NaN for a row that is not finite.
+template <class Cfg>
+__device__ __noinline__ float stage_q_parts(const uint4 *src, uint32_t q0, int row, int ch0, int ch1) {
+  // the row's largest magnitude, as bits (a 16-bit float's order is its bits')
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int k = 0; k < Cfg::D / 8; ++k) {
+    const uint4 v = src ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+    top = __vmaxu2(__vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)),
+                   top);
+  }
+  const uint32_t big = max(top & 0xffffu, top >> 16);
+  const bool finite = big < (Cfg::OUT_BF ? 0x7f80u : 0x7c00u);
+  const float m = Cfg::OUT_BF ? __uint_as_float(big << 16) : __half2float(__ushort_as_half((unsigned short)big));
+  int e = 0;
+  const float f = frexpf(finite ? m : 0.f, &e);  // m = f 2^e; 448 = 0.875 * 2^9
+  const int sh = m > 0.f && finite ? min((f <= 0.875f ? 9 : 8) - e, 120) : 0;
+  const float up = ldexpf(1.f, sh);
+#pragma unroll 1
+  for (int ch = ch0; ch < ch1; ++ch) {
+    const uint4 v0 = src ? __ldg(src + 2 * ch) : make_uint4(0, 0, 0, 0);
+    const uint4 v1 = src ? __ldg(src + 2 * ch + 1) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t part[Cfg::QPARTS][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2 x = Cfg::OUT_BF ? unpack2(BF16{}, w[i]) : unpack2(F16{}, w[i]);
+      x.x *= up;
+      x.y *= up;
+#pragma unroll
+      for (int q = 0; q < Cfg::QPARTS; ++q) {
+        const uint32_t r = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+        const float2 y = unpack2_e4m3((uint16_t)r);
+        x.x -= y.x;
+        x.y -= y.y;
+        if (i & 1)
+          part[q][i >> 1] |= r << 16;
+        else
+          part[q][i >> 1] = r;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < Cfg::QPARTS; ++q)
+      sts128(q0 + q * Cfg::Q_PART + kmajor_off<Cfg::D>(row, ch), make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
+  }
+  fence_proxy_async();
+  return finite ? ldexpf(1.f, -sh) : __int_as_float(0x7fc00000);
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tree_tile_fp8_kernel(const __grid_constant__ TreeTileParams tp, const __grid_constant__ CUtensorMap tmK,
@@ -145,6 +197,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
   __shared__ float red[2][2][Cfg::M];
   __shared__ float red_l[2][Cfg::M];
+  // per tile, by block: {k_b, log2 v_b, 1 / v_b, 0}, or {1, 0, 1, 1} and {k_b, v_b}
+  // in `literal` for scales that are not positive finite numbers
+  __shared__ __align__(16) float4 scales[Cfg::SCALES][Cfg::BLOCKS];
+  __shared__ float2 literal[Cfg::SCALES][Cfg::BLOCKS];
   __shared__ TreeFind find;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_flags, k_issued, r_issued;
@@ -169,7 +225,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
 #pragma unroll
     for (int s = 0; s < Cfg::SBUF; ++s) {
-      mbar_init(&s_full[s], 1);
+      mbar_init(&s_full[s], 2);  // the MMAs' completion, and the issuer's own arrival (orders the block scales)
       mbar_init(&p_full[s], Cfg::SOFTMAX / 32);
       mbar_init(&pv_done[s], 1);
     }
@@ -234,6 +290,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     int bad = 0;
     struct Pend {
       int id, h;
+      float ks, vs;
       bool none;
     };
     auto fetch = [&]() -> Pend {
@@ -243,7 +300,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       f.h = cs.h;
       f.none = lb >= nblk || (lb + 1) * kBlock <= cs.first;
       f.id = f.none ? 0 : __ldg(p.block_table + (size_t)cs.b * p.max_blocks + lb);
+      f.ks = f.vs = 1.f;  // (a block that does not exist: its columns are masked)
       return f;
+    };
+    auto load_scales = [&](Pend &f) {  // once the id is here, a tile ahead of their use
+      if (warp == Cfg::PRODUCER && !f.none && f.id >= 0 && (int64_t)f.id < p.num_blocks) {
+        f.ks = __ldg(p.k_scale + (size_t)f.id * p.Hkv + f.h);
+        f.vs = __ldg(p.v_scale + (size_t)f.id * p.Hkv + f.h);
+      }
     };
     auto row_of = [&](const Pend &f) -> int64_t {  // the box past the tensor (zeros) for none or a bad id
       if (f.none) return p.num_blocks * p.Hkv;
@@ -252,7 +316,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       return good ? (int64_t)f.id * p.Hkv + f.h : p.num_blocks * p.Hkv;
     };
     bool ok = true;
-    const Pend nil{0, 0, true};
+    const Pend nil{0, 0, 1.f, 1.f, true};
     bool h0 = step();
     Pend f0 = h0 ? fetch() : nil;
     bool h1 = h0 && step();
@@ -265,9 +329,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int stages = vw ? Cfg::VRAW : Cfg::KSTAGES, lines = vw ? Cfg::V_LINES : Cfg::K_LINES;
     const CUtensorMap *tm = vw ? &tmV : &tmK;
     int *issued = vw ? &r_issued : &k_issued;
+    load_scales(f0);
     for (int g = 0; h0; ++g) {
       const bool h3 = h2 && step();
       const Pend f3 = h3 ? fetch() : nil;
+      load_scales(f1);
       const int y = (int)(row_of(f0) * lines);
       const int s = g % stages;
       if (g >= stages) ok = warp_wait(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
@@ -275,6 +341,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         ok = false;
         break;
       }
+      if (!vw && lane < Cfg::BLOCKS) {
+        const bool plain = f0.ks > 0.f && f0.vs > 0.f && f0.ks <= 3.402823466e38f && f0.vs <= 3.402823466e38f;
+        scales[g % Cfg::SCALES][lane] =
+            plain ? make_float4(f0.ks, __log2f(f0.vs), __fdividef(1.f, f0.vs), 0.f) : make_float4(1.f, 0.f, 1.f, 1.f);
+        literal[g % Cfg::SCALES][lane] = make_float2(f0.ks, f0.vs);
+      }
+      __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&full[s], Cfg::RAW_BYTES);
       __syncwarp();
       if (lane < Cfg::BLOCKS)
@@ -337,6 +410,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (lane == 0) {
           mma_s_tile_e4m3<Cfg>(tbase + (uint32_t)(sb * Cfg::N), smem_u32(sQ), smem_u32(sK + (size_t)ks * Cfg::RAW_BYTES));
           tc::commit(&s_full[sb]);
+          mbar_arrive(&s_full[sb]);
           tc::commit(&k_empty[ks]);
         }
         __syncwarp();
@@ -388,73 +462,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(
           static_cast<const uint16_t *>(p.q) +
           (((size_t)s.b * p.q_len + (live ? node : 0)) * p.Hq + s.h * p.G + gq) * Cfg::D);
-      // the row's largest magnitude, as bits (a 16-bit float's order is its bits'; both halves)
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int k = 0; k < Cfg::D / 8; ++k) {
-        const uint4 v = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-        top = __vmaxu2(__vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)), top);
-      }
-      const uint32_t big = max(top & 0xffffu, top >> 16);
-      const bool finite = big < (Cfg::OUT_BF ? 0x7f80u : 0x7c00u);
-      const float m = Cfg::OUT_BF ? __uint_as_float(big << 16) : __half2float(__ushort_as_half((unsigned short)big));
-      int e = 0;
-      const float f = frexpf(finite ? m : 0.f, &e);  // m = f 2^e; 448 = 0.875 * 2^9
-      const int sh = m > 0.f && finite ? min((f <= 0.875f ? 9 : 8) - e, 120) : 0;
-      const float up = ldexpf(1.f, sh);
-#pragma unroll 1
-      for (int k = 0; k < Cfg::D / 32; ++k) {  // 16 elements: one chunk of each part
-        const int ch = half * (Cfg::D / 32) + k;
-        const uint4 v0 = live ? __ldg(src + 2 * ch) : make_uint4(0, 0, 0, 0);
-        const uint4 v1 = live ? __ldg(src + 2 * ch + 1) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        uint32_t part[Cfg::QPARTS][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 x = Cfg::OUT_BF ? unpack2(BF16{}, w[i]) : unpack2(F16{}, w[i]);
-          x.x *= up;
-          x.y *= up;
-#pragma unroll
-          for (int q = 0; q < Cfg::QPARTS; ++q) {
-            const uint32_t r = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-            const float2 y = unpack2_e4m3((uint16_t)r);
-            x.x -= y.x;
-            x.y -= y.y;
-            if (i & 1)
-              part[q][i >> 1] |= r << 16;
-            else
-              part[q][i >> 1] = r;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < Cfg::QPARTS; ++q)
-          sts128(smem_u32(sQ + q * Cfg::Q_PART) + kmajor_off<Cfg::D>(row, ch),
-                 make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
-      }
-      fence_proxy_async();
-      return finite ? c * ldexpf(1.f, -sh) : __int_as_float(0x7fc00000);
+      return c * stage_q_parts<Cfg>(live ? src : nullptr, smem_u32(sQ), row, half * (Cfg::D / 32), (half + 1) * (Cfg::D / 32));
     };
     auto release_q = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
     };
-    // block scales of a tile's columns of this half: lane 2 b + kv (< 2 NB) holds
-    // block b's K (0) or V (1) scale; the block id is loaded two tiles and the
-    // scale one tile ahead (1 for a block that does not exist: its columns are masked)
-    auto block_id = [&](const MqSeg &s, int j) -> int {
-      const int lb = (s.j_first + j) * Cfg::BLOCKS + half * NB + ((lane >> 1) & (NB - 1));
-      if (j >= s.j1 || lb >= (s.ctx + kBlock - 1) / kBlock || (lb + 1) * kBlock <= s.first) return -1;
-      return __ldg(p.block_table + (size_t)s.b * p.max_blocks + lb);
-    };
-    auto scale_of = [&](const MqSeg &s, int id) -> float {
-      return id >= 0 && (int64_t)id < p.num_blocks ? __ldg((lane & 1 ? p.v_scale : p.k_scale) + (size_t)id * p.Hkv + s.h)
-                                                   : 1.f;
-    };
     MqWalk wk;
     wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg sg{}, nx{};
     bool have = next_item(wk, sg);
-    const int id0 = have ? block_id(sg, sg.j0) : -1;
     float cq = have ? stage_q(sg) : 0.f, cq_next = 0.f;
     if (rt == 0 && tid == 0) {  // (rt 0 has rows in every item with any)
       TreeCut cut{rg.t0, 0, 0, 0, 0};
@@ -462,17 +479,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       tp.cuts[group] = cut;
     }
     if (have) release_q();
-    float sc_n = have ? scale_of(sg, id0) : 1.f;
     bool nhave = have && next_item(wk, nx);
-    int id1 = -1;  // the block id of the tile after the current one
-    if (have && sg.j1 - sg.j0 > 1) id1 = block_id(sg, sg.j0 + 1);
     bool ok = true;
     int g = 0, si = 0;
     while (have && ok) {
       const int n = sg.j1 - sg.j0;
-      if (n == 1 && nhave) id1 = block_id(nx, nx.j0);  // (not known while the previous item's last tile ran)
       // what this row sees: [lo, start), then node t at start + t iff bit t of mask
       const bool live = node < sg.n;
+      const bool dead = rt * Cfg::M + (warp & 3) * 32 >= sg.n * p.G;  // no live row in this warp (nor in the one that shares its rows)
       const int start = sg.ctx - sg.n;
       uint64_t mask = 0;
       int lo = INT32_MAX;
@@ -484,45 +498,39 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       float m_run = -INFINITY, l = 0.f;  // l: sum of p' / v_b
       for (int j = 0; j < n; ++j) {
         const int gj = g + j, sb = gj % Cfg::SBUF, par = gj & 1;
-        const float sc = sc_n;
         const bool last = j + 1 == n;
-        sc_n = last ? (nhave ? scale_of(nx, id1) : 1.f) : scale_of(sg, id1);  // the next tile's
-        if (j + 2 < n)
-          id1 = block_id(sg, sg.j0 + j + 2);
-        else if (nhave)  // the next item's first, then its second (if it has one)
-          id1 = block_id(nx, nx.j0 + j + 2 - n);
         ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         // the item's last S has read Q: the next item's may come in
         if (last && nhave) cq_next = stage_q(nx);
+        if (dead) {  // (rows past the nodes: their P and O are never looked at)
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[sb]);
+          continue;
+        }
         const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);
-        uint32_t s[SC];
         const int kvh = (sg.j_first + sg.j0 + j) * Cfg::N + half * SC;  // first position of this half
+        // per block: the score's factor c k_b, log2 v_b and 1 / v_b
+        float ck[NB], lv[NB], rv[NB];
+        uint32_t lit = 0;  // blocks with literal products
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float4 v = scales[gj % Cfg::SCALES][half * NB + b];
+          ck[b] = cq * v.x;
+          lv[b] = v.y;
+          rv[b] = v.z;
+          lit |= v.w != 0.f ? 1u << b : 0u;
+        }
+        const float2 *raw = &literal[gj % Cfg::SCALES][half * NB];
+        // (warp-uniform) the tree or a window's edge is in these columns
+        const bool edge = kvh + SC > start || kvh < lo_all;
+        if (edge || lit) fix_scores(scol, edge ? tree_columns(mask, start, lo, kvh) : ~0ull, raw, lit);
+        uint32_t s[SC];
 #pragma unroll
         for (int q = 0; q < SC / 32; ++q)
           tc::ld32(scol + (uint32_t)(q * 32), *reinterpret_cast<uint32_t(*)[32]>(&s[q * 32]));
-        // per block: the score's factor c k_b, log2 v_b and 1 / v_b
-        const bool plain = __all_sync(kFull, sc > 0.f && sc <= 3.402823466e38f);
-        float ck[NB], lv[NB], rv[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float kb = __shfl_sync(kFull, sc, 2 * b), vb = __shfl_sync(kFull, sc, 2 * b + 1);
-          ck[b] = plain ? cq * kb : cq;
-          lv[b] = plain ? __log2f(vb) : 0.f;
-          rv[b] = plain ? __fdividef(1.f, vb) : 1.f;
-          if (!plain) {
-#pragma unroll
-            for (int e = 0; e < kBlock; ++e) s[b * kBlock + e] = __float_as_uint(__uint_as_float(s[b * kBlock + e]) * kb);
-          }
-        }
-        if (kvh + SC > start || kvh < lo_all) {  // (warp-uniform) the tree or a window's edge is in these columns
-          const uint64_t sees = tree_columns(mask, start, lo, kvh);
-          const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
-#pragma unroll
-          for (int e = 0; e < SC; ++e)
-            if (!(((e < 32 ? s0 : s1) >> (e & 31)) & 1)) s[e] = 0xff800000u;  // -inf
-        }
         float mx = -INFINITY;  // max of s c k_b + lv_b
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -562,26 +570,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const float2 sp = f2_unpack(sum2);
           sum = fmaf(sp.x + sp.y, rv[b], sum);
         }
-        if (!plain) {  // the V scales as products
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const float vb = __shfl_sync(kFull, sc, 2 * b + 1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 x = unpack2(F16{}, w[b * 8 + e]);
-              w[b * 8 + e] = pack_f16x2(x.x * vb, x.y * vb);
-            }
-          }
-        }
         if (rescale && j > 0) {  // O must hold P . V of the item's previous tile before it is scaled
           ok = warp_wait(&pv_done[(gj - 1) % Cfg::SBUF], (uint32_t)((gj - 1) / Cfg::SBUF) & 1u, p.timeout_ns);
           if (!ok) break;
           tc::fence_after();
-          scale_o<Cfg>(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), alpha);
+          rescale_o(tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), alpha, OC);
         }
         l = l * alpha + sum;
         tc::st32(scol, w);  // P over this thread's own (already read) S columns
         tc::wait_st();
+        if (lit) fix_weights(scol, raw, lit);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
