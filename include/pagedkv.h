@@ -549,9 +549,8 @@ int paged_kv_copy_blocks(void *k_cache, void *v_cache, int cache_dtype,
  *   which = PKV_ROUTE_PREFILL (the prefill kernel's schedule):
  *           PKV_ROUTE_AUTO, PKV_PREFILL_PERSISTENT, PKV_PREFILL_PER_ITEM
  *   which = PKV_ROUTE_TREE (paged_tree_attention):
- *           PKV_ROUTE_AUTO, PKV_TREE_TRANSPOSED (the transposed tensor-core
- *           kernel), PKV_TREE_TILES (the split 128-row tile kernel),
- *           PKV_TREE_UNITS (the decode kernel's units)
+ *           PKV_ROUTE_AUTO, PKV_TREE_TILES (the split 128-row tile kernel; not
+ *           for fp32 caches), PKV_TREE_UNITS (the decode kernel's units)
  * Returns PKV_EINVAL for an unknown `which` or `choice`; pkv_get_route
  * returns the current setting (or PKV_EINVAL).
  */
@@ -564,9 +563,8 @@ int paged_kv_copy_blocks(void *k_cache, void *v_cache, int cache_dtype,
 #define PKV_MQ_UNITS 3
 #define PKV_PREFILL_PERSISTENT 1
 #define PKV_PREFILL_PER_ITEM 2
-#define PKV_TREE_TRANSPOSED 1
-#define PKV_TREE_TILES 2
-#define PKV_TREE_UNITS 3
+#define PKV_TREE_TILES 1
+#define PKV_TREE_UNITS 2
 int pkv_set_route(int which, int choice);
 int pkv_get_route(int which);
 

@@ -121,7 +121,7 @@ def pkv_version():
 # Kernel-route decisions that pkv_set_route can force (include/pagedkv.h).
 ROUTES = {"multi_query": (0, ("auto", "transposed", "prefill", "units")),
           "prefill": (1, ("auto", "persistent", "tiles")),
-          "tree": (2, ("auto", "transposed", "tiles", "units"))}
+          "tree": (2, ("auto", "tiles", "units"))}
 
 
 def pkv_set_route(which, choice):

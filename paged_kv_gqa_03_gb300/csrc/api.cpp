@@ -655,7 +655,7 @@ static MqParams mq_params(const MqWsLayout &M, void *out, const void *q, const f
 static int run_mq(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache, int cache_dtype,
                   const float *k_scale, const float *v_scale, const int32_t *block_table, int max_blocks_per_seq,
                   const int32_t *context_lens, int B, int q_len, int window, int Hq, int Hkv, int64_t num_blocks,
-                  float scale, void *workspace, int sms, pkv_stream_t stream, const TreeArgs *tree) {
+                  float scale, void *workspace, int sms, pkv_stream_t stream) {
   const MqWsLayout M = mq_ws_layout(B, sms);
   CUtensorMap tmK, tmV;
   int rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, kMqHeadDim);
@@ -663,7 +663,7 @@ static int run_mq(void *out, const void *q, int q_dtype, const void *k_cache, co
   rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, kMqHeadDim);
   if (rc != PKV_OK) return rc;
   const MqParams mp = mq_params(M, out, q, k_scale, v_scale, block_table, max_blocks_per_seq, context_lens, B, q_len,
-                                window, Hq, Hkv, num_blocks, scale, workspace, tree);
+                                window, Hq, Hkv, num_blocks, scale, workspace, nullptr);
   return cuda_status(launch_mq_decode(mp, cache_dtype, q_dtype, tmK, tmV, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -729,7 +729,7 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
       if (workspace_bytes >= mq_ws_layout(B, sms).total)
         return run_mq(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table,
                       max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, sms,
-                      stream, nullptr);
+                      stream);
     }
     if (!units && (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && scale > 0.f && prefill_fills) {
       CUtensorMap tmK, tmV;
@@ -770,19 +770,34 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
 }
 
 // Kernels of paged_tree_attention (PKV_TREE_*): which one a shape takes, or the
-// forced one (pkv_set_route) where it applies.
-static bool tree_mq_applies(int cache_dtype, int B, int R, int D) {
-  return (cache_dtype == PKV_BF16 || cache_dtype == PKV_F16) && D == kMqHeadDim && R <= kMqRows && B <= kMqMaxBatch;
-}
+// forced one (pkv_set_route) where it applies.  The row tiles read an item's
+// cache once for 128 rows and split it anywhere; the units read it once per 8
+// rows or fewer.  Up to 8 rows per kv head (fp8: 16) both read it once (or
+// twice, from L2) and the choice is by what the table can hold.  Units / tiles, us:
+//   16-bit, D = 128: the tiles, but for many items (a range then holds the ends
+//     of several): 1 x 16384, 8 heads of 8 rows 58 / 26, 16 x 8192 99 / 98,
+//     64 x 500, 8 heads of 8 42 / 44, 16 x 1000, 32 heads of 8 61 / 65,
+//     64 x 500, 32 heads of 4 104 / 124;
+//   D = 64 and fp8 (half the bytes a tile, or V to widen for 128 rows): the
+//     tiles for small work: bf16 D = 64, 8 rows, 1 x 16384 46 / 20, 16 x 1000
+//     22 / 18, 64 x 500 28 / 33, 16 x 4096 40 / 53; fp8 D = 128, 8 heads of 4 /
+//     16 rows, 1 x 500 21, 26 / 16, 17, 16 x 1000 25, 36 / 23, 4 x 8192 39, 50 /
+//     38, 39, 8 x 8192 45, 58 / 57, 57, 64 x 500 32, 56 / 52, 16 x 8192 63, 81 /
+//     93, 94.
+// Above, the tiles everywhere: 16-bit D = 128, 16 x 8192, 16 rows 117 / 98; D =
+// 64, 16 x 4096, 16 rows 56 / 54; fp8 16 x 8192, 32 rows 132 / 95.
 static bool tree_tiles_apply(int cache_dtype, int B) {
   return cache_dtype != PKV_F32 && B <= kMqMaxBatch;
 }
-static int tree_route(int cache_dtype, int B, int R, int D) {
+static int tree_route(int cache_dtype, int B, int R, int Hkv, int D, int max_blocks) {
   const int force = g_route[PKV_ROUTE_TREE].load(std::memory_order_relaxed);
-  const bool mq = tree_mq_applies(cache_dtype, B, R, D), tiles = tree_tiles_apply(cache_dtype, B);
-  if (force == PKV_TREE_UNITS || (force == PKV_TREE_TRANSPOSED && mq) || (force == PKV_TREE_TILES && tiles)) return force;
-  if (mq && R <= 32) return PKV_TREE_TRANSPOSED;
-  return tiles && R > 8 ? PKV_TREE_TILES : PKV_TREE_UNITS;
+  const bool fp8 = cache_dtype == PKV_FP8_E4M3;
+  if (!tree_tiles_apply(cache_dtype, B) || force == PKV_TREE_UNITS) return PKV_TREE_UNITS;
+  if (force == PKV_TREE_TILES || R > (fp8 ? 16 : 8)) return PKV_TREE_TILES;
+  const int64_t items = (int64_t)B * Hkv;
+  if (!fp8 && D == 128) return items < 512 ? PKV_TREE_TILES : PKV_TREE_UNITS;
+  const int64_t rows = items * max_blocks * kBlock;  // K rows, at most
+  return rows <= (items <= 32 ? 1 << 18 : 1 << 17) ? PKV_TREE_TILES : PKV_TREE_UNITS;
 }
 
 int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cache_dtype, int q_dtype,
@@ -799,7 +814,6 @@ int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cac
   rc = device_sm_count(&sms);
   if (rc != PKV_OK) return rc;
   const int R = q_len * (Hq / Hkv);
-  if (tree_mq_applies(cache_dtype, B, R, D)) total = std::max(total, mq_ws_layout(B, sms).total);
   if (tree_tiles_apply(cache_dtype, B)) {
     int RT = 0, groups = 0;
     tree_tiles_grid(R, sms, &RT, &groups);
@@ -830,13 +844,7 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   int sms = 0;
   rc = device_sm_count(&sms);
   if (rc != PKV_OK) return rc;
-  const int route = tree_route(cache_dtype, B, R, D);
-  if (route == PKV_TREE_TRANSPOSED) {
-    if (workspace_bytes < mq_ws_layout(B, sms).total) return PKV_EWORKSPACE;
-    return run_mq(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_table, max_blocks_per_seq,
-                  context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, sms, stream, &tree);
-  }
-  if (route == PKV_TREE_TILES) {
+  if (tree_route(cache_dtype, B, R, Hkv, D, max_blocks_per_seq) == PKV_TREE_TILES) {
     CUtensorMap tmK, tmV;
     rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D, cache_dtype == PKV_FP8_E4M3 && D == 64);
     if (rc != PKV_OK) return rc;

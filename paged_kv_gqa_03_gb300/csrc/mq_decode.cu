@@ -48,12 +48,8 @@ namespace pkv {
 // An fp8 cache is widened to f16 in shared memory (exact: every E4M3 value
 // is an f16 value) and the MMAs run on f16 (Q converted when staged), so
 // BF (the MMA operand type) is false for it while OUT_BF follows the query.
-// TREE_: the new tokens form a tree (paged_tree_attention): positions before
-// the tree as above, then node j at position start + j for the rows whose
-// node's mask has bit j.  Tiles wholly before the tree take the unmasked path.
-template <class T, int NRH_, class QT = T, bool TREE_ = false>
+template <class T, int NRH_, class QT = T>
 struct MqCfg {
-  static constexpr bool TREE = TREE_;
   static constexpr int D = kMqHeadDim;
   static constexpr bool FP8 = T::kBytes == 1;
   static constexpr bool BF = !FP8 && T::kCode == PKV_BF16;
@@ -262,11 +258,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ float red[2][2][4][32];  // partial row maxima [tile parity][half][warp quarter][row]
   __shared__ float red_l[2][4][32];   // partial row sums [half][warp quarter][row]
   __shared__ MqPlan plan;
-  // (tree) which rows of a half see node t (bit e: row NRH * half + e), and the
-  // first cached position each row sees: of the segment in work, the next one
-  // (staged with its Q) and the one other warps may still be finishing
-  __shared__ uint32_t t_rows[Cfg::TREE ? 3 : 1][2][Cfg::TREE ? 64 : 1];
-  __shared__ int t_lo[Cfg::TREE ? 3 : 1][Cfg::TREE ? NR : 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_flags, k_consumed, v_consumed, k_issued, v_issued;
 
@@ -555,30 +546,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const float c = p.scale_log2;
     // Q of segment s into buffer qb: NR rows x 16 chunks of 16 bytes, row r =
     // (new token r / G, query head r % G of kv head s.h), zeros past R
-    auto stage_q = [&](const MqSeg &s, int qb, bool async, int seg) {
-      const int R = Cfg::TREE ? s.n * p.G : p.R;
-      if constexpr (Cfg::TREE) {
-        if (qd == 0) {  // one warp per half: lane e transposes row row0 + e's mask
-          uint64_t m = 0;
-          int lo = INT32_MAX;
-          const int r = row0 + lane;
-          if (lane < NRH && r < R) {
-            const int start = s.ctx - s.n;
-            m = __ldg(p.tree_mask + (size_t)s.b * p.mask_stride + r / p.G) & (~0ull >> (64 - s.n));
-            lo = p.window > 0 ? start + max(1, __popcll(m)) - p.window : 0;
-          }
-          if (lane < NRH) t_lo[seg % 3][r] = lo;
-          for (int t = 0; t < s.n; ++t) {
-            const uint32_t rows = __ballot_sync(kFull, (m >> t) & 1);
-            if (lane == (t & 31)) t_rows[seg % 3][hf][t] = rows;
-          }
-        }
-      }
+    auto stage_q = [&](const MqSeg &s, int qb, bool async) {
       uint8_t *q0 = sQ + (size_t)qb * Cfg::Q_BYTES;
       for (int i = tid; i < NR * 16; i += Cfg::SOFTMAX) {
         const int r = i >> 4, cc = i & 15;
         const uint32_t dst = smem_u32(q0 + (cc >> 3) * Cfg::PANEL_Q + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-        if (r < R) {
+        if (r < p.R) {
           const int ii = r / p.G, gq = r - ii * p.G;
           const uint4 *src = reinterpret_cast<const uint4 *>(
               static_cast<const uint16_t *>(p.q) + (((size_t)s.b * p.q_len + ii) * p.Hq + s.h * p.G + gq) * Cfg::D) + cc;
@@ -622,7 +595,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool have = wk.next(p, sg);
     bool nhave = have && wk.next(p, nx);
     if (have) {
-      stage_q(sg, 0, false, 0);
+      stage_q(sg, 0, false);
       release_q(0, false);
     }
     bool ok = true;
@@ -638,7 +611,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // at this segment's last tile (once its last S^T has landed)
       bool staged = false;
       if (Cfg::QBUF == 2 && nhave) {
-        stage_q(nx, (si + 1) % Cfg::QBUF, true, si + 1);
+        stage_q(nx, (si + 1) % Cfg::QBUF, true);
         staged = true;
       }
 #pragma unroll
@@ -681,8 +654,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (gj + 1 < ntiles && !(ok = widen(gj + 1, false))) break;
         }
         ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
-        // (tree) orders the segment's masks, staged with its Q, before their use
-        if (Cfg::TREE && ok && j == 0) ok = warp_wait(&q_full[si % Cfg::QBUF], (uint32_t)(si / Cfg::QBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         // S^T of this thread's position and rows, masked: new token i sees the
@@ -691,29 +662,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int imin = pos - sg.ctx + p.q_len;
         const int rlo = imin > 0 ? (imin < p.q_len ? imin * p.G : p.R) : 0;
         const int rhi = p.window > 0 ? (imin + p.window >= p.q_len ? p.R : max(0, imin + p.window) * p.G) : p.R;
-        [[maybe_unused]] uint32_t rows = ~0u;  // (tree) the rows that see this position
-        if constexpr (Cfg::TREE) {
-          const int start = sg.ctx - sg.n, t = pos - start;
-          if (t >= 0) {
-            rows = t < sg.n ? t_rows[si % 3][hf][t] : 0u;
-          } else if (p.window > 0 && pos < start + p.q_len - p.window) {
-            for (int e = 0; e < NRH; ++e)
-              if (pos < t_lo[si % 3][row0 + e]) rows &= ~(1u << e);
-          }
-        }
         float s[NRH];
         auto load_s = [&]() {
           uint32_t sr[NRH];
           ld_cols<NRH>(scol, sr);
 #pragma unroll
           for (int e = 0; e < NRH; ++e) s[e] = __uint_as_float(sr[e]) * ksc;  // (fp8: the block's K scale)
-          if constexpr (Cfg::TREE) {
-            if (rows != ~0u) {
-#pragma unroll
-              for (int e = 0; e < NRH; ++e)
-                if (!((rows >> e) & 1)) s[e] = -INFINITY;
-            }
-          } else if (!(rlo <= row0 && rhi >= row0 + NRH)) {
+          if (!(rlo <= row0 && rhi >= row0 + NRH)) {
 #pragma unroll
             for (int e = 0; e < NRH; ++e)
               if (row0 + e < rlo || row0 + e >= rhi) s[e] = -INFINITY;
@@ -739,7 +694,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           mrow = reduce_scatter<NRH, true>(mx, lane);
         }
         if (Cfg::QBUF == 1 && j + 1 == n && nhave) {
-          stage_q(nx, 0, true, si + 1);
+          stage_q(nx, 0, true);
           staged = true;
         }
         if (lane < NRH) red[par][hf][qd][lane] = mrow;
@@ -868,11 +823,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int e = 0; e < NRH; ++e) {
           const int r = row0 + e;
           const float L = __shfl_sync(kFull, lt, e);
-          if (r < (Cfg::TREE ? sg.n * p.G : p.R)) {
+          if (r < p.R) {
             const int ii = r / p.G, gq = r - ii * p.G;
             const size_t idx = (((size_t)sg.b * p.q_len + ii) * p.Hq + sg.h * p.G + gq) * Cfg::D + d;
-            // a row that sees nothing gives 0 (tree: and a NaN stays one)
-            const float v = (Cfg::TREE ? L != 0.f : L > 0.f) ? __uint_as_float(o[e]) / L : 0.f;
+            const float v = L > 0.f ? __uint_as_float(o[e]) / L : 0.f;  // a row that sees nothing gives 0
             if constexpr (Cfg::OUT_BF)
               store_scalar(BF16{}, p.out, idx, v);
             else
@@ -886,8 +840,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < NRH; ++e) {
           const float L = __shfl_sync(kFull, lt, e);
-          po[(size_t)(row0 + e) * Cfg::D + d] = (Cfg::TREE ? L != 0.f : L > 0.f) ? __uint_as_float(o[e]) / L : 0.f;
-          if (Cfg::TREE && lane == e && L != L) mine = INFINITY;  // the merge gives NaN
+          po[(size_t)(row0 + e) * Cfg::D + d] = L > 0.f ? __uint_as_float(o[e]) / L : 0.f;
           if (lane == e && L > 0.f) mine = (m_run[e] == -INFINITY ? 0.f : m_run[e]) + log2f(L);
         }
         if (qd == 0 && lane < NRH) p.part_lse[part * kMqRows + row0 + lane] = mine;
@@ -902,14 +855,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // sequences with no tile (no visible position for any new token): zeros,
       // sequence b by CTA b mod grid
       const size_t per_seq = (size_t)p.q_len * p.Hq * Cfg::D / 8;
-      for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        const MqSeq s = mq_seq(p, b);
-        if (s.T == 0) {
+      for (int b = blockIdx.x; b < B; b += gridDim.x)
+        if (mq_seq(p, b).T == 0) {
           uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (size_t)b * per_seq * 8);
-          const size_t rows = Cfg::TREE ? (size_t)s.n * p.Hq * Cfg::D / 8 : per_seq;  // (tree) its nodes only
-          for (size_t i = tid; i < rows; i += Cfg::SOFTMAX) dst[i] = make_uint4(0, 0, 0, 0);
+          for (size_t i = tid; i < per_seq; i += Cfg::SOFTMAX) dst[i] = make_uint4(0, 0, 0, 0);
         }
-      }
     }
     if (!ok && lane == 0) {
       atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
@@ -949,8 +899,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 
 // Finishes the items cut by range ends: block c takes the boundary between
 // CTAs c and c + 1 and, if it falls inside an item and is that item's first,
-// merges the partials of the item written by the CTAs c .. wl (a CTA whose range starts at or after the item's first tile
-// wrote slot 0, the one before slot 1) — weights 2^(lse - max lse), rows
+// merges the partials of the item written by the CTAs c .. wl (a CTA whose
+// range starts at or after the item's first tile wrote slot 0, the one before
+// slot 1) — weights 2^(lse - max lse), rows
 // every partial leaves empty give 0.  Block 0 also publishes the call's
 // status bits (the OR of every CTA's).
 __global__ void __launch_bounds__(256) mq_merge_kernel(const MqParams p, int P, int out_bf16) {
@@ -982,8 +933,7 @@ __global__ void __launch_bounds__(256) mq_merge_kernel(const MqParams p, int P, 
   if (mq_cut(W, active, c) > a) return;           // an earlier cut inside the item merges it
   const int wl = (int)(((int64_t)e * active - 1) / W);  // the CTA holding the item's last tile
   constexpr int D = kMqHeadDim;
-  const int R = (p.tree_lens != nullptr ? min(max(__ldg(p.tree_lens + b), 0), p.q_len) : p.q_len) * p.G;
-  for (int i = threadIdx.x; i < R * (D / 4); i += blockDim.x) {
+  for (int i = threadIdx.x; i < p.R * (D / 4); i += blockDim.x) {
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
     float M = -INFINITY;
     for (int w = c; w <= wl; ++w) {
@@ -1067,25 +1017,20 @@ static cudaError_t launch_mq_cfg(const MqParams &p, const CUtensorMap &tmK, cons
   return cudaLaunchKernelEx(&mc, mq_merge_kernel, p, grid, Cfg::OUT_BF ? 1 : 0);
 }
 
-template <class T, class QT = T, bool TREE = false>
+template <class T, class QT = T>
 static cudaError_t launch_mq_rows(const MqParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, int grid,
                                   cudaStream_t stream) {
-  if (p.R <= 16) return launch_mq_cfg<MqCfg<T, 8, QT, TREE>>(p, tmK, tmV, grid, stream);
-  if (p.R <= 32) return launch_mq_cfg<MqCfg<T, 16, QT, TREE>>(p, tmK, tmV, grid, stream);
+  if (p.R <= 16) return launch_mq_cfg<MqCfg<T, 8, QT>>(p, tmK, tmV, grid, stream);
+  if (p.R <= 32) return launch_mq_cfg<MqCfg<T, 16, QT>>(p, tmK, tmV, grid, stream);
   if constexpr (T::kBytes == 1)
     return cudaErrorNotSupported;  // fp8: up to 32 rows
   else
-    return launch_mq_cfg<MqCfg<T, 32, QT, TREE>>(p, tmK, tmV, grid, stream);
+    return launch_mq_cfg<MqCfg<T, 32, QT>>(p, tmK, tmV, grid, stream);
 }
 
 cudaError_t launch_mq_decode(const MqParams &p, int cache_dtype, int q_dtype, const CUtensorMap &tmK,
                              const CUtensorMap &tmV, int grid, cudaStream_t stream) {
   if (p.R < 1 || p.R > kMqRows || p.B < 1 || p.B > kMqMaxBatch || grid < 1) return cudaErrorNotSupported;
-  if (p.tree_mask != nullptr) {  // 16-bit caches
-    if (cache_dtype == PKV_BF16) return launch_mq_rows<BF16, BF16, true>(p, tmK, tmV, grid, stream);
-    if (cache_dtype == PKV_F16) return launch_mq_rows<F16, F16, true>(p, tmK, tmV, grid, stream);
-    return cudaErrorNotSupported;
-  }
   if (cache_dtype == PKV_BF16) return launch_mq_rows<BF16>(p, tmK, tmV, grid, stream);
   if (cache_dtype == PKV_F16) return launch_mq_rows<F16>(p, tmK, tmV, grid, stream);
   if (cache_dtype == PKV_FP8_E4M3 && p.R <= kMqRowsFp8) {

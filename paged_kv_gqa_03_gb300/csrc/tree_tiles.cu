@@ -1,6 +1,7 @@
 // tree_tiles.cu — attention of a tree of drafted tokens over the paged cache on
-// the tensor cores with the query rows on the M side: kv heads with more rows
-// than the transposed kernel (mq_decode.cu) takes, and head dim 64.
+// the tensor cores with the query rows on the M side.  A tile is 128 rows however
+// few of them a call has: its K / V bytes bound it up to about 64 rows per kv
+// head, so this kernel serves few rows too (tree_route in api.cpp).
 //
 // The tile pipeline is that of prefill_common.cuh (S = Q . K^T and O += P . V of
 // 128 rows x 128 positions, tcgen05, S / P / O in tensor memory, TMA rings
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const Pend f3 = h3 ? fetch() : nil;
       const int64_t trow = row_of(f0);
       const int s = g % stages;
-      if (g >= stages) ok = warp_wait(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
+      if (g >= stages) ok = tile_wait(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
       if (!ok || __any_sync(kFull, *(volatile int *)&abort_flag)) {
         ok = false;
         break;
@@ -196,13 +197,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     MqSeg sg{};
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
-      ok = warp_wait(&q_full, (uint32_t)si & 1u, p.timeout_ns);
+      ok = tile_wait(&q_full, (uint32_t)si & 1u, p.timeout_ns);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int ks = g % Cfg::KSTAGES, sb = g % Cfg::SBUF;
-        ok = warp_wait(&k_full[ks], (uint32_t)(g / Cfg::KSTAGES) & 1u, p.timeout_ns);
+        ok = tile_wait(&k_full[ks], (uint32_t)(g / Cfg::KSTAGES) & 1u, p.timeout_ns);
         // S overwrites the buffer whose P . V of tile g - SBUF read P from it
         if (ok && g >= Cfg::SBUF)
-          ok = warp_wait(&pv_done[sb], (uint32_t)((g / Cfg::SBUF) - 1) & 1u, p.timeout_ns);
+          ok = tile_wait(&pv_done[sb], (uint32_t)((g / Cfg::SBUF) - 1) & 1u, p.timeout_ns);
         if (!ok) break;
         if (lane == 0) k_consumed = g + 1;
         tc::fence_after();
@@ -227,12 +228,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     MqSeg sg{};
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
-      if (si > 0) ok = warp_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
+      if (si > 0) ok = tile_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
       const int nblk = (sg.ctx + kBlock - 1) / kBlock;
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int vs = g % Cfg::VSTAGES, sb = g % Cfg::SBUF;
-        ok = warp_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
-        if (ok) ok = warp_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
+        ok = tile_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
+        if (ok) ok = tile_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         if (lane == 0) v_consumed = g + 1;
         uint8_t *vt = sV + (size_t)vs * Cfg::KV_BYTES;
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       float m_run = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int gj = g + j, sb = gj % Cfg::SBUF, par = gj & 1;
-        ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
+        ok = tile_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         // the item's last S has read Q: the next item's may come in
@@ -379,12 +380,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (nhave) release_q();
       // ---- epilogue of the item: O / l, or a normalised partial and its lse ----
       const int gl = g + n - 1;
-      ok = warp_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
+      ok = tile_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
       if (ok) {
         red_l[half][row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&xl);
-        ok = warp_wait(&xl, (uint32_t)si & 1u, p.timeout_ns);
+        ok = tile_wait(&xl, (uint32_t)si & 1u, p.timeout_ns);
       }
       if (!ok) break;
       tc::fence_after();

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       for (int j = 0; j < n; ++j) {
         const int gj = g + j, sb = gj % Cfg::SBUF, par = gj & 1;
         const bool last = j + 1 == n;
-        ok = warp_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
+        ok = tile_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         // the item's last S has read Q: the next item's may come in
@@ -588,12 +588,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (nhave) release_q();
       // ---- epilogue of the item: O / l, or a normalised partial and its lse ----
       const int gl = g + n - 1;
-      ok = warp_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
+      ok = tile_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
       if (ok) {
         red_l[half][row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&xl);
-        ok = warp_wait(&xl, (uint32_t)si & 1u, p.timeout_ns);
+        ok = tile_wait(&xl, (uint32_t)si & 1u, p.timeout_ns);
       }
       if (!ok) break;
       tc::fence_after();
