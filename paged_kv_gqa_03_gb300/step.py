@@ -18,12 +18,18 @@ k_new, v_new and the host-produced slot mapping / copy pairs / tables /
 lengths cross to the device, all from ONE pinned staging buffer with one copy
 (two staging buffers alternate so the host can prepare step n+1 while step n's
 copy is in flight).  Everything is asynchronous on `stream`.
+
+TreeStep is the step of speculative decoding with a tree of drafted tokens per
+sequence: the same chain with the tree's masks in the attention, then the
+verification of the drafts, the move of the accepted path's rows in the cache
+and, on the host, the release of the rejected positions.
 """
 import numpy as np
 import torch
 
 from . import (BlockManager, lib, paged_decode_attention, paged_decode_workspace_bytes,
-               paged_kv_append, paged_kv_copy_blocks, pkv_copy)
+               paged_kv_append, paged_kv_copy_blocks, paged_tree_attention, paged_tree_commit,
+               paged_tree_verify, paged_tree_workspace_bytes, pkv_copy)
 
 _ALIGN = 256
 
@@ -74,19 +80,22 @@ class DecodeStep:
         self._ran = False
 
     # -- buffers ---------------------------------------------------------------
-    def _layout(self, B):
+    def _sections(self, B):
+        """The staging buffer's sections, the step's inputs first."""
         L = self.q_len
         rows = (B, self.Hq, self.D) if L == 1 else (B, L, self.Hq, self.D)
         kv = (B, self.Hkv, self.D) if L == 1 else (B, L, self.Hkv, self.D)
-        sections = [("q", rows, self.q_dtype),
-                    ("k_new", kv, self.new_dtype),
-                    ("v_new", kv, self.new_dtype),
-                    ("slots", (B * L,), torch.int64),
-                    ("pairs", (2 * B * L,), torch.int32),
-                    ("table", (B, self.max_blocks), torch.int32),
-                    ("lens", (B,), torch.int32)]
+        return [("q", rows, self.q_dtype),
+                ("k_new", kv, self.new_dtype),
+                ("v_new", kv, self.new_dtype),
+                ("slots", (B * L,), torch.int64),
+                ("pairs", (2 * B * L,), torch.int32),
+                ("table", (B, self.max_blocks), torch.int32),
+                ("lens", (B,), torch.int32)]
+
+    def _layout(self, B):
         layout, off = {}, 0
-        for name, shape, dtype in sections:
+        for name, shape, dtype in self._sections(B):
             layout[name] = (off, shape, dtype)
             n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
             off = (off + n + _ALIGN - 1) // _ALIGN * _ALIGN
@@ -110,9 +119,11 @@ class DecodeStep:
         self.d_slots, self.d_pairs = self._dev["slots"], self._dev["pairs"]
         self.d_table, self.d_lens = self._dev["table"], self._dev["lens"]
         self._select(self._turn)
-        n = paged_decode_workspace_bytes(B, self.Hq, self.Hkv, self.D, self.k_cache.dtype,
-                                         self.q_dtype, self.num_splits, q_len=self.q_len)
-        self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._ws = torch.empty(self._workspace_bytes(B), dtype=torch.uint8, device=self.device)
+
+    def _workspace_bytes(self, B):
+        return paged_decode_workspace_bytes(B, self.Hq, self.Hkv, self.D, self.k_cache.dtype,
+                                            self.q_dtype, self.num_splits, q_len=self.q_len)
 
     def _select(self, turn):
         hs = self._host[turn]
@@ -131,6 +142,17 @@ class DecodeStep:
         tables and lengths of q_len new tokens per sequence into it.  Returns
         the number of copy-on-write pairs (raises on OOM)."""
         seqs = self.seqs if seqs is None else seqs
+        self._switch(seqs)
+        if self.q_len == 1:
+            tok_seqs = self.h_seqs
+        else:
+            tok_seqs = self.h_tok_seqs
+            tok_seqs.reshape(-1, self.q_len)[:] = self.h_seqs[:, None]
+        self._reserve(tok_seqs, self.h_slots.numpy(), seqs)
+        return self.ncow
+
+    def _switch(self, seqs):
+        """The other staging buffer, and the window's releases."""
         self._buffers(len(seqs))
         self._turn ^= 1
         if self._host[self._turn].done is not None:
@@ -140,12 +162,10 @@ class DecodeStep:
         if self.window:
             for seq in seqs:
                 self.bm.release_outside_window(int(seq), self.window)
-        if self.q_len == 1:
-            tok_seqs = self.h_seqs
-        else:
-            tok_seqs = self.h_tok_seqs
-            tok_seqs.reshape(-1, self.q_len)[:] = self.h_seqs[:, None]
-        ncow = self.bm.append_slots_into(tok_seqs, self.h_slots.numpy(), self.h_pairs.numpy())
+
+    def _reserve(self, tok_seqs, slots, seqs):
+        """Reserves a slot per entry of tok_seqs and exports tables and lengths."""
+        ncow = self.bm.append_slots_into(tok_seqs, slots, self.h_pairs.numpy())
         if ncow < 0:
             raise MemoryError("block manager out of blocks")
         self.ncow = ncow
@@ -153,7 +173,6 @@ class DecodeStep:
                                  self.h_table.data_ptr(), self.max_blocks, self.h_lens.data_ptr())
         if rc != 0:
             raise RuntimeError(f"export failed [{rc}]")
-        return ncow
 
     def _copy_in(self, with_inputs):
         """One host->device copy of the current staging buffer (the step's
@@ -186,9 +205,8 @@ class DecodeStep:
         key = ("append", k_new.data_ptr(), v_new.data_ptr(), self.d_slots.data_ptr())
         call = self._calls.get(key)
         if call is None:
-            if self.q_len > 1:
-                k_new = k_new.view(-1, self.Hkv, self.D)
-                v_new = v_new.view(-1, self.Hkv, self.D)
+            k_new = k_new.view(-1, self.Hkv, self.D)
+            v_new = v_new.view(-1, self.Hkv, self.D)
             call = self._remember(key, paged_kv_append(
                 k_new, v_new, self.k_cache, self.v_cache, self.d_slots, self.k_scale, self.v_scale,
                 stream=s, calibrated=self.calibrated, prepare=True))
@@ -302,3 +320,117 @@ class DecodeStep:
     def replay(self):
         with torch.cuda.stream(self.stream):
             self.graph.replay()
+
+
+class TreeStep(DecodeStep):
+    """One step of speculative decoding with a tree of at most `nodes` drafted
+    tokens per sequence, node 0 the last confirmed token:
+
+        step.prepare(masks, lens)          # host: slots, tables, masks
+        step.upload()                      # (or run(h_out), from host memory)
+        step.launch(q, k_new, v_new, out)  # append the nodes, attend the tree
+        ... the model's remaining work: the target's probabilities ...
+        step.verify(draft_tokens, target_probs, draft_probs, uniforms)
+        step.commit()                      # the accepted path's rows, together
+        path_len, next_token = step.finish()
+
+    finish() waits for the stream and shortens each sequence to its accepted
+    tokens; the next step's node 0 is next_token.  A model of several layers
+    attends and commits on each layer's cache (commit(k_cache, v_cache, ...))
+    and finishes once.  The device tensors d_path, d_path_len, d_next_token and
+    d_new_lens hold the last verify's and commit's results."""
+
+    def __init__(self, k_cache, v_cache, Hq, q_dtype, max_blocks, nodes, k_scale=None, v_scale=None,
+                 stream=None, scale=None, window=0, calibrated=False):
+        super().__init__(k_cache, v_cache, Hq, q_dtype, max_blocks, k_scale, v_scale, stream=stream,
+                         scale=scale, q_len=nodes, window=window, calibrated=calibrated)
+
+    def _sections(self, B):
+        L = self.q_len
+        s = super()._sections(B)
+        inputs = [("q", (B, L, self.Hq, self.D), self.q_dtype),     # (also for one node)
+                  ("k_new", (B, L, self.Hkv, self.D), self.new_dtype),
+                  ("v_new", (B, L, self.Hkv, self.D), self.new_dtype)]
+        return inputs + s[3:] + [("mask", (B, L), torch.int64), ("tree_lens", (B,), torch.int32)]
+
+    def _workspace_bytes(self, B):
+        return paged_tree_workspace_bytes(B, self.q_len, self.Hq, self.Hkv, self.D, self.k_cache.dtype, self.q_dtype)
+
+    def _buffers(self, B):
+        if self._B == B:
+            return
+        super()._buffers(B)
+        dev = self.device
+        self.d_mask, self.d_tree_lens = self._dev["mask"], self._dev["tree_lens"]
+        self.d_path = torch.empty((B, self.q_len), dtype=torch.int32, device=dev)
+        self.d_path_len = torch.empty(B, dtype=torch.int32, device=dev)
+        self.d_new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        self.d_next_token = torch.empty(B, dtype=torch.int64, device=dev)
+        pin = torch.cuda.is_available()
+        self.h_path_len = torch.empty(B, dtype=torch.int32, pin_memory=pin)
+        self.h_next_token = torch.empty(B, dtype=torch.int64, pin_memory=pin)
+
+    def _select(self, turn):
+        super()._select(turn)
+        self.h_mask, self.h_tree_lens = self._host[turn]["mask"], self._host[turn]["tree_lens"]
+
+    def prepare(self, masks, lens=None, seqs=None):
+        """Host part of a step: reserves lens[b] slots for sequence b (None:
+        `nodes` each) and writes masks ([B, nodes] or [nodes], bit j of node
+        i's: i sees j), slots, copy pairs, tables and lengths into the other
+        staging buffer.  Returns the number of copy-on-write pairs (raises on
+        OOM: nothing is reserved then)."""
+        seqs = self.seqs if seqs is None else seqs
+        L, B = self.q_len, len(seqs)
+        lens = np.full(B, L, dtype=np.int32) if lens is None else np.asarray(lens, dtype=np.int32)
+        if lens.shape != (B,) or (lens < 0).any() or (lens > L).any():
+            raise ValueError(f"lens must be {B} numbers in [0, {L}]")
+        masks = np.ascontiguousarray(np.asarray(masks)).astype(np.uint64, copy=False)
+        if masks.shape not in ((L,), (B, L)):
+            raise ValueError(f"masks must be [{B}, {L}] or [{L}], got {list(masks.shape)}")
+        self._switch(seqs)
+        self.h_mask.numpy()[:] = masks.view(np.int64)
+        self.h_tree_lens.numpy()[:] = lens
+        slots = np.empty(int(lens.sum()), dtype=np.int64)
+        self._reserve(np.repeat(self.h_seqs, lens), slots, seqs)
+        h = self.h_slots.numpy().reshape(B, L)
+        h.fill(-1)                                   # rows past a tree's nodes: skipped by the append
+        h[np.arange(L)[None, :] < lens[:, None]] = slots
+        return self.ncow
+
+    def attend(self, q, out):
+        key = ("attend", q.data_ptr(), out.data_ptr(), self.d_table.data_ptr())
+        call = self._calls.get(key)
+        if call is None:
+            call = self._remember(key, paged_tree_attention(
+                out, q, self.k_cache, self.v_cache, self.d_table, self.d_lens, self.d_mask, self.scale,
+                tree_lens=self.d_tree_lens, k_scale=self.k_scale, v_scale=self.v_scale, window=self.window,
+                workspace=self._ws, stream=self.stream, prepare=True))
+        call()
+
+    def verify(self, draft_tokens, target_probs, draft_probs=None, uniforms=None):
+        """paged_tree_verify of the step's trees; (path, path_len, next_token)."""
+        paged_tree_verify(self.d_path, self.d_path_len, self.d_next_token, draft_tokens, self.d_mask,
+                          target_probs, draft_probs, uniforms, self.d_tree_lens, stream=self.stream)
+        return self.d_path, self.d_path_len, self.d_next_token
+
+    def commit(self, k_cache=None, v_cache=None, k_scale=None, v_scale=None):
+        """Moves the accepted path's rows of the step's cache, or of another
+        layer's with the same tables."""
+        if k_cache is None:
+            k_cache, v_cache, k_scale, v_scale = self.k_cache, self.v_cache, self.k_scale, self.v_scale
+        paged_tree_commit(k_cache, v_cache, self.d_path, self.d_path_len, self.d_table, self.d_lens,
+                          k_scale, v_scale, self.d_tree_lens, self.d_new_lens, stream=self.stream)
+
+    def finish(self):
+        """Waits for the step and releases the rejected positions on the host;
+        (path_len, next_token) as numpy arrays."""
+        with torch.cuda.stream(self.stream):
+            self.h_path_len.copy_(self.d_path_len, non_blocking=True)
+            self.h_next_token.copy_(self.d_next_token, non_blocking=True)
+        self.stream.synchronize()
+        path_len, next_token = self.h_path_len.numpy().copy(), self.h_next_token.numpy().copy()
+        kept = self.h_lens.numpy() - self.h_tree_lens.numpy() + path_len
+        for seq, n in zip(self.h_seqs, kept):
+            self.bm.truncate(int(seq), int(n))
+        return path_len, next_token
