@@ -507,7 +507,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (dead) {  // (rows past the nodes: their P and O are never looked at)
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[sb]);
+          if (lane == 0) {
+            mbar_arrive(&xch[warp & 3][par]);  // (its phases count tiles, whoever is alive in them)
+            mbar_arrive(&p_full[sb]);
+          }
           continue;
         }
         const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);

@@ -310,3 +310,16 @@ def test_fp8_queries_of_all_sizes(D, q_dtype):
         x.q[1, 2] = 0
         x.scale /= 40
         _run(x)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("fp8_e4m3", 128), ("fp8_e4m3", 64)])
+def test_small_and_wide_trees_one_after_another(dtype, D):
+    """A CTA's items alternate between trees that leave most of a row tile's
+    warps without rows and trees that fill it, an odd number of tiles each: the
+    warps' exchange keeps step with the tiles through both."""
+    rng = np.random.default_rng(7)
+    B, n = 240, 40
+    nodes = [int(rng.choice([1, 2, 33, 40])) for _ in range(B)]
+    ctx = [max(m, int(rng.choice([50, 128, 300]))) for m in nodes]
+    with routes(tree="tiles"):
+        _run(Inputs(51, ctx, n, 3, 3, D, dtype, nodes=nodes))
