@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool nhave = have && next_item(wk, nx);
     if (have) release_q();
     bool ok = true;
-    int g = 0, si = 0;
+    int g = 0, si = 0, xn = 0;  // tiles and items so far, exchanges of this warp (none in tiles without its rows)
     while (have && ok) {
       const int n = sg.j1 - sg.j0;
       // what this row sees: [lo, start), then node t at start + t iff bit t of mask
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const int lo_all = p.window > 0 ? start + p.q_len - p.window : 0;  // no row's lo is above it
       float m_run = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int gj = g + j, sb = gj % Cfg::SBUF, par = gj & 1;
+        const int gj = g + j, sb = gj % Cfg::SBUF;
         ok = tile_wait(&s_full[sb], (uint32_t)(gj / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
@@ -321,10 +321,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (dead) {  // (rows past the nodes: their P and O are never looked at)
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&xch[warp & 3][par]);  // (its phases count tiles, whoever is alive in them)
-            mbar_arrive(&p_full[sb]);
-          }
+          if (lane == 0) mbar_arrive(&p_full[sb]);
           continue;
         }
         const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);
@@ -339,10 +336,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < SC; e += 2) mx = fmax3(mx, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         // the row max over both halves (double-buffered exchange, bounded wait)
+        const int par = xn & 1;
         red[par][half][row] = mx;
         __syncwarp();
         if (lane == 0) mbar_arrive(&xch[warp & 3][par]);
-        ok = warp_wait(&xch[warp & 3][par], (uint32_t)(gj >> 1) & 1u, p.timeout_ns);
+        ok = warp_wait(&xch[warp & 3][par], (uint32_t)(xn++ >> 1) & 1u, p.timeout_ns);
         if (!ok) break;
         mx = fmaxf(mx, red[par][half ^ 1][row]);
         const float m_new = fmaxf(m_run, mx * c);
