@@ -88,8 +88,10 @@ struct MqPlan {
 };
 // Ranges that receive work.
 __device__ __forceinline__ int mq_active(int W, int parts) { return W < parts ? (W > 0 ? W : 1) : parts; }
+// floor(W part / active), in 32 bits (active is at most the SM count)
 __device__ __forceinline__ int mq_cut(int W, int active, int part) {
-  return part < active ? (int)((int64_t)W * part / active) : W;
+  const unsigned q = (unsigned)W / (unsigned)active, rem = (unsigned)W - q * (unsigned)active;
+  return part < active ? (int)(q * (unsigned)part + rem * (unsigned)part / (unsigned)active) : W;
 }
 // Block-wide (every thread of the CTA calls it).
 template <int THREADS>

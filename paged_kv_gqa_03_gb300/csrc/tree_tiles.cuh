@@ -26,26 +26,21 @@ struct TreeRange {
 // Block-wide; `find` is shared memory for the scan: the sequences holding the
 // range's ends.
 struct TreeFind {
-  int32_t wsum[8], b[2], base[2];
+  int32_t wsum[8], b[2], base[2], T[2];
 };
 template <int THREADS>
 __device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int groups, TreeFind *find, int *cta_flags) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = p.B, per = (B + THREADS - 1) / THREADS;
-  int tk[kMqMaxBatch / THREADS];
+  const int B = p.B, per = (B + THREADS - 1) / THREADS, b_end = min(B, (tid + 1) * per);
   int own = 0, incl = 0;
+  // (loops, not unrolled: this code runs once, from a cold instruction cache)
   if (tid < THREADS) {
-    int bad = 0;
-#pragma unroll
-    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
-      const int b = tid * per + k;
-      tk[k] = 0;
-      if (k < per && b < B) {
-        const MqSeq s = mq_seq(p, b);
-        tk[k] = s.T * p.Hkv;
-        bad |= s.bad_ctx ? 1 : 0;
-      }
-      own += tk[k];
+    bool bad = false;
+#pragma unroll 1
+    for (int b = tid * per; b < b_end; ++b) {
+      const MqSeq s = mq_seq(p, b);
+      own += s.T * p.Hkv;
+      bad |= s.bad_ctx;
     }
     incl = own;
 #pragma unroll
@@ -57,35 +52,36 @@ __device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int
     if (blockIdx.x == 0 && __any_sync(kFull, bad) && lane == 0) atomicOr(cta_flags, PKV_FLAG_BAD_LEN);
   }
   __syncthreads();
-  int W = 0, before = 0;
+  int W = 0, run = incl - own;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = W;
-    W += find->wsum[w];
+    const int n = find->wsum[w];
+    run += w < warp ? n : 0;
+    W += n;
   }
   const int active = mq_active(W, groups);
   TreeRange r;
   r.t0 = mq_cut(W, active, group);
   r.t1 = mq_cut(W, active, group + 1);
-  if (tid < THREADS) {
-    int run = before + incl - own;
+  if (tid < THREADS && ((run <= r.t0 && r.t0 < run + own) || (run <= r.t1 && r.t1 < run + own))) {
+#pragma unroll 1
+    for (int b = tid * per; b < b_end; ++b) {
+      const int T = mq_seq(p, b).T, n = T * p.Hkv;
 #pragma unroll
-    for (int k = 0; k < kMqMaxBatch / THREADS; ++k) {
-      const int b = tid * per + k;
-      if (run <= r.t0 && r.t0 < run + tk[k]) {
-        find->b[0] = b;
-        find->base[0] = run;
+      for (int i = 0; i < 2; ++i) {
+        const int t = i == 0 ? r.t0 : r.t1;
+        if (run <= t && t < run + n) {
+          find->b[i] = b;
+          find->base[i] = run;
+          find->T[i] = T;
+        }
       }
-      if (run <= r.t1 && r.t1 < run + tk[k]) {
-        find->b[1] = b;
-        find->base[1] = run;
-      }
-      run += tk[k];
+      run += n;
     }
   }
   __syncthreads();
-  auto snap = [&](int t, int b, int base) -> int {
-    const int T = mq_seq(p, b).T, d = (t - base) % T;
+  auto snap = [&](int t, int i) -> int {
+    const int T = find->T[i], d = (t - find->base[i]) % T;
     return d <= kSnapTiles ? t - d : (T - d <= kSnapTiles ? t + T - d : t);
   };
   r.b0 = B;
@@ -93,9 +89,9 @@ __device__ __forceinline__ TreeRange tree_plan(const MqParams &p, int group, int
   if (r.t0 < W) {  // (else an empty range)
     r.b0 = find->b[0];
     r.base0 = find->base[0];
-    r.t0 = snap(r.t0, r.b0, r.base0);
+    r.t0 = snap(r.t0, 0);
   }
-  if (r.t1 < W) r.t1 = snap(r.t1, find->b[1], find->base[1]);
+  if (r.t1 < W) r.t1 = snap(r.t1, 1);
   return r;
 }
 
