@@ -25,8 +25,12 @@ struct WsHeader {
   int32_t W;           // total (unit, block) work items
   int32_t B;
   int32_t HU;          // units per sequence = Hkv * NC
-  int32_t pad[58];     // 256 bytes
+  // a call whose kernel has no merge behind it: status = kStatusPerCta | CTAs,
+  // and each CTA's own bits (paged_decode_status joins them)
+  uint8_t cta_status[224];
+  int32_t pad[2];      // 256 bytes
 };
+constexpr int32_t kStatusPerCta = 1 << 30;
 
 // Batches up to this size are planned inside the decode kernel (each CTA
 // scans context_lens into shared memory); larger ones use the plan kernel.

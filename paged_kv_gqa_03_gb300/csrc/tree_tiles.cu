@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == Cfg::ISSUER) tc::dealloc(tbase, Cfg::TMEM_COLS);
-  if (tid == 0) p.cta_flags[blockIdx.x] = cta_flags;
+  if (tid == 0) write_status(tp, cta_flags);
 }
 
 // Finishes the items cut between groups: block (x, y) takes row tile x % RT and
@@ -611,7 +611,7 @@ static cudaError_t launch_tiles_cfg(const TreeTileParams &p, const CUtensorMap &
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<Cfg>, p, tmK, tmV);
   if (e != cudaSuccess) return e;
-  return launch_tree_merge(p, grid, Cfg::BF ? 1 : 0, stream);
+  return p.cta_status ? cudaSuccess : launch_tree_merge(p, grid, Cfg::BF ? 1 : 0, stream);
 }
 
 cudaError_t launch_tree_tiles(const TreeTileParams &p, int cache_dtype, int q_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,

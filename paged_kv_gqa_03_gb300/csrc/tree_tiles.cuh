@@ -7,11 +7,6 @@
 
 namespace pkv {
 
-// A cut of the schedule that falls within this many tiles of an item's end is
-// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
-// and the item needs no partials and no merge.
-constexpr int kSnapTiles = 4;
-
 // What group g's range is, for the merge kernel: its first tile, and the item
 // that tile cuts ([a, e) its tiles), e = 0 if the range starts at an item's end.
 struct TreeCut {
@@ -171,6 +166,16 @@ static __device__ __noinline__ void rescale_o(uint32_t ta, float alpha, int cols
 // sees nothing, +inf for a sum that is NaN, so that the merge gives NaN.
 __device__ __forceinline__ float partial_lse(float m, float l) {
   return l > 0.f ? m + log2f(l) : (l == 0.f ? -INFINITY : INFINITY);
+}
+
+// A CTA's status bits: for the merge kernel, or into the header if none follows.
+__device__ __forceinline__ void write_status(const TreeTileParams &tp, int flags) {
+  if (tp.cta_status == nullptr) {
+    tp.m.cta_flags[blockIdx.x] = flags;
+    return;
+  }
+  tp.cta_status[blockIdx.x] = (uint8_t)flags;
+  if (blockIdx.x == 0) *tp.m.status = kStatusPerCta | (int)gridDim.x;
 }
 
 // The schedule's launch (tree_tiles.cu): joins the items cut between groups.

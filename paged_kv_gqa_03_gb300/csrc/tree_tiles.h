@@ -9,9 +9,16 @@ namespace pkv {
 
 constexpr int kTreeTileRows = 128;  // query rows of one CTA
 
+// A cut of the schedule that falls within this many tiles of an item's end is
+// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
+// and the item needs no partials and no merge.
+constexpr int kSnapTiles = 4;
+constexpr int kUncutTiles = 2 * kSnapTiles + 1;  // items of up to this many tiles are never cut
+
 struct TreeCut;
 struct TreeTileParams {
   MqParams m;     // part_o / part_lse sized for this kernel (tree_tiles_ws_layout)
+  uint8_t *cta_status;  // WsHeader::cta_status if no item can be cut (no merge follows), else null
   TreeCut *cuts;  // [groups] workspace (MqWsLayout's `prefix`)
   int D;
   int RT;       // row tiles per (sequence, kv head): ceil(R / 128)

@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == Cfg::ISSUER) tc::dealloc(tbase, Cfg::TMEM_COLS);
-  if (tid == 0) p.cta_flags[blockIdx.x] = cta_flags;
+  if (tid == 0) write_status(tp, cta_flags);
 }
 
 template <class Cfg>
@@ -698,7 +698,7 @@ static cudaError_t launch_fp8_cfg(const TreeTileParams &p, const CUtensorMap &tm
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_tile_fp8_kernel<Cfg>, p, tmK, tmV);
   if (e != cudaSuccess) return e;
-  return launch_tree_merge(p, grid, Cfg::OUT_BF ? 1 : 0, stream);
+  return p.cta_status ? cudaSuccess : launch_tree_merge(p, grid, Cfg::OUT_BF ? 1 : 0, stream);
 }
 
 cudaError_t launch_tree_tiles_fp8(const TreeTileParams &p, int q_dtype, const CUtensorMap &tmK, const CUtensorMap &tmV,
