@@ -119,29 +119,46 @@ __device__ __forceinline__ bool positive(float p, float q, F2 a) {
   return __fmaf_rn(-a.l, q, __fmaf_rn(-a.h, q, p)) > 0.f;
 }
 
-// Four elements per lane of the 128 that start at `t`: neighbours (vec: one
-// aligned 4-element load) or 32 apart.  Elements at or past `end` are 0.
-__device__ __forceinline__ int index4(int t, int lane, int e, bool vec) { return vec ? t + 4 * lane + e : t + lane + 32 * e; }
+// Four neighbouring elements of a row as they are stored, element i first; those
+// outside [lo, end) are 0.  One load where all four are inside and `vec` (i's
+// address is a multiple of the four).
 template <class T>
-__device__ __forceinline__ void load4(const void *row, int t, int lane, bool vec, int end, float (&x)[4]) {
-  if (vec && t + 4 * lane + 4 <= end) {
-    const int i = t + 4 * lane;
-    if constexpr (T::kBytes == 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+struct Quad {
+  using Raw = uint2;
+  Raw v;
+  __device__ __forceinline__ void load(const void *row, int i, int lo, int end, bool vec) {
+    const uint16_t *x = static_cast<const uint16_t *>(row);
+    if (vec && i >= lo && i + 4 <= end) {
+      v = *reinterpret_cast<const Raw *>(x + i);
     } else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + i);
-      const float2 a = unpack2(T{}, v.x), b = unpack2(T{}, v.y);
-      x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-    }
-  } else {
+      uint32_t e[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = index4(t, lane, e, vec);
-      x[e] = i < end ? load_scalar(T{}, row, (size_t)i) : 0.f;
+      for (int k = 0; k < 4; ++k) e[k] = i + k >= lo && i + k < end ? x[i + k] : 0u;
+      v = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
     }
   }
-}
+  __device__ __forceinline__ float4 get() const {
+    const float2 a = unpack2(T{}, v.x), b = unpack2(T{}, v.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+template <>
+struct Quad<F32> {
+  using Raw = float4;
+  Raw v;
+  __device__ __forceinline__ void load(const void *row, int i, int lo, int end, bool vec) {
+    const float *x = static_cast<const float *>(row);
+    if (vec && i >= lo && i + 4 <= end) {
+      v = *reinterpret_cast<const Raw *>(x + i);
+    } else {
+      v.x = i >= lo && i < end ? x[i] : 0.f;
+      v.y = i + 1 >= lo && i + 1 < end ? x[i + 1] : 0.f;
+      v.z = i + 2 >= lo && i + 2 < end ? x[i + 2] : 0.f;
+      v.w = i + 3 >= lo && i + 3 < end ? x[i + 3] : 0.f;
+    }
+  }
+  __device__ __forceinline__ float4 get() const { return v; }
+};
 
 }  // namespace
 
@@ -303,8 +320,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
   const int me = rank * WARPS + warp;
   int lo, hi;  // this warp's part of the vocabulary
   warp_part(p.V, me, C * WARPS, &lo, &hi);
-  constexpr uintptr_t kAlign = 4 * T::kBytes;
-  constexpr int U = 4;  // loads in flight per row
+  // loads in flight per lane, of one row and of each of two: 8 are a warp's part of a vocabulary
+  // of 128000 in one round trip to memory (what the registers allow for two fp32 rows is 4)
+  constexpr int U1 = 8, U2 = T::kBytes == 4 ? 4 : 8;
   for (int pass = 0;; ++pass) {
     if (warp == 0) {
       const Cmd c = advance();
@@ -319,24 +337,30 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
     const int par = pass & 1;
     const void *pr = row(p.target, p.ld_target, c.node);
     const void *qr = draft ? row(p.draft, p.ld_draft, c.node) : nullptr;
-    const bool vec = reinterpret_cast<uintptr_t>(pr) % kAlign == 0 && reinterpret_cast<uintptr_t>(qr) % kAlign == 0;
+    // quads start where p's addresses are multiples of four elements (before lo, if need
+    // be); q's are there too if its row has the same offset
+    const int off = (int)(reinterpret_cast<uintptr_t>(pr) / T::kBytes + (unsigned)lo) & 3, from = lo - off + 4 * lane;
+    const bool vec = ((reinterpret_cast<uintptr_t>(pr) - reinterpret_cast<uintptr_t>(qr)) / T::kBytes & 3) == 0;
     if (c.op == kArgmax) {
       float m = -INFINITY;
       int at = INT32_MAX;
-      for (int t = lo; t < hi; t += 128 * U) {
-        float x[U][4];
+      for (int t = from; t < hi; t += 128 * U1) {
+        Quad<T> x[U1];
 #pragma unroll
-        for (int k = 0; k < U; ++k) load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
+        for (int k = 0; k < U1; ++k) x[k].load(pr, t + 128 * k, lo, hi, true);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int k = 0; k < U1; ++k) {
+          const float4 v = x[k].get();
+          const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // (a lane's indexes grow: the first of equals stays)
-            const int i = index4(t + 128 * k, lane, e, vec);
-            if (i < hi && (x[k][e] > m || (x[k][e] == m && at == INT32_MAX))) {
-              m = x[k][e];
+            const int i = t + 128 * k + e;
+            if (i >= lo && i < hi && (f[e] > m || (f[e] == m && at == INT32_MAX))) {
+              m = f[e];
               at = i;
             }
           }
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -354,41 +378,43 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) tree_verify_kernel(co
       const uint64_t lost = draft ? 0 : lost_in(walk, walk.kids[c.node], lo, hi, lane);
       Sums s{{0.f, 0.f}, {0.f, 0.f}};
       if (c.a.h == 0.f) {  // no refusal of a sampled draft: the weights are p, and q is not read
-        for (int t = lo; t < hi; t += 128 * U) {
-          float x[U][4];
+        for (int t = from; t < hi; t += 128 * U1) {
+          Quad<T> x[U1];
 #pragma unroll
-          for (int k = 0; k < U; ++k) load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
-          for (uint64_t l = lost; l; l &= l - 1) {
-            const int tok = walk.tok[__ffsll((long long)l) - 1];
+          for (int k = 0; k < U1; ++k) x[k].load(pr, t + 128 * k, lo, hi, true);
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (index4(t + 128 * k, lane, e, vec) == tok) x[k][e] = 0.f;
-          }
-#pragma unroll
-          for (int k = 0; k < U; ++k)
+          for (int k = 0; k < U1; ++k)
             if (t + 128 * k < hi) {
+              const float4 v = x[k].get();
+              float f[4] = {v.x, v.y, v.z, v.w};
+              for (uint64_t l = lost; l; l &= l - 1) {
+                const int tok = walk.tok[__ffsll((long long)l) - 1] - (t + 128 * k);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s.p.add(x[k][e] > 0.f ? x[k][e] : 0.f);
+                for (int e = 0; e < 4; ++e)
+                  if (e == tok) f[e] = 0.f;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s.p.add(f[e] > 0.f ? f[e] : 0.f);
             }
         }
       } else {
-        for (int t = lo; t < hi; t += 128 * U) {
-          float x[U][4], y[U][4];
+        for (int t = from; t < hi; t += 128 * U2) {
+          Quad<T> x[U2], y[U2];
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            load4<T>(pr, t + 128 * k, lane, vec, hi, x[k]);
-            load4<T>(qr, t + 128 * k, lane, vec, hi, y[k]);
+          for (int k = 0; k < U2; ++k) {
+            x[k].load(pr, t + 128 * k, lo, hi, true);
+            y[k].load(qr, t + 128 * k, lo, hi, vec);
           }
 #pragma unroll
-          for (int k = 0; k < U; ++k)
+          for (int k = 0; k < U2; ++k)
             if (t + 128 * k < hi) {
+              const float4 v = x[k].get(), w = y[k].get();
+              const float f[4] = {v.x, v.y, v.z, v.w}, g[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const bool pos = positive(x[k][e], y[k][e], c.a);
-                s.p.add(pos ? x[k][e] : 0.f);
-                s.q.add(pos ? y[k][e] : 0.f);
+                const bool pos = positive(f[e], g[e], c.a);
+                s.p.add(pos ? f[e] : 0.f);
+                s.q.add(pos ? g[e] : 0.f);
               }
             }
         }
