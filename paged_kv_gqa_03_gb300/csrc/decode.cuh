@@ -104,12 +104,13 @@ struct Producer {
   float win_ks, win_vs;
 };
 
+template <bool TREE>
 __device__ __forceinline__ void load_seq(Producer &pr, const DecodeParams &p) {
   const int ctx = clamped_len(p, __ldg(p.context_lens + pr.b));
   pr.ctx = ctx;
   pr.n = (ctx + kBlock - 1) / kBlock;
-  if (p.tree_lens != nullptr && seq_rows(p, pr.b) == 0) pr.n = 0;  // no query rows: nothing to stream
-  pr.j0 = first_block(p, pr.b, ctx);
+  if (TREE && p.tree_lens != nullptr && seq_rows(p, pr.b) == 0) pr.n = 0;  // no query rows: nothing to stream
+  pr.j0 = first_block<TREE>(p, pr.b, ctx);
 }
 
 // Block-table entry (and, for fp8, the block's K / V scales) of block jj of
@@ -232,7 +233,7 @@ __device__ __forceinline__ int produce(Producer &pr, const DecodeParams &p, cons
       pr.hu = 0;
       do {
         ++pr.b;
-        load_seq(pr, p);
+        load_seq<Cfg::TREE>(pr, p);
       } while (pr.n == 0 && pr.b < p.B - 1);
     }
     pr.j = pr.j0;
@@ -1009,11 +1010,13 @@ __device__ __forceinline__ void simt_finish(SimtState<Cfg> &st, const DecodePara
 // needed; CTA 0 also stores it for the merge kernel.  Lengths are clamped to
 // [0, 16 * max_blocks] and flagged.
 // ---------------------------------------------------------------------------
+template <bool TREE>
 __device__ __forceinline__ int clamp_len(const DecodeParams &p, int b, int ctx, int *flags) {
-  *flags |= len_flags(p, b, ctx);
+  *flags |= len_flags<TREE>(p, b, ctx);
   return clamped_len(p, ctx);
 }
 
+template <bool TREE>
 __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_prefix, int32_t *s_scan,
                                             int *cta_flags) {
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = T >> 5;
@@ -1021,7 +1024,7 @@ __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_pr
   const int b0 = tid * k;
   int sum = 0, flags = 0;
   for (int i = 0; i < k; ++i)
-    if (b0 + i < p.B) sum += seq_items(p, b0 + i, clamp_len(p, b0 + i, __ldg(p.context_lens + b0 + i), &flags));
+    if (b0 + i < p.B) sum += seq_items<TREE>(p, b0 + i, clamp_len<TREE>(p, b0 + i, __ldg(p.context_lens + b0 + i), &flags));
   int x = sum;  // inclusive scan within the warp
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -1047,7 +1050,7 @@ __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_pr
     const int b = b0 + i;
     if (b < p.B) {
       s_prefix[b] = run;
-      run += seq_items(p, b, clamp_len(p, b, __ldg(p.context_lens + b), &unused));
+      run += seq_items<TREE>(p, b, clamp_len<TREE>(p, b, __ldg(p.context_lens + b), &unused));
       if (b == p.B - 1) s_prefix[p.B] = run;
     }
   }
@@ -1058,6 +1061,7 @@ __device__ __forceinline__ void inline_plan(const DecodeParams &p, int32_t *s_pr
 }
 
 // Partition w's first item {s, b, hu, j} and its end, from the prefix.
+template <bool TREE>
 __device__ __forceinline__ int4 locate(const DecodeParams &p, const int32_t *pre, int w, int *end) {
   const int64_t W = (int64_t)p.HU * pre[p.B];
   const int64_t Pe = active_partitions(p, W);
@@ -1074,7 +1078,7 @@ __device__ __forceinline__ int4 locate(const DecodeParams &p, const int32_t *pre
   }
   const int n = pre[lo + 1] - pre[lo];
   const int64_t rr = s - (int64_t)p.HU * pre[lo];
-  const int j0 = first_block(p, lo, clamped_len(p, __ldg(p.context_lens + lo)));
+  const int j0 = first_block<TREE>(p, lo, clamped_len(p, __ldg(p.context_lens + lo)));
   return make_int4((int)s, lo, (int)(rr / n), j0 + (int)(rr % n));
 }
 
@@ -1111,14 +1115,14 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
   }
   __syncwarp();
   grid_dep_wait();  // the previous kernel's writes are visible from here on
-  if (p.inline_plan) inline_plan(p, s_prefix, s_scan, &cta_flags);
+  if (p.inline_plan) inline_plan<Cfg::TREE>(p, s_prefix, s_scan, &cta_flags);
 
   const int w = blockIdx.x * Cfg::WARPS + wib;
   if (w < p.P) {
     int e;
     int4 st0;
     if (p.inline_plan) {
-      st0 = locate(p, s_prefix, w, &e);
+      st0 = locate<Cfg::TREE>(p, s_prefix, w, &e);
     } else {
       st0 = p.starts[w];
       e = p.starts[w + 1].x;
@@ -1150,7 +1154,7 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
       pr.win_j0 = 0;
       pr.win_id = 0;
       pr.win_ks = pr.win_vs = 0.f;
-      load_seq(pr, p);
+      load_seq<Cfg::TREE>(pr, p);
       if constexpr (Cfg::BPS == 2) {
         // two-block stages: items issued / consumed are counted apart from
         // the stages that carry them

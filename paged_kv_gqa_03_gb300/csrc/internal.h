@@ -92,26 +92,31 @@ struct DecodeParams {
 __device__ __forceinline__ int clamped_len(const DecodeParams &p, int ctx) {
   return ctx < 0 ? 0 : (ctx > p.max_blocks * kBlock ? p.max_blocks * kBlock : ctx);
 }
+// (TREE false: in kernels that no tree reaches, where nothing of it is looked at.)
 // New tokens of sequence b: q_len, or its tree's node count (clamped to [0, q_len]).
+template <bool TREE = true>
 __device__ __forceinline__ int seq_rows(const DecodeParams &p, int b) {
-  return p.tree_lens == nullptr ? p.q_len : min(max(__ldg(p.tree_lens + b), 0), p.q_len);
+  return !TREE || p.tree_lens == nullptr ? p.q_len : min(max(__ldg(p.tree_lens + b), 0), p.q_len);
 }
 // First block any row of sequence b, of (clamped) length ctx, can see: with a
 // window, row 0's window starts at ctx - (n - 1) - W, n its new tokens (tree
 // nodes of depth 1 see as far back).
+template <bool TREE = true>
 __device__ __forceinline__ int first_block(const DecodeParams &p, int b, int ctx) {
-  const int lo = p.window > 0 ? ctx - (seq_rows(p, b) - 1) - p.window : 0;
+  const int lo = p.window > 0 ? ctx - (seq_rows<TREE>(p, b) - 1) - p.window : 0;
   return lo > 0 ? lo / kBlock : 0;
 }
 // Work items (blocks streamed per unit) of sequence b of (clamped) length ctx.
+template <bool TREE = true>
 __device__ __forceinline__ int seq_items(const DecodeParams &p, int b, int ctx) {
-  if (p.tree_lens != nullptr && seq_rows(p, b) == 0) return 0;
-  return (ctx + kBlock - 1) / kBlock - first_block(p, b, ctx);
+  if (TREE && p.tree_lens != nullptr && seq_rows(p, b) == 0) return 0;
+  return (ctx + kBlock - 1) / kBlock - first_block<TREE>(p, b, ctx);
 }
 // PKV_FLAG_BAD_LEN if sequence b's length or tree size is out of range (both are clamped).
+template <bool TREE = true>
 __device__ __forceinline__ int len_flags(const DecodeParams &p, int b, int ctx) {
   bool bad = ctx < 0 || ctx > p.max_blocks * kBlock;
-  if (p.tree_lens != nullptr) {
+  if (TREE && p.tree_lens != nullptr) {
     const int n = __ldg(p.tree_lens + b);
     bad |= n < 0 || n > p.q_len;
   }

@@ -145,6 +145,7 @@ __device__ __forceinline__ void store4_out(int dtype, void *p, size_t i, float4 
   }
 }
 
+template <bool TREE>
 __global__ void __launch_bounds__(512) splitk_merge_kernel(const DecodeParams p) {
   constexpr int kSegChunk = 32;
   constexpr int kBatch = 8;  // partials whose loads are in flight together
@@ -166,8 +167,8 @@ __global__ void __launch_bounds__(512) splitk_merge_kernel(const DecodeParams p)
   const int u = blockIdx.x;
   const int b = u / p.HU, hu = u % p.HU;
   const int h = hu / p.NC, r0 = (hu % p.NC) * p.GC;
-  const int gc = min(p.GC, (p.tree_lens ? seq_rows(p, b) * p.G : p.R) - r0);
-  if (gc <= 0) return;  // (tree) rows past the sequence's nodes are left as they were
+  const int gc = min(p.GC, (TREE ? seq_rows(p, b) * p.G : p.R) - r0);
+  if (TREE && gc <= 0) return;  // rows past the sequence's nodes are left as they were
   const int D = p.D;
   const int pb = p.prefix[b];
   const int n = p.prefix[b + 1] - pb;
@@ -261,7 +262,7 @@ cudaError_t launch_splitk_merge(const DecodeParams &p, cudaStream_t stream, bool
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, splitk_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, p.tree_mask ? splitk_merge_kernel<true> : splitk_merge_kernel<false>, p);
 }
 
 // ---------------------------------------------------------------------------
