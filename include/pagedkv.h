@@ -302,7 +302,25 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
  *   workspace  paged_tree_workspace_bytes(...) bytes, 256-byte aligned, as for
  *              paged_decode_attention (status: paged_decode_status)
  * Types, layouts, block_table, context_lens and errors as for
- * paged_decode_attention_multi.
+ * paged_decode_attention_multi.  K rows that a row does not see may hold anything.
+ * V rows at positions below context_lens[b] must be finite, seen or not: the
+ * tensor cores multiply a hidden one by a weight of 0.  (Positions at or past
+ * context_lens[b], in a block or in the table, may hold anything.)
+ *
+ * Kernels, all meeting the same error bound (pkv_set_route(PKV_ROUTE_TREE, ...)
+ * forces one where it applies):
+ *  - PKV_TREE_TILES: 128 query rows of a (sequence, kv head) on the MMA's M side,
+ *    its K / V tiles split over the SMs and joined by a merge (no merge is launched
+ *    where max_blocks_per_seq * 16 <= 1152).  F16, BF16 and FP8 caches, B <= 2048.
+ *    FP8: K enters the MMA as stored, q as a sum of E4M3 parts (elements below 2^-10
+ *    of their row's largest, 2^-7 for f16, are held to 2^-19 of it);
+ *  - PKV_TREE_UNITS: the decode kernel in units of 8 rows (FP8: 16, F32: 2), each
+ *    streaming the K / V once.  F32 caches, larger batches, and few rows on many
+ *    items or (FP8, D = 64) on more than small caches, where it is faster.
+ * Weights enter P . V as in the decode kernels: bf16 caches as a high part plus
+ * residual, f16 and FP8 caches as f16.  The same call gives the same bits.  Calls
+ * that may overlap need workspaces of their own; captured graphs that do may not
+ * share one.
  */
 int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D,
                                int cache_dtype, int q_dtype, size_t *bytes_out);

@@ -1,6 +1,7 @@
 // decode_tree_fp8.cu — decode-attention kernel variants for a tree of drafted
 // tokens (paged_tree_attention) on fp8-E4M3 caches: the pipeline shapes of
-// decode_fp8.cu with the tree's masks.
+// decode_fp8.cu with the tree's masks: up to 16 rows per kv head on more than a small
+// cache (16 x 8192, 32 / 8 heads, 1 / 2 / 4 nodes 62 / 65 / 81 us against the tile kernel's 93).
 #include "decode.cuh"
 
 namespace pkv {

@@ -10,8 +10,11 @@ namespace pkv {
 constexpr int kTreeTileRows = 128;  // query rows of one CTA
 
 // A cut of the schedule that falls within this many tiles of an item's end is
-// moved there: the two groups' loads differ by as many tiles (1.3 - 1.5 us each),
-// and the item needs no partials and no merge.
+// moved there: the two groups' loads differ by as many tiles (1.3 us each), and the
+// item needs no partials.  0 / 1 / 2 / 3 / 4 tiles, us: 8 x 1000, 8 heads, 19.9 / 19.5 / 23.2 /
+// 22.9 / 18.9; 16 x 1000 - 4000 52.5 / 51.8 / 51.8 / 52.2 / 53.0; 24 x 512 - 2048, 32 heads, 98.8 /
+// 96.2 / 96.8 / 96.9 / 97.1; 1 x 333 14.3 / 12.9 / 12.3 / 11.6 / 11.8; 64 x 500, 32 heads, 130 /
+// 129 / 125 / 125 / 124.
 constexpr int kSnapTiles = 4;
 constexpr int kUncutTiles = 2 * kSnapTiles + 1;  // items of up to this many tiles are never cut
 
