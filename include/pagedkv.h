@@ -302,10 +302,12 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
  *   workspace  paged_tree_workspace_bytes(...) bytes, 256-byte aligned, as for
  *              paged_decode_attention (status: paged_decode_status)
  * Types, layouts, block_table, context_lens and errors as for
- * paged_decode_attention_multi.  K rows that a row does not see may hold anything.
- * V rows at positions below context_lens[b] must be finite, seen or not: the
- * tensor cores multiply a hidden one by a weight of 0.  (Positions at or past
- * context_lens[b], in a block or in the table, may hold anything.)
+ * paged_decode_attention_multi.  What a row does not see may hold anything: the K and
+ * V rows of nodes outside its mask, of positions before its window, and of positions
+ * at or past context_lens[b].  A V element of a node (or of a position at a
+ * window's edge) that is not finite gives infinity or NaN in that element of the rows that
+ * see it, as the formula does; V at the positions before the tree that every
+ * row sees must be finite (an infinity there may give NaN).
  *
  * Kernels, all meeting the same error bound (pkv_set_route(PKV_ROUTE_TREE, ...)
  * forces one where it applies):

@@ -580,6 +580,7 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
     p.tree_mask = tree->mask;
     p.tree_lens = tree->lens;
     p.mask_stride = tree->mask_stride;
+    p.v_cache = v_cache;
   }
   take_stall(p, PKV_STALL_DECODE);
 
@@ -859,6 +860,7 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
     tp.m = mq_params(M, out, q, k_scale, v_scale, block_table,
                      max_blocks_per_seq, context_lens, B, q_len, window, Hq, Hkv, num_blocks, scale, workspace, &tree);
     tp.cuts = reinterpret_cast<TreeCut *>(tp.m.prefix);
+    tp.v_cache = v_cache;
     // a table too short for an item to be cut: the merge's launch would join nothing
     // (1 sequence of 333, 7 nodes: 14.8 us with it, 12.1 without)
     WsHeader *hdr = static_cast<WsHeader *>(workspace);

@@ -45,6 +45,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tree_finite.cuh"
 
 namespace pkv {
 
@@ -381,6 +382,35 @@ __device__ __forceinline__ void mma_begin(MmaState<Cfg> &st, const DecodeParams 
   }
 }
 
+// (tree) What not every row sees.
+template <class Cfg>
+__device__ __forceinline__ TreePartial unit_partial(const MmaState<Cfg> &st, const DecodeParams &p) {
+  return TreePartial{p.window > 0 ? max(0, st.start + 1 - p.window) : 0, st.lo_hi, st.start};
+}
+// (tree) Clears what is not finite in a V block's rows, positions pos0 + r, r < nvalid, that not
+// every row sees, and notes it in the warp's `spoiled` (tree_finite.cuh).  A context's last
+// blocks only: out of line.
+template <class T, int ROWB>
+static __device__ __noinline__ void clean_v_block(uint32_t vb, int pos0, int nvalid, TreePartial t, TreeSpoiled *spoiled) {
+  constexpr int CPR = ROWB / 16;
+  const int lane = threadIdx.x & 31;
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int i = lane; i < kBlock * CPR; i += 32)
+    if (i / CPR < nvalid) bad |= nonfinite_any<T>(lds128(vb + tile_off<ROWB>(i / CPR, (i % CPR) * 16)));
+  if (!__any_sync(kFull, bad != 0)) return;
+  uint32_t rows = 0;
+#pragma unroll 1
+  for (int i = lane; i < kBlock * CPR; i += 32) {
+    const int r = i / CPR;
+    if (r < nvalid && t.holds(pos0 + r) && clear_nonfinite<T>(vb + tile_off<ROWB>(r, (i % CPR) * 16))) rows |= 1u << r;
+  }
+  rows = __reduce_or_sync(kFull, rows);
+  if (lane == 0)
+    for (; rows; rows &= rows - 1) spoiled->note(t, pos0 + __ffs((int)rows) - 1);
+  __syncwarp();
+}
+
 // A block's K and V operands in registers (MMA fragments, or raw fp8 words).
 template <class Cfg>
 struct MmaFrags {
@@ -639,7 +669,7 @@ __device__ __forceinline__ void fp8_pv(MmaState<Cfg> &st, const uint8_t *tv, int
 
 template <class Cfg>
 __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &p, const StageMeta &m,
-                                         uint8_t *tk0, int lane) {
+                                         uint8_t *tk0, int lane, TreeSpoiled *spoiled) {
   static_assert(Cfg::FP8, "two-block stages are the fp8 path");
   constexpr int ROWB = Cfg::ROWB, NH = MmaState<Cfg>::NH;
   const int gid = lane >> 2;
@@ -648,6 +678,13 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
   const int rem0 = m.rem, rem1 = m.rem - kBlock;
   if (rem0 < kBlock) zero_tail_rows<ROWB>(tv0, rem0, lane);
   if (two && rem1 < kBlock) zero_tail_rows<ROWB>(tv1, rem1, lane);
+  if constexpr (Cfg::TREE) {
+    if (!st.all_see(m.j * kBlock, two ? 2 * kBlock : kBlock)) {
+      const TreePartial t = unit_partial<Cfg>(st, p);
+      clean_v_block<typename Cfg::Cache, ROWB>(smem_u32(tv0), m.j * kBlock, rem0, t, spoiled);
+      if (two) clean_v_block<typename Cfg::Cache, ROWB>(smem_u32(tv1), (m.j + 1) * kBlock, rem1, t, spoiled);
+    }
+  }
 
   float s[NH][4], t[NH][4];
   fp8_scores<Cfg>(st, tk0, lane, s);
@@ -749,11 +786,35 @@ __device__ __forceinline__ int mma_dim(int mt, int r, int gid) {
 
 template <class Cfg>
 __device__ __forceinline__ void mma_finish(MmaState<Cfg> &st, const DecodeParams &p, const StageMeta &m,
-                                           int w, int lane) {
+                                           int w, int lane, const TreeSpoiled *spoiled) {
   const int gid = lane >> 2, tig = lane & 3;
   const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
   const int gc = unit_rows<Cfg>(p, m.b, r0);
   const bool complete = m.flags & kComplete;
+  if constexpr (Cfg::TREE) {
+    if (spoiled->any()) {  // (tree_finite.cuh)
+      const TreePartial t = unit_partial<Cfg>(st, p);
+#pragma unroll 1
+      for (int edge = 0; edge < 2; ++edge)
+#pragma unroll 1
+        for (uint64_t bits = edge ? spoiled->edge : spoiled->nodes; bits; bits &= bits - 1) {
+          const int pos = (edge ? t.first : t.start) + __ffsll((long long)bits) - 1;
+          const int64_t blk = __ldg(p.block_table + (size_t)m.b * p.max_blocks + pos / kBlock);
+          const size_t row = ((size_t)(blk * p.Hkv + h) * kBlock + pos % kBlock) * Cfg::D;
+#pragma unroll
+          for (int mt = 0; mt < MmaState<Cfg>::MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float x = nonfinite_value<typename Cfg::Cache>(p.v_cache, row + mma_dim<Cfg>(mt, r, gid));
+#pragma unroll
+              for (int nh = 0; nh < MmaState<Cfg>::NH; ++nh)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (tree_sees(st.row[nh][c], st.start, pos)) st.acc[nh][mt][2 * r + c] += x;
+            }
+        }
+    }
+  }
   // partials: [worker][slot][GC rows][D]
   const size_t base = ((size_t)w * 2 + ((m.flags & kWFirst) ? 0 : 1)) * Cfg::GC;
 #pragma unroll
@@ -968,7 +1029,8 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
     for (int g = 0; g < GC; ++g) {
       const float pt = __shfl_sync(kFull, pw[g], tt);
 #pragma unroll
-      for (int e = 0; e < DPL; ++e) st.acc[g][e] = fmaf(pt, vf[e], st.acc[g][e]);
+      for (int e = 0; e < DPL; ++e)
+        st.acc[g][e] = Cfg::TREE && pt == 0.f ? st.acc[g][e] : fmaf(pt, vf[e], st.acc[g][e]);  // (a hidden V may be anything)
     }
   }
 }
@@ -1101,6 +1163,8 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
                 wib * Cfg::GC * Cfg::D;
   int32_t *s_prefix =
       reinterpret_cast<int32_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES + Cfg::BAR_BYTES + Cfg::QBUF_BYTES);
+  __shared__ TreeSpoiled s_spoiled[Cfg::TREE ? Cfg::WARPS : 1];
+  TreeSpoiled *spoiled = &s_spoiled[Cfg::TREE ? wib : 0];  // (tree) the warp's unit's
   __shared__ int32_t s_scan[32];
   __shared__ int cta_flags;
   __shared__ __align__(8) uint64_t dead_bar;  // failure-path test hook: nothing ever arrives on it
@@ -1174,13 +1238,16 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
             break;
           }
           const StageMeta m = meta[stage];
-          if (m.flags & kFirst) mma_begin<Cfg>(state, p, m, lane);
-          mma_pair<Cfg>(state, p, m, tiles + (size_t)stage * Cfg::STAGE_BYTES, lane);
+          if (m.flags & kFirst) {
+            mma_begin<Cfg>(state, p, m, lane);
+            if (Cfg::TREE) *spoiled = TreeSpoiled{0, 0};
+          }
+          mma_pair<Cfg>(state, p, m, tiles + (size_t)stage * Cfg::STAGE_BYTES, lane, spoiled);
           if (issued < total) {  // refilled once its fragments are consumed (as below)
             issued += produce<Cfg>(pr, p, &tmK, &tmV, tiles, meta, bars, stage, lane, &cta_flags);
             ++nst;
           }
-          if (m.flags & kLast) mma_finish<Cfg>(state, p, m, w, lane);
+          if (m.flags & kLast) mma_finish<Cfg>(state, p, m, w, lane, spoiled);
           done += m.nb;
         }
       } else {
@@ -1208,7 +1275,13 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
           // has been consumed by then, so the TMA overwrite needs no proxy
           // fence.  (Refilling it right after the fragments reach registers
           // measured 1-2 % slower on GB300.)
-          if (m.flags & kFirst) mma_begin<Cfg>(state, p, m, lane);
+          if (m.flags & kFirst) {
+            mma_begin<Cfg>(state, p, m, lane);
+            if (Cfg::TREE) *spoiled = TreeSpoiled{0, 0};
+          }
+          if constexpr (Cfg::TREE)
+            if (!state.all_see(m.j * kBlock, kBlock))
+              clean_v_block<typename Cfg::Cache, Cfg::ROWB>(smem_u32(tv), m.j * kBlock, m.nvalid, unit_partial<Cfg>(state, p), spoiled);
           MmaFrags<Cfg> frags;
           mma_load<Cfg>(frags, tk, tv, m.nvalid, lane);
           mma_compute<Cfg>(state, frags, p, m, lane);
@@ -1226,7 +1299,7 @@ __global__ void __launch_bounds__(Cfg::WARPS * 32, Cfg::MIN_CTAS)
         }
         if (m.flags & kLast) {
           if constexpr (Cfg::MMA)
-            mma_finish<Cfg>(state, p, m, w, lane);
+            mma_finish<Cfg>(state, p, m, w, lane, spoiled);
           else
             simt_finish<Cfg>(state, p, m, w, lane);
         }

@@ -85,6 +85,7 @@ struct DecodeParams {
   const uint64_t *tree_mask;
   const int32_t *tree_lens;  // [B] nodes of each sequence (<= q_len), or null: q_len
   int mask_stride;           // q_len, or 0: one tree for every sequence
+  const void *v_cache;       // (tree_finite.cuh)
 };
 
 #ifdef __CUDACC__

@@ -42,11 +42,50 @@ namespace pkv {
 
 template <class T, int D_>
 struct TreeCfg : PrefillCfg<T, D_> {
+  using Cache = T;
   using Base = PrefillCfg<T, D_>;
   static constexpr int STAGE_BYTES = Base::SOFTMAX / 32 * 2048;  // output staging, 2 KiB per softmax warp
   static constexpr size_t SMEM = Base::SMEM + STAGE_BYTES;
   static_assert(SMEM + 6144 <= 232448, "shared memory");
 };
+
+// (tree_finite.cuh) The rows of a V tile, positions kv0 + r below ctx, that not every row of Q sees:
+// what is not finite becomes 0, noted in `spoiled`.  Warp-wide, out of the issuing loop.
+template <class Cfg>
+static __device__ __noinline__ void clean_v_rows(uint8_t *vt, int kv0, int ctx, TreePartial t, unsigned long long *spoiled) {
+  constexpr int CPR = 8 * Cfg::PANELS, U = 8;  // chunks per row, in flight
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int i) {
+    const int r = i / CPR, c = i % CPR;
+    return smem_u32(vt + (c >> 3) * Cfg::PANEL_KV + r * 128 + (c & 7) * 16);
+  };
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {  // the tree's rows, a window's edge
+    const int i0 = part ? lane : max(t.start - kv0, 0) * CPR + lane;
+    const int i1 = min(part ? t.edge - kv0 : Cfg::N, min(ctx - kv0, Cfg::N)) * CPR;
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 32 * U) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = lds128(at(min(i + 32 * u, i1 - 1)));  // (the last chunk again past the end)
+      uint32_t bad = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) bad |= nonfinite_any<typename Cfg::Cache>(v[u]);
+      if (bad != 0) {
+        TreeSpoiled s{0, 0};
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const int k = i + 32 * u;
+          if (k < i1 && clear_nonfinite<typename Cfg::Cache>(at(k))) s.note(t, kv0 + k / CPR);
+        }
+        if (s.nodes) atomicOr(&spoiled[0], (unsigned long long)s.nodes);
+        if (s.edge) atomicOr(&spoiled[1], (unsigned long long)s.edge);
+        fence_proxy_async();
+      }
+    }
+  }
+  __syncwarp();
+}
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -66,6 +105,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
   __shared__ float red[2][2][Cfg::M];
   __shared__ float red_l[2][Cfg::M];
+  __shared__ __align__(16) unsigned long long spoiled[2][2];  // [item parity][nodes, window's edge]
   __shared__ TreeFind find;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_flags, k_consumed, v_consumed, k_issued, v_issued;
@@ -243,15 +283,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
       if (si > 0) ok = tile_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
+      if (lane < 2) spoiled[si & 1][lane] = 0;  // (last used two items ago, whose O was read out)
+      __syncwarp();
+      const PartialTiles part = partial_tiles(p, sg);
       const int nblk = (sg.ctx + kBlock - 1) / kBlock;
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int vs = g % Cfg::VSTAGES, sb = g % Cfg::SBUF;
         ok = tile_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
+        uint8_t *vt = sV + (size_t)vs * Cfg::KV_BYTES;
+        const int kv0 = (sg.j_first + j) * Cfg::N;  // first position of the tile
+        if (ok && part.has(j)) clean_v_rows<Cfg>(vt, kv0, sg.ctx, tree_partial(p, sg), spoiled[si & 1]);
         if (ok) ok = tile_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         if (lane == 0) v_consumed = g + 1;
-        uint8_t *vt = sV + (size_t)vs * Cfg::KV_BYTES;
-        const int kv0 = (sg.j_first + j) * Cfg::N;  // first position of the tile
         zero_v_rows<Cfg>(vt, sg.ctx - kv0, min(nblk * kBlock - kv0, Cfg::N), lane);
         __syncwarp();
         tc::fence_after();
@@ -406,6 +450,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       tc::fence_after();
       const float lt = l + red_l[half ^ 1][row];
       const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing gives 0 (and a NaN stays one)
+      const ulonglong2 sp = *reinterpret_cast<const ulonglong2 *>(spoiled[si & 1]);
+      if (sp.x | sp.y)
+        add_spoiled<typename Cfg::Cache, Cfg::D>(tp, tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), sg.b, sg.h, start, sg.first, sp.x,
+                                                 sp.y, mask, lo, half * OC);
       uint32_t o[OC / 32][32];
 #pragma unroll
       for (int q = 0; q < OC / 32; ++q)

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "mq_walk.cuh"
+#include "tree_finite.cuh"
 #include "tree_tiles.h"
 
 namespace pkv {
@@ -158,6 +159,50 @@ static __device__ __noinline__ void rescale_o(uint32_t ta, float alpha, int cols
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
     tc::st8(ta + (uint32_t)q, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+  }
+  tc::wait_st();
+}
+
+// What not every row of an item sees (tree_finite.cuh), and which of its tiles hold such
+// positions: j >= tree or j < edge.
+__device__ __forceinline__ TreePartial tree_partial(const MqParams &p, const MqSeg &sg) {
+  const int start = sg.ctx - sg.n;
+  return TreePartial{sg.first, p.window > 0 ? start + p.q_len - p.window : 0, start};
+}
+struct PartialTiles {
+  int tree, edge;
+  __device__ __forceinline__ bool has(int j) const { return j >= tree || j < edge; }
+};
+__device__ __forceinline__ PartialTiles partial_tiles(const MqParams &p, const MqSeg &sg) {
+  const TreePartial t = tree_partial(p, sg);
+  return PartialTiles{max(t.start, 0) / 128 - sg.j_first, t.edge > 0 ? (t.edge - 1) / 128 + 1 - sg.j_first : 0};
+}
+// Adds the elements of the item's noted V rows that are not finite to O, for the rows that
+// see them: columns col0 .. col0 + D / 2 - 1, at ta.  Warp-wide.
+template <class T, int D>
+static __device__ __noinline__ void add_spoiled(const TreeTileParams &tp, uint32_t ta, int b, int h, int start, int first,
+                                                uint64_t nodes, uint64_t edges, uint64_t mask, int lo, int col0) {
+  const MqParams &p = tp.m;
+#pragma unroll 1
+  for (int edge = 0; edge < 2; ++edge) {
+#pragma unroll 1
+    for (uint64_t m = edge ? edges : nodes; m; m &= m - 1) {
+      const int bit = __ffsll((long long)m) - 1, pos = (edge ? first : start) + bit;
+      const bool sees = edge ? pos >= lo : ((mask >> bit) & 1) != 0;
+      const int64_t blk = __ldg(p.block_table + (size_t)b * p.max_blocks + pos / kBlock);
+      const size_t row = ((size_t)(blk * p.Hkv + h) * kBlock + pos % kBlock) * D + col0;
+#pragma unroll 1
+      for (int q = 0; q < D / 2; q += 8) {
+        uint32_t o[8];
+        tc::ld8(ta + (uint32_t)q, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = nonfinite_value<T>(tp.v_cache, row + q + e);
+          if (sees) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+        }
+        tc::st8(ta + (uint32_t)q, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+      }
+    }
   }
   tc::wait_st();
 }

@@ -21,6 +21,7 @@ constexpr int kUncutTiles = 2 * kSnapTiles + 1;  // items of up to this many til
 struct TreeCut;
 struct TreeTileParams {
   MqParams m;     // part_o / part_lse sized for this kernel (tree_tiles_ws_layout)
+  const void *v_cache;
   uint8_t *cta_status;  // WsHeader::cta_status if no item can be cut (no merge follows), else null
   TreeCut *cuts;  // [groups] workspace (MqWsLayout's `prefix`)
   int D;

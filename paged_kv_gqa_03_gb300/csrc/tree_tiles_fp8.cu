@@ -96,6 +96,22 @@ __device__ __forceinline__ void mma_s_tile_e4m3(uint32_t dS, uint32_t q0, uint32
 
 // The widening warps' part of one tile: chunk i = t, t + 64, ...; rows at or past
 // `zero_from` (stale positions past the context) become zeros.
+// (tree_finite.cuh) The same chunks of the rows that not every row sees, positions kv0 + r < ctx:
+// what is NaN becomes 0, noted in `spoiled`.
+template <class Cfg>
+__device__ __forceinline__ void clean_raw_tile(uint8_t *raw, int kv0, int ctx, TreePartial t, int thread, unsigned long long *spoiled) {
+  constexpr int CPR = Cfg::D / 16;
+#pragma unroll 1
+  for (int i = thread; i < Cfg::N * CPR; i += Cfg::WIDENERS) {
+    const int r = i / CPR, pos = kv0 + r;
+    if (pos < ctx && t.holds(pos) && clear_nonfinite<E4M3>(smem_u32(raw) + raw_off<Cfg::D>(r, i % CPR))) {
+      TreeSpoiled s{0, 0};
+      s.note(t, pos);
+      if (s.nodes) atomicOr(&spoiled[0], (unsigned long long)s.nodes);
+      if (s.edge) atomicOr(&spoiled[1], (unsigned long long)s.edge);
+    }
+  }
+}
 template <class Cfg>
 __device__ __forceinline__ void widen_tile(const uint8_t *raw, uint8_t *op, int zero_from, int t) {
   constexpr int CPR = Cfg::D / 16;                       // chunks per row
@@ -201,6 +217,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
   __shared__ float red[2][2][Cfg::M];
   __shared__ float red_l[2][Cfg::M];
+  // [item parity][nodes, window's edge], and what the widening warps noted of a V slot's tile
+  __shared__ __align__(16) unsigned long long spoiled[2][2], slot_spoiled[Cfg::VSTAGES][2];
   // per tile, by block: {k_b, log2 v_b, 1 / v_b, 0}, or {1, 0, 1, 1} and {k_b, v_b}
   // in `literal` for scales that are not positive finite numbers
   __shared__ __align__(16) float4 scales[Cfg::SCALES][Cfg::BLOCKS];
@@ -242,6 +260,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     mbar_init(&o_free, Cfg::SOFTMAX / 32);
     mbar_init(&xl, Cfg::SOFTMAX / 32);
     mbar_init(&fin, 2);  // one commit from each issuing warp
+    for (int s = 0; s < Cfg::VSTAGES; ++s) slot_spoiled[s][0] = slot_spoiled[s][1] = 0;
     fence_barrier_init();
     abort_flag = 0;
     cta_flags = 0;
@@ -374,7 +393,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
     MqSeg sg{};
     int g = 0;
-    while (ok && next_item(wk, sg))
+    while (ok && next_item(wk, sg)) {
+      const PartialTiles part = partial_tiles(p, sg);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int rs = g % Cfg::VRAW, os = g % Cfg::VSTAGES;
         ok = warp_wait(&r_full[rs], (uint32_t)(g / Cfg::VRAW) & 1u, p.timeout_ns);
@@ -384,6 +404,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           ok = false;
           break;
         }
+        if (part.has(j))
+          clean_raw_tile<Cfg>(sR + (size_t)rs * Cfg::RAW_BYTES, (sg.j_first + j) * Cfg::N, sg.ctx, tree_partial(p, sg), t,
+                              slot_spoiled[os]);
         widen_tile<Cfg>(sR + (size_t)rs * Cfg::RAW_BYTES, sV + (size_t)os * Cfg::KV_BYTES,
                         sg.ctx - (sg.j_first + j) * Cfg::N, t);
         fence_proxy_async();
@@ -393,6 +416,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           mbar_arrive(&v_full[os]);
         }
       }
+    }
     if (!ok) fail();
   } else if (warp == Cfg::ISSUER) {
     // ---------------- S issue: in tile order as K lands ----------------
@@ -431,12 +455,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
       if (si > 0) ok = warp_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
+      if (lane < 2) spoiled[si & 1][lane] = 0;  // (last used two items ago, whose O was read out)
+      const PartialTiles part = partial_tiles(p, sg);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int vs = g % Cfg::VSTAGES, sb = g % Cfg::SBUF;
         ok = warp_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
+        if (ok && part.has(j) && lane < 2) {
+          spoiled[si & 1][lane] |= slot_spoiled[vs][lane];
+          slot_spoiled[vs][lane] = 0;
+        }
         if (ok) ok = warp_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
+        __syncwarp();
         if (lane == 0) {
           mma_pv_tile<Cfg>(tbase + Cfg::COL_O, tbase + (uint32_t)(sb * Cfg::N), smem_u32(sV + (size_t)vs * Cfg::KV_BYTES),
                            j > sg.j0);
@@ -604,6 +635,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       tc::fence_after();
       const float lt = l + red_l[half ^ 1][row];
       const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing gives 0 (and a NaN stays one)
+      const ulonglong2 sp = *reinterpret_cast<const ulonglong2 *>(spoiled[si & 1]);
+      if (sp.x | sp.y)
+        add_spoiled<E4M3, Cfg::D>(tp, tbase + lane_base + Cfg::COL_O + (uint32_t)(half * OC), sg.b, sg.h, start, sg.first, sp.x,
+                                                 sp.y, mask, lo, half * OC);
       uint32_t o[OC / 32][32];
 #pragma unroll
       for (int q = 0; q < OC / 32; ++q)

@@ -1,12 +1,14 @@
 """paged_tree_attention against its definition in 64 bits, through the binding:
 types, head layouts, tree shapes, lengths, masks, windows, and the calls around
 it (streams, graphs, status)."""
+import copy
+
 import numpy as np
 import pytest
 import torch
 
 from gpu_helpers import routes
-from tree_reference import Inputs, check_attention, masks_of, to_i64
+from tree_reference import Inputs, attention, check_attention, masks_of, to_i64
 
 pytestmark = pytest.mark.gpu
 
@@ -323,3 +325,73 @@ def test_small_and_wide_trees_one_after_another(dtype, D):
     ctx = [max(m, int(rng.choice([50, 128, 300]))) for m in nodes]
     with routes(tree="tiles"):
         _run(Inputs(51, ctx, n, 3, 3, D, dtype, nodes=nodes))
+
+
+def _spoil(x, b, pos, h, cols, values):
+    """V elements of a position that are not finite."""
+    blk = int(x.table[b, pos // 16])
+    if x.dtype == "fp8_e4m3":
+        x.vc.view(torch.uint8)[blk, h, pos % 16, cols] = torch.tensor([0x7F, 0xFF] * len(cols), dtype=torch.uint8)[:len(cols)]
+    else:
+        x.vc[blk, h, pos % 16, cols] = torch.tensor([values[i % len(values)] for i in range(len(cols))], dtype=x.vc.dtype)
+
+
+def _check_spoiled(out, x, window=0):
+    with np.errstate(invalid="ignore"):
+        ref, _ = attention(x, window)
+    c = copy.copy(x)                                  # the bound of the other elements
+    c.vc = torch.where(torch.isfinite(x.vc.float()), x.vc.float(), 0.0).to(x.vc.dtype)
+    _, bound = attention(c, window)
+    got = out.double().cpu().numpy()
+    wild = ~np.isfinite(ref)
+    assert wild.any() and not wild.all()
+    for b in range(x.B):
+        m = x.nodes[b]
+        g, r, w = got[b, :m], ref[b, :m], wild[b, :m]
+        assert np.array_equal(np.isnan(g[w]), np.isnan(r[w])) and np.array_equal(g[w] > 0, r[w] > 0)
+        err = np.abs(g[~w] - r[~w])
+        assert (err <= bound[b, :m][~w]).all(), f"sequence {b}: {int((~(err <= bound[b, :m][~w])).sum())} of {err.size}"
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 6), ("bf16", 16, 1, 128, 40), ("f16", 4, 2, 64, 9), ("f16", 4, 4, 128, 33),
+                                              ("fp8_e4m3", 8, 2, 128, 6), ("fp8_e4m3", 4, 1, 64, 40), ("f32", 4, 2, 64, 9),
+                                              ("f32", 2, 1, 128, 5)])
+def test_values_that_are_not_finite_stay_in_their_branch(route, dtype, Hq, Hkv, D, n):
+    """Infinities and NaN in the V rows of some nodes: rows that see such a node
+    get what the formula gives, element by element; the others nothing of it."""
+    inf, nan = float("inf"), float("nan")
+    with routes(tree=route):
+        x = Inputs(61, [n, n + 7, 130 + n, 128, 2000], n, Hq, Hkv, D, dtype, nodes=[n, n, n, max(2, n // 2), n])
+        for b in range(x.B):
+            start, m = x.ctx[b] - x.nodes[b], x.nodes[b]
+            for k, node in enumerate((1, m - 1, m // 2)):
+                for h in range(Hkv):
+                    _spoil(x, b, start + node, h, [k, 7 + k, D // 2 + 5 * k, D - 1 - k], (inf, nan, -inf, inf))
+        out, _ = _call(x)
+        _check_spoiled(out, x)
+        again, _ = _call(x)
+        assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,n", [("bf16", 8, 2, 128, 7), ("f16", 16, 1, 64, 40), ("fp8_e4m3", 8, 2, 128, 7),
+                                              ("fp8_e4m3", 4, 1, 64, 40), ("f32", 4, 2, 64, 7)])
+@pytest.mark.parametrize("window", [5, 30, 200])
+def test_values_that_are_not_finite_at_a_windows_edge(route, dtype, Hq, Hkv, D, n, window):
+    """Cached positions before every row's window may hold anything; one that the
+    windows of some rows have left touches only those that still see it."""
+    inf, nan = float("inf"), float("nan")
+    with routes(tree=route):
+        x = Inputs(62, [n + 3, 130 + n, 517, 2000], n, Hq, Hkv, D, dtype)
+        for b in range(x.B):
+            start = x.ctx[b] - n
+            first = max(0, start + 1 - window)
+            for h in range(Hkv):
+                for pos in range(first // 16 * 16, first):        # no row sees them
+                    _spoil(x, b, pos, h, list(range(D)), (nan, inf))
+                # (a position that every row sees has to be finite)
+                for k, pos in enumerate(range(first, min(start + n - window, first + 3))):
+                    _spoil(x, b, pos, h, [3 * k, D - 1 - k], (inf, nan))
+        out, _ = _call(x, window)
+        _check_spoiled(out, x, window)
