@@ -205,8 +205,9 @@ class DecodeStep:
         key = ("append", k_new.data_ptr(), v_new.data_ptr(), self.d_slots.data_ptr())
         call = self._calls.get(key)
         if call is None:
-            k_new = k_new.view(-1, self.Hkv, self.D)
-            v_new = v_new.view(-1, self.Hkv, self.D)
+            if k_new.dim() == 4:
+                k_new = k_new.view(-1, self.Hkv, self.D)
+                v_new = v_new.view(-1, self.Hkv, self.D)
             call = self._remember(key, paged_kv_append(
                 k_new, v_new, self.k_cache, self.v_cache, self.d_slots, self.k_scale, self.v_scale,
                 stream=s, calibrated=self.calibrated, prepare=True))
