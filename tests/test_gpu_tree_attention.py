@@ -395,3 +395,54 @@ def test_values_that_are_not_finite_at_a_windows_edge(route, dtype, Hq, Hkv, D, 
                     _spoil(x, b, pos, h, [3 * k, D - 1 - k], (inf, nan))
         out, _ = _call(x, window)
         _check_spoiled(out, x, window)
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("dtype,blocks", [("bf16", 140000), ("fp8_e4m3", 280000)])
+def test_caches_beyond_32_bit_offsets(route, dtype, blocks):
+    """Blocks whose bytes and elements lie past 2^32 and 2^31 of the cache."""
+    pkv, dev = _pkv(), "cuda"
+    Hq, Hkv, D, n = 16, 8, 128, 6
+    assert blocks * Hkv * 16 * D * (1 if dtype == "fp8_e4m3" else 2) > 2 ** 32 and blocks * Hkv * 16 * D > 2 ** 31
+    x = Inputs(71, [300, 77, n], n, Hq, Hkv, D, dtype)
+    ids = torch.arange(x.num_blocks, device=dev) + (blocks - x.num_blocks)
+    ids[::3] = torch.arange(len(ids[::3]), device=dev)          # some at the front as well
+    big = []
+    for c in (x.kc, x.vc):
+        t = torch.empty((blocks,) + tuple(c.shape[1:]), dtype=torch.uint8 if dtype == "fp8_e4m3" else c.dtype, device=dev)
+        t[ids] = (c.view(torch.uint8) if dtype == "fp8_e4m3" else c).to(dev)
+        big.append(t.view(c.dtype))
+    scales = [None, None]
+    if dtype == "fp8_e4m3":
+        scales = [torch.ones((blocks, Hkv), device=dev).index_copy_(0, ids, s.to(dev)) for s in (x.ks, x.vs)]
+    table = torch.from_numpy(x.table).to(dev)
+    table = torch.where(table >= 0, ids[table.clamp(min=0).long()].int(), table)
+    out = torch.empty(x.q.shape, dtype=x.q.dtype, device=dev)
+    with routes(tree=route):
+        ws = pkv.paged_tree_attention(out, x.q.to(dev), *big, table, torch.tensor(x.ctx, dtype=torch.int32, device=dev),
+                                      x.mask.to(dev), x.scale, k_scale=scales[0], v_scale=scales[1])
+    assert pkv.paged_decode_status(ws) == (0, 0)
+    check_attention(out, x)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, over one cache."""
+    pkv, dev = _pkv(), "cuda"
+    for dtype, Hq, n in (("bf16", 16, 40), ("fp8_e4m3", 8, 6), ("bf16", 4, 3)):
+        x = Inputs(81, [3000, 45, 1280, 700], n, Hq, 2, 128, dtype)
+        up = lambda t: None if t is None else t.to(dev)  # noqa: E731
+        a = [up(t) for t in (x.q, x.kc, x.vc, torch.from_numpy(x.table), torch.tensor(x.ctx, dtype=torch.int32), x.mask)]
+        ks, vs = up(x.ks), up(x.vs)
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs = [[torch.full_like(a[0], 7.0) for _ in range(6)] for _ in streams]
+        nbytes = pkv.paged_tree_workspace_bytes(x.B, n, Hq, 2, 128, x.kc.dtype, x.q.dtype)
+        works = [torch.empty(nbytes, dtype=torch.uint8, device=dev) for _ in streams]
+        torch.cuda.synchronize()
+        for k in range(6):
+            for s, o, w in zip(streams, outs, works):
+                pkv.paged_tree_attention(o[k], *a, x.scale, k_scale=ks, v_scale=vs, workspace=w, stream=s)
+        torch.cuda.synchronize()
+        check_attention(outs[0][0], x)
+        for o in outs:
+            for t in o:
+                assert torch.equal(t, outs[0][0])

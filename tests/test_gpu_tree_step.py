@@ -179,3 +179,71 @@ def test_refusals():
     with pytest.raises(MemoryError):               # 62 + 4 tokens do not fit 4 blocks
         step.prepare([1, 3, 5, 9])
     assert step.bm.export([0], 4)[1].tolist() == [62]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_a_step_captured_into_a_graph(dtype):
+    """Append, attention, verification and commit as one graph, replayed on
+    other inputs in the same buffers: the bits of the eager step."""
+    from paged_kv_gqa_03_gb300.step import TreeStep
+    dev, n, Hq, Hkv, D, V, B = "cuda", 9, 8, 2, 128, 1000, 3
+    g, rng = torch.Generator().manual_seed(4), np.random.default_rng(4)
+    fp8 = dtype == torch.float8_e4m3fn
+    raw = [torch.randn(40, Hkv, 16, D, generator=g).to(dtype).to(dev) for _ in range(2)]
+    kc, vc = (t.clone() for t in raw)
+    sc = [torch.full((40, Hkv), 0.01, device=dev) for _ in range(2)] if fp8 else [None, None]
+    st = torch.cuda.Stream()
+    step = TreeStep(kc, vc, Hq, torch.bfloat16, 16, n, *sc, stream=st)
+    step.seqs = [0, 1, 2]
+    for seq, length in zip(step.seqs, (100, 7, 32)):
+        assert step.bm.allocate(seq, length)
+    parents = [random_parents(n, rng) for _ in range(B)]
+    step.prepare(torch.stack([to_i64(masks_of(p)) for p in parents]).numpy(), [n, 4, n])
+    step.upload()
+    mk = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    buf = [mk(B, n, Hq, D).bfloat16().to(dev), mk(B, n, Hkv, D).bfloat16().to(dev), mk(B, n, Hkv, D).bfloat16().to(dev)]
+    target, draft, tokens, u = (t.to(dev) for t in _drafts(rng, g, B, n, V, True, parents))
+    out = torch.empty_like(buf[0])
+
+    def body():
+        step.launch(*buf, out)
+        step.verify(tokens, target, draft, u)
+        step.commit()
+
+    def reset():
+        for c, r in zip((kc, vc), raw):
+            c.view(torch.uint8).copy_(r.view(torch.uint8))
+        for s in sc:
+            if s is not None:
+                s.fill_(0.01)
+        torch.cuda.synchronize()
+
+    def results():
+        st.synchronize()
+        return [t.clone().view(torch.uint8) for t in (out, step.d_path, step.d_path_len, step.d_next_token, step.d_new_lens, kc, vc)]
+
+    inputs = []
+    for _ in range(3):
+        t, d, k, x = _drafts(rng, g, B, n, V, True, parents)
+        inputs.append([mk(B, n, Hq, D).bfloat16(), mk(B, n, Hkv, D).bfloat16(), mk(B, n, Hkv, D).bfloat16(), t, d, k, x])
+
+    def fill(values):
+        for b, v in zip(buf + [target, draft, tokens, u], values):
+            b.copy_(v)
+        reset()
+
+    eager = []
+    for values in inputs:
+        fill(values)
+        body()
+        eager.append(results())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        body()
+    for values, want in zip(inputs, eager):
+        fill(values)
+        with torch.cuda.stream(st):
+            graph.replay()
+        for a, b in zip(results(), want):
+            assert torch.equal(a, b)
+    assert any(not torch.equal(a, b) for a, b in zip(eager[0], eager[1]))

@@ -244,3 +244,29 @@ def test_commit_large_batch_and_graph():
     torch.cuda.synchronize()
     for got, ref in zip((kc, vc), commit(x, path, length)):
         assert np.array_equal(got.view(torch.uint8).cpu().numpy().reshape(ref.shape), ref)
+
+
+@pytest.mark.parametrize("dtype,blocks", [("bf16", 140000), ("fp8_e4m3", 280000)])
+def test_commit_beyond_32_bit_offsets(dtype, blocks):
+    """Rows whose bytes lie past 2^32 of the cache."""
+    pkv, dev = _pkv(), "cuda"
+    Hkv, D, n = 8, 128, 40
+    x = Inputs(91, [n + 11, 700], n, 8, Hkv, D, dtype, stale=False)
+    path, length = _paths(x, 3, 12)
+    ids = torch.arange(x.num_blocks, device=dev) + (blocks - x.num_blocks)
+    raw, big = [], []
+    for c in (x.kc, x.vc):
+        t = torch.empty((blocks,) + tuple(c.shape[1:]), dtype=torch.uint8 if dtype == "fp8_e4m3" else c.dtype, device=dev)
+        t[ids] = (c.view(torch.uint8) if dtype == "fp8_e4m3" else c).to(dev)
+        raw.append(t)
+        big.append(t.view(c.dtype))
+    scales = [None, None]
+    if dtype == "fp8_e4m3":
+        scales = [torch.ones((blocks, Hkv), device=dev).index_copy_(0, ids, s.to(dev)) for s in (x.ks, x.vs)]
+    table = torch.from_numpy(x.table).to(dev)
+    table = torch.where(table >= 0, ids[table.clamp(min=0).long()].int(), table)
+    pkv.paged_tree_commit(*big, torch.as_tensor(path, dtype=torch.int32).to(dev), torch.as_tensor(length, dtype=torch.int32).to(dev), table,
+                          torch.tensor(x.ctx, dtype=torch.int32, device=dev), k_scale=scales[0], v_scale=scales[1])
+    for t, want in zip(raw, commit(x, path, length)):
+        got = t[ids].contiguous().view(torch.uint8).cpu().numpy().reshape(want.shape)
+        assert np.array_equal(got, want)
