@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   __shared__ __align__(8) uint64_t xch[Cfg::SOFTMAX / 64][2];
   __shared__ float red[2][2][Cfg::M];
   __shared__ float red_l[2][Cfg::M];
+  __shared__ TreeItem items[4];
+  __shared__ __align__(8) uint64_t item_full[4];
   __shared__ __align__(16) unsigned long long spoiled[2][2];  // [item parity][nodes, window's edge]
   __shared__ TreeFind find;
   __shared__ uint32_t tmem_base;
@@ -135,6 +137,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       mbar_init(&xch[pr][0], 2);
       mbar_init(&xch[pr][1], 2);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mbar_init(&item_full[i], 1);
     mbar_init(&q_full, Cfg::SOFTMAX / 32);
     mbar_init(&o_free, Cfg::SOFTMAX / 32);
     mbar_init(&xl, Cfg::SOFTMAX / 32);
@@ -249,9 +253,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool ok = true;
     MqWalk wk;
     wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
-    MqSeg sg{};
+    MqSeg sg{}, nx{};
     int g = 0;
-    for (int si = 0; ok && next_item(wk, sg); ++si) {
+    auto publish = [&](int k, const MqSeg &s, bool have) {
+      if (lane == 0) {
+        items[k & 3] = TreeItem{s, have ? 1 : 0};
+        mbar_arrive(&item_full[k & 3]);
+      }
+      __syncwarp();
+    };
+    bool have = next_item(wk, nx);
+    publish(0, nx, have);
+    for (int si = 0; ok && have; ++si) {
+      sg = nx;
+      have = next_item(wk, nx);
+      publish(si + 1, nx, have);
       ok = tile_wait(&q_full, (uint32_t)si & 1u, p.timeout_ns);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int ks = g % Cfg::KSTAGES, sb = g % Cfg::SBUF;
@@ -342,22 +358,24 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
     };
-    MqWalk wk;
-    wk.start(rg.b0, rg.base0, rg.t0, rg.t1);
-    MqSeg sg{}, nx{};
-    bool have = next_item(wk, sg);
-    if (have) stage_q(sg);
+    bool ok = true;
+    auto next = [&](int k) -> bool {  // waits until item k is published; whether there is one
+      ok = tile_wait(&item_full[k & 3], (uint32_t)(k >> 2) & 1u, p.timeout_ns);
+      return ok && items[k & 3].have != 0;
+    };
+    bool have = next(0);
+    if (have) stage_q(items[0].s);
     if (rt == 0 && tid == 0) {  // (rt 0 has rows in every item with any)
       TreeCut cut{rg.t0, 0, 0, 0, 0};
+      const MqSeg &sg = items[0].s;
       if (have && sg.j0 > 0) cut = TreeCut{rg.t0, sg.b, sg.h, rg.t0 - sg.j0, rg.t0 - sg.j0 + sg.T};
       tp.cuts[group] = cut;
     }
-    bool nhave = have && next_item(wk, nx);
     if (have) release_q();
-    bool ok = true;
     int g = 0, si = 0, xn = 0;  // tiles and items so far, exchanges of this warp (none in tiles without its rows)
     while (have && ok) {
-      const int n = sg.j1 - sg.j0;
+      const MqSeg &sg = items[si & 3].s;
+      const int n = sg.j1 - sg.j0, tile0 = sg.j_first + sg.j0;
       // what this row sees: [lo, start), then node t at start + t iff bit t of mask
       const bool live = node < sg.n;
       const bool dead = rt * Cfg::M + (warp & 3) * 32 >= sg.n * p.G;  // no live row in this warp (nor in the one that shares its rows)
@@ -376,7 +394,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (!ok) break;
         tc::fence_after();
         // the item's last S has read Q: the next item's may come in
-        if (j + 1 == n && nhave) stage_q(nx);
+        if (j + 1 == n) {
+          have = next(si + 1);
+          if (!ok) break;
+          if (have) stage_q(items[(si + 1) & 3].s);
+        }
         if (dead) {  // (rows past the nodes: their P and O are never looked at)
           tc::fence_before();
           __syncwarp();
@@ -384,7 +406,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           continue;
         }
         const uint32_t scol = tbase + lane_base + (uint32_t)(sb * Cfg::N + half * SC);
-        const int kvh = (sg.j_first + sg.j0 + j) * Cfg::N + half * SC;  // first position of this half
+        const int kvh = (tile0 + j) * Cfg::N + half * SC;  // first position of this half
         if (kvh + SC > start || kvh < lo_all)  // (warp-uniform) the tree or a window's edge is in these columns
           fix_scores(scol, tree_columns(mask, start, lo, kvh), nullptr, 0);
         uint32_t s[SC];
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (lane == 0) mbar_arrive(&p_full[sb]);
       }
       if (!ok) break;
-      if (nhave) release_q();
+      if (have) release_q();  // (the next item's)
       // ---- epilogue of the item: O / l, or a normalised partial and its lse ----
       const int gl = g + n - 1;
       ok = tile_wait(&pv_done[gl % Cfg::SBUF], (uint32_t)(gl / Cfg::SBUF) & 1u, p.timeout_ns);
@@ -482,9 +504,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       g += n;
       ++si;
-      sg = nx;
-      have = nhave;
-      nhave = have && next_item(wk, nx);
     }
     if (ok) {  // sequences with rows but no tile (an empty context): zeros, sequence b by CTA b mod grid
       for (int b = blockIdx.x; b < p.B; b += gridDim.x) {

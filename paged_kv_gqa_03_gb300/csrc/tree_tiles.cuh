@@ -163,6 +163,15 @@ static __device__ __noinline__ void rescale_o(uint32_t ta, float alpha, int cols
   tc::wait_st();
 }
 
+// The items of a CTA as its S-issuing warp publishes them for the softmax warps, one item ahead
+// (four entries: the softmax may still write an item's output while the one after the
+// next is published).  Kept in shared memory, they cost the tile loop no registers, which
+// are what it is short of.
+struct TreeItem {
+  MqSeg s;
+  int have;  // 0: past the last
+};
+
 // What not every row of an item sees (tree_finite.cuh), and which of its tiles hold such
 // positions: j >= tree or j < edge.
 __device__ __forceinline__ TreePartial tree_partial(const MqParams &p, const MqSeg &sg) {
