@@ -786,7 +786,7 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
 //     38, 39, 8 x 8192 45, 58 / 57, 57, 64 x 500 32, 56 / 52, 16 x 8192 63, 81 /
 //     93, 94.
 // Above, the tiles everywhere: 16-bit D = 128, 16 x 8192, 16 rows 117 / 98; D =
-// 64, 16 x 4096, 16 rows 56 / 54; fp8 16 x 8192, 32 rows 132 / 95.
+// 64, 16 x 4096, 16 rows 56 / 54; fp8 16 x 8192, 32 rows 132 / 89.
 static bool tree_tiles_apply(int cache_dtype, int B) {
   return cache_dtype != PKV_F32 && B <= kMqMaxBatch;
 }

@@ -25,17 +25,18 @@
 // What bounds it.  Up to about 64 rows per kv head, the K / V bytes: 64 / 8 heads,
 // 16 x 8192, 1 - 8 nodes 98 - 100 us (5.4 TB/s with ~11 us of start, first tile and
 // merge), 32 x 8192, 1 - 4 nodes 176 us (6.1 TB/s); DRAM reads are 1.002 - 1.005 times
-// the bytes.  With full tiles about 2400 clocks a tile: its MMAs are 1536 (bf16: P's high parts
+// the bytes.  With full tiles about 2250 clocks a tile: its MMAs are 1536 (bf16: P's high parts
 // and residuals are two products; f16 1024), its operands and copies 192 KiB of
-// shared memory traffic, 1536 clocks too, and the eight softmax warps issue 41% of the
-// time (one sequence of 131072, 26 nodes: 158 us, tensor pipe 58% active; 32 x 8192, 64
-// nodes: 600 us, 915 TFLOP/s as the formula counts them and 1370 as issued, near the board's
-// power limit).  Measured beside it and slower or equal (157
-// and 591 then): a second group of softmax
-// warps taking every other tile (152 and 563 - 600 us for those two, but 106 against 97
-// for 24 x 512 - 2048 with 32 heads), two groups with S and O of their own (188 and 717), part
-// of the 2^x as polynomials on the FMA pipes (153 and 581; f16 100 against 97), deeper
-// rings at head dim 64 (equal).
+// shared memory traffic, 1536 clocks too, and the eight softmax warps issue over 40% of the
+// time (one sequence of 131072, 26 nodes: 150 us, tensor pipe 60% active; 32 x 8192, 64
+// nodes: 562 us, 980 TFLOP/s as the formula counts them and 1460 as issued, near the board's
+// power limit).  The tile loop is short of registers: with every softmax thread walking the
+// items by itself it spilled and these two took 159 and 604 us.  Measured against that
+// version, at 157 and 591 us without the check of V, and slower or equal: a second group of
+// softmax warps taking every other tile (152 and 563 - 600, but 106 against 97 for 24 x
+// 512 - 2048 with 32 heads), two groups with S and O of their own (188 and 717), part of the
+// 2^x as polynomials on the FMA pipes (153 and 581; f16 100 against 97), deeper rings at head
+// dim 64 (equal).
 #include "prefill_common.cuh"
 #include "tree_tiles.cuh"
 

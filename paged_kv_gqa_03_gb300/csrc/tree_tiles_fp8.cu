@@ -23,11 +23,11 @@
 // element is multiplied by a scale at all.  A tile with a scale that is not a
 // positive finite number takes the literal products instead.
 //
-// What bounds it: a tile takes ~1.25 us (head dim 128) against 0.73 for its bytes from
+// What bounds it: a tile takes ~1.2 us (head dim 128) against 0.73 for its bytes from
 // HBM and 0.7 for its 176 KiB of shared-memory traffic: the softmax of a lane quarter,
-// whose two warps share one scheduler, is 2270 clocks long (1100 of them the weights, 350 the
-// exchange of maxima, 290 the block scales).  16 x 32768, 32 / 8 heads, 8 nodes 290 us (3.7
-// TB/s); 16 x 8192, 64 nodes 165 us (830 TFLOP/s).  Tried and slower: widening K as well (2.1
+// whose two warps share one scheduler, is ~2200 clocks long (1100 of them the weights, 350 the
+// exchange of maxima, 290 the block scales).  16 x 32768, 32 / 8 heads, 8 nodes 275 us (3.9
+// TB/s); 16 x 8192, 64 nodes 157 us (880 TFLOP/s).  Tried and slower: widening K as well (2.1
 // us a tile), one K stage less (64 nodes 187), the rows of a small tree copied into all
 // four lane quarters, each taking every fourth tile (2.0 us a tile: the others' weights have to
 // be cleared).
