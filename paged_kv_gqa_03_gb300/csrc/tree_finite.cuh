@@ -57,7 +57,6 @@ __device__ __forceinline__ float nonfinite_value(const void *cache, size_t i) {
 // before `first` no row sees) and the tree's, from `start` on.
 struct TreePartial {
   int first, edge, start;
-  __device__ __forceinline__ bool touches(int pos, int count) const { return pos + count > start || pos < edge; }
   __device__ __forceinline__ bool holds(int pos) const { return pos >= start || pos < edge; }
 };
 // Such positions with elements that are not finite, as bits: node `bit`, or position
