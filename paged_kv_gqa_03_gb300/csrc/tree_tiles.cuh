@@ -105,12 +105,15 @@ __device__ __forceinline__ uint64_t tree_columns(uint64_t mask, int start, int l
 }
 
 // warp_wait (prefill_common.cuh) with all but its first try out of line: the tile
-// loops hold many waits, and most are over when they are reached.
+// loops hold many waits, and most are over when they are reached.  ROLE: a copy for
+// warps with another register count (setmaxnreg).
+template <int ROLE>
 static __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
   return warp_wait(bar, parity, limit_ns);
 }
+template <int ROLE = 0>
 __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(kFull, mbar_try_wait(bar, parity)) || wait_longer(bar, parity, limit_ns);
+  return __all_sync(kFull, mbar_try_wait(bar, parity)) || wait_longer<ROLE>(bar, parity, limit_ns);
 }
 
 // What a softmax warp does to its 64 columns of a tile's S, P or its half of O only

@@ -198,6 +198,17 @@ __device__ __noinline__ float stage_q_parts(const uint4 *src, uint32_t q0, int r
   return finite ? ldexpf(1.f, -sh) : __int_as_float(0x7fc00000);
 }
 
+// A wait of the warps beside the softmax: its slow part out of line (tile_wait) at head
+// dim 64, where the widening loop's instruction fetch counts (64 x 4096, 16 nodes 150 us, inline
+// 166), inline at 128 (16 x 8192, 64 nodes 156 us, out of line 162).
+template <class Cfg>
+__device__ __forceinline__ bool other_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if constexpr (Cfg::D == 64)
+    return tile_wait<1>(bar, parity, limit_ns);
+  else
+    return warp_wait(bar, parity, limit_ns);
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tree_tile_fp8_kernel(const __grid_constant__ TreeTileParams tp, const __grid_constant__ CUtensorMap tmK,
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       load_scales(f1);
       const int y = (int)(row_of(f0) * lines);
       const int s = g % stages;
-      if (g >= stages) ok = warp_wait(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
+      if (g >= stages) ok = other_wait<Cfg>(&empty[s], (uint32_t)((g / stages) - 1) & 1u, p.timeout_ns);
       if (!ok || aborted()) {
         ok = false;
         break;
@@ -401,9 +412,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const PartialTiles part = partial_tiles(p, sg);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int rs = g % Cfg::VRAW, os = g % Cfg::VSTAGES;
-        ok = warp_wait(&r_full[rs], (uint32_t)(g / Cfg::VRAW) & 1u, p.timeout_ns);
+        ok = other_wait<Cfg>(&r_full[rs], (uint32_t)(g / Cfg::VRAW) & 1u, p.timeout_ns);
         // the operand slot is free once P . V of tile g - VSTAGES has read it
-        if (ok && g >= Cfg::VSTAGES) ok = warp_wait(&v_empty[os], (uint32_t)((g / Cfg::VSTAGES) - 1) & 1u, p.timeout_ns);
+        if (ok && g >= Cfg::VSTAGES) ok = other_wait<Cfg>(&v_empty[os], (uint32_t)((g / Cfg::VSTAGES) - 1) & 1u, p.timeout_ns);
         if (!ok || aborted()) {
           ok = false;
           break;
@@ -442,13 +453,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       sg = nx;
       have = next_item(wk, nx);
       publish(si + 1, nx, have);
-      ok = warp_wait(&q_full, (uint32_t)si & 1u, p.timeout_ns);
+      ok = other_wait<Cfg>(&q_full, (uint32_t)si & 1u, p.timeout_ns);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int ks = g % Cfg::KSTAGES, sb = g % Cfg::SBUF;
-        ok = warp_wait(&k_full[ks], (uint32_t)(g / Cfg::KSTAGES) & 1u, p.timeout_ns);
+        ok = other_wait<Cfg>(&k_full[ks], (uint32_t)(g / Cfg::KSTAGES) & 1u, p.timeout_ns);
         // S overwrites the buffer whose P . V of tile g - SBUF read P from it
         if (ok && g >= Cfg::SBUF)
-          ok = warp_wait(&pv_done[sb], (uint32_t)((g / Cfg::SBUF) - 1) & 1u, p.timeout_ns);
+          ok = other_wait<Cfg>(&pv_done[sb], (uint32_t)((g / Cfg::SBUF) - 1) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         if (lane == 0) {
@@ -470,17 +481,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     MqSeg sg{};
     int g = 0;
     for (int si = 0; ok && next_item(wk, sg); ++si) {
-      if (si > 0) ok = warp_wait(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
+      if (si > 0) ok = other_wait<Cfg>(&o_free, (uint32_t)(si - 1) & 1u, p.timeout_ns);
       if (lane < 2) spoiled[si & 1][lane] = 0;  // (last used two items ago, whose O was read out)
       const PartialTiles part = partial_tiles(p, sg);
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int vs = g % Cfg::VSTAGES, sb = g % Cfg::SBUF;
-        ok = warp_wait(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
+        ok = other_wait<Cfg>(&v_full[vs], (uint32_t)(g / Cfg::VSTAGES) & 1u, p.timeout_ns);
         if (ok && part.has(j) && lane < 2) {
           spoiled[si & 1][lane] |= slot_spoiled[vs][lane];
           slot_spoiled[vs][lane] = 0;
         }
-        if (ok) ok = warp_wait(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
+        if (ok) ok = other_wait<Cfg>(&p_full[sb], (uint32_t)(g / Cfg::SBUF) & 1u, p.timeout_ns);
         if (!ok) break;
         tc::fence_after();
         __syncwarp();
