@@ -307,7 +307,9 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
  * at or past context_lens[b].  A V element of a node (or of a position at a
  * window's edge) that is not finite gives infinity or NaN in that element of the rows that
  * see it, as the formula does; V at the positions before the tree that every
- * row sees must be finite (an infinity there may give NaN).
+ * row sees must be finite (an infinity there may give NaN).  FP8: a block scale that is
+ * not finite (its opener overflowed) gives NaN in the rows that see a position of the
+ * block, and nothing in the others.
  *
  * Kernels, all meeting the same error bound (pkv_set_route(PKV_ROUTE_TREE, ...)
  * forces one where it applies):

@@ -691,7 +691,13 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
   if (two) fp8_scores<Cfg>(st, tk1, lane, t);
 
   const uint32_t wl = (uint32_t)p.wlen;
-  const float sc0 = p.scale_log2 * m.ks, sc1 = p.scale_log2 * m.ks1;
+  float sc0 = p.scale_log2 * m.ks, sc1 = p.scale_log2 * m.ks1, vs0 = m.vs, vs1 = m.vs1;
+  if constexpr (Cfg::TREE) {
+    // a scale that is not finite (an overflowed branch opened the block): NaN for the rows
+    // that see the block, and hidden weights stay 0 (0 times infinity would be NaN)
+    if (!(fabsf(m.ks) < INFINITY && fabsf(vs0) < INFINITY)) sc0 = __int_as_float(0x7fc00000), vs0 = 0.f;
+    if (!(fabsf(m.ks1) < INFINITY && fabsf(vs1) < INFINITY)) sc1 = __int_as_float(0x7fc00000), vs1 = 0.f;
+  }
   // 16-row units: when every row of the stage is visible to every column of
   // the unit (the common case: not the last blocks of a context, no window
   // edge inside) no mask is applied — warp-uniform, from the stage's position
@@ -766,10 +772,10 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
     st.l[nh][0] += (p0 + p2) + (q0 + q2);
     st.l[nh][1] += (p1 + p3) + (q1 + q3);
     // the V scales folded into the weights
-    pa[nh][0] = movmatrix_trans(pack_f16x2(p0 * m.vs, p1 * m.vs));
-    pa[nh][1] = movmatrix_trans(pack_f16x2(p2 * m.vs, p3 * m.vs));
-    pc[nh][0] = movmatrix_trans(pack_f16x2(q0 * m.vs1, q1 * m.vs1));
-    pc[nh][1] = movmatrix_trans(pack_f16x2(q2 * m.vs1, q3 * m.vs1));
+    pa[nh][0] = movmatrix_trans(pack_f16x2(p0 * vs0, p1 * vs0));
+    pa[nh][1] = movmatrix_trans(pack_f16x2(p2 * vs0, p3 * vs0));
+    pc[nh][0] = movmatrix_trans(pack_f16x2(q0 * vs1, q1 * vs1));
+    pc[nh][1] = movmatrix_trans(pack_f16x2(q2 * vs1, q3 * vs1));
   }
   fp8_pv<Cfg>(st, tv0, lane, pa);
   if (two) fp8_pv<Cfg>(st, tv1, lane, pc);

@@ -20,8 +20,11 @@
 //   out = sum p' dec / sum p' / v_b,
 // so that the weights the tensor core takes are <= 1 whatever the scales
 // (weights times v_b would leave f16's normal range for small V), and no
-// element is multiplied by a scale at all.  A tile with a scale that is not a
-// positive finite number takes the literal products instead.
+// element is multiplied by a scale at all.  A block with a scale that is not a
+// positive finite number takes the literal products instead; one with a scale that is not
+// finite (an overflowed branch opened the block) enters as a K scale of NaN and a V
+// scale of 0, so that the rows that see it are NaN and hidden weights stay 0 (0 times
+// infinity would be NaN in every row).
 //
 // What bounds it: a tile takes ~1.2 us (head dim 128) against 0.73 for its bytes from
 // HBM and 0.7 for its 176 KiB of shared-memory traffic: the softmax of a lane quarter,
@@ -383,7 +386,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const bool plain = f0.ks > 0.f && f0.vs > 0.f && f0.ks <= 3.402823466e38f && f0.vs <= 3.402823466e38f;
         scales[g % Cfg::SCALES][lane] =
             plain ? make_float4(f0.ks, __log2f(f0.vs), __fdividef(1.f, f0.vs), 0.f) : make_float4(1.f, 0.f, 1.f, 1.f);
-        literal[g % Cfg::SCALES][lane] = make_float2(f0.ks, f0.vs);
+        const bool finite = fabsf(f0.ks) < INFINITY && fabsf(f0.vs) < INFINITY;
+        literal[g % Cfg::SCALES][lane] = finite ? make_float2(f0.ks, f0.vs) : make_float2(__int_as_float(0x7fc00000), 0.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&full[s], Cfg::RAW_BYTES);
