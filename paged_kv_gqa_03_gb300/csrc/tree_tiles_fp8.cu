@@ -563,6 +563,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         lo = p.window > 0 ? start + max(1, __popcll(mask)) - p.window : 0;
       }
       const int lo_all = p.window > 0 ? start + p.q_len - p.window : 0;  // no row's lo is above it
+      // a row that sees nothing gives 0 whatever its query holds: -inf times the factor NaN
+      // of a query that is not finite would be NaN
+      if (start <= max(lo, 0) && (start < 0 ? mask >> -start : mask) == 0) cq = 1.f;
       float m_run = -INFINITY, l = 0.f;  // l: sum of p' / v_b
       for (int j = 0; j < n; ++j) {
         const int gj = g + j, sb = gj % Cfg::SBUF;

@@ -1,4 +1,5 @@
-"""Tree attention on fp8 caches whose block scales are not ordinary numbers."""
+"""Tree attention on fp8 caches whose block scales are not ordinary numbers, and
+queries that are not."""
 import numpy as np
 import pytest
 import torch
@@ -79,3 +80,22 @@ def test_an_overflowed_draft_through_the_append():
             ref, bound = attention(x)
         assert (np.abs(got[:, :opens] - ref[:, :opens]) <= bound[:, :opens]).all()
         assert np.isnan(got[:, opens:]).all()
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("dtype,q_dtype", [("fp8_e4m3", "bf16"), ("fp8_e4m3", "f16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("window", [0, 1])
+def test_a_query_that_is_not_finite_and_sees_nothing(route, dtype, q_dtype, window):
+    """A row that sees nothing gives 0, whatever its query holds."""
+    n = 6
+    ctx = [n, n] if window == 0 else [n + 300, n + 17]       # (window 1: a node without a mask sees nothing)
+    x = Inputs(71, ctx, n, 4, 2, 128, dtype, q_dtype)
+    x.masks = [[m if i % 2 == 0 else 0 for i, m in enumerate(ms)] for ms in x.masks]
+    x.mask = torch.stack([to_i64(m) for m in x.masks])
+    x.q[:, 1, :, 3] = float("nan")
+    x.q[:, 3, :, 5] = float("inf")
+    x.q[:, 4, 1, 0] = float("nan")
+    with routes(tree=route):
+        got = _call(x, window)
+    assert (got[:, 1::2] == 0).all()
+    assert np.isnan(got[:, 4, 1]).all() and np.isfinite(got[:, [0, 2]]).all()
