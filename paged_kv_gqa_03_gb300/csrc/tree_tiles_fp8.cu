@@ -601,7 +601,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const float2 *raw = &literal[gj % Cfg::SCALES][half * NB];
         // (warp-uniform) the tree or a window's edge is in these columns
         const bool edge = kvh + SC > start || kvh < lo_all;
-        if (edge || lit) fix_scores(scol, edge ? tree_columns(mask, start, lo, kvh) : ~0ull, raw, lit);
+        if (edge || lit) {
+          fix_scores(scol, edge ? tree_columns(mask, start, lo, kvh) : ~0ull, raw, lit);
+          // hidden scores are -inf: a factor that left 32 bits (a tiny query on a tiny block
+          // scale) would make them NaN.  (A NaN factor stays.)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) ck[b] = ck[b] < 1.17549435e-38f ? 1.17549435e-38f : ck[b];
+        }
         uint32_t s[SC];
 #pragma unroll
         for (int q = 0; q < SC / 32; ++q)

@@ -99,3 +99,18 @@ def test_a_query_that_is_not_finite_and_sees_nothing(route, dtype, q_dtype, wind
         got = _call(x, window)
     assert (got[:, 1::2] == 0).all()
     assert np.isnan(got[:, 4, 1]).all() and np.isfinite(got[:, [0, 2]]).all()
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiny_queries_on_tiny_scales(route, D):
+    """Scores whose factor leaves 32 bits: the visible positions weigh the same,
+    the hidden ones nothing."""
+    n = 7
+    x = Inputs(72, [n, 140, 500], n, 4, 1, D, "fp8_e4m3")
+    x.q = (x.q.float() * 2.0 ** -110).bfloat16()
+    x.ks = torch.full_like(x.ks, 2.0 ** -50)
+    ref, bound = attention(x)
+    with routes(tree=route):
+        got = _call(x)
+    assert (np.abs(got - ref) <= bound).all()
