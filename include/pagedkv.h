@@ -395,7 +395,10 @@ int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token,
  * FP8 caches: a row that stays in its block keeps its bytes; one that changes
  * blocks is stored as e4m3_rne_sat( fp32( decode(q) * s_src ) / s_dst ) with the
  * destination block's scale, which stays as it is.
- *   new_lens   [B] int32 or NULL: receives start_b + path_len[b]
+ *   new_lens   [B] int32 or NULL: receives start_b + path_len[b].  Not context_lens
+ *              itself, nor any memory of context_lens, tree_lens, path_len, path or
+ *              block_table (PKV_EINVAL): other warps, and the other layers' calls, still
+ *              read those
  */
 int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype,
                       const float *k_scale, const float *v_scale,

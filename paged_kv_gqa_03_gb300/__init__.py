@@ -488,7 +488,8 @@ def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_len
                       v_scale=None, tree_lens=None, new_lens=None, stream=None, prepare=False):
     """Moves the accepted path's K/V rows together in the paged cache, in
     place: position context_lens[b] - n_b + k takes the row of node path[b, k].
-    new_lens (optional int32 [B]) receives the lengths that remain."""
+    new_lens (optional int32 [B], memory of its own) receives the lengths that
+    remain."""
     i32 = _torch().int32
     shape = path.shape
     if len(shape) != 2:
@@ -497,11 +498,16 @@ def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_len
     dev, one = _device_of(k_cache, "k_cache"), (B,)
     k, v, ks, vs, num_blocks, Hkv, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     table, max_blocks = _table(block_table, B, dev)
-    args = (k, v, _code(k_cache), ks, vs, _arg(path, "path", i32, shape, dev),
-            _arg(path_len, "path_len", i32, one, dev), table, max_blocks,
-            _arg(context_lens, "context_lens", i32, one, dev),
-            None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, one, dev),
-            None if new_lens is None else _arg(new_lens, "new_lens", i32, one, dev), B, n, Hkv, D, num_blocks,
+    rows, row_lens = _arg(path, "path", i32, shape, dev), _arg(path_len, "path_len", i32, one, dev)
+    lens = _arg(context_lens, "context_lens", i32, one, dev)
+    nodes = None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, one, dev)
+    new = None
+    if new_lens is not None:   # the call still reads the others when it writes it
+        new, per = _arg(new_lens, "new_lens", i32, one, dev), 4 * B
+        if (abs(new - lens) < per or abs(new - row_lens) < per or (nodes is not None and abs(new - nodes) < per)
+                or rows - per < new < rows + per * n or table - per < new < table + per * max_blocks):
+            raise ValueError("new_lens must not share memory with context_lens, tree_lens, path_len, path or block_table")
+    args = (k, v, _code(k_cache), ks, vs, rows, row_lens, table, max_blocks, lens, nodes, new, B, n, Hkv, D, num_blocks,
             _stream(stream, dev))
     if prepare:
         return Prepared(_L.paged_tree_commit, args, "paged_tree_commit")

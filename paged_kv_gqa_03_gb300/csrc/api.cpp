@@ -175,6 +175,12 @@ int esize_of(int dtype) {
   return 0;
 }
 
+// [a, a + na) and [b, b + nb) share a byte (null: no memory).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Tensor map over a [num_blocks][Hkv][16][D] cache as 2-D rows of 128 bytes
@@ -929,6 +935,12 @@ int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float
   if (!k_cache || !v_cache || !path || !path_len || !block_table || !context_lens) return PKV_EINVAL;
   if (cache_dtype == PKV_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_EINVAL;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_EINVAL;
+  // a sequence's new length is written while other warps still read what it comes from
+  const size_t per = sizeof(int32_t) * (size_t)B;
+  if (overlap(new_lens, per, context_lens, per) || overlap(new_lens, per, tree_lens, per) ||
+      overlap(new_lens, per, path_len, per) || overlap(new_lens, per, path, per * q_len) ||
+      overlap(new_lens, per, block_table, per * max_blocks_per_seq))
+    return PKV_EINVAL;
   CommitParams p;
   std::memset(&p, 0, sizeof(p));
   p.k_cache = static_cast<uint8_t *>(k_cache);

@@ -1,0 +1,40 @@
+"""CPU checks of what the tree calls refuse and keep: tensors that share memory,
+limits of each route, and who owns a workspace.  Nothing is launched."""
+import pytest
+import torch
+
+from test_tree_cpu import _gpu, _pkv, _recorded
+from tree_reference import Inputs
+
+
+def test_commit_refuses_new_lens_on_the_memory_it_reads():
+    """C: new_lens[b] is written by one warp while others still read the rest."""
+    pkv = _pkv()
+    L = pkv.lib()
+    # pointers that nothing follows: the call ends before any launch
+    at = dict(k=1 << 20, v=2 << 20, path=0x1000, plen=0x2000, bt=0x3000, cl=0x4000, tl=0x5000, nl=0x6000)
+
+    def call(**kw):
+        a = dict(at, **kw)
+        return L.paged_tree_commit(a["k"], a["v"], 2, None, None, a["path"], a["plen"], a["bt"], 4, a["cl"], a["tl"], a["nl"],
+                                   2, 8, 2, 128, 10, None)
+    for name, size in (("cl", 8), ("tl", 8), ("plen", 8), ("path", 64), ("bt", 32)):
+        for off in (0, 4, -4, size - 4):
+            assert call(nl=at[name] + off) == pkv.PKV_EINVAL, (name, off)
+
+
+def test_binding_refuses_new_lens_on_the_memory_it_reads(monkeypatch):
+    pkv = _pkv()
+    x = Inputs(1, [40, 33], 4, 4, 2, 64, "bf16")
+    made = _recorded(monkeypatch, pkv)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    lens = i32(6)
+    good = dict(k_cache=x.kc, v_cache=x.vc, path=i32(2, 4), path_len=lens[:2], block_table=torch.from_numpy(x.table),
+                context_lens=lens[2:4], tree_lens=i32(2), new_lens=lens[4:])
+    pkv.paged_tree_commit(**{k: _gpu(v) for k, v in good.items()})   # parts of one tensor that do not meet
+    assert len(made) == 1
+    for bad in (good["context_lens"], good["path_len"], good["tree_lens"], good["path"].view(-1)[2:4], lens[3:5],
+                good["block_table"].view(-1)[:2]):
+        with pytest.raises(ValueError, match="share memory"):
+            pkv.paged_tree_commit(**{k: _gpu(v) for k, v in dict(good, new_lens=bad).items()})
+    assert len(made) == 1
