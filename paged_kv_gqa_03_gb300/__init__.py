@@ -216,12 +216,13 @@ class Prepared:
     """One C call with its arguments marshalled once (returned by the calls
     below when given prepare=True): calling it issues the call again on the
     same buffers and stream, for a decode loop that runs the same step every
-    iteration.  The buffers must stay alive and keep their addresses."""
+    iteration.  The buffers must stay alive and keep their addresses; a
+    workspace that the call allocated itself is kept here (`workspace`)."""
 
-    __slots__ = ("fn", "args", "name")
+    __slots__ = ("fn", "args", "name", "workspace")
 
-    def __init__(self, fn, args, name):
-        self.fn, self.args, self.name = fn, args, name
+    def __init__(self, fn, args, name, workspace=None):
+        self.fn, self.args, self.name, self.workspace = fn, args, name, workspace
 
     def __call__(self):
         rc = self.fn(*self.args)
@@ -273,7 +274,7 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_table, context_lens, 
     window > 0: each row sees only its `window` most recent positions.
     workspace: a uint8 CUDA tensor of paged_decode_workspace_bytes(...) bytes;
     allocated here (by torch) when None.  prepare=True returns the call as a
-    Prepared object instead of issuing it."""
+    Prepared object, which holds the workspace, instead of issuing it."""
     torch = _torch()
     if q.dim() == 4:
         B, q_len, Hq, D = q.shape
@@ -299,7 +300,7 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_table, context_lens, 
         fn, name = _L.paged_decode_attention, "paged_decode_attention"
         full = (_out(out), _dev(q, "q"), _code(q), *args, B, Hq, Hkv, D, *tail)
     if prepare:
-        return Prepared(fn, full, name)
+        return Prepared(fn, full, name, workspace)
     _check(fn(*full), name)
     return workspace
 
@@ -397,7 +398,7 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_table, context_lens, tr
     past n_b of out are left as they were).  workspace: a uint8 CUDA tensor of
     paged_tree_workspace_bytes(...) bytes, allocated here (by torch) when None;
     returned for paged_decode_status.  prepare=True returns the call as a
-    Prepared object instead of issuing it."""
+    Prepared object, which holds the workspace, instead of issuing it."""
     torch = _torch()
     shape = q.shape
     if len(shape) != 4:
@@ -424,7 +425,7 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_table, context_lens, tr
             num_blocks, float(scale), _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
             workspace.nbytes, _stream(stream, dev))
     if prepare:
-        return Prepared(_L.paged_tree_attention, args, "paged_tree_attention")
+        return Prepared(_L.paged_tree_attention, args, "paged_tree_attention", workspace)
     rc = _L.paged_tree_attention(*args)
     if rc != PKV_OK:
         raise PagedKVError(rc, "paged_tree_attention")

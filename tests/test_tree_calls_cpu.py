@@ -1,9 +1,12 @@
 """CPU checks of what the tree calls refuse and keep: tensors that share memory,
 limits of each route, and who owns a workspace.  Nothing is launched."""
+import gc
+import weakref
+
 import pytest
 import torch
 
-from test_tree_cpu import _gpu, _pkv, _recorded
+from test_tree_cpu import OnGpu, _gpu, _pkv, _recorded
 from tree_reference import Inputs
 
 
@@ -38,3 +41,44 @@ def test_binding_refuses_new_lens_on_the_memory_it_reads(monkeypatch):
         with pytest.raises(ValueError, match="share memory"):
             pkv.paged_tree_commit(**{k: _gpu(v) for k, v in dict(good, new_lens=bad).items()})
     assert len(made) == 1
+
+
+def _attention_calls(x):
+    """The two calls that allocate a workspace when given none."""
+    table, lens = torch.from_numpy(x.table), torch.tensor(x.ctx, dtype=torch.int32)
+    common = dict(out=torch.empty_like(x.q), q=x.q, k_cache=x.kc, v_cache=x.vc, block_table=table, context_lens=lens, scale=0.1)
+    return [("paged_tree_attention", dict(common, tree_mask=x.mask)), ("paged_decode_attention", common)]
+
+
+def _allocations(monkeypatch):
+    """Every torch.empty, on "device 0": a list of weak references."""
+    made, real = [], torch.empty
+
+    def empty(*a, **kw):
+        t = real(*a, **kw).as_subclass(OnGpu)
+        made.append(weakref.ref(t))
+        return t
+    monkeypatch.setattr(torch, "empty", empty)
+    return made
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_prepared_call_keeps_the_workspace_it_allocated(monkeypatch, which):
+    pkv = _pkv()
+    x = Inputs(1, [40, 33], 4, 4, 2, 64, "bf16")
+    calls = _recorded(monkeypatch, pkv)
+    monkeypatch.setattr(pkv, f"paged_{('tree', 'decode')[which]}_workspace_bytes", lambda *a, **kw: 4096)
+    name, kw = _attention_calls(x)[which]
+    kw = {k: _gpu(v) for k, v in kw.items()}
+    made = _allocations(monkeypatch)
+    call = getattr(pkv, name)(**kw, prepare=True)
+    gc.collect()
+    assert len(made) == 1 and made[0]() is not None and made[0]().data_ptr() in call.args
+    assert call.workspace is made[0]()
+    call()
+    assert calls[-1][0].startswith(name) and made[0]().data_ptr() in calls[-1][1]
+    own = torch.empty(4096, dtype=torch.uint8)
+    assert getattr(pkv, name)(**kw, workspace=own, prepare=True).workspace is own
+    del call
+    gc.collect()
+    assert made[0]() is None
