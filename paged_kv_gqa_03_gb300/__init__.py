@@ -212,6 +212,17 @@ def _stream(stream, device=None):
     return stream.cuda_stream
 
 
+def _workspace(nbytes, device, stream):
+    """A workspace for a call on `stream` (None: the current one), allocated by
+    torch as that stream's memory: if the caller drops it while the call runs,
+    it is handed out again behind the call."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 class Prepared:
     """One C call with its arguments marshalled once (returned by the calls
     below when given prepare=True): calling it issues the call again on the
@@ -286,7 +297,7 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_table, context_lens, 
     if workspace is None:
         n = paged_decode_workspace_bytes(B, Hq, Hkv, D, _code(k_cache), _code(q), num_splits,
                                          q_len=q_len)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _workspace(n, q.device, stream)
     args = (_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _code(k_cache), _dev(k_scale, "k_scale", torch.float32),
             _dev(v_scale, "v_scale", torch.float32), _dev(block_table, "block_table", torch.int32),
@@ -418,7 +429,7 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_table, context_lens, tr
             raise ValueError(f"out must be {dtype} of shape {tuple(shape)}")
     qc, kc = _code(q), _code(k_cache)
     if workspace is None:
-        workspace = torch.empty(paged_tree_workspace_bytes(B, n, Hq, Hkv, D, kc, qc), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(paged_tree_workspace_bytes(B, n, Hq, Hkv, D, kc, qc), q.device, stream)
     args = (o, _arg(q, "q", dtype, shape, dev), qc, k, v, kc, ks, vs, table, max_blocks,
             _arg(context_lens, "context_lens", i32, (B,), dev), mask, per_seq,
             None if tree_lens is None else _arg(tree_lens, "tree_lens", i32, (B,), dev), B, n, int(window), Hq, Hkv, D,

@@ -82,3 +82,34 @@ def test_a_prepared_call_keeps_the_workspace_it_allocated(monkeypatch, which):
     del call
     gc.collect()
     assert made[0]() is None
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_an_allocated_workspace_belongs_to_the_calls_stream(monkeypatch, which):
+    """Allocated as the current stream's memory it would be handed out again,
+    once dropped, while a call on another stream still runs."""
+    pkv = _pkv()
+    x = Inputs(1, [40, 33], 4, 4, 2, 64, "bf16")
+    _recorded(monkeypatch, pkv)
+    monkeypatch.setattr(pkv, f"paged_{('tree', 'decode')[which]}_workspace_bytes", lambda *a, **kw: 4096)
+    name, kw = _attention_calls(x)[which]
+    kw = {k: _gpu(v) for k, v in kw.items()}
+    inside, at = [], []
+
+    class Stream:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            inside.append(self.s)
+
+        def __exit__(self, *a):
+            inside.pop()
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: ("raw", s))
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: at.append(list(inside)) or real(*a, **k).as_subclass(OnGpu))
+    side = object()
+    for stream, want in ((None, []), (side, [side]), (77, [("raw", 77)])):
+        getattr(pkv, name)(**kw, stream=stream)
+        assert at.pop() == want and not at
