@@ -321,6 +321,9 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
  *  - PKV_TREE_UNITS: the decode kernel in units of 8 rows (FP8: 16, F32: 2), each
  *    streaming the K / V once.  F32 caches, larger batches, and few rows on many
  *    items or (FP8, D = 64) on more than small caches, where it is faster.
+ * PKV_EUNSUPPORTED where a count leaves 32 bits: B * q_len * Hq query rows, num_blocks *
+ * Hkv * 16 cached rows, B * Hkv * ceil(max_blocks_per_seq / 8) tiles or, of the units,
+ * B * Hkv * ceil(q_len * Hq / Hkv / rows of a unit) * max_blocks_per_seq (unit, block) pairs.
  * Weights enter P . V as in the decode kernels: bf16 caches as a high part plus
  * residual, f16 and FP8 caches as f16.  The same call gives the same bits.  Calls
  * that may overlap need workspaces of their own; captured graphs that do may not

@@ -335,8 +335,10 @@ int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c, bool tr
   return PKV_OK;
 }
 
-int validate_decode_shapes(int q_dtype, int cache_dtype, int B, int q_len, int Hq, int Hkv, int D,
-                           int64_t num_blocks, int max_blocks) {
+constexpr double kCountLimit = 2147483000.0;  // 32-bit counts
+
+int validate_shapes(int q_dtype, int cache_dtype, int B, int q_len, int Hq, int Hkv, int D, int64_t num_blocks,
+                    int max_blocks) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || num_blocks <= 0 || max_blocks <= 0) return PKV_EINVAL;
   if (q_len < 1 || q_len > PKV_MAX_Q_LEN) return PKV_EINVAL;
   if (max_blocks > (1 << 26)) return PKV_EUNSUPPORTED;  // 16 * max_blocks stays below 2^30
@@ -346,10 +348,18 @@ int validate_decode_shapes(int q_dtype, int cache_dtype, int B, int q_len, int H
   if (cache_dtype == PKV_F32 && q_dtype != PKV_F32) return PKV_EUNSUPPORTED;
   if ((cache_dtype == PKV_F16 || cache_dtype == PKV_BF16) && q_dtype != cache_dtype) return PKV_EUNSUPPORTED;
   if (cache_dtype == PKV_FP8_E4M3 && q_dtype == PKV_F32) return PKV_EUNSUPPORTED;
-  // TMA row coordinates and the work-item count are 32-bit
-  if ((double)num_blocks * Hkv * kBlock >= 2147483000.0) return PKV_EUNSUPPORTED;
+  // TMA row coordinates are 32-bit
+  if ((double)num_blocks * Hkv * kBlock >= kCountLimit) return PKV_EUNSUPPORTED;
+  return PKV_OK;
+}
+
+int validate_decode_shapes(int q_dtype, int cache_dtype, int B, int q_len, int Hq, int Hkv, int D,
+                           int64_t num_blocks, int max_blocks) {
+  const int rc = validate_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks);
+  if (rc != PKV_OK) return rc;
+  // the work-item count is 32-bit
   const int R = q_len * (Hq / Hkv);  // query rows per kv head; units per kv head <= R
-  if ((double)B * max_blocks * Hkv * R >= 2147483000.0) return PKV_EUNSUPPORTED;
+  if ((double)B * max_blocks * Hkv * R >= kCountLimit) return PKV_EUNSUPPORTED;
   return PKV_OK;
 }
 
@@ -807,10 +817,25 @@ static int tree_route(int cache_dtype, int B, int R, int Hkv, int D, int max_blo
   return rows <= (items <= 32 ? 1 << 18 : 1 << 17) ? PKV_TREE_TILES : PKV_TREE_UNITS;
 }
 
+// Shapes of a tree call: a tree has up to 64 nodes' rows, so the decode kernel's limit
+// (a unit per row at worst) would refuse long tables of wide batches that either kernel
+// serves.  Query rows are counted in 32 bits, ...
+static int validate_tree_shapes(int q_dtype, int cache_dtype, int B, int q_len, int Hq, int Hkv, int D,
+                                int64_t num_blocks, int max_blocks) {
+  const int rc = validate_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks);
+  if (rc != PKV_OK) return rc;
+  return (double)std::max(B, 1) * q_len * Hq < kCountLimit ? PKV_OK : PKV_EUNSUPPORTED;
+}
+// ... and so are the route's work items: K / V tiles of 128 positions, or (unit, block) pairs.
+static int tree_items(int route, const Choice &c, int B, int Hkv, int max_blocks) {
+  const double items = route == PKV_TREE_TILES ? (double)B * Hkv * ((max_blocks + 7) / 8) : (double)B * Hkv * c.NC * max_blocks;
+  return items < kCountLimit ? PKV_OK : PKV_EUNSUPPORTED;
+}
+
 int paged_tree_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int cache_dtype, int q_dtype,
                                size_t *bytes_out) {
   if (!bytes_out) return PKV_EINVAL;
-  int rc = validate_decode_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, 1, 1);
+  int rc = validate_tree_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, 1, 1);
   if (rc != PKV_OK) return rc;
   Choice c;
   int P = 0;
@@ -836,7 +861,12 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
                          int mask_per_seq, const int32_t *tree_lens, int B, int q_len, int window, int Hq, int Hkv,
                          int D, int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
                          pkv_stream_t stream) {
-  int rc = validate_decode_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks_per_seq);
+  int rc = validate_tree_shapes(q_dtype, cache_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks_per_seq);
+  if (rc != PKV_OK) return rc;
+  const int R = q_len * (Hq / Hkv), route = tree_route(cache_dtype, B, R, Hkv, D, max_blocks_per_seq);
+  Choice c;
+  rc = choose_kernel(cache_dtype, q_dtype, D, R, &c, true);
+  if (rc == PKV_OK) rc = tree_items(route, c, B, Hkv, max_blocks_per_seq);
   if (rc != PKV_OK) return rc;
   if (window < 0 || (mask_per_seq != 0 && mask_per_seq != 1)) return PKV_EINVAL;
   if (!(scale > 0.f) || !std::isfinite(scale)) return PKV_EINVAL;
@@ -847,11 +877,10 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
   if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return PKV_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_EWORKSPACE;
   const TreeArgs tree{tree_mask, tree_lens, mask_per_seq ? q_len : 0};
-  const int R = q_len * (Hq / Hkv);
   int sms = 0;
   rc = device_sm_count(&sms);
   if (rc != PKV_OK) return rc;
-  if (tree_route(cache_dtype, B, R, Hkv, D, max_blocks_per_seq) == PKV_TREE_TILES) {
+  if (route == PKV_TREE_TILES) {
     CUtensorMap tmK, tmV;
     rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D, cache_dtype == PKV_FP8_E4M3 && D == 64);
     if (rc != PKV_OK) return rc;
@@ -874,7 +903,6 @@ int paged_tree_attention(void *out, const void *q, int q_dtype, const void *k_ca
       tp.cta_status = hdr->cta_status;
     return cuda_status(launch_tree_tiles(tp, cache_dtype, q_dtype, tmK, tmV, reinterpret_cast<cudaStream_t>(stream)));
   }
-  Choice c;
   int P = 0;
   rc = plan_call(cache_dtype, q_dtype, B, q_len, Hq, Hkv, D, 0, &c, &P, true);
   if (rc != PKV_OK) return rc;

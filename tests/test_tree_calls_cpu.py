@@ -113,3 +113,40 @@ def test_an_allocated_workspace_belongs_to_the_calls_stream(monkeypatch, which):
     for stream, want in ((None, []), (side, [side]), (77, [("raw", 77)])):
         getattr(pkv, name)(**kw, stream=stream)
         assert at.pop() == want and not at
+
+
+@pytest.mark.parametrize("route,shape,over", [
+    # 64 sequences with room for 131072 positions each, the widest tree on 64 / 8 heads
+    ("auto", dict(B=64, mb=8192, Hq=64, Hkv=8, n=64, cd=2), False),
+    ("auto", dict(B=64, mb=8192, Hq=64, Hkv=8, n=64, cd=3), False),
+    # tiles: B * Hkv * ceil(mb / 8) either side of 2^31
+    ("auto", dict(B=2048, mb=(1 << 20) - 8, Hq=64, Hkv=8, n=64, cd=2), False),
+    ("auto", dict(B=2048, mb=1 << 20, Hq=64, Hkv=8, n=64, cd=2), True),
+    ("tiles", dict(B=2048, mb=(1 << 20) - 8, Hq=8, Hkv=8, n=1, cd=1), False),
+    # units: B * Hkv * ceil(R / rows) * mb, of 2 rows (fp32), 8 (16-bit) and 16 (fp8)
+    ("auto", dict(B=4, mb=(1 << 18) - 1, Hq=64, Hkv=8, n=64, cd=0), False),
+    ("auto", dict(B=4, mb=1 << 18, Hq=64, Hkv=8, n=64, cd=0), True),
+    ("units", dict(B=64, mb=65535, Hq=64, Hkv=8, n=64, cd=2), False),
+    ("units", dict(B=64, mb=65536, Hq=64, Hkv=8, n=64, cd=2), True),
+    ("units", dict(B=64, mb=131071, Hq=64, Hkv=8, n=64, cd=3), False),
+    ("units", dict(B=64, mb=131072, Hq=64, Hkv=8, n=64, cd=3), True),
+    ("auto", dict(B=4096, mb=65535, Hq=8, Hkv=8, n=8, cd=2), False),   # more than the tile kernel's plan holds
+    ("auto", dict(B=4096, mb=65536, Hq=8, Hkv=8, n=8, cd=2), True),
+    # query rows
+    ("auto", dict(B=2048, mb=1, Hq=16376, Hkv=8, n=64, cd=2), False),
+    ("auto", dict(B=2048, mb=1, Hq=16384, Hkv=8, n=64, cd=2), True),
+    ("auto", dict(B=1, mb=1, Hq=(1 << 31) - 8, Hkv=1, n=64, cd=2), True)])
+def test_attention_refuses_what_its_route_cannot_count(route, shape, over):
+    """A long table alone does not refuse a call that the route's counts hold."""
+    pkv = _pkv()
+    a = dict(out=16, q=16, qd=2, k=16, v=16, cd=2, ks=16, vs=16, bt=16, mb=4, cl=16, mask=16, per=1, tl=None, B=2, n=4, w=0,
+             Hq=8, Hkv=2, D=128, nb=10, scale=0.1, ws=256, wsb=0, st=None)
+    a.update(shape)
+    a["qd"] = {3: 2}.get(a["cd"], a["cd"])
+    was = pkv.pkv_set_route("tree", route)
+    try:
+        rc = pkv.lib().paged_tree_attention(*a.values())
+    finally:
+        pkv.pkv_set_route("tree", was)
+    # (no workspace: a call that is not refused for its shape ends there, or without a GPU)
+    assert rc == pkv.PKV_EUNSUPPORTED if over else rc in (pkv.PKV_EWORKSPACE, pkv.PKV_ECUDA), rc
