@@ -397,7 +397,8 @@ int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token,
  * shared with another sequence (pkv_bm_append_slots sees to that).
  * FP8 caches: a row that stays in its block keeps its bytes; one that changes
  * blocks is stored as e4m3_rne_sat( fp32( decode(q) * s_src ) / s_dst ) with the
- * destination block's scale, which stays as it is.
+ * destination block's scale, which stays as it is (the plain append's rule: a block's
+ * first row chose it; for caches of the calibrated append see below).
  *   new_lens   [B] int32 or NULL: receives start_b + path_len[b].  Not context_lens
  *              itself, nor any memory of context_lens, tree_lens, path_len, path or
  *              block_table (PKV_EINVAL): other warps, and the other layers' calls, still
@@ -410,6 +411,22 @@ int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype,
                       const int32_t *context_lens, const int32_t *tree_lens,
                       int32_t *new_lens, int B, int q_len, int Hkv, int D,
                       int64_t num_blocks, pkv_stream_t stream);
+
+/*
+ * paged_tree_commit for a cache written by paged_kv_append_calibrated: no row that
+ * moves saturates.  For an FP8 cache the entries are applied in path order; where the
+ * smallest power of two p with max|row| <= 448 p is above the destination block's
+ * scale, that scale becomes p and the block's rows before position context_lens[b] are
+ * re-quantised first, e4m3_rne_sat( fp32( decode(q) * p_old ) / p ).  A scale that a
+ * rejected row has raised stays.  Other cache types: exactly paged_tree_commit.
+ */
+int paged_tree_commit_calibrated(void *k_cache, void *v_cache, int cache_dtype,
+                                 float *k_scale, float *v_scale,
+                                 const int32_t *path, const int32_t *path_len,
+                                 const int32_t *block_table, int max_blocks_per_seq,
+                                 const int32_t *context_lens, const int32_t *tree_lens,
+                                 int32_t *new_lens, int B, int q_len, int Hkv, int D,
+                                 int64_t num_blocks, pkv_stream_t stream);
 
 /*
  * Paged prefill attention on the tensor cores (tcgen05): sequence b's

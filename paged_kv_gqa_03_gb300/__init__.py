@@ -58,6 +58,8 @@ _sig("paged_tree_verify", _i32, _P, _P, _P, _P, _P, _i32, _P, _P, _i64, _P, _i64
      _i32, _i32, _i32, _P)
 _sig("paged_tree_commit", _i32, _P, _P, _i32, _P, _P, _P, _P, _P, _i32, _P, _P, _P,
      _i32, _i32, _i32, _i32, _i64, _P)
+_sig("paged_tree_commit_calibrated", _i32, _P, _P, _i32, _P, _P, _P, _P, _P, _i32, _P, _P, _P,
+     _i32, _i32, _i32, _i32, _i64, _P)
 _sig("paged_decode_status", _i32, _P, _sz, _P, ctypes.POINTER(_i32))
 _sig("paged_decode_attention_static", _i32, _P, _P, _i32, _P, _P, _i32, _P, _P, _P, _i32, _P,
      _i32, _i32, _i32, _i32, _i64, ctypes.c_float, _i32, _P)
@@ -497,11 +499,13 @@ def paged_tree_verify(path, path_len, next_token, draft_tokens, tree_mask, targe
 
 
 def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_lens, k_scale=None,
-                      v_scale=None, tree_lens=None, new_lens=None, stream=None, prepare=False):
+                      v_scale=None, tree_lens=None, new_lens=None, stream=None, prepare=False, calibrated=False):
     """Moves the accepted path's K/V rows together in the paged cache, in
     place: position context_lens[b] - n_b + k takes the row of node path[b, k].
     new_lens (optional int32 [B], memory of its own) receives the lengths that
-    remain."""
+    remain.  calibrated=True, for caches of the calibrated append: FP8 block
+    scales follow the rows moved in, so that none saturates
+    (paged_tree_commit_calibrated)."""
     i32 = _torch().int32
     shape = path.shape
     if len(shape) != 2:
@@ -521,9 +525,10 @@ def paged_tree_commit(k_cache, v_cache, path, path_len, block_table, context_len
             raise ValueError("new_lens must not share memory with context_lens, tree_lens, path_len, path or block_table")
     args = (k, v, _code(k_cache), ks, vs, rows, row_lens, table, max_blocks, lens, nodes, new, B, n, Hkv, D, num_blocks,
             _stream(stream, dev))
+    fn = _L.paged_tree_commit_calibrated if calibrated else _L.paged_tree_commit
     if prepare:
-        return Prepared(_L.paged_tree_commit, args, "paged_tree_commit")
-    rc = _L.paged_tree_commit(*args)
+        return Prepared(fn, args, "paged_tree_commit")
+    rc = fn(*args)
     if rc != PKV_OK:
         raise PagedKVError(rc, "paged_tree_commit")
 

@@ -950,10 +950,11 @@ int paged_tree_verify(int32_t *path, int32_t *path_len, int64_t *next_token, con
   return cuda_status(launch_tree_verify(p, prob_dtype, B, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
+static int run_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale, float *v_scale,
                       const int32_t *path, const int32_t *path_len, const int32_t *block_table,
                       int max_blocks_per_seq, const int32_t *context_lens, const int32_t *tree_lens,
-                      int32_t *new_lens, int B, int q_len, int Hkv, int D, int64_t num_blocks, pkv_stream_t stream) {
+                      int32_t *new_lens, int B, int q_len, int Hkv, int D, int64_t num_blocks, bool calibrated,
+                      pkv_stream_t stream) {
   if (B < 0 || Hkv <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0) return PKV_EINVAL;
   if (q_len < 1 || q_len > PKV_MAX_Q_LEN) return PKV_EINVAL;
   if (esize_of(cache_dtype) == 0) return PKV_EINVAL;
@@ -989,7 +990,26 @@ int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float
   p.Hkv = Hkv;
   p.max_blocks = max_blocks_per_seq;
   p.row_bytes = D * esize_of(cache_dtype);
+  p.calibrated = calibrated ? 1 : 0;
   return cuda_status(launch_tree_commit(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int paged_tree_commit(void *k_cache, void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
+                      const int32_t *path, const int32_t *path_len, const int32_t *block_table,
+                      int max_blocks_per_seq, const int32_t *context_lens, const int32_t *tree_lens,
+                      int32_t *new_lens, int B, int q_len, int Hkv, int D, int64_t num_blocks, pkv_stream_t stream) {
+  return run_commit(k_cache, v_cache, cache_dtype, const_cast<float *>(k_scale), const_cast<float *>(v_scale), path, path_len,
+                    block_table, max_blocks_per_seq, context_lens, tree_lens, new_lens, B, q_len, Hkv, D, num_blocks, false,
+                    stream);
+}
+
+int paged_tree_commit_calibrated(void *k_cache, void *v_cache, int cache_dtype, float *k_scale, float *v_scale,
+                                 const int32_t *path, const int32_t *path_len, const int32_t *block_table,
+                                 int max_blocks_per_seq, const int32_t *context_lens, const int32_t *tree_lens,
+                                 int32_t *new_lens, int B, int q_len, int Hkv, int D, int64_t num_blocks,
+                                 pkv_stream_t stream) {
+  return run_commit(k_cache, v_cache, cache_dtype, k_scale, v_scale, path, path_len, block_table, max_blocks_per_seq,
+                    context_lens, tree_lens, new_lens, B, q_len, Hkv, D, num_blocks, true, stream);
 }
 
 int paged_prefill_attention(void *out, const void *q, int q_dtype, const void *k_cache, const void *v_cache,

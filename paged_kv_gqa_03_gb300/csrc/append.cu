@@ -13,6 +13,7 @@
 // never reads the scale while the opener writes it.
 #include "common.cuh"
 #include "internal.h"
+#include "pow2_scale.cuh"
 
 namespace pkv {
 
@@ -121,13 +122,6 @@ cudaError_t launch_append(const void *k_new, const void *v_new, int new_dtype, v
 // the tokens of a run are applied in order, each lane owning the same head-dim
 // bytes of every row, so earlier rows it re-quantises are its own writes.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float pow2_scale(float amax) {
-  if (!(amax > 0.f)) return 1.f;
-  int e;
-  const float m = frexpf(amax, &e);  // amax = m * 2^e, 0.5 <= m < 1
-  return ldexpf(1.f, m <= 0.875f ? e - 9 : e - 8);  // amax <= 448 * 2^k = 0.875 * 2^(9 + k)
-}
-
 template <class NewT>
 __global__ void __launch_bounds__(128)
     append_calibrated_kernel(const void *__restrict__ k_new, const void *__restrict__ v_new, uint8_t *k_cache,

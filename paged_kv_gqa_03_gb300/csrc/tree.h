@@ -21,12 +21,13 @@ cudaError_t launch_tree_verify(const VerifyParams &p, int dtype, int B, int sms,
 
 struct CommitParams {
   uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;   // fp8 caches, else null
+  float *k_scale, *v_scale;         // fp8 caches, else null; written by calibrated calls alone
   const int32_t *path, *path_len;   // [B][n], [B]
   const int32_t *block_table, *context_lens, *tree_lens;
   int32_t *new_lens;                // [B] or null
   int64_t num_blocks;
   int B, n, Hkv, max_blocks, row_bytes;
+  int calibrated;                   // fp8: block scales follow the rows moved in
 };
 cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t stream);
 

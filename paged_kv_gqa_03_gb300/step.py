@@ -421,7 +421,8 @@ class TreeStep(DecodeStep):
         if k_cache is None:
             k_cache, v_cache, k_scale, v_scale = self.k_cache, self.v_cache, self.k_scale, self.v_scale
         paged_tree_commit(k_cache, v_cache, self.d_path, self.d_path_len, self.d_table, self.d_lens,
-                          k_scale, v_scale, self.d_tree_lens, self.d_new_lens, stream=self.stream)
+                          k_scale, v_scale, self.d_tree_lens, self.d_new_lens, stream=self.stream,
+                          calibrated=self.calibrated)
 
     def finish(self):
         """Waits for the step and releases the rejected positions on the host;
