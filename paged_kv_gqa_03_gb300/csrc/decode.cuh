@@ -692,11 +692,17 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
 
   const uint32_t wl = (uint32_t)p.wlen;
   float sc0 = p.scale_log2 * m.ks, sc1 = p.scale_log2 * m.ks1, vs0 = m.vs, vs1 = m.vs1;
+  float lv0 = 0.f, lv1 = 0.f, rv0 = 1.f, rv1 = 1.f;
   if constexpr (Cfg::TREE) {
     // a scale that is not finite (an overflowed branch opened the block): NaN for the rows
     // that see the block, and hidden weights stay 0 (0 times infinity would be NaN)
     if (!(fabsf(m.ks) < INFINITY && fabsf(vs0) < INFINITY)) sc0 = __int_as_float(0x7fc00000), vs0 = 0.f;
     if (!(fabsf(m.ks1) < INFINITY && fabsf(vs1) < INFINITY)) sc1 = __int_as_float(0x7fc00000), vs1 = 0.f;
+    // V's scales go into the exponent, as in the tile kernel: the weight 2^(x + log2 v - m) is
+    // at most 1 whatever the scales, and l sums weight / v.  (Folded into the weights, as
+    // below, small scales leave f16's normal range.)  Other scales stay literal factors.
+    if (vs0 >= 0x1p-100f && vs0 <= 0x1p118f) lv0 = __log2f(vs0), rv0 = __fdividef(1.f, vs0), vs0 = 1.f;
+    if (vs1 >= 0x1p-100f && vs1 <= 0x1p118f) lv1 = __log2f(vs1), rv1 = __fdividef(1.f, vs1), vs1 = 1.f;
   }
   // 16-row units: when every row of the stage is visible to every column of
   // the unit (the common case: not the last blocks of a context, no window
@@ -713,6 +719,8 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
       y0 = t[nh][0] * sc1; y1 = t[nh][1] * sc1; y2 = t[nh][2] * sc1; y3 = t[nh][3] * sc1;
     }
     if constexpr (Cfg::TREE) {
+      x0 += lv0; x1 += lv0; x2 += lv0; x3 += lv0;
+      y0 += lv1; y1 += lv1; y2 += lv1; y3 += lv1;
       const int pos = m.j * kBlock;
       if (!st.all_see(pos, two ? 2 * kBlock : kBlock)) {
         const TreeRow &ra = st.row[nh][0], &rb = st.row[nh][1];
@@ -769,8 +777,13 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
     const float mb1 = st.m[nh][1] == -INFINITY ? 0.f : st.m[nh][1];
     const float p0 = exp2f(x0 - mb0), p1 = exp2f(x1 - mb1), p2 = exp2f(x2 - mb0), p3 = exp2f(x3 - mb1);
     const float q0 = exp2f(y0 - mb0), q1 = exp2f(y1 - mb1), q2 = exp2f(y2 - mb0), q3 = exp2f(y3 - mb1);
-    st.l[nh][0] += (p0 + p2) + (q0 + q2);
-    st.l[nh][1] += (p1 + p3) + (q1 + q3);
+    if constexpr (Cfg::TREE) {
+      st.l[nh][0] += (p0 + p2) * rv0 + (q0 + q2) * rv1;
+      st.l[nh][1] += (p1 + p3) * rv0 + (q1 + q3) * rv1;
+    } else {
+      st.l[nh][0] += (p0 + p2) + (q0 + q2);
+      st.l[nh][1] += (p1 + p3) + (q1 + q3);
+    }
     // the V scales folded into the weights
     pa[nh][0] = movmatrix_trans(pack_f16x2(p0 * vs0, p1 * vs0));
     pa[nh][1] = movmatrix_trans(pack_f16x2(p2 * vs0, p3 * vs0));

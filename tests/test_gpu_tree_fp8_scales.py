@@ -1,11 +1,12 @@
 """Tree attention on fp8 caches whose block scales are not ordinary numbers, and
-queries that are not."""
+queries that are not; and how near the kernels come when the scales are small
+or differ."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_helpers import routes
-from tree_reference import Inputs, attention, to_i64
+from tree_reference import BLOCK, TORCH, Inputs, attention, seen_positions, to_i64
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +115,67 @@ def test_tiny_queries_on_tiny_scales(route, D):
     with routes(tree=route):
         got = _call(x)
     assert (np.abs(got - ref) <= bound).all()
+
+
+def tight_bound(x, window=0):
+    """(out, bound [B, n, Hq, D]): the definition in 64 bits and how far a kernel
+    may be from it: a bound that counts the weights' steps against the largest weight
+    times scale of the row, not against the largest value a byte can stand for.  As
+    attention()'s bound (half a step of the output; 2^-13 of
+    A = sum w |v| for the scores and the fp32 sums; 2^-11 of A for weights rounded to
+    f16), but for weights below f16's normal range: with v_b the block scales a weight
+    enters as 2^(s + log2 v_b - m), m a running maximum of that exponent, so the weight is
+    at most 1 (2^8 before a maximum is taken over) and what it stands for is
+    w v_b / max(w v_b); half a subnormal step is 2^-25 of max(w v_b), against the
+    decoded value, for every position.  A running maximum that is still below the
+    last one makes the step smaller, not larger."""
+    out, _ = attention(x, window)
+    bound = np.full_like(out, np.inf)
+    G, half = x.Hq // x.Hkv, torch.finfo(TORCH[x.q_dtype]).eps / 2
+    q = x.q.double().numpy()
+    for b in range(x.B):
+        for h in range(x.Hkv):
+            K, V = (x.rows(b, h, w, np.arange(x.ctx[b])) for w in (0, 1))
+            vb = x.vs.double().numpy()[x.table[b, np.arange(x.ctx[b]) // BLOCK], h]
+            for i in range(x.nodes[b]):
+                t = seen_positions(x, b, i, window)
+                if not t:
+                    bound[b, i, h * G:(h + 1) * G] = 0
+                    continue
+                s = q[b, i, h * G:(h + 1) * G] @ K[t].T * x.scale
+                w = np.exp(s - s.max(-1, keepdims=True))
+                l = w.sum(-1, keepdims=True)
+                A = w / l @ np.abs(V[t])
+                dec = (np.abs(V[t]) / vb[t][:, None]).sum(0)
+                step = 2.0 ** -25 * (w * vb[t]).max(-1, keepdims=True) * dec / l
+                o = out[b, i, h * G:(h + 1) * G]
+                bound[b, i, h * G:(h + 1) * G] = half * np.abs(o) + (2.0 ** -13 + 2.0 ** -11) * A + step
+    return out, bound
+
+
+def _blind(ref, bound):
+    """The part of the outputs for which 0 would be within the bound."""
+    return float((np.abs(ref) <= bound).mean())
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("D,q_dtype,n", [(128, "bf16", 9), (64, "f16", 9), (128, "f16", 3), (64, "bf16", 2)])
+@pytest.mark.parametrize("spread,level", [(0.0, 1.0), (0.0, 2.0 ** -12), (2.0, 2.0 ** -12), (3.0, 1.0), (1.0, 2.0 ** 20), (0.0, 2.0 ** -40)])
+def test_every_scale_meets_the_same_bound(route, D, q_dtype, n, spread, level):
+    x = Inputs(50 + n, [n, 130, 400, 1000], n, 8, 2, D, "fp8_e4m3", q_dtype)
+    g = torch.Generator().manual_seed(7)
+    x.ks = (x.ks * torch.exp2(0.3 * spread * torch.randn(x.ks.shape, generator=g))).contiguous()
+    x.vs = (x.vs * level * torch.exp2(spread * torch.randn(x.vs.shape, generator=g))).contiguous()
+    if level not in (1.0, 2.0 ** -12):   # (outputs outside f16's range)
+        x.q_dtype = "bf16"
+        x.q = x.q.bfloat16()
+    ref, bound = tight_bound(x)
+    if spread == 0:
+        assert _blind(ref, bound) < 0.05
+    with routes(tree=route):
+        got = _call(x)
+    # (outputs below the output type's normal range: half its subnormal step)
+    tiny = torch.finfo(TORCH[x.q_dtype]).smallest_normal * torch.finfo(TORCH[x.q_dtype]).eps / 2
+    err = np.abs(got - ref) - tiny
+    bad = ~(err <= bound)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} out of bound, worst {np.nanmax(err / bound):.3g} of it"
