@@ -379,11 +379,14 @@ class TreeStep(DecodeStep):
         """Host part of a step: reserves lens[b] slots for sequence b (None:
         `nodes` each) and writes masks ([B, nodes] or [nodes], bit j of node
         i's: i sees j), slots, copy pairs, tables and lengths into the other
-        staging buffer.  Returns the number of copy-on-write pairs (raises on
-        OOM: nothing is reserved then)."""
-        seqs = self.seqs if seqs is None else seqs
+        staging buffer.  seqs: distinct ids (None: self.seqs).  Returns the
+        number of copy-on-write pairs (raises on OOM: nothing is reserved
+        then)."""
+        seqs = self.seqs if seqs is None else [int(s) for s in seqs]
         L, B = self.q_len, len(seqs)
         lens = np.full(B, L, dtype=np.int32) if lens is None else np.asarray(lens, dtype=np.int32)
+        if len(set(seqs)) != B:   # (its nodes would be appended twice, behind each other)
+            raise ValueError("a sequence may appear once in a step")
         if lens.shape != (B,) or (lens < 0).any() or (lens > L).any():
             raise ValueError(f"lens must be {B} numbers in [0, {L}]")
         masks = np.ascontiguousarray(np.asarray(masks)).astype(np.uint64, copy=False)
