@@ -34,6 +34,12 @@ from . import (BlockManager, lib, paged_decode_attention, paged_decode_workspace
 _ALIGN = 256
 
 
+def _buffer(t):
+    """What a call marshalled for this tensor depends on: a tensor of another
+    shape or type at the same address is another buffer."""
+    return t.data_ptr(), t.dtype, t.shape, t.stride()
+
+
 class _Staging:
     """One contiguous byte buffer with typed sections at 256-byte offsets."""
 
@@ -202,7 +208,7 @@ class DecodeStep:
         if self.ncow:
             paged_kv_copy_blocks(self.k_cache, self.v_cache, self.d_pairs[:2 * self.ncow].view(-1, 2),
                                  self.k_scale, self.v_scale, stream=s)
-        key = ("append", k_new.data_ptr(), v_new.data_ptr(), self.d_slots.data_ptr())
+        key = ("append", _buffer(k_new), _buffer(v_new), self.d_slots.data_ptr())
         call = self._calls.get(key)
         if call is None:
             if k_new.dim() == 4:
@@ -217,7 +223,7 @@ class DecodeStep:
     def attend(self, q, out):
         """a4-a8 on the current bookkeeping.  The C call's arguments are
         marshalled once per (q, out) pair and reused."""
-        key = ("attend", q.data_ptr(), out.data_ptr(), self.d_table.data_ptr())
+        key = ("attend", _buffer(q), _buffer(out), self.d_table.data_ptr())
         call = self._calls.get(key)
         if call is None:
             call = self._remember(key, paged_decode_attention(
@@ -301,7 +307,7 @@ class DecodeStep:
             self._graph_body(h_out)
             self._ran = True
             return
-        key = (self._turn, h_out.data_ptr())
+        key = (self._turn, _buffer(h_out))
         graph = self._graphs.get(key)
         if graph is None:
             graph = torch.cuda.CUDAGraph()
@@ -403,7 +409,7 @@ class TreeStep(DecodeStep):
         return self.ncow
 
     def attend(self, q, out):
-        key = ("attend", q.data_ptr(), out.data_ptr(), self.d_table.data_ptr())
+        key = ("attend", _buffer(q), _buffer(out), self.d_table.data_ptr())
         call = self._calls.get(key)
         if call is None:
             call = self._remember(key, paged_tree_attention(

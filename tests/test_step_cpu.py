@@ -30,3 +30,76 @@ def test_a_sequence_appears_once(monkeypatch):
     assert [s.bm.num_tokens(i) for i in (0, 1)] == [20, 20]
     s.prepare([1, 3, 5, 9], seqs=[1, 0])
     assert s.h_lens.tolist() == [24, 24]
+
+
+@pytest.mark.parametrize("tree", [True, False])
+def test_a_marshalled_call_is_not_reused_for_another_tensor_at_its_address(monkeypatch, tree):
+    """The checks of the first call say nothing of a smaller, strided or otherwise
+    typed tensor at the same address: it would be read or written past its end."""
+    s, pkv = _step(monkeypatch, tree)
+    if tree:
+        s.prepare([1, 3, 5, 9])
+    else:
+        s.prepare()
+    made = _recorded(monkeypatch, pkv)
+    for name in ("d_table", "d_lens", "d_slots", "_ws") + (("d_mask", "d_tree_lens") if tree else ()):
+        setattr(s, name, _gpu(getattr(s, name)))
+    L = (4,) if tree else ()
+    q, out = (_gpu(torch.zeros(2, *L, 4, 64, dtype=torch.bfloat16)) for _ in range(2))
+    kn, vn = (_gpu(torch.zeros(2, *L, 2, 64, dtype=torch.bfloat16)) for _ in range(2))
+    s.launch(q, kn, vn, out)
+    assert len(made) == 2
+    args = [m[1] for m in made]
+    s.launch(q, kn, vn, out)
+    assert [m[1] for m in made[2:]] == args          # the same buffers: the same call
+    bad = [out[:1], out.view(torch.float16), out.transpose(-1, -2)]
+    for o in bad:
+        assert o.data_ptr() == out.data_ptr()
+        before = len(made)
+        if o.dtype != out.dtype and not tree:
+            continue                                 # (the decode call takes its type from q)
+        with pytest.raises((ValueError, TypeError)):
+            s.attend(q, o)
+        assert len(made) == before
+    with pytest.raises((ValueError, TypeError, RuntimeError)):   # (several nodes' rows: refused by view)
+        s.launch(q, kn.transpose(-1, -2), vn, out)
+
+
+def test_a_graph_is_not_replayed_into_another_output(monkeypatch):
+    """run() keeps one graph per output buffer: one of another shape at the same
+    address gets its own."""
+    s, pkv = _step(monkeypatch, False)
+    s.prepare()
+    h = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(torch.Tensor, "is_pinned", lambda self: True)
+    ran = []
+
+    class Stream:
+        cuda_stream = 5
+    s.stream, s._ran = Stream(), True
+    monkeypatch.setattr(s, "_graph_body", lambda o: ran.append(tuple(o.shape)))
+
+    class Graph:
+        def replay(self):
+            pass
+
+    class Event:
+        def record(self, st):
+            pass
+
+    class Context:
+        def __init__(self, *a, **kw):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            pass
+    for name, v in (("CUDAGraph", Graph), ("Event", Event), ("graph", Context), ("stream", Context)):
+        monkeypatch.setattr(torch.cuda, name, v)
+    s.run(h)
+    s.run(h)
+    assert ran == [(2, 4, 64)]
+    s.run(h[:1])
+    assert ran == [(2, 4, 64), (1, 4, 64)]
