@@ -118,14 +118,17 @@ class DecodeStep:
         layout, total = self._layout(B)
         pin = torch.cuda.is_available()
         self._host = [_Staging(layout, total, torch.device("cpu"), pin) for _ in range(2)]
-        self._dev = _Staging(layout, total, self.device, False)
+        # memory of the step's stream: what torch hands out here may still be in use on the
+        # current one, and what is let go of is handed out again behind the step
+        with torch.cuda.stream(self.stream):
+            self._dev = _Staging(layout, total, self.device, False)
+            self._ws = torch.empty(self._workspace_bytes(B), dtype=torch.uint8, device=self.device)
         self.h_seqs = np.empty(B, dtype=np.int64)
         self.h_tok_seqs = np.empty(B * self.q_len, dtype=np.int64)
         self.d_q, self.d_k_new, self.d_v_new = self._dev["q"], self._dev["k_new"], self._dev["v_new"]
         self.d_slots, self.d_pairs = self._dev["slots"], self._dev["pairs"]
         self.d_table, self.d_lens = self._dev["table"], self._dev["lens"]
         self._select(self._turn)
-        self._ws = torch.empty(self._workspace_bytes(B), dtype=torch.uint8, device=self.device)
 
     def _workspace_bytes(self, B):
         return paged_decode_workspace_bytes(B, self.Hq, self.Hkv, self.D, self.k_cache.dtype,
@@ -369,10 +372,11 @@ class TreeStep(DecodeStep):
         super()._buffers(B)
         dev = self.device
         self.d_mask, self.d_tree_lens = self._dev["mask"], self._dev["tree_lens"]
-        self.d_path = torch.empty((B, self.q_len), dtype=torch.int32, device=dev)
-        self.d_path_len = torch.empty(B, dtype=torch.int32, device=dev)
-        self.d_new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        self.d_next_token = torch.empty(B, dtype=torch.int64, device=dev)
+        with torch.cuda.stream(self.stream):
+            self.d_path = torch.empty((B, self.q_len), dtype=torch.int32, device=dev)
+            self.d_path_len = torch.empty(B, dtype=torch.int32, device=dev)
+            self.d_new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            self.d_next_token = torch.empty(B, dtype=torch.int64, device=dev)
         pin = torch.cuda.is_available()
         self.h_path_len = torch.empty(B, dtype=torch.int32, pin_memory=pin)
         self.h_next_token = torch.empty(B, dtype=torch.int64, pin_memory=pin)

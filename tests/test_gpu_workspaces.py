@@ -51,3 +51,21 @@ def test_default_streams():
         ws = pkv.paged_tree_attention(out, q, kc, vc, table, lens, x.mask.cuda(), x.scale, stream=stream)
         assert pkv.paged_decode_status(ws) == (0, 0)
         check_attention(out, x)
+
+
+@pytest.mark.parametrize("tree", [True, False])
+def test_a_steps_buffers_belong_to_its_stream(tree):
+    """By torch's own record of which stream a segment was allocated for."""
+    from paged_kv_gqa_03_gb300.step import DecodeStep, TreeStep
+    st = torch.cuda.Stream()
+    kc, vc = (torch.zeros(16, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    step = TreeStep(kc, vc, 4, torch.bfloat16, 8, 4, stream=st) if tree else DecodeStep(kc, vc, 4, torch.bfloat16, 8, stream=st)
+    for seq in (0, 1):
+        assert step.bm.allocate(seq, 20)
+    step.seqs = [0, 1]
+    step.prepare(*([[1, 3, 5, 9]] if tree else []))
+    segments = torch.cuda.memory_snapshot()
+    mine = [step._dev.buf, step.workspace] + ([step.d_path, step.d_path_len, step.d_new_lens, step.d_next_token] if tree else [])
+    for t in mine:
+        at = [s for s in segments if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+        assert len(at) == 1 and at[0]["stream"] == st.cuda_stream

@@ -1,5 +1,7 @@
 """CPU checks of the step objects' host side: what they refuse, what they keep and
 which stream their memory belongs to.  Nothing is launched."""
+import contextlib
+
 import pytest
 import torch
 
@@ -14,6 +16,7 @@ def _step(monkeypatch, tree=True, B=2, **kw):
     args = (kc, vc, 4, torch.bfloat16, 8) + ((4,) if tree else ())
     s = (mod.TreeStep if tree else mod.DecodeStep)(*args, stream=object(), **kw)
     monkeypatch.setattr(type(s), "_workspace_bytes", lambda self, B: 256)
+    monkeypatch.setattr(torch.cuda, "stream", lambda st: contextlib.nullcontext())
     for seq in range(B):
         assert s.bm.allocate(seq, 20)
     s.seqs = list(range(B))
@@ -103,3 +106,32 @@ def test_a_graph_is_not_replayed_into_another_output(monkeypatch):
     assert ran == [(2, 4, 64)]
     s.run(h[:1])
     assert ran == [(2, 4, 64), (1, 4, 64)]
+
+
+@pytest.mark.parametrize("tree", [True, False])
+def test_device_buffers_are_the_steps_streams_memory(monkeypatch, tree):
+    """Memory of the current stream may still be in use there when the step's
+    stream writes it."""
+    s, pkv = _step(monkeypatch, tree)
+    inside, made, real = [], [], torch.empty
+
+    class Context:
+        def __init__(self, st):
+            self.st = st
+
+        def __enter__(self):
+            inside.append(self.st)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+    def empty(*a, **kw):
+        if kw.get("device") != s.device:
+            return real(*a, **kw)
+        made.append(list(inside))
+        return real(*a, **dict(kw, device="cpu"))
+    s.device = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    monkeypatch.setattr(torch, "empty", empty)
+    s._buffers(2)
+    assert len(made) == (6 if tree else 2) and all(m == [s.stream] for m in made)
