@@ -78,6 +78,7 @@ class DecodeStep:
         self.seqs = []
         self._ws = None
         self._B = None
+        self._host = ()
         self._turn = 0
         self.ncow = 0
         self.graph = None
@@ -115,6 +116,9 @@ class DecodeStep:
         self._B = B
         self._calls.clear()     # their buffers are about to be replaced
         self._graphs.clear()
+        for hs in self._host:   # a copy out of a buffer that is let go of here may be in flight
+            if hs.done is not None:
+                hs.done.synchronize()
         layout, total = self._layout(B)
         pin = torch.cuda.is_available()
         self._host = [_Staging(layout, total, torch.device("cpu"), pin) for _ in range(2)]

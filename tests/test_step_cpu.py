@@ -135,3 +135,23 @@ def test_device_buffers_are_the_steps_streams_memory(monkeypatch, tree):
     monkeypatch.setattr(torch, "empty", empty)
     s._buffers(2)
     assert len(made) == (6 if tree else 2) and all(m == [s.stream] for m in made)
+
+
+@pytest.mark.parametrize("tree", [True, False])
+def test_another_batch_size_waits_for_the_copies_in_flight(monkeypatch, tree):
+    """The pinned staging buffers of the old size are let go of, and their memory
+    may be written by the next owner: not before the copies out of them are done."""
+    s, pkv = _step(monkeypatch, tree)
+    prepare = lambda **kw: s.prepare(*([[1, 3, 5, 9]] if tree else []), **kw)  # noqa: E731
+    prepare()
+    waited = []
+
+    class Event:
+        def __init__(self, name):
+            self.name = name
+
+        def synchronize(self):
+            waited.append(self.name)
+    s._host[0].done, s._host[1].done = Event(0), Event(1)
+    prepare(seqs=[1])
+    assert sorted(waited[:2]) == [0, 1] and s.h_lens.numel() == 1
