@@ -306,6 +306,7 @@ struct MmaTree {};
 template <int NH>
 struct MmaTree<NH, true> {
   TreeRow row[NH][2];  // of score columns 8 nh + 2 tig, 8 nh + 2 tig + 1
+  float qs[NH][2];     // (fp8 caches, bf16 queries) what those rows were divided by
   int start, lo_hi;    // the tree's first position; no row's view starts after lo_hi
   // every row sees positions [pos, pos + count)
   __device__ __forceinline__ bool all_see(int pos, int count) const { return pos + count <= start && pos >= lo_hi; }
@@ -344,6 +345,26 @@ __device__ __forceinline__ void mma_begin(MmaState<Cfg> &st, const DecodeParams 
   for (int nh = 0; nh < MmaState<Cfg>::NH; ++nh) {
     const int rq = 8 * nh + gid;  // the q row (B-operand column) this lane loads
     const size_t row = rq < gc ? query_row(p, m.b, h, r0 + rq) : 0;
+    // (tree) a bf16 row enters as f16 with its largest element in [2^14, 2^15): bf16 reaches
+    // further both ways, and the tile kernel takes any row
+    float up = 1.f;
+    if constexpr (Cfg::TREE && Cfg::FP8 && Cfg::Q::kCode == PKV_BF16) {
+      uint32_t top = 0;
+      if (rq < gc)
+#pragma unroll
+        for (int ks = 0; ks < MmaState<Cfg>::KS; ++ks) {
+          const uint2 raw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p.q) + row + 16 * ks + 4 * tig);
+          top = __vmaxu2(top, __vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu));
+        }
+      top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
+      const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);  // the largest element's exponent field
+      const int f = e > 0 && e < 255 ? min(254 + 14 - e, 253) : 127;  // 2^(14 - exponent), as one
+      up = __int_as_float(f << 23);
+      const float down = __int_as_float((254 - f) << 23);
+      st.qs[nh][0] = __shfl_sync(kFull, down, 8 * tig);  // rows 2 tig and 2 tig + 1: lanes of gid 2 tig, 2 tig + 1
+      st.qs[nh][1] = __shfl_sync(kFull, down, 8 * tig + 4);
+    }
     st.back[nh][0] = row_back(p, r0 + 8 * nh + 2 * tig);
     st.back[nh][1] = row_back(p, r0 + 8 * nh + 2 * tig + 1);
 #pragma unroll
@@ -358,6 +379,7 @@ __device__ __forceinline__ void mma_begin(MmaState<Cfg> &st, const DecodeParams 
           if constexpr (Cfg::Q::kCode == PKV_BF16) {
             x0 = unpack2(BF16{}, raw.x);
             x1 = unpack2(BF16{}, raw.y);
+            if constexpr (Cfg::TREE) x0.x *= up, x0.y *= up, x1.x *= up, x1.y *= up;
           } else {
             x0 = unpack2(F16{}, raw.x);
             x1 = unpack2(F16{}, raw.y);
@@ -713,14 +735,22 @@ __device__ __forceinline__ void mma_pair(MmaState<Cfg> &st, const DecodeParams &
   uint32_t pa[NH][2], pc[NH][2];  // B operands of the first and second block
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh) {
-    float x0 = s[nh][0] * sc0, x1 = s[nh][1] * sc0, x2 = s[nh][2] * sc0, x3 = s[nh][3] * sc0;
-    float y0 = -INFINITY, y1 = -INFINITY, y2 = -INFINITY, y3 = -INFINITY;
-    if (two) {
-      y0 = t[nh][0] * sc1; y1 = t[nh][1] * sc1; y2 = t[nh][2] * sc1; y3 = t[nh][3] * sc1;
+    float x0, x1, x2, x3, y0 = -INFINITY, y1 = -INFINITY, y2 = -INFINITY, y3 = -INFINITY;
+    if constexpr (Cfg::TREE) {
+      float f0 = 1.f, f1 = 1.f;  // the rows' own factors
+      if constexpr (Cfg::Q::kCode == PKV_BF16) f0 = st.qs[nh][0], f1 = st.qs[nh][1];
+      const float a0 = sc0 * f0, a1 = sc0 * f1, b0 = sc1 * f0, b1 = sc1 * f1;
+      x0 = fmaf(s[nh][0], a0, lv0); x1 = fmaf(s[nh][1], a1, lv0); x2 = fmaf(s[nh][2], a0, lv0); x3 = fmaf(s[nh][3], a1, lv0);
+      if (two) {
+        y0 = fmaf(t[nh][0], b0, lv1); y1 = fmaf(t[nh][1], b1, lv1); y2 = fmaf(t[nh][2], b0, lv1); y3 = fmaf(t[nh][3], b1, lv1);
+      }
+    } else {
+      x0 = s[nh][0] * sc0; x1 = s[nh][1] * sc0; x2 = s[nh][2] * sc0; x3 = s[nh][3] * sc0;
+      if (two) {
+        y0 = t[nh][0] * sc1; y1 = t[nh][1] * sc1; y2 = t[nh][2] * sc1; y3 = t[nh][3] * sc1;
+      }
     }
     if constexpr (Cfg::TREE) {
-      x0 += lv0; x1 += lv0; x2 += lv0; x3 += lv0;
-      y0 += lv1; y1 += lv1; y2 += lv1; y3 += lv1;
       const int pos = m.j * kBlock;
       if (!st.all_see(pos, two ? 2 * kBlock : kBlock)) {
         const TreeRow &ra = st.row[nh][0], &rb = st.row[nh][1];

@@ -179,3 +179,18 @@ def test_every_scale_meets_the_same_bound(route, D, q_dtype, n, spread, level):
     err = np.abs(got - ref) - tiny
     bad = ~(err <= bound)
     assert not bad.any(), f"{int(bad.sum())} of {bad.size} out of bound, worst {np.nanmax(err / bound):.3g} of it"
+
+
+@pytest.mark.parametrize("route", ["tiles", "units"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [40, 17, -17, -40, -100])
+def test_queries_of_any_size(route, D, power):
+    """bf16 queries reach far beyond f16 both ways; the scale undoes the factor, so
+    the formula's outputs are those of ordinary queries."""
+    x = Inputs(91, [9, 140, 1500], 9, 6, 2, D, "fp8_e4m3")
+    x.q = (x.q.float() * 2.0 ** power).bfloat16()
+    x.scale *= 2.0 ** -power
+    ref, bound = tight_bound(x)
+    with routes(tree=route):
+        got = _call(x)
+    assert (np.abs(got - ref) <= bound).all()
