@@ -316,8 +316,8 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype,
  *  - PKV_TREE_TILES: 128 query rows of a (sequence, kv head) on the MMA's M side,
  *    its K / V tiles split over the SMs and joined by a merge (no merge is launched
  *    where max_blocks_per_seq * 16 <= 1152).  F16, BF16 and FP8 caches, B <= 2048.
- *    FP8: K enters the MMA as stored, q as a sum of E4M3 parts (elements below 2^-10
- *    of their row's largest, 2^-7 for f16, are held to 2^-19 of it);
+ *    FP8: K enters the MMA as stored, q as a sum of E4M3 parts (elements below 2^-9
+ *    of their row's largest, 2^-6 for f16, are held to 2^-17 of it);
  *  - PKV_TREE_UNITS: the decode kernel in units of 8 rows (FP8: 16, F32: 2), each
  *    streaming the K / V once.  F32 caches, larger batches, and few rows on many
  *    items or (FP8, D = 64) on more than small caches, where it is faster.

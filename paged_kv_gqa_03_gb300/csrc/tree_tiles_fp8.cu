@@ -5,8 +5,9 @@
 // S = Q . K^T takes K as it is stored: kind::f8f6f4 on E4M3, with Q as a sum of E4M3
 // parts.  A row of Q is scaled by a power of two to at most 448 and split by
 // rounding, q1 = e4m3(x), q2 = e4m3(x - q1), ..: each part holds 4 significant bits, so
-// two parts are a bf16 element and three an f16 one exactly (elements below
-// 2^-10 of the row's largest, 2^-7 for f16, are held to 2^-19 of it).  The MMA
+// two parts are a bf16 element and three an f16 one exactly, down to E4M3's subnormal
+// step of 2^-9: elements below 2^-9 of the row's largest (2^-6 for f16; the largest lies in
+// (224, 448]) are held to half that step, 2^-17.8 of the largest.  The MMA
 // runs at twice the 16-bit rate, so two parts cost what one f16 product would,
 // and K is never widened.
 // P . V runs on f16: four warps widen each V tile to f16 in shared memory (exact),
