@@ -353,7 +353,11 @@ int paged_tree_attention(void *out, const void *q, int q_dtype,
  *      w_j(t) = max(p_v(t) - a_j q_v(t), 0), z_j = sum_t w_j(t),
  *      a_0 = 0, z_0 = 1, a_(j+1) = a_j + z_j
  *    (speculative sampling: each refusal leaves the normalised residual
- *    max(r - q, 0)), so that the tokens are distributed as the target's.
+ *    max(r - q, 0)), so that the tokens are distributed as the target's: for
+ *    children that were drawn from q_v independently, repeats among them as they
+ *    fall.  Children drawn without replacement (or otherwise depending on one
+ *    another) come out accepted by the same rule, but the tokens then are not the
+ *    target's.
  *  - draft_probs NULL, uniforms given: deterministic drafts (each node's most
  *    likely continuations).  Child c is accepted iff
  *    u_c (1 - sum of p_v over the distinct tokens refused) < p_v(c); a token

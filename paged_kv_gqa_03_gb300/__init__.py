@@ -471,7 +471,8 @@ def paged_tree_verify(path, path_len, next_token, draft_tokens, tree_mask, targe
     Writes path int32 [B, n] (accepted nodes, then -1), path_len int32 [B] and
     next_token int64 [B].  draft_tokens int64 [B, n]; target_probs, draft_probs
     [B, n, V] fp32 / fp16 / bf16 of one type, rows a fixed distance apart;
-    uniforms fp32 [B, n].  With draft_probs: sampled drafts; without: each
+    uniforms fp32 [B, n].  With draft_probs: sampled drafts, a node's children
+    drawn independently from its row; without: each
     node's deterministic continuations; without uniforms too: greedy."""
     torch = _torch()
     i32, i64 = torch.int32, torch.int64
