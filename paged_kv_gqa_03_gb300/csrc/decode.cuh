@@ -1049,8 +1049,9 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
 #pragma unroll
   for (int g = 0; g < GC; ++g) {
     float x = part[g] + __shfl_xor_sync(kFull, part[g], 16);
+    const bool seen = !Cfg::TREE || tree_sees(st.row[Cfg::TREE ? g : 0], st.start, m.j * kBlock + t);
     if constexpr (Cfg::TREE)
-      x = tree_sees(st.row[g], st.start, m.j * kBlock + t) ? x * sc : -INFINITY;
+      x = seen ? x * sc : -INFINITY;
     else
       x = ((uint32_t)(t - (m.rem - st.back[g] - p.wlen)) < (uint32_t)p.wlen) ? x * sc : -INFINITY;
     float bm = x;
@@ -1065,7 +1066,7 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
     for (int off = 1; off < 16; off <<= 1) bs += __shfl_xor_sync(kFull, bs, off);
     st.l[g] = st.l[g] * al + bs;
     st.m[g] = mn;
-    pw[g] = pg * m.vs;
+    pw[g] = seen ? pg * m.vs : -1.f;  // (tree: -1 marks a hidden position)
 #pragma unroll
     for (int e = 0; e < DPL; ++e) st.acc[g][e] *= al;
   }
@@ -1079,7 +1080,8 @@ __device__ __forceinline__ void simt_block(SimtState<Cfg> &st, const DecodeParam
       const float pt = __shfl_sync(kFull, pw[g], tt);
 #pragma unroll
       for (int e = 0; e < DPL; ++e)
-        st.acc[g][e] = Cfg::TREE && pt == 0.f ? st.acc[g][e] : fmaf(pt, vf[e], st.acc[g][e]);  // (a hidden V may be anything)
+        // a hidden V may be anything; one that is seen counts also with a weight of 0
+        st.acc[g][e] = Cfg::TREE && pt < 0.f ? st.acc[g][e] : fmaf(pt, vf[e], st.acc[g][e]);
     }
   }
 }
