@@ -129,7 +129,7 @@ ROUTES = {"multi_query": (0, ("auto", "transposed", "prefill", "units")),
 def pkv_set_route(which, choice):
     """Forces one kernel-route decision process-wide ("multi_query":
     auto / transposed / prefill / units; "prefill": auto / persistent /
-    tiles); returns the previous choice.  "auto" restores the library's rule."""
+    tiles; "tree": auto / tiles / units); returns the previous choice.  "auto" restores the library's rule."""
     idx, names = ROUTES[which]
     prev = names[_L.pkv_get_route(idx)]
     _check(_L.pkv_set_route(idx, names.index(choice)), "pkv_set_route")

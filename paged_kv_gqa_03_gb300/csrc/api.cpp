@@ -790,19 +790,20 @@ int paged_decode_attention_multi(void *out, const void *q, int q_dtype, const vo
 // forced one (pkv_set_route) where it applies.  The row tiles read an item's
 // cache once for 128 rows and split it anywhere; the units read it once per 8
 // rows or fewer.  Up to 8 rows per kv head (fp8: 16) both read it once (or
-// twice, from L2) and the choice is by what the table can hold.  Units / tiles, us:
+// twice, from L2) and the choice is by what the table can hold.  Units / tiles, us, out of a cold L2:
 //   16-bit, D = 128: the tiles, but for many items (a range then holds the ends
-//     of several): 1 x 16384, 8 heads of 8 rows 58 / 26, 16 x 8192 99 / 98,
-//     64 x 500, 8 heads of 8 42 / 44, 16 x 1000, 32 heads of 8 61 / 65,
-//     64 x 500, 32 heads of 4 104 / 124;
+//     of several), where both are equal: 1 x 16384, 8 heads of 8 rows 60 / 34,
+//     16 x 8192 115 / 113, 64 x 500 47 / 46, 16 x 1000, 32 heads of 8 71 / 70, 64 x
+//     500, 32 heads of 4 122 / 122;
 //   D = 64 and fp8 (half the bytes a tile, or V to widen for 128 rows): the
-//     tiles for small work: bf16 D = 64, 8 rows, 1 x 16384 46 / 20, 16 x 1000
-//     22 / 18, 64 x 500 28 / 33, 16 x 4096 40 / 53; fp8 D = 128, 8 heads of 4 /
-//     16 rows, 1 x 500 21, 26 / 16, 17, 16 x 1000 25, 36 / 23, 4 x 8192 39, 50 /
-//     38, 39, 8 x 8192 45, 58 / 57, 57, 64 x 500 32, 56 / 52, 16 x 8192 63, 81 /
-//     93, 94.
-// Above, the tiles everywhere: 16-bit D = 128, 16 x 8192, 16 rows 117 / 98; D =
-// 64, 16 x 4096, 16 rows 56 / 54; fp8 16 x 8192, 32 rows 132 / 89.
+//     tiles for small work: bf16 D = 64, 8 rows, 1 x 16384 53 / 28, 16 x 1000
+//     25 / 22, 64 x 500 31 / 36, 16 x 4096 46 / 52; fp8 D = 128, 8 heads of 4 /
+//     16 rows, 1 x 500 23, 29 / 19, 19, 16 x 1000 31, 42 / 25, 25, 4 x 8192 42, 52 /
+//     41, 42, 8 x 8192 53, 62 / 59, 60, 64 x 500 36, 58 / 53, 53, 32 x 2000 50, 67 /
+//     70, 71, 16 x 8192 74, 90 / 94, 94; fp8 D = 64, 16 rows, 16 x 1000 31 / 22,
+//     64 x 500 40 / 44, 16 x 2000 38 / 36, 64 x 4096 123 / 150.
+// Above, the tiles everywhere: 16-bit D = 128, 16 x 8192, 16 rows 128 / 113; D =
+// 64, 16 x 4096, 16 rows 59 / 52; fp8 16 x 8192, 32 rows 145 / 95.
 static bool tree_tiles_apply(int cache_dtype, int B) {
   return cache_dtype != PKV_F32 && B <= kMqMaxBatch;
 }

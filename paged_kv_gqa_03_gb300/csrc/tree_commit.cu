@@ -12,7 +12,8 @@
 // of row_bytes / 16 lanes, several rows per load, every load of a group issued
 // before its first store.  The kernel is three dependent latencies (path,
 // block table, rows) and a few KB per warp; nothing else bounds it: 1 sequence of 16
-// nodes 1.9 us, 128 of 64 (fp8, rows between blocks re-quantised) 3.8 us on the device.
+// nodes 1.9 us, 128 of 64 (fp8, rows between blocks re-quantised) 3.8 us on the device; out of
+// cold caches 6 and 8 us.
 //
 // FP8 caches: a row moved inside its block keeps its bytes; one that changes
 // blocks is re-quantised with the destination block's scale (which stays),
@@ -22,7 +23,8 @@
 // saturates.  There a destination block whose scale does not cover a row moved into it
 // first gets the smallest power of two that does, its rows re-quantised, as a token that
 // outgrows its block does in the calibrated append.  The rows of a warp then depend on
-// one another through the scales, and move one after another.
+// one another through the scales, and move one after another: 128 sequences of 64 nodes
+// 6 us more than the plain call, 25 us out of cold caches.
 #include "common.cuh"
 #include "internal.h"
 #include "pow2_scale.cuh"

@@ -28,9 +28,9 @@
 // the bytes.  With full tiles about 2250 clocks a tile: its MMAs are 1536 (bf16: P's high parts
 // and residuals are two products; f16 1024), its operands and copies 192 KiB of
 // shared memory traffic, 1536 clocks too, and the eight softmax warps issue over 40% of the
-// time (one sequence of 131072, 26 nodes: 150 us, tensor pipe 60% active; 32 x 8192, 64
-// nodes: 562 us, 980 TFLOP/s as the formula counts them and 1460 as issued, near the board's
-// power limit).  The tile loop is short of registers: with every softmax thread walking the
+// time (one sequence of 131072, 26 nodes: 150 - 159 us, tensor pipe 60% active; 32 x 8192, 64
+// nodes: 562 - 609 us, 900 - 980 TFLOP/s as the formula counts them and 1350 - 1460 as issued, near
+// the board's power limit).  The tile loop is short of registers: with every softmax thread walking the
 // items by itself it spilled and these two took 159 and 604 us.  Measured against that
 // version, at 157 and 591 us without the check of V, and slower or equal: a second group of
 // softmax warps taking every other tile (152 and 563 - 600, but 106 against 97 for 24 x

@@ -30,8 +30,10 @@
 // What bounds it: a tile takes ~1.2 us (head dim 128) against 0.73 for its bytes from
 // HBM and 0.7 for its 176 KiB of shared-memory traffic: the softmax of a lane quarter,
 // whose two warps share one scheduler, is ~2200 clocks long (1100 of them the weights, 350 the
-// exchange of maxima, 290 the block scales).  16 x 32768, 32 / 8 heads, 8 nodes 275 us (3.9
-// TB/s); 16 x 8192, 64 nodes 157 us (880 TFLOP/s).  Tried and slower: widening K as well (2.1
+// exchange of maxima, 290 the block scales).  16 x 32768, 32 / 8 heads, 8 nodes 274 - 278 us (3.9
+// TB/s); 16 x 8192, 64 nodes 157 - 162 us (850 - 880 TFLOP/s).  At head dim 64 a tile holds half the bytes
+// and costs nearly the same softmax, scales and barriers: 64 x 4096, 32 / 8 heads, 16 nodes 150 us
+// (1.4 us a tile, 1.8 TB/s; its bytes alone 40).  Tried and slower: widening K as well (2.1
 // us a tile), one K stage less (64 nodes 187), the rows of a small tree copied into all
 // four lane quarters, each taking every fourth tile (2.0 us a tile: the others' weights have to
 // be cleared).

@@ -33,11 +33,11 @@
 // is sum p - a sum q over the terms that are positive: 19 operations a term, about
 // two thirds of the time the terms take to arrive from HBM.
 //
-// Measured (fp32 rows, device time): a chain of 6, V 32000 8.9 us; 64 trees of 24, V
-// 128000 46 us: every refusal reads 64 x 2 rows of 512 KB, the first from HBM (10 us),
-// the next from L2 (8 us each); 16 trees of 16, greedy, 17 us (2 - 3 passes of ~4 us, each a
+// Measured (fp32 rows, device time): a chain of 6, V 32000 9 us (15 out of cold caches); 64 trees
+// of 24, V 128000 46 - 54 us: every refusal reads 64 x 2 rows of 512 KB, the first from HBM (10 us),
+// the next from L2 (8 us each); 16 trees of 16, greedy, 17 - 21 us (2 - 3 passes of ~4 us, each a
 // round trip to memory, a cluster barrier and the join); 32 trees of 64 with deterministic
-// drafts, V 50257, bf16, 12 us.  1024 threads a CTA: chain 13.5 us, and fewer clusters fit
+// drafts, V 50257, bf16, 12 - 14 us.  (The fp32 kernels spill 32 bytes at their 64 registers.)  1024 threads a CTA: chain 13.5 us, and fewer clusters fit
 // side by side.
 #include <cooperative_groups.h>
 
