@@ -22,6 +22,10 @@
 // item is copied into the one Q buffer while the current item's last tile is in
 // the softmax (its last S has been read by then).
 //
+// Weights enter P . V as in the decode kernels: bf16 caches a high part plus residual (16
+// bits), f16 caches as f16 (2^-11 each, 2.9e-4 of the outputs' size with their own rounding
+// against 2.1e-4 by fp32 weights; a second f16 part would cost another product).
+//
 // What bounds it.  Up to about 64 rows per kv head, the K / V bytes: 64 / 8 heads,
 // 16 x 8192, 1 - 8 nodes 98 - 100 us (5.4 TB/s with ~11 us of start, first tile and
 // merge), 32 x 8192, 1 - 4 nodes 176 us (6.1 TB/s); DRAM reads are 1.002 - 1.005 times
