@@ -580,6 +580,126 @@ int paged_kv_copy_blocks(void *k_cache, void *v_cache, int cache_dtype,
                          pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* A cache held in 4 bits.                                                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * Pages of 4-bit floating point: 0.5625 bytes an element, just over half of an FP8 cache
+ * (the INT8 / INT4 caches that "LLM推理优化核心技术" names, in the type this GPU converts
+ * by itself).  16 neighbouring elements of a row share a scale: with
+ * y = x / unit,
+ *   s = e4m3(max|y| / 6), saturating at 448;   code = e2m1(y / s), saturating at +-6;
+ *   value = code * s * unit
+ * both rounded to nearest even, divisions in fp32; E2M1 has the values 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives.  k_unit and v_unit are positive finite numbers that belong
+ * to the cache (one for all its keys, one for all its values): 1 serves elements whose
+ * groups reach 0.1 to 2688; smaller or larger ones want a unit near their typical
+ * magnitude (a group whose largest y is below 6 * 2^-10 becomes 0).  A group with an
+ * element that is not finite reads as NaN, all 16 of it.  A token's rows do not depend on
+ * other tokens: there is no order of appends, and nothing is ever re-quantised.
+ *
+ *   cache   uint8 [num_blocks][Hkv][18 D], 16-byte aligned: K and V of 16 tokens of a
+ *           block and kv head in one run, D = 64 or 128.  Within the run the library
+ *           orders codes and scales for its kernels (the order is the same for every
+ *           cache of a head dim; a block can be copied or moved as bytes); values go in and out through
+ *           the calls below.
+ *
+ * paged_kv4_append: new tokens' rows into their slots, as paged_kv_append.
+ *   k_new, v_new  T rows [Hkv][D] of new_dtype (F32, F16, BF16), ld_k / ld_v elements from
+ *                 a token to the next (>= Hkv * D; for instance the columns of one
+ *                 projection); rows 16-byte aligned
+ *   slot_mapping  [T] int64; < 0 or past the cache: skipped.  Distinct within a call.
+ */
+int64_t paged_kv4_tile_bytes(int D); /* 18 D; 0 for a head dim that is not served */
+int paged_kv4_append(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_v, int new_dtype,
+                     void *cache, const int64_t *slot_mapping, int T, int Hkv, int D,
+                     int64_t num_blocks, float k_unit, float v_unit, pkv_stream_t stream);
+
+/*
+ * Whole blocks between a cache of `dtype` (F32, F16, BF16; [blocks][Hkv][16][D], as for
+ * paged_kv_append) and a 4-bit one, for each pair {src, dst} (int32, device): pack
+ * quantises block src of k_cache / v_cache into block dst of the 4-bit cache, expand
+ * writes the values of 4-bit block src (rounded to dtype) to block dst of k_cache /
+ * v_cache.  So a prompt can be computed on 16-bit pages (paged_prefill_attention) and kept in 4, and a 4-bit
+ * prefix expanded for the next chunk's attention.  All 16 rows are converted, stale ones too.
+ * Pairs with an id outside either cache are skipped; destinations must be distinct.
+ */
+int paged_kv4_pack_blocks(void *cache, int64_t num_blocks, const void *k_cache, const void *v_cache,
+                          int dtype, int64_t num_src_blocks, const int32_t *src_dst_pairs, int n_pairs,
+                          int Hkv, int D, float k_unit, float v_unit, pkv_stream_t stream);
+int paged_kv4_expand_blocks(void *k_cache, void *v_cache, int dtype, int64_t num_dst_blocks,
+                            const void *cache, int64_t num_blocks, const int32_t *src_dst_pairs,
+                            int n_pairs, int Hkv, int D, float k_unit, float v_unit, pkv_stream_t stream);
+/* paged_kv_copy_blocks for a 4-bit cache (copy on write); same rules. */
+int paged_kv4_copy_blocks(void *cache, const int32_t *src_dst_pairs, int n_pairs, int Hkv, int D,
+                          int64_t num_blocks, pkv_stream_t stream);
+
+/*
+ * paged_decode_attention_multi over a 4-bit cache: q_len new tokens per sequence (already appended),
+ * causal, with an optional sliding window; q_len = 1 is plain decode.
+ *   q, out     [B][q_len][Hq][D], F16 or BF16 (PKV_EUNSUPPORTED for F32), 16-byte aligned
+ *   workspace  paged_kv4_decode_workspace_bytes(...) bytes, 256-byte aligned (status:
+ *              paged_decode_status)
+ * Block tables, lengths, window, scale, num_splits, clamping, flags and errors as there.
+ * A row that sees nothing gives 0.  What a row does not see may hold anything: positions
+ * at or past context_lens[b], newer tokens of the step, positions before the window.  A
+ * position that reads as NaN gives NaN in the rows that see it (of V: in the group's 16
+ * elements), and in no others.  Kernel: units of 8 query rows per kv head, 16 where
+ * q_len * Hq / Hkv > 8, each streaming the blocks once (a head with more rows streams
+ * them again, mostly from L2).  Calls that may overlap need workspaces of their own.
+ */
+int paged_kv4_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int q_dtype,
+                                     int num_splits, size_t *bytes_out);
+int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void *cache,
+                               const int32_t *block_table, int max_blocks_per_seq,
+                               const int32_t *context_lens, int B, int q_len, int window,
+                               int Hq, int Hkv, int D, int64_t num_blocks, float scale,
+                               float k_unit, float v_unit, int num_splits,
+                               void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions.                                                        */
+/* ------------------------------------------------------------------------ */
+/*
+ * The rotation of queries and keys in front of the cache update ("大模型推理加速——KV
+ * Cache篇" §3.1 Attention.forward, apply_rotary_emb).  Pair i of a head's first rot_dim
+ * elements is turned by the angle position * f_i and scaled by `magnitude`:
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin),
+ * a pair being elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1; the
+ * head's other elements stay.  Angles are exact at any position; the rotation is fp32,
+ * rounded once to the rows' type.
+ *   turns        [rot_dim / 2] uint64, device: f_i / 2 pi in 2^-64, from pkv_rope_turns
+ *                (a host call: frequencies are radians a position, >= 0 and finite; any scaling
+ *                for long contexts is in the frequencies and the magnitude)
+ *   positions    [T] int64, device (any value; equal ones may repeat)
+ *   q, k, v      T rows [Hq or Hkv][D] of dtype F32, F16 or BF16, ld_* elements from a token
+ *                to the next, rows 16-byte aligned; D 64 or 128
+ *   rot_dim      a multiple of 16, at most D
+ *   q_out, k_out may be q, k themselves (same ld), else apart from all that the call reads
+ *
+ * paged_rope rotates rows only (Hq or Hkv may be 0).  paged_rope_append writes the
+ * rotated keys and the values to their slots of a cache of the same dtype (slots as for
+ * paged_kv_append; q_out is written for skipped tokens too), paged_kv4_rope_append those of a
+ * 4-bit cache: bit for bit what paged_rope and then paged_kv_append / paged_kv4_append give.  FP8 caches:
+ * paged_rope, then the append of the cache's scale rule.
+ */
+int pkv_rope_turns(uint64_t *turns, const double *frequencies, int n);
+int paged_rope(void *q_out, int64_t ld_q_out, const void *q, int64_t ld_q, void *k_out, int64_t ld_k_out,
+               const void *k, int64_t ld_k, int dtype, const int64_t *positions, const uint64_t *turns,
+               int rot_dim, int interleaved, float magnitude, int T, int Hq, int Hkv, int D,
+               pkv_stream_t stream);
+int paged_rope_append(void *q_out, int64_t ld_q_out, const void *q, int64_t ld_q, const void *k_new,
+                      int64_t ld_k, const void *v_new, int64_t ld_v, int dtype, const int64_t *positions,
+                      const uint64_t *turns, int rot_dim, int interleaved, float magnitude,
+                      void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                      int T, int Hq, int Hkv, int D, int64_t num_blocks, pkv_stream_t stream);
+int paged_kv4_rope_append(void *q_out, int64_t ld_q_out, const void *q, int64_t ld_q, const void *k_new,
+                          int64_t ld_k, const void *v_new, int64_t ld_v, int dtype,
+                          const int64_t *positions, const uint64_t *turns, int rot_dim, int interleaved,
+                          float magnitude, void *cache, const int64_t *slot_mapping,
+                          int T, int Hq, int Hkv, int D, int64_t num_blocks, float k_unit, float v_unit,
+                          pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Route overrides (measurement and tests).                                 */
 /* ------------------------------------------------------------------------ */
 /*

@@ -15,6 +15,9 @@ __all__ = [
     "PagedKVError", "paged_kv_append", "paged_decode_workspace_bytes",
     "paged_decode_attention", "paged_prefill_attention", "paged_decode_status", "paged_decode_merge",
     "paged_decode_attention_static", "paged_decode_static_status",
+    "paged_kv4_append", "paged_kv4_pack_blocks", "paged_kv4_expand_blocks", "paged_kv4_copy_blocks",
+    "paged_kv4_decode_workspace_bytes", "paged_kv4_decode_attention",
+    "RopeTable", "paged_rope", "paged_rope_append", "paged_kv4_rope_append",
     "paged_tree_workspace_bytes", "paged_tree_attention", "paged_tree_verify", "paged_tree_commit",
     "paged_kv_copy_blocks", "pkv_copy", "pkv_status_string", "pkv_version", "pkv_set_route",
     "pkv_get_route", "pkv_test_stall_next", "BlockManager", "Prepared",
@@ -66,6 +69,22 @@ _sig("paged_decode_attention_static", _i32, _P, _P, _i32, _P, _P, _i32, _P, _P, 
 _sig("paged_decode_static_status", _i32, _P, ctypes.POINTER(_i32))
 _sig("paged_decode_merge", _i32, _P, _i32, _P, _P, _i32, _i32, _i32, _i32, _P)
 _sig("paged_kv_copy_blocks", _i32, _P, _P, _i32, _P, _P, _P, _i32, _i32, _i32, _i64, _P)
+_f32 = ctypes.c_float
+_sig("paged_kv4_tile_bytes", _i64, _i32)
+_sig("paged_kv4_append", _i32, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _i32, _i64, _f32, _f32, _P)
+_sig("paged_kv4_pack_blocks", _i32, _P, _i64, _P, _P, _i32, _i64, _P, _i32, _i32, _i32, _f32, _f32, _P)
+_sig("paged_kv4_expand_blocks", _i32, _P, _P, _i32, _i64, _P, _i64, _P, _i32, _i32, _i32, _f32, _f32, _P)
+_sig("paged_kv4_copy_blocks", _i32, _P, _P, _i32, _i32, _i32, _i64, _P)
+_sig("paged_kv4_decode_workspace_bytes", _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz))
+_sig("paged_kv4_decode_attention", _i32, _P, _P, _i32, _P, _P, _i32, _P, _i32, _i32, _i32, _i32, _i32, _i32,
+     _i64, _f32, _f32, _f32, _i32, _P, _sz, _P)
+_sig("pkv_rope_turns", _i32, _P, _P, _i32)
+_sig("paged_rope", _i32, _P, _i64, _P, _i64, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _f32,
+     _i32, _i32, _i32, _i32, _P)
+_sig("paged_rope_append", _i32, _P, _i64, _P, _i64, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _f32,
+     _P, _P, _P, _i32, _i32, _i32, _i32, _i64, _P)
+_sig("paged_kv4_rope_append", _i32, _P, _i64, _P, _i64, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _f32,
+     _P, _P, _i32, _i32, _i32, _i32, _i64, _f32, _f32, _P)
 _sig("pkv_copy", _i32, _P, _P, _sz, _P)
 _sig("pkv_status_string", ctypes.c_char_p, _i32)
 _sig("pkv_last_cuda_error", _i32)
@@ -606,6 +625,258 @@ def paged_kv_copy_blocks(k_cache, v_cache, src_dst_pairs, k_scale=None, v_scale=
         _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
         _dev(src_dst_pairs, "src_dst_pairs", torch.int32), n, k_cache.shape[1],
         k_cache.shape[3], k_cache.shape[0], _stream(stream)), "paged_kv_copy_blocks")
+
+
+def _issue(fn, args, name, prepare, workspace=None):
+    if prepare:
+        return Prepared(fn, args, name, workspace)
+    rc = fn(*args)
+    if rc != PKV_OK:
+        raise PagedKVError(rc, name)
+    return workspace
+
+
+def _token_rows(t, name, shape, dtype, device):
+    """(pointer, elements from a token to the next) of rows [T, heads, D] whose
+    heads lie side by side; a token's row may be a part of a wider one."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    T, heads, D = shape
+    ld, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (heads > 1 and sh != D)):
+        raise ValueError(f"{name}: the {heads} heads of a token must lie side by side, strides {t.stride()}")
+    return t.data_ptr(), (ld if T > 1 else heads * D)
+
+
+def _cache4(cache, device):
+    """(pointer, num_blocks, Hkv, D) of a 4-bit cache, uint8 [num_blocks, Hkv, 18 D]."""
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] not in (18 * 64, 18 * 128):
+        raise ValueError(f"a 4-bit cache must be [num_blocks, Hkv, 18 * D], D 64 or 128, got {tuple(shape)}")
+    return _arg(cache, "cache", _torch().uint8, shape, device), shape[0], shape[1], shape[2] // 18
+
+
+def paged_kv4_append(k_new, v_new, cache, slot_mapping, k_unit=1.0, v_unit=1.0, stream=None, prepare=False):
+    """Quantises k_new / v_new [T, Hkv, D] (f32, f16 or bf16; a token's row may
+    be a slice of a wider one) into the 4-bit cache, uint8 [num_blocks, Hkv,
+    18 * D], at slot_mapping [T] (int64; < 0 skips)."""
+    dev = _device_of(cache, "cache")
+    ptr, num_blocks, Hkv, D = _cache4(cache, dev)
+    T = k_new.shape[0]
+    shape = (T, Hkv, D)
+    k, ld_k = _token_rows(k_new, "k_new", shape, k_new.dtype, dev)
+    v, ld_v = _token_rows(v_new, "v_new", shape, k_new.dtype, dev)
+    args = (k, ld_k, v, ld_v, _code(k_new), ptr, _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev),
+            T, Hkv, D, num_blocks, float(k_unit), float(v_unit), _stream(stream, dev))
+    return _issue(_L.paged_kv4_append, args, "paged_kv4_append", prepare)
+
+
+def _pages(cache, k_cache, v_cache, pairs):
+    dev = _device_of(cache, "cache")
+    ptr, num_blocks, Hkv, D = _cache4(cache, dev)
+    shape = (k_cache.shape[0], Hkv, 16, D)
+    k = _arg(k_cache, "k_cache", k_cache.dtype, shape, dev)
+    v = _arg(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    n = pairs.shape[0]
+    return dev, ptr, num_blocks, k, v, shape[0], _arg(pairs, "src_dst_pairs", _torch().int32, (n, 2), dev), n, Hkv, D
+
+
+def paged_kv4_pack_blocks(cache, k_cache, v_cache, src_dst_pairs, k_unit=1.0, v_unit=1.0, stream=None,
+                          prepare=False):
+    """4-bit block dst of cache = quantised block src of k_cache / v_cache
+    [blocks, Hkv, 16, D] (f32, f16, bf16), for each (src, dst) of int32 [n, 2]."""
+    dev, ptr, num_blocks, k, v, src, pairs, n, Hkv, D = _pages(cache, k_cache, v_cache, src_dst_pairs)
+    args = (ptr, num_blocks, k, v, _code(k_cache), src, pairs, n, Hkv, D, float(k_unit), float(v_unit),
+            _stream(stream, dev))
+    return _issue(_L.paged_kv4_pack_blocks, args, "paged_kv4_pack_blocks", prepare)
+
+
+def paged_kv4_expand_blocks(k_cache, v_cache, cache, src_dst_pairs, k_unit=1.0, v_unit=1.0, stream=None,
+                            prepare=False):
+    """Block dst of k_cache / v_cache [blocks, Hkv, 16, D] (f32, f16, bf16) =
+    the values of 4-bit block src of cache, for each (src, dst) of int32 [n, 2]."""
+    dev, ptr, num_blocks, k, v, dst, pairs, n, Hkv, D = _pages(cache, k_cache, v_cache, src_dst_pairs)
+    args = (k, v, _code(k_cache), dst, ptr, num_blocks, pairs, n, Hkv, D, float(k_unit), float(v_unit),
+            _stream(stream, dev))
+    return _issue(_L.paged_kv4_expand_blocks, args, "paged_kv4_expand_blocks", prepare)
+
+
+def paged_kv4_copy_blocks(cache, src_dst_pairs, stream=None, prepare=False):
+    """cache[dst] = cache[src] for each (src, dst) row of the int32 [n, 2] tensor (copy on write)."""
+    dev = _device_of(cache, "cache")
+    ptr, num_blocks, Hkv, D = _cache4(cache, dev)
+    n = src_dst_pairs.shape[0]
+    args = (ptr, _arg(src_dst_pairs, "src_dst_pairs", _torch().int32, (n, 2), dev), n, Hkv, D, num_blocks,
+            _stream(stream, dev))
+    return _issue(_L.paged_kv4_copy_blocks, args, "paged_kv4_copy_blocks", prepare)
+
+
+def paged_kv4_decode_workspace_bytes(B, Hq, Hkv, D, q_dtype, num_splits=0, q_len=1):
+    """Workspace size for paged_kv4_decode_attention on the current device.
+    q_dtype: a torch dtype or C code."""
+    code = q_dtype if isinstance(q_dtype, int) else _code(_torch().empty(0, dtype=q_dtype))
+    out = _sz(0)
+    _check(_L.paged_kv4_decode_workspace_bytes(B, q_len, Hq, Hkv, D, code, num_splits, ctypes.byref(out)),
+           "paged_kv4_decode_workspace_bytes")
+    return out.value
+
+
+def paged_kv4_decode_attention(out, q, cache, block_table, context_lens, scale, k_unit=1.0, v_unit=1.0,
+                               num_splits=0, workspace=None, stream=None, window=0, prepare=False):
+    """paged_decode_attention over a 4-bit cache, uint8 [num_blocks, Hkv, 18 * D].
+
+    q, out [B, Hq, D]: one new token per sequence; [B, q_len, Hq, D]: q_len of
+    them, token i seeing the cache up to its own position (f16 or bf16; out may be
+    pinned host memory).  window > 0: each row sees its `window` most recent positions.
+    workspace: a uint8 CUDA tensor of paged_kv4_decode_workspace_bytes(...) bytes, allocated
+    here (by torch) when None; returned for paged_decode_status.  prepare=True
+    returns the call as a Prepared object, which holds the workspace."""
+    torch = _torch()
+    dev, shape = _device_of(q, "q"), q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(shape)}")
+    if out.shape != shape or out.dtype is not q.dtype:
+        raise ValueError(f"out must be {tuple(shape)} of {q.dtype}, got {tuple(out.shape)} of {out.dtype}")
+    if out.is_cuda and out.get_device() != dev:
+        raise ValueError(f"out is on {out.device}, expected cuda:{dev}")
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    q_len = shape[1] if len(shape) == 4 else 1
+    ptr, num_blocks, Hkv, cD = _cache4(cache, dev)
+    if cD != D:
+        raise ValueError(f"the cache's head dim is {cD}, q's {D}")
+    table, max_blocks = _table(block_table, B, dev)
+    lens = _arg(context_lens, "context_lens", torch.int32, (B,), dev)
+    if workspace is None:
+        workspace = _workspace(paged_kv4_decode_workspace_bytes(B, Hq, Hkv, D, _code(q), num_splits, q_len),
+                               q.device, stream)
+    args = (_out(out), _arg(q, "q", q.dtype, shape, dev), _code(q), ptr, table, max_blocks, lens, B, q_len,
+            int(window), Hq, Hkv, D, num_blocks, float(scale), float(k_unit), float(v_unit), num_splits,
+            _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream, dev))
+    return _issue(_L.paged_kv4_decode_attention, args, "paged_kv4_decode_attention", prepare, workspace)
+
+
+class RopeTable:
+    """The frequencies of rotary positions, as the rope calls take them.
+
+    Pair i of rot_dim elements turns by position * f_i radians,
+    f_i = base ** (-2 i / rot_dim), changed by `scaling` for contexts longer than the
+    original_positions the model was trained on:
+      "none"    as it is;
+      "linear"  f_i / factor (positions interpolated);
+      "base"    the base raised by factor ** (rot_dim / (rot_dim - 2)), so that the slowest
+                pair is interpolated by the factor and the fastest stays;
+      "parts"   by the turns r_i = original_positions * f_i / 2 pi that a pair makes over the
+                original context: f_i where r_i >= fast, f_i / factor where r_i <= slow, and
+                linear in r_i between.
+    frequencies: f_i themselves (float64 [rot_dim / 2]), instead of base and scaling.
+    magnitude scales the rotated elements (0.1 ln(factor) + 1 goes with "parts" where the
+    model was trained so; 1 leaves them).  interleaved: pairs are elements
+    (2 i, 2 i + 1), not (i, i + rot_dim / 2).  `turns` is the device tensor of the table; it
+    belongs to one device."""
+
+    def __init__(self, rot_dim, base=10000.0, scaling="none", factor=1.0, original_positions=0, slow=1.0, fast=32.0,
+                 magnitude=1.0, interleaved=False, frequencies=None, device=None):
+        import numpy as np
+        torch = _torch()
+        if rot_dim <= 0 or rot_dim % 2:
+            raise ValueError(f"rot_dim must be even and positive, got {rot_dim}")
+        if frequencies is None:
+            if scaling not in ("none", "linear", "base", "parts"):
+                raise ValueError(f"unknown scaling {scaling!r}")
+            if not (base > 0 and factor > 0):
+                raise ValueError("base and factor must be positive")
+            if scaling == "base":
+                if rot_dim < 4:
+                    raise ValueError("scaling by the base needs rot_dim >= 4")
+                base = base * factor ** (rot_dim / (rot_dim - 2))
+            f = float(base) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+            if scaling == "linear":
+                f = f / factor
+            elif scaling == "parts":
+                if not (original_positions > 0 and fast > slow):
+                    raise ValueError("scaling by parts needs original_positions > 0 and fast > slow")
+                keep = np.clip((original_positions * f / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+                f = f * keep + f / factor * (1 - keep)
+        else:
+            f = np.ascontiguousarray(np.asarray(frequencies, dtype=np.float64))
+            if f.shape != (rot_dim // 2,):
+                raise ValueError(f"frequencies must be {rot_dim // 2} numbers, got shape {f.shape}")
+        f = np.ascontiguousarray(f)
+        host = np.empty(rot_dim // 2, dtype=np.uint64)
+        _check(_L.pkv_rope_turns(host.ctypes.data, f.ctypes.data, rot_dim // 2), "pkv_rope_turns")
+        self.rot_dim, self.magnitude, self.interleaved, self.frequencies = rot_dim, float(magnitude), bool(interleaved), f
+        self.turns = torch.from_numpy(host.view(np.int64)).to("cuda" if device is None else device)
+
+
+def _rope_args(table, positions, T, device):
+    torch = _torch()
+    return (_arg(positions, "positions", torch.int64, (T,), device),
+            _arg(table.turns, "the table's turns", torch.int64, (table.rot_dim // 2,), device),
+            table.rot_dim, 1 if table.interleaved else 0, table.magnitude)
+
+
+def paged_rope(q, k, positions, table, q_out=None, k_out=None, stream=None, prepare=False):
+    """Rotates q [T, Hq, D] and k [T, Hkv, D] (either may be None) by their
+    positions [T] (int64) and the RopeTable, into q_out / k_out (None: in place).  A token's
+    row may be a slice of a wider one (one projection's columns)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("paged_rope needs q or k")
+    dev, dtype = _device_of(first, "q" if q is not None else "k"), first.dtype
+    T, _, D = first.shape
+    side = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            side.append((None, 0, None, 0, 0))
+            continue
+        shape = (T, x.shape[1], D)
+        p, ld = _token_rows(x, name, shape, dtype, dev)
+        po, ldo = (p, ld) if out is None else _token_rows(out, name + "_out", shape, dtype, dev)
+        side.append((po, ldo, p, ld, shape[1]))
+    args = (*side[0][:4], *side[1][:4], _code(first), *_rope_args(table, positions, T, dev), T, side[0][4], side[1][4], D,
+            _stream(stream, dev))
+    return _issue(_L.paged_rope, args, "paged_rope", prepare)
+
+
+def _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev):
+    T, Hq = q.shape[0], q.shape[1]
+    dtype, kv = q.dtype, (T, Hkv, D)
+    p, ld = _token_rows(q, "q", (T, Hq, D), dtype, dev)
+    po, ldo = (p, ld) if q_out is None else _token_rows(q_out, "q_out", (T, Hq, D), dtype, dev)
+    return (po, ldo, p, ld, *_token_rows(k_new, "k_new", kv, dtype, dev), *_token_rows(v_new, "v_new", kv, dtype, dev), _code(q)), T, Hq
+
+
+def paged_rope_append(q, k_new, v_new, positions, table, k_cache, v_cache, slot_mapping, q_out=None, stream=None,
+                      prepare=False):
+    """Rotates q [T, Hq, D] (into q_out; None: in place) and k_new [T, Hkv, D]
+    by their positions [T] (int64), and writes the rotated keys and v_new into the caches
+    [num_blocks, Hkv, 16, D] of the same type at slot_mapping [T] (int64; < 0 skips)."""
+    dev = _device_of(q, "q")
+    k, v, _, _, num_blocks, Hkv, D = _cache(k_cache, v_cache, None, None, dev)
+    if k_cache.dtype is not q.dtype:
+        raise TypeError(f"the cache must be {q.dtype}, got {k_cache.dtype}")
+    rows, T, Hq = _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev)
+    args = (*rows, *_rope_args(table, positions, T, dev), k, v,
+            _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev), T, Hq, Hkv, D, num_blocks, _stream(stream, dev))
+    return _issue(_L.paged_rope_append, args, "paged_rope_append", prepare)
+
+
+def paged_kv4_rope_append(q, k_new, v_new, positions, table, cache, slot_mapping, k_unit=1.0, v_unit=1.0, q_out=None,
+                          stream=None, prepare=False):
+    """paged_rope_append into a 4-bit cache, uint8 [num_blocks, Hkv, 18 * D]."""
+    dev = _device_of(q, "q")
+    ptr, num_blocks, Hkv, D = _cache4(cache, dev)
+    rows, T, Hq = _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev)
+    args = (*rows, *_rope_args(table, positions, T, dev), ptr,
+            _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev), T, Hq, Hkv, D, num_blocks, float(k_unit),
+            float(v_unit), _stream(stream, dev))
+    return _issue(_L.paged_kv4_rope_append, args, "paged_kv4_rope_append", prepare)
 
 
 class BlockManager:

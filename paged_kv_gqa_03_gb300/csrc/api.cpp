@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "kv4.h"
 #include "pagedkv.h"
 #include "mq_decode.h"
 #include "prefill.h"
@@ -76,6 +77,7 @@ Registry &registry() {
     r.n += register_decode_f32(r.k + r.n);
     r.n += register_decode_tree(r.k + r.n);
     r.n += register_decode_tree_fp8(r.k + r.n);
+    r.n += register_decode_kv4(r.k + r.n);
   });
   return r;
 }
@@ -270,7 +272,7 @@ struct Choice {
 };
 
 // Picks the kernel for a shape: tensor cores (8-row units, unused columns
-// padded; 16-row units on fp8 caches past 8 rows) for every group size on
+// padded; 16-row units on fp8 and 4-bit caches past 8 rows) for every group size on
 // 16-bit and fp8 caches — even for
 // MHA the mma.sync block step measured faster on GB300 than the CUDA-core one
 // (5.83 vs 5.56 TB/s, fp16 MHA layer) — and CUDA cores for fp32 caches.  The
@@ -308,7 +310,7 @@ int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c, bool tr
   // 32K fp8 layer at 16 rows, one 16-row unit per kv head against two 8-row
   // units streaming the same blocks)
   int GC = mma ? 8 : (R >= 2 ? 2 : 1);
-  if (mma && cache_dtype == PKV_FP8_E4M3 && R > 8 && want_gc != 8) GC = 16;
+  if (mma && (cache_dtype == PKV_FP8_E4M3 || cache_dtype == kKv4) && R > 8 && want_gc != 8) GC = 16;
   Registry &r = registry();
   int first = -1;
   for (int pass = 0; pass < 2 && first < 0; ++pass) {
@@ -533,32 +535,13 @@ static cudaError_t launch_prefill_auto(const PrefillParams &p, int cache_dtype, 
   return tiles ? launch_prefill_tiles(p, cache_dtype, tmK, tmV, s) : launch_prefill(p, cache_dtype, tmK, tmV, s);
 }
 
-// The decode kernel (8- or 16-row units, one partition per warp) and its
-// split-KV merge: single-token decode, and several new tokens per sequence on
-// the unit route, causal or (tree) under per-node masks.
-struct TreeArgs {
-  const uint64_t *mask;
-  const int32_t *lens;
-  int mask_stride;
-};
-static int run_units(const Choice &c, int P, void *out, const void *q, int q_dtype, const void *k_cache,
-                     const void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
-                     const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens, int B, int q_len,
-                     int window, int Hq, int Hkv, int D, int64_t num_blocks, float scale, void *workspace,
-                     pkv_stream_t stream, const TreeArgs *tree) {
+// A call's parameters for the decode kernels that stream units (decode.cuh,
+// kv4_decode.cu) and for their merge.
+static DecodeParams unit_params(const Choice &c, int P, void *out, const void *q, int q_dtype, const float *k_scale,
+                                const float *v_scale, const int32_t *block_table, int max_blocks_per_seq,
+                                const int32_t *context_lens, int B, int q_len, int window, int Hq, int Hkv, int D,
+                                int64_t num_blocks, float scale, void *workspace) {
   const WsLayout L = ws_layout(B, P, D, c.GC);
-  int rc = PKV_OK;
-  const DecodeKernel &k = registry().k[c.ki];
-  int ctas = 0, sms = 0;
-  rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
-  if (rc != PKV_OK) return rc;
-
-  CUtensorMap tmK, tmV;
-  rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
-  if (rc != PKV_OK) return rc;
-  rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
-  if (rc != PKV_OK) return rc;
-
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));
@@ -592,23 +575,19 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
   p.max_blocks = max_blocks_per_seq;
   p.out_dtype = q_dtype;
   p.scale_log2 = scale * 1.4426950408889634f;
-  if (tree) {
-    p.tree_mask = tree->mask;
-    p.tree_lens = tree->lens;
-    p.mask_stride = tree->mask_stride;
-    p.v_cache = v_cache;
-  }
-  take_stall(p, PKV_STALL_DECODE);
-
   p.inline_plan = B + 1 <= kInlinePrefix ? 1 : 0;
-  p.n_ctas = (P + k.warps - 1) / k.warps;
+  p.n_ctas = (P + registry().k[c.ki].warps - 1) / registry().k[c.ki].warps;
+  take_stall(p, PKV_STALL_DECODE);
+  return p;
+}
 
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+// Plan (large batches), decode kernel and merge.
+static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, void **args, cudaStream_t s) {
   const bool pdl = s != nullptr;  // programmatic launch on explicit streams only
   cudaError_t e = cudaSuccess;
   if (!p.inline_plan) {
     e = launch_plan(p, s);
-    if (e != cudaSuccess) return cuda_status(e);
+    if (e != cudaSuccess) return e;
   }
 
   cudaLaunchConfig_t cfg = {};
@@ -621,11 +600,44 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  void *args[3] = {&p, &tmK, &tmV};
   e = cudaLaunchKernelExC(&cfg, k.fn, args);
-  if (e != cudaSuccess) return cuda_status(e);
-  e = launch_splitk_merge(p, s, pdl);
-  return cuda_status(e);
+  if (e != cudaSuccess) return e;
+  return launch_splitk_merge(p, s, pdl);
+}
+
+// The decode kernel (8- or 16-row units, one partition per warp) and its
+// split-KV merge: single-token decode, and several new tokens per sequence on
+// the unit route, causal or (tree) under per-node masks.
+struct TreeArgs {
+  const uint64_t *mask;
+  const int32_t *lens;
+  int mask_stride;
+};
+static int run_units(const Choice &c, int P, void *out, const void *q, int q_dtype, const void *k_cache,
+                     const void *v_cache, int cache_dtype, const float *k_scale, const float *v_scale,
+                     const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens, int B, int q_len,
+                     int window, int Hq, int Hkv, int D, int64_t num_blocks, float scale, void *workspace,
+                     pkv_stream_t stream, const TreeArgs *tree) {
+  int ctas = 0, sms = 0;
+  int rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
+  if (rc != PKV_OK) return rc;
+
+  CUtensorMap tmK, tmV;
+  rc = cache_map(&tmK, k_cache, cache_dtype, num_blocks, Hkv, D);
+  if (rc != PKV_OK) return rc;
+  rc = cache_map(&tmV, v_cache, cache_dtype, num_blocks, Hkv, D);
+  if (rc != PKV_OK) return rc;
+
+  DecodeParams p = unit_params(c, P, out, q, q_dtype, k_scale, v_scale, block_table, max_blocks_per_seq, context_lens, B,
+                               q_len, window, Hq, Hkv, D, num_blocks, scale, workspace);
+  if (tree) {
+    p.tree_mask = tree->mask;
+    p.tree_lens = tree->lens;
+    p.mask_stride = tree->mask_stride;
+    p.v_cache = v_cache;
+  }
+  void *args[3] = {&p, &tmK, &tmV};
+  return cuda_status(launch_units(registry().k[c.ki], p, args, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // The call's parameters for the kernels that share the stream-K schedule
@@ -1112,6 +1124,52 @@ int pkv_copy(void *dst, const void *src, size_t bytes, pkv_stream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_copy(dst, src, bytes, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int paged_kv4_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int q_dtype, int num_splits,
+                                     size_t *bytes_out) {
+  if (!bytes_out) return PKV_EINVAL;
+  if (q_dtype == PKV_F32) return PKV_EUNSUPPORTED;
+  int rc = validate_decode_shapes(q_dtype, q_dtype, B, q_len, Hq, Hkv, D, 1, 1);
+  if (rc != PKV_OK) return rc;
+  Choice c;
+  int P = 0;
+  rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
+  if (rc != PKV_OK) return rc;
+  *bytes_out = ws_layout(B, P, D, c.GC).total;
+  return PKV_OK;
+}
+
+int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void *cache, const int32_t *block_table,
+                               int max_blocks_per_seq, const int32_t *context_lens, int B, int q_len, int window,
+                               int Hq, int Hkv, int D, int64_t num_blocks, float scale, float k_unit, float v_unit,
+                               int num_splits, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (q_dtype == PKV_F32) return PKV_EUNSUPPORTED;
+  int rc = validate_decode_shapes(q_dtype, q_dtype, B, q_len, Hq, Hkv, D, num_blocks, max_blocks_per_seq);
+  if (rc != PKV_OK) return rc;
+  if (window < 0 || !kv4_unit_ok(k_unit) || !kv4_unit_ok(v_unit)) return PKV_EINVAL;
+  const float s = scale * k_unit;
+  if (!std::isfinite(scale) || !std::isfinite(s * 1.4426950408889634f)) return PKV_EINVAL;
+  if (B == 0) return PKV_OK;
+  if (!out || !q || !cache || !block_table || !context_lens) return PKV_EINVAL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(cache)) return PKV_EINVAL;
+  Choice c;
+  int P = 0;
+  rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
+  if (rc != PKV_OK) return rc;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < ws_layout(B, P, D, c.GC).total)
+    return PKV_EWORKSPACE;
+  int ctas = 0, sms = 0;
+  rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
+  if (rc != PKV_OK) return rc;
+  Kv4Params p;
+  p.d = unit_params(c, P, out, q, q_dtype, nullptr, nullptr, block_table, max_blocks_per_seq, context_lens, B, q_len,
+                    window, Hq, Hkv, D, num_blocks, s, workspace);
+  p.cache = static_cast<const uint8_t *>(cache);
+  p.v_unit = v_unit;
+  void *args[1] = {&p};
+  return cuda_status(launch_units(registry().k[c.ki], p.d, args, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,165 @@
+// kv4_pages.cu — rows into and out of the 4-bit cache's pages (kv4.cuh): the
+// append of new tokens, whole pages packed from 16 bits and expanded back, and
+// the copy-on-write copy.
+//
+// One thread quantises or expands a group of 16 elements: the scale needs
+// nothing of another thread, a warp's loads and stores of codes are whole
+// lines, and every output byte is written by one thread.  All are bound by
+// HBM: a token and head read or write 4 D bytes in 16 bits and 18 D / 16 in 4.
+#include "kv4.cuh"
+#include "kv4.h"
+
+namespace pkv {
+
+constexpr int kThreads = 256;
+
+static cudaLaunchConfig_t config(int64_t threads, cudaLaunchAttribute *attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = stream != nullptr ? 1 : 0;  // early launch on explicit streams only
+  return cfg;
+}
+
+// Thread -> (token, K or V, head, group), the group fastest.
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+    kv4_append_kernel(const void *__restrict__ k_new, int64_t ld_k, const void *__restrict__ v_new, int64_t ld_v,
+                      uint8_t *cache, const int64_t *__restrict__ slots, int T_, int Hkv, int64_t num_blocks,
+                      float k_unit, float v_unit) {
+  grid_dep_wait();
+  constexpr int G = D / 16;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int g = (int)(i % G);
+  const int64_t row = i / G;
+  const int per = 2 * Hkv;
+  const int64_t t = row / per;
+  if (t >= T_) return;
+  const int hv = (int)(row - t * per), h = hv < Hkv ? hv : hv - Hkv;
+  const bool v = hv >= Hkv;
+  const int64_t slot = slots[t];
+  if (slot < 0 || slot / kBlock >= num_blocks) return;
+  float y[16];
+  load16<T>(v ? v_new : k_new, (size_t)(t * (v ? ld_v : ld_k)) + (size_t)h * D + 16 * g, y);
+  const Kv4Group x = kv4_quantise(y, v ? v_unit : k_unit);
+  kv4_store<D>(cache + (size_t)(slot / kBlock * Hkv + h) * Kv4Tile<D>::kBytes, v, (int)(slot % kBlock), g, x);
+}
+
+// Thread -> (pair, head, K or V, token, group), the group fastest.
+struct PageThread {
+  int64_t pair;
+  int h, tok, g;
+  bool v;
+};
+template <int D>
+__device__ __forceinline__ PageThread page_thread(int Hkv) {
+  constexpr int G = D / 16, kTile = 2 * kBlock * G;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int in = (int)(i % kTile);
+  const int64_t tile = i / kTile;
+  PageThread p;
+  p.g = in % G;
+  p.tok = in / G % kBlock;
+  p.v = in >= kTile / 2;
+  p.pair = tile / Hkv;
+  p.h = (int)(tile - p.pair * Hkv);
+  return p;
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+    kv4_pack_kernel(uint8_t *cache, int64_t num_blocks, const void *__restrict__ k, const void *__restrict__ vv,
+                    int64_t num_src, const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
+  grid_dep_wait();
+  const PageThread p = page_thread<D>(Hkv);
+  if (p.pair >= n) return;
+  const int src = pairs[2 * p.pair], dst = pairs[2 * p.pair + 1];
+  if (src < 0 || src >= num_src || dst < 0 || dst >= num_blocks) return;
+  float y[16];
+  load16<T>(p.v ? vv : k, (((size_t)src * Hkv + p.h) * kBlock + p.tok) * D + 16 * p.g, y);
+  const Kv4Group x = kv4_quantise(y, p.v ? v_unit : k_unit);
+  kv4_store<D>(cache + ((size_t)dst * Hkv + p.h) * Kv4Tile<D>::kBytes, p.v, p.tok, p.g, x);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+    kv4_expand_kernel(void *k, void *vv, int64_t num_dst, const uint8_t *__restrict__ cache, int64_t num_blocks,
+                      const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
+  grid_dep_wait();
+  const PageThread p = page_thread<D>(Hkv);
+  if (p.pair >= n) return;
+  const int src = pairs[2 * p.pair], dst = pairs[2 * p.pair + 1];
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_dst) return;
+  const Kv4Group x =
+      kv4_load<D>(cache + ((size_t)src * Hkv + p.h) * Kv4Tile<D>::kBytes, p.v, p.tok, p.g);
+  float y[16];
+  kv4_values(x, p.v ? v_unit : k_unit, y);
+  store16<T>(p.v ? vv : k, (((size_t)dst * Hkv + p.h) * kBlock + p.tok) * D + 16 * p.g, y);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    kv4_copy_kernel(uint8_t *cache, const int32_t *__restrict__ pairs, size_t block_bytes, int64_t num_blocks) {
+  grid_dep_wait();
+  const int src = pairs[2 * blockIdx.x], dst = pairs[2 * blockIdx.x + 1];
+  if (src < 0 || dst < 0 || src >= num_blocks || dst >= num_blocks || src == dst) return;
+  const uint4 *s = reinterpret_cast<const uint4 *>(cache + (size_t)src * block_bytes);
+  uint4 *d = reinterpret_cast<uint4 *>(cache + (size_t)dst * block_bytes);
+  for (size_t i = threadIdx.x; i < block_bytes / 16; i += kThreads) d[i] = s[i];
+}
+
+// f(T{}, integral_constant<int, D>) of a (dtype, head dim).
+template <class F>
+static cudaError_t dispatch(int dtype, int D, F f) {
+  if (dtype == PKV_F32) return D == 128 ? f(F32{}, Kv4Tile<128>{}) : f(F32{}, Kv4Tile<64>{});
+  if (dtype == PKV_F16) return D == 128 ? f(F16{}, Kv4Tile<128>{}) : f(F16{}, Kv4Tile<64>{});
+  return D == 128 ? f(BF16{}, Kv4Tile<128>{}) : f(BF16{}, Kv4Tile<64>{});
+}
+
+cudaError_t launch_kv4_append(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_v, int new_dtype,
+                              uint8_t *cache, const int64_t *slots, int T, int Hkv, int D, int64_t num_blocks,
+                              float k_unit, float v_unit, cudaStream_t stream) {
+  return dispatch(new_dtype, D, [&](auto type, auto tile) {
+    constexpr int DD = decltype(tile)::kGroups * 16;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config((int64_t)T * 2 * Hkv * (DD / 16), attr, stream);
+    return cudaLaunchKernelEx(&cfg, kv4_append_kernel<decltype(type), DD>, k_new, ld_k, v_new, ld_v, cache, slots, T,
+                              Hkv, num_blocks, k_unit, v_unit);
+  });
+}
+
+cudaError_t launch_kv4_pack(uint8_t *cache, int64_t num_blocks, const void *k, const void *v, int dtype,
+                            int64_t num_src, const int32_t *pairs, int n, int Hkv, int D, float k_unit, float v_unit,
+                            cudaStream_t stream) {
+  return dispatch(dtype, D, [&](auto type, auto tile) {
+    constexpr int DD = decltype(tile)::kGroups * 16;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * 2 * kBlock * (DD / 16), attr, stream);
+    return cudaLaunchKernelEx(&cfg, kv4_pack_kernel<decltype(type), DD>, cache, num_blocks, k, v, num_src, pairs, n,
+                              Hkv, k_unit, v_unit);
+  });
+}
+
+cudaError_t launch_kv4_expand(void *k, void *v, int dtype, int64_t num_dst, const uint8_t *cache, int64_t num_blocks,
+                              const int32_t *pairs, int n, int Hkv, int D, float k_unit, float v_unit,
+                              cudaStream_t stream) {
+  return dispatch(dtype, D, [&](auto type, auto tile) {
+    constexpr int DD = decltype(tile)::kGroups * 16;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * 2 * kBlock * (DD / 16), attr, stream);
+    return cudaLaunchKernelEx(&cfg, kv4_expand_kernel<decltype(type), DD>, k, v, num_dst, cache, num_blocks, pairs, n,
+                              Hkv, k_unit, v_unit);
+  });
+}
+
+cudaError_t launch_kv4_copy(uint8_t *cache, const int32_t *pairs, int n, size_t block_bytes, int64_t num_blocks,
+                            cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config((int64_t)n * kThreads, attr, stream);
+  return cudaLaunchKernelEx(&cfg, kv4_copy_kernel, cache, pairs, block_bytes, num_blocks);
+}
+
+}  // namespace pkv
