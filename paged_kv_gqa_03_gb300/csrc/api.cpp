@@ -54,6 +54,27 @@ WsLayout ws_layout(int B, int P, int D, int GC) {
   return L;
 }
 
+Kv4WsLayout kv4_ws_layout(int B, int P, int D, int GC, int hg, int warps) {
+  Kv4WsLayout L;
+  size_t o = 0;
+  L.hdr = o;
+  o = align_up(o + sizeof(WsHeader), 256);
+  L.prefix = o;
+  o = align_up(o + sizeof(int32_t) * (size_t)(B + 1), 256);
+  L.starts = o;
+  o = align_up(o + sizeof(int4) * (size_t)(P + 1), 256);
+  L.records = o;
+  o = align_up(o + sizeof(int4) * (size_t)P, 256);
+  L.part_o = o;  // [P][2][hg][GC][D]
+  o = align_up(o + sizeof(float) * (size_t)P * 2 * hg * GC * D, 256);
+  L.part_lse = o;
+  o = align_up(o + sizeof(float) * (size_t)P * 2 * hg * GC, 256);
+  L.first_o = o;
+  o = align_up(o + sizeof(float) * (size_t)P * warps * GC * D, 256);
+  L.total = o;
+  return L;
+}
+
 // ---------------------------------------------------------------------------
 // Kernel registry and per-device facts.
 // ---------------------------------------------------------------------------
@@ -127,7 +148,7 @@ int kernel_occupancy(int ki, int *ctas_per_sm, int *sm_count) {
     e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem_bytes);
     if (e != cudaSuccess) return cuda_status(e);
     int nb = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, k.fn, k.warps * 32, k.smem_bytes);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, k.fn, k.threads, k.smem_bytes);
     if (e != cudaSuccess) return cuda_status(e);
     if (nb <= 0) return PKV_EUNSUPPORTED;
     f.ctas_per_sm[ki] = nb;
@@ -581,7 +602,12 @@ static DecodeParams unit_params(const Choice &c, int P, void *out, const void *q
   return p;
 }
 
-// Plan (large batches), decode kernel and merge.
+// Ranges of the 4-bit attention, one per CTA: num_splits, or one per SM.
+static int kv4_ranges(int P, int ki, int num_splits) {
+  return std::min(num_splits > 0 ? num_splits : P / registry().k[ki].warps, kKv4MaxRanges);
+}
+
+// Plan (large batches) and decode kernel.
 static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, void **args, cudaStream_t s) {
   const bool pdl = s != nullptr;  // programmatic launch on explicit streams only
   cudaError_t e = cudaSuccess;
@@ -592,7 +618,7 @@ static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, vo
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_ctas);
-  cfg.blockDim = dim3(k.warps * 32);
+  cfg.blockDim = dim3(k.threads);
   cfg.dynamicSmemBytes = k.smem_bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -600,9 +626,7 @@ static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, vo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelExC(&cfg, k.fn, args);
-  if (e != cudaSuccess) return e;
-  return launch_splitk_merge(p, s, pdl);
+  return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
 // The decode kernel (8- or 16-row units, one partition per warp) and its
@@ -637,7 +661,10 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
     p.v_cache = v_cache;
   }
   void *args[3] = {&p, &tmK, &tmV};
-  return cuda_status(launch_units(registry().k[c.ki], p, args, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_units(registry().k[c.ki], p, args, s);
+  if (e == cudaSuccess) e = launch_splitk_merge(p, s, s != nullptr);
+  return cuda_status(e);
 }
 
 // The call's parameters for the kernels that share the stream-K schedule
@@ -1136,7 +1163,7 @@ int paged_kv4_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, i
   int P = 0;
   rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
   if (rc != PKV_OK) return rc;
-  *bytes_out = ws_layout(B, P, D, c.GC).total;
+  *bytes_out = kv4_ws_layout(B, kv4_ranges(P, c.ki, num_splits), D, c.GC, kv4_heads(Hkv), registry().k[c.ki].warps).total;
   return PKV_OK;
 }
 
@@ -1157,19 +1184,38 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   int P = 0;
   rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
   if (rc != PKV_OK) return rc;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < ws_layout(B, P, D, c.GC).total)
+  P = kv4_ranges(P, c.ki, num_splits);
+  const DecodeKernel &k = registry().k[c.ki];
+  const Kv4WsLayout L = kv4_ws_layout(B, P, D, c.GC, kv4_heads(Hkv), k.warps);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < L.total)
     return PKV_EWORKSPACE;
   int ctas = 0, sms = 0;
   rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
   if (rc != PKV_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   Kv4Params p;
   p.d = unit_params(c, P, out, q, q_dtype, nullptr, nullptr, block_table, max_blocks_per_seq, context_lens, B, q_len,
                     window, Hq, Hkv, D, num_blocks, s, workspace);
+  p.d.hdr = reinterpret_cast<WsHeader *>(ws + L.hdr);
+  p.d.prefix = reinterpret_cast<int32_t *>(ws + L.prefix);
+  p.d.starts = reinterpret_cast<int4 *>(ws + L.starts);
+  p.d.part_o = reinterpret_cast<float *>(ws + L.part_o);
+  p.d.part_lse = reinterpret_cast<float *>(ws + L.part_lse);
+  p.d.cta_flags = nullptr;
+  p.d.n_ctas = P;
+  p.d.inline_plan = B + 1 <= kKv4Prefix ? 1 : 0;
   p.cache = static_cast<const uint8_t *>(cache);
+  p.hg = kv4_heads(Hkv);
+  p.d.HU = Hkv / p.hg * c.NC;
+  p.records = reinterpret_cast<int4 *>(ws + L.records);
+  p.first_o = reinterpret_cast<float *>(ws + L.first_o);
   p.v_unit = v_unit;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   void *args[1] = {&p};
-  return cuda_status(launch_units(registry().k[c.ki], p.d, args, reinterpret_cast<cudaStream_t>(stream)));
+  cudaError_t e = launch_units(k, p.d, args, st);
+  // a table of no more blocks: no unit is cut between CTAs
+  if (e == cudaSuccess && max_blocks_per_seq > kKv4Whole && P > 1) e = launch_kv4_merge(p, st, st != nullptr);
+  return cuda_status(e);
 }
 
 }  // extern "C"

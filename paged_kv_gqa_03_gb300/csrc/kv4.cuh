@@ -10,9 +10,10 @@
 //
 // A (block, kv head) tile is 18 D bytes, one contiguous run that one bulk copy fetches:
 //   K codes [16 tokens][D / 2], the even element of a pair in the byte's lower half;
-//   V codes [8 token pairs][128 or 64 bytes]: 16 bytes (D = 128: 16 elements of both tokens of
-//     the pair, D = 64: 8 bytes, 8 elements of both) at chunk c ^ 2 (u & 3) (D = 64: c ^ 4 (u / 2 & 1))
-//     of pair u: the decode kernel's lanes then read all of V without bank conflicts;
+//   V codes [8 token pairs][D bytes]: byte d holds element d of both tokens, the even one in
+//     the lower half: that is how the decode kernel's MMA operand pairs them.  Chunks c of 16 bytes (D = 128;
+//     8 at D = 64) stand at c ^ 2 (u & 3) (D = 64: c ^ 4 (u / 2 & 1)) of pair u: the kernel's lanes then read
+//     all of V without bank conflicts;
 //   K scales [16 tokens][D / 16];
 //   V scales [8 token pairs][D / 16][2 tokens]: the pair's two scales are one 16-bit load.
 #pragma once
@@ -29,13 +30,12 @@ struct Kv4Tile {
   static constexpr int kVCodes = 8 * D, kKScales = 16 * D, kVScales = 17 * D, kBytes = 18 * D;
   static __device__ __forceinline__ int k_code(int tok, int g) { return tok * (D / 2) + 8 * g; }
   static __device__ __forceinline__ int k_scale(int tok, int g) { return kKScales + tok * kGroups + g; }
-  // D = 128: 8 bytes.  D = 64: 4 bytes here and 4 bytes 8 further.
-  static __device__ __forceinline__ int v_code(int tok, int g) {
-    const int u = tok >> 1;
+  // 16 bytes: elements 16 g .. of the token pair u (D = 64: two chunks, which stay neighbours)
+  static __device__ __forceinline__ int v_code(int u, int g) {
     if constexpr (D == 128)
-      return kVCodes + u * 128 + ((g ^ (2 * (u & 3))) << 4) + (tok & 1) * 8;
+      return kVCodes + u * 128 + ((g ^ (2 * (u & 3))) << 4);
     else
-      return kVCodes + u * 64 + (((2 * g) ^ (4 * ((u >> 1) & 1))) << 3) + (tok & 1) * 4;
+      return kVCodes + u * 64 + (((2 * g) ^ (4 * ((u >> 1) & 1))) << 3);
   }
   static __device__ __forceinline__ int v_scale(int tok, int g) {
     return kVScales + (tok >> 1) * (2 * kGroups) + 2 * g + (tok & 1);
@@ -103,42 +103,70 @@ __device__ __forceinline__ void kv4_values(const Kv4Group &g, float unit, float 
   }
 }
 
-template <int D>
-__device__ __forceinline__ void kv4_store(uint8_t *tile, bool v, int tok, int g, const Kv4Group &x) {
-  using Tile = Kv4Tile<D>;
-  if (!v) {
-    *reinterpret_cast<uint2 *>(tile + Tile::k_code(tok, g)) = x.codes;
-    tile[Tile::k_scale(tok, g)] = x.scale;
-  } else {
-    uint8_t *c = tile + Tile::v_code(tok, g);
-    if constexpr (D == 128) {
-      *reinterpret_cast<uint2 *>(c) = x.codes;
-    } else {
-      *reinterpret_cast<uint32_t *>(c) = x.codes.x;
-      *reinterpret_cast<uint32_t *>(c + 8) = x.codes.y;
-    }
-    tile[Tile::v_scale(tok, g)] = x.scale;
-  }
+// Codes of 16 elements of two tokens <-> bytes that hold an element of both.
+__device__ __forceinline__ uint32_t spread_nibbles(uint32_t w) {  // 4 nibbles (low half) -> the low halves of 4 bytes
+  w = (w | (w << 8)) & 0x00ff00ffu;
+  return (w | (w << 4)) & 0x0f0f0f0fu;
+}
+__device__ __forceinline__ uint32_t gather_nibbles(uint32_t w) {  // and back
+  w &= 0x0f0f0f0fu;
+  w = (w | (w >> 4)) & 0x00ff00ffu;
+  return (w | (w >> 8)) & 0xffffu;
+}
+__device__ __forceinline__ uint4 spread16(uint2 c) {
+  return make_uint4(spread_nibbles(c.x & 0xffffu), spread_nibbles(c.x >> 16), spread_nibbles(c.y & 0xffffu),
+                    spread_nibbles(c.y >> 16));
 }
 
 template <int D>
-__device__ __forceinline__ Kv4Group kv4_load(const uint8_t *tile, bool v, int tok, int g) {
+__device__ __forceinline__ void kv4_store_k(uint8_t *tile, int tok, int g, const Kv4Group &x) {
+  using Tile = Kv4Tile<D>;
+  *reinterpret_cast<uint2 *>(tile + Tile::k_code(tok, g)) = x.codes;
+  tile[Tile::k_scale(tok, g)] = x.scale;
+}
+// Both tokens of pair u.
+template <int D>
+__device__ __forceinline__ void kv4_store_v2(uint8_t *tile, int u, int g, const Kv4Group &a, const Kv4Group &b) {
+  using Tile = Kv4Tile<D>;
+  const uint4 x = spread16(a.codes), y = spread16(b.codes);
+  *reinterpret_cast<uint4 *>(tile + Tile::v_code(u, g)) = make_uint4(x.x | y.x << 4, x.y | y.y << 4, x.z | y.z << 4, x.w | y.w << 4);
+  *reinterpret_cast<uint16_t *>(tile + Tile::v_scale(2 * u, g)) = (uint16_t)(a.scale | b.scale << 8);
+}
+// One token, whose neighbour's nibbles another thread may be writing: the difference to what stands there
+// in this token's own nibbles, which no one else writes, goes in by an exclusive or.
+template <int D>
+__device__ __forceinline__ void kv4_store_v1(uint8_t *tile, int tok, int g, const Kv4Group &a) {
+  using Tile = Kv4Tile<D>;
+  const int sh = 4 * (tok & 1);
+  const uint4 x = spread16(a.codes);
+  uint32_t *c = reinterpret_cast<uint32_t *>(tile + Tile::v_code(tok >> 1, g));
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t old = *reinterpret_cast<volatile uint32_t *>(c + i);
+    atomicXor(c + i, (old ^ (w[i] << sh)) & (0x0f0f0f0fu << sh));
+  }
+  tile[Tile::v_scale(tok, g)] = a.scale;
+}
+
+template <int D>
+__device__ __forceinline__ Kv4Group kv4_load_k(const uint8_t *tile, int tok, int g) {
   using Tile = Kv4Tile<D>;
   Kv4Group x;
-  if (!v) {
-    x.codes = *reinterpret_cast<const uint2 *>(tile + Tile::k_code(tok, g));
-    x.scale = tile[Tile::k_scale(tok, g)];
-  } else {
-    const uint8_t *c = tile + Tile::v_code(tok, g);
-    if constexpr (D == 128) {
-      x.codes = *reinterpret_cast<const uint2 *>(c);
-    } else {
-      x.codes.x = *reinterpret_cast<const uint32_t *>(c);
-      x.codes.y = *reinterpret_cast<const uint32_t *>(c + 8);
-    }
-    x.scale = tile[Tile::v_scale(tok, g)];
-  }
+  x.codes = *reinterpret_cast<const uint2 *>(tile + Tile::k_code(tok, g));
+  x.scale = tile[Tile::k_scale(tok, g)];
   return x;
+}
+template <int D>
+__device__ __forceinline__ void kv4_load_v2(const uint8_t *tile, int u, int g, Kv4Group &a, Kv4Group &b) {
+  using Tile = Kv4Tile<D>;
+  const uint4 c = *reinterpret_cast<const uint4 *>(tile + Tile::v_code(u, g));
+  const uint16_t sc = *reinterpret_cast<const uint16_t *>(tile + Tile::v_scale(2 * u, g));
+  a.codes = make_uint2(gather_nibbles(c.x) | gather_nibbles(c.y) << 16, gather_nibbles(c.z) | gather_nibbles(c.w) << 16);
+  b.codes = make_uint2(gather_nibbles(c.x >> 4) | gather_nibbles(c.y >> 4) << 16,
+                       gather_nibbles(c.z >> 4) | gather_nibbles(c.w >> 4) << 16);
+  a.scale = (uint8_t)(sc & 0xff);
+  b.scale = (uint8_t)(sc >> 8);
 }
 
 // 16 consecutive elements (16-byte aligned) <-> floats.

@@ -11,12 +11,31 @@ inline bool kv4_unit_ok(float u) { return u > 0.f && u <= 3.402823466e38f; }
 
 constexpr int kKv4 = 4;  // DecodeKernel::cache_dtype of the 4-bit variants (no public dtype code)
 
+constexpr int kKv4MaxRanges = 224;  // WsHeader::cta_status
+
+// Batches of fewer sequences are planned inside the decode kernel.
+constexpr int kKv4Prefix = 512;
+
+// Units of at most this many blocks are not cut between CTAs (kv4_decode.cu).
+constexpr int kKv4Whole = 48;
+
 struct Kv4Params {
-  DecodeParams d;  // (k_scale, v_scale unused; scale_log2 holds K's unit)
+  DecodeParams d;  // P: ranges, one per CTA; scale_log2 holds K's unit; k_scale, v_scale, cta_flags unused
   const uint8_t *cache;
+  int hg;          // heads of a unit (d.HU: units of a sequence = Hkv / hg * d.NC)
+  int4 *records;   // [P]: the units that a CTA's range cuts (kv4_decode.cu)
+  float *first_o;  // [P][warps][GC][D]: a ring's first segment, to be joined in its CTA
   float v_unit;
 };
+struct Kv4WsLayout {
+  size_t hdr, prefix, starts, records, part_o, part_lse, first_o, total;
+};
+Kv4WsLayout kv4_ws_layout(int B, int P, int D, int GC, int hg, int warps);
+// Heads that a unit takes together: neighbours in the cache, read by one copy.
+inline int kv4_heads(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
 int register_decode_kv4(DecodeKernel *out);
+// Joins the units cut between CTAs.
+cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t stream, bool pdl);
 
 // Rows of new tokens, `ld` elements apart.
 cudaError_t launch_kv4_append(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_v, int new_dtype,

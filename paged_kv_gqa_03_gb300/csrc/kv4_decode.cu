@@ -1,9 +1,18 @@
 // kv4_decode.cu — decode attention over the 4-bit cache (kv4.cuh).
 //
-// The mathematics, the work split and the workspace are the decode kernel's
-// (decode.cuh): units of 8 or 16 query rows of a (sequence, kv head), their
-// blocks cut into equal ranges, one per warp, an online softmax per warp, and the
-// split-KV merge.  What differs is what 4 bits change.
+// The mathematics is the decode kernel's (decode.cuh): units of 8 or 16 query rows of a
+// (sequence, kv head), an online softmax per warp, partial results joined by their log-sum-exp.
+//
+// Split.  A unit is 8 or 16 rows of hg = 4 (2, 1) neighbouring kv heads of a sequence, which are
+// neighbours in the cache too: hg warps share a ring, one copy of hg tiles feeds them all, each takes its head's.  (The
+// issue of copies bounds otherwise: a warp issues one in 220 cycles, four warps of an SM one in 85, so
+// that copies of one tile reach 27 bytes a cycle out of L2 where 4-tile copies reach 70.)  The list
+// of all units' blocks is cut into equal ranges, one per CTA, and a range into one per ring.
+// What rings hold of one unit is joined in the CTA, through the rings' shared memory; a unit cut
+// between CTAs leaves one partial result in each, which a merge kernel joins.  (Joined there ring by
+// ring, a long context's 228 partial results a unit took the merge 53 us.)  A CTA's cut that falls into a unit of at
+// most kKv4Whole blocks moves to the unit's nearer end: 2 us of work at most, where the merge launch
+// costs 3 to 5; with no longer table it is not launched at all.
 //
 // Bound.  A token and kv head are 144 bytes (D = 128) for 256 elements to be
 // widened, so at HBM speed an SM has 0.4 cycles an element: instructions, not bytes,
@@ -12,13 +21,15 @@
 // mma.sync m16n8k16 in f16 with 32-bit sums.
 //  * A stage is NB = 4 blocks of one unit: one barrier, one record and one softmax
 //    update (maximum exchange, rescale) for 64 tokens.
-//  * A block's tile is one bulk copy, issued by the lane of its own block.
+//  * Four producer warps fill the rings, a lane each: the walk over units and table entries and the copies
+//    then cost the consumers nothing; they were 80 instructions a block.  (16-byte cp.async by the consumers
+//    reaches HBM speed later, 4.3 TB/s while the rings fill.)
 //  * K: a lane owns 32 consecutive elements (two scale groups) of rows gid and
 //    gid + 8: one 16-byte load a row, the order of d within the contraction being free
 //    (q's fragments are loaded in the same order).
 //  * V: a lane owns 16 elements (D = 64: 8) of d for token pairs tig and tig + 4.  A
-//    fragment pairs neighbouring tokens, so the two tokens' words are interleaved by
-//    nibbles (a shift and a lop3 for 8 pairs) before the conversion.
+//    fragment pairs neighbouring tokens, and so do the cache's bytes: one conversion is one
+//    register of the fragment.
 //  * Blocks that every row of the unit sees whole take no mask.
 //
 // Weights.  exp2(x - m + 15): f16 then holds a weight to 11 bits down to 2^-29 of
@@ -35,39 +46,44 @@
 
 namespace pkv {
 
+// WARPS_ consumer warps (a multiple of 4), rings of STAGES_ stages of NB_ blocks (per head of a unit), and four
+// producer warps.  Registers: the launch's even share, moved to the consumers.
 template <class QT, int D_, int NH_, int WARPS_, int STAGES_, int NB_>
 struct Kv4Cfg {
   using Q = QT;
   static constexpr int D = D_, NH = NH_, GC = 8 * NH_, WARPS = WARPS_, STAGES = STAGES_, NB = NB_;
+  static constexpr int THREADS = (WARPS + 4) * 32;
+  static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
+  static constexpr int REGS_PRODUCER = WARPS == 12 ? 56 : 88;
+  static constexpr int REGS_CONSUMER = REGS_LAUNCH + (REGS_LAUNCH - REGS_PRODUCER) * 4 / WARPS / 8 * 8;
+  static_assert(WARPS % 4 == 0, "warpgroups");
+  static_assert(REGS_CONSUMER * WARPS + REGS_PRODUCER * 4 <= REGS_LAUNCH * (WARPS + 4), "registers of the launch");
   static constexpr int TILE = Kv4Tile<D>::kBytes;
   static constexpr int STAGE_BYTES = NB * TILE;
   static constexpr int KS = D / 16, MT = D / 16;
   static constexpr size_t TILES_BYTES = (size_t)WARPS * STAGES * STAGE_BYTES;
-  static constexpr size_t META_BYTES = (size_t)WARPS * STAGES * 32;
-  static constexpr size_t BAR_BYTES = (size_t)WARPS * STAGES * 8;
-  static constexpr size_t SMEM = TILES_BYTES + META_BYTES + BAR_BYTES + (size_t)kInlinePrefix * 4;
-  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static constexpr size_t META_BYTES = (size_t)WARPS * STAGES * 16;
+  static constexpr size_t BAR_BYTES = (size_t)WARPS * STAGES * 16;  // full, empty
+  static constexpr size_t SMEM = TILES_BYTES + META_BYTES + BAR_BYTES + (size_t)kKv4Prefix * 4;
+  static_assert(SMEM + WARPS * (24 * GC + 256) + 512 <= 232448, "shared memory of a CTA");
 };
 
-struct Kv4Meta {
-  int32_t b, hu, j, rem;  // first block, and the sequence's positions from it on
-  int32_t flags, nb, bad; // bad: bit i: block i's id is out of range
-  int32_t pad;
-};
+// (beside kFirst, kLast of decode.cuh)
+constexpr int32_t kOpens = 4;   // the segment begins with the unit's first block
+constexpr int32_t kCloses = 8;  // it ends with its last
+constexpr int32_t kEnds = 16;   // the worker's last segment
 
-struct Kv4Producer {
-  int pi, e, s;
-  int b, hu, j, n, ctx, j0;
-  int seg_j0, seg_wfirst;
-  int win_b, win_j0, win_id, nxt_id;  // 32 block-table entries, a lane each, and the 32 after them
-};
+constexpr int kPollNs = 100;   // between a producer's looks at rings that are all full
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
+constexpr int kMinItems = 24;  // blocks (of a head each) of a CTA's range, at least
+
+// A stage's record: its unit, the sequence's positions from its first block on, and
+// flags | blocks << 8 | (bit i: block i's id is out of range) << 16.
+struct __align__(16) Kv4Meta {
+  int32_t b, hu, rem, flags;
+  __device__ __forceinline__ int nb() const { return (flags >> 8) & 0xff; }
+  __device__ __forceinline__ uint32_t bad() const { return (uint32_t)flags >> 16; }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -75,92 +91,122 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void load_seq(Kv4Producer &pr, const DecodeParams &p) {
-  pr.ctx = clamped_len(p, __ldg(p.context_lens + pr.b));
-  pr.n = (pr.ctx + kBlock - 1) / kBlock;
-  pr.j0 = first_block<false>(p, pr.b, pr.ctx);
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Fills a stage with the next blocks (up to NB) of the worker's current unit.
-template <class Cfg>
-__device__ __forceinline__ int produce(Kv4Producer &pr, const Kv4Params &kp, uint8_t *tiles, Kv4Meta *meta,
-                                       uint64_t *bars, int stage, int lane, int *cta_flags) {
-  const DecodeParams &p = kp.d;
-  __syncwarp();
-  const int nb = min(Cfg::NB, min(pr.e - pr.pi, pr.n - pr.j));
-  if (!(pr.b == pr.win_b && pr.j >= pr.win_j0 && pr.j + nb <= pr.win_j0 + 32)) {
-    const int32_t *row = p.block_table + (size_t)pr.b * p.max_blocks;
-    if (pr.b == pr.win_b && pr.j == pr.win_j0 + 32)
-      pr.win_id = pr.nxt_id;
+// A producer lane: walks the range of items [pi, e) of its ring's consumer.
+// Table entries come through shared memory, 64 a ring: windows k (entries 32 k ..) of the current sequence, k even and odd,
+// fetched by the whole warp with cp.async, the next one ahead (a register load by one lane would hold up
+// the other lanes' fills for its latency).
+template <int NB>
+struct Kv4Producer {
+  int pi, e, s;
+  int b, hu, j, n, ctx, j0;
+  int opens;             // kOpens of the current segment
+  int tag_b, tag0, tag1;  // the windows that are there or on their way; ready: bit per window
+  uint32_t ready;
+
+  __device__ __forceinline__ void load_seq(const DecodeParams &p) {
+    ctx = clamped_len(p, __ldg(p.context_lens + b));
+    n = (ctx + kBlock - 1) / kBlock;
+    j0 = first_block<false>(p, b, ctx);
+  }
+  __device__ __forceinline__ int blocks() const { return min(NB, min(e - pi, n - j)); }
+  __device__ __forceinline__ bool has(int k) const { return tag_b == b && ((k & 1) ? tag1 : tag0) == k; }
+  // Window k of the current sequence will be there.
+  __device__ __forceinline__ void expect(int k) {
+    if (tag_b != b) tag0 = tag1 = -1, ready = 0;
+    tag_b = b;
+    if (k & 1)
+      tag1 = k;
     else
-      pr.win_id = pr.j + lane < pr.n ? __ldg(row + pr.j + lane) : 0;
-    pr.win_b = pr.b;
-    pr.win_j0 = pr.j;
-    pr.nxt_id = pr.j + 32 + lane < pr.n ? __ldg(row + pr.j + 32 + lane) : 0;
+      tag0 = k;
+    ready &= ~(1u << (k & 1));
   }
-  int id = __shfl_sync(kFull, pr.win_id, (pr.j - pr.win_j0 + lane) & 31);
-  const bool bad = lane < nb && (id < 0 || (int64_t)id >= p.num_blocks);
-  if (bad) id = 0;  // read, and its values taken as zeros
-  const uint32_t badmask = __ballot_sync(kFull, bad);
-  int flags = 0;
-  if (pr.pi == pr.s || pr.j == pr.j0) {
-    flags |= kFirst;
-    pr.seg_j0 = pr.j;
-    pr.seg_wfirst = (pr.pi == pr.s);
-  }
-  const int jn = pr.j + nb;
-  if (pr.pi + nb == pr.e || jn == pr.n) {
-    flags |= kLast;
-    if (pr.seg_j0 == pr.j0 && jn == pr.n) flags |= kComplete;
-  }
-  if (pr.seg_wfirst) flags |= kWFirst;
-  if (lane == 0) {
-    Kv4Meta m;
-    m.b = pr.b;
-    m.hu = pr.hu;
-    m.j = pr.j;
-    m.rem = pr.ctx - pr.j * kBlock;
-    m.flags = flags;
-    m.nb = nb;
-    m.bad = (int)badmask;
-    m.pad = 0;
-    meta[stage] = m;
-    if (badmask) atomicOr(cta_flags, PKV_FLAG_BAD_BLOCK);
-    mbar_arrive_expect_tx(&bars[stage], nb * Cfg::TILE);
-  }
-  __syncwarp();
-  if (lane < nb)
-    bulk_load(tiles + (size_t)stage * Cfg::STAGE_BYTES + lane * Cfg::TILE,
-              kp.cache + ((size_t)id * p.Hkv + pr.hu / p.NC) * Cfg::TILE, Cfg::TILE, &bars[stage]);
-  pr.pi += nb;
-  pr.j = jn;
-  if (pr.j == pr.n && pr.pi < pr.e) {
-    if (++pr.hu == p.HU) {
-      pr.hu = 0;
-      do {
-        ++pr.b;
-        load_seq(pr, p);
-      } while (pr.n == 0 && pr.b < p.B - 1);
+  // Fills a stage with the next blocks (up to NB) of the current unit.
+  template <class Cfg>
+  __device__ __forceinline__ void fill(const Kv4Params &kp, const int32_t *ids, uint8_t *tiles, Kv4Meta *meta,
+                                       uint64_t *full, int *cta_flags) {
+    const DecodeParams &p = kp.d;
+    const int nb = blocks();
+    int id[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) id[i] = i < nb ? ids[(j + i) & 63] : 0;
+    int flags = nb << 8;
+    if (pi == s || j == j0) {
+      flags |= kFirst;
+      opens = j == j0 ? kOpens : 0;
     }
-    pr.j = pr.j0;
+    flags |= opens;
+    const int jn = j + nb;
+    if (pi + nb == e) flags |= kLast | kEnds;
+    if (jn == n) flags |= kLast | kCloses;
+    const int bytes = kp.hg * Cfg::TILE;  // a block's tiles of the unit's heads
+    const uint8_t *head = kp.cache + (size_t)(hu / p.NC) * bytes;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if ((uint64_t)(int64_t)id[i] >= (uint64_t)p.num_blocks) {
+        id[i] = 0;  // block 0 is read, and its values taken as zeros
+        flags |= 0x10000 << i;
+      }
+    if (flags >> 16) atomicOr(cta_flags, PKV_FLAG_BAD_BLOCK);
+    *meta = Kv4Meta{b, hu, ctx - j * kBlock, flags};
+    mbar_arrive_expect_tx(full, nb * bytes);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (i < nb) bulk_load(tiles + i * bytes, head + (size_t)id[i] * p.Hkv * Cfg::TILE, bytes, full);
+    pi += nb;
+    j = jn;
+    if (pi < e && j == n) {
+      if (++hu == p.HU) {
+        hu = 0;
+        do {
+          ++b;
+          load_seq(p);
+        } while (n == 0 && b < p.B - 1);
+      }
+      j = j0;
+    }
   }
-  return nb;
-}
+};
 
 template <class Cfg>
 struct Kv4State {
   uint32_t qb[Cfg::NH][Cfg::KS][2];
   float acc[Cfg::NH][Cfg::MT][4];
   float m[Cfg::NH][2], l[Cfg::NH][2];  // of score columns 8 nh + 2 tig, + 1; m: largest raw score
-  float sc[Cfg::NH][2];                // raw score -> log2 domain
+  float sc[Cfg::NH][2], off[Cfg::NH][2];  // weight = 2^(raw score * sc + off)
   int back[Cfg::NH][2];
   int bk_lo, bk_hi;
 };
 
 template <class Cfg>
-__device__ __forceinline__ void begin(Kv4State<Cfg> &st, const DecodeParams &p, const Kv4Meta &m, int lane) {
+__device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, int b, int hu, int sub, int lane) {
+  const DecodeParams &p = kp.d;
   const int gid = lane >> 2, tig = lane & 3;
-  const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
+  const int h = hu / p.NC * kp.hg + sub, r0 = (hu % p.NC) * Cfg::GC;
   const int gc = min(Cfg::GC, p.R - r0);
   st.bk_lo = row_back(p, r0 + Cfg::GC - 1);
   st.bk_hi = row_back(p, r0);
@@ -171,7 +217,7 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const DecodeParams &p, 
   for (int nh = 0; nh < Cfg::NH; ++nh) {
     const int rq = 8 * nh + gid;
     const bool live = rq < gc && !none;
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + (live ? query_row(p, m.b, h, r0 + rq) : 0) +
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + (live ? query_row(p, b, h, r0 + rq) : 0) +
                         (Cfg::D / 4) * tig;
     uint2 raw[Cfg::KS];
 #pragma unroll
@@ -207,7 +253,7 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const DecodeParams &p, 
     st.back[nh][0] = row_back(p, r0 + 8 * nh + 2 * tig);
     st.back[nh][1] = row_back(p, r0 + 8 * nh + 2 * tig + 1);
     st.m[nh][0] = st.m[nh][1] = -INFINITY;
-    st.l[nh][0] = st.l[nh][1] = 0.f;
+    st.l[nh][0] = st.l[nh][1] = st.off[nh][0] = st.off[nh][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < Cfg::MT; ++mt)
 #pragma unroll
@@ -215,6 +261,14 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const DecodeParams &p, 
   }
 }
 
+// mma16816<false> onto 0.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), s);
   return *reinterpret_cast<const uint32_t *>(&r);
@@ -226,17 +280,16 @@ __device__ __forceinline__ __half2 scales2(uint32_t w) {  // two E4M3 bytes -> f
 
 // S^T = K . Q^T of one block's 16 tokens.
 template <class Cfg>
-__device__ __forceinline__ void scores(const Kv4State<Cfg> &st, uint32_t tile, int lane, bool zero,
-                                       float (&s)[Cfg::NH][4]) {
+__device__ __forceinline__ void scores(const Kv4State<Cfg> &st, uint32_t tile, int lane, float (&s)[Cfg::NH][4]) {
   constexpr int W = Cfg::D / 32;  // words of a lane's run of a row
-  uint32_t k[2][W];
+  uint32_t k[2][W], x[2][4];
   __half2 sc[2][2];               // scale of the run's first and second half, by row
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     if constexpr (Cfg::D == 128) {
       const uint4 v = lds128(tile + r * 512 + lane * 16);
       k[r][0] = v.x; k[r][1] = v.y; k[r][2] = v.z; k[r][3] = v.w;
-      const __half2 two = scales2(zero ? 0u : lds16(tile + Kv4Tile<128>::kKScales + r * 64 + lane * 2));
+      const __half2 two = scales2(lds16(tile + Kv4Tile<128>::kKScales + r * 64 + lane * 2));
       sc[r][0] = __half2half2(__low2half(two));
       sc[r][1] = __half2half2(__high2half(two));
     } else {
@@ -244,16 +297,10 @@ __device__ __forceinline__ void scores(const Kv4State<Cfg> &st, uint32_t tile, i
       k[r][0] = v.x; k[r][1] = v.y;
       // row gid's four scales are one word; the run's is byte tig
       const uint32_t w = lds32(tile + Kv4Tile<64>::kKScales + r * 32 + (lane & ~3));
-      const __half2 two = scales2(zero ? 0u : (w >> (8 * (lane & 3))) & 0xffu);
+      const __half2 two = scales2((w >> (8 * (lane & 3))) & 0xffu);
       sc[r][0] = sc[r][1] = __half2half2(__low2half(two));
     }
   }
-  float t[Cfg::NH][4];
-  uint32_t x[2][4];
-#pragma unroll
-  for (int nh = 0; nh < Cfg::NH; ++nh)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[nh][i] = t[nh][i] = 0.f;
 #pragma unroll
   for (int ks = 0; ks < Cfg::KS; ++ks) {
     const int half = ks >= Cfg::KS / 2, by = 2 * (ks & 1);
@@ -268,41 +315,39 @@ __device__ __forceinline__ void scores(const Kv4State<Cfg> &st, uint32_t tile, i
     a[3] = mul2(x[1][by + 1], sc[1][half]);
 #pragma unroll
     for (int nh = 0; nh < Cfg::NH; ++nh) {
-      if (Cfg::NH == 1 && (ks & 1))  // two chains
-        mma16816<false>(t[nh], a, st.qb[nh][ks][0], st.qb[nh][ks][1]);
+      if (ks == 0)
+        mma16816_zero(s[nh], a, st.qb[nh][ks][0], st.qb[nh][ks][1]);
       else
         mma16816<false>(s[nh], a, st.qb[nh][ks][0], st.qb[nh][ks][1]);
     }
   }
-  if constexpr (Cfg::NH == 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[0][i] += t[0][i];
 }
 
-// A block's V scales of the lane's tokens (pairs tig, tig + 4) and group; for a block that some row
-// does not see whole, those past the context and those of NaN as 0, the latter's tokens noted.
+// A block's V scales of the lane's tokens (pairs tig, tig + 4) and group.
 template <class Cfg>
-__device__ __forceinline__ void v_scales(uint32_t tile, int lane, bool zero, bool edge, int rem, uint32_t (&w)[2],
-                                         uint32_t &spoiled) {
+__device__ __forceinline__ void v_scales(uint32_t tile, int lane, uint32_t (&w)[2]) {
   const int gid = lane >> 2, tig = lane & 3;
   const int g = Cfg::D == 128 ? gid : gid >> 1;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[i] = zero ? 0u : lds16(tile + Kv4Tile<Cfg::D>::kVScales + (tig + 4 * i) * (Cfg::D / 8) + 2 * g);
-    if (edge) {
+  for (int i = 0; i < 2; ++i) w[i] = lds16(tile + Kv4Tile<Cfg::D>::kVScales + (tig + 4 * i) * (Cfg::D / 8) + 2 * g);
+}
+// Those past the context (rem positions are left) as 0, those of NaN too and their tokens noted.
+__device__ __forceinline__ uint32_t clean_scales(uint32_t (&w)[2], int lane, int rem) {
+  uint32_t spoiled = 0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int tok = 2 * tig + 8 * i + c;
-        const uint32_t mask = 0xffu << (8 * c);
-        if (tok >= rem) {
-          w[i] &= ~mask;
-        } else if (((w[i] >> (8 * c)) & 0x7fu) == 0x7fu) {
-          w[i] &= ~mask;
-          spoiled |= 1u << tok;
-        }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int tok = 2 * (lane & 3) + 8 * i + c;
+      const uint32_t mask = 0xffu << (8 * c);
+      if (tok >= rem) {
+        w[i] &= ~mask;
+      } else if (((w[i] >> (8 * c)) & 0x7fu) == 0x7fu) {
+        w[i] &= ~mask;
+        spoiled |= 1u << tok;
       }
     }
-  }
+  return spoiled;
 }
 
 // O^T += V^T . P^T of one block.
@@ -310,40 +355,32 @@ template <class Cfg>
 __device__ __forceinline__ void values(Kv4State<Cfg> &st, uint32_t tile, int lane, const uint32_t (&w)[2],
                                        const uint32_t (&pb)[Cfg::NH][2]) {
   const int gid = lane >> 2, tig = lane & 3;
-  constexpr int NW = Cfg::D / 64;  // words of a token's run
-  uint32_t lo[2][NW], hi[2][NW];   // nibbles of the pair's two tokens side by side: even and odd d
+  constexpr int NW = Cfg::D / 32;  // words of a pair's run
+  uint32_t c[2][NW], x[2][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int u = tig + 4 * i;
-    uint32_t a[NW], b[NW];
     if constexpr (Cfg::D == 128) {
       const uint4 v = lds128(tile + Kv4Tile<128>::kVCodes + u * 128 + ((gid ^ (2 * (u & 3))) << 4));
-      a[0] = v.x; a[1] = v.y; b[0] = v.z; b[1] = v.w;
+      c[i][0] = v.x; c[i][1] = v.y; c[i][2] = v.z; c[i][3] = v.w;
     } else {
       const uint2 v = lds64(tile + Kv4Tile<64>::kVCodes + u * 64 + ((gid ^ (4 * ((u >> 1) & 1))) << 3));
-      a[0] = v.x; b[0] = v.y;
-    }
-#pragma unroll
-    for (int n = 0; n < NW; ++n) {
-      lo[i][n] = (a[n] & 0x0f0f0f0fu) | ((b[n] << 4) & 0xf0f0f0f0u);
-      hi[i][n] = ((a[n] >> 4) & 0x0f0f0f0fu) | (b[n] & 0xf0f0f0f0u);
+      c[i][0] = v.x; c[i][1] = v.y;
     }
   }
   const __half2 s0 = scales2(w[0]), s1 = scales2(w[1]);
-  uint32_t x[4][4];
 #pragma unroll
   for (int mt = 0; mt < Cfg::MT; ++mt) {  // rows gid and gid + 8: d = run + 2 mt, 2 mt + 1
-    if (mt % 4 == 0) {
-      e2m1x8_to_f16(lo[0][mt / 4], x[0]);
-      e2m1x8_to_f16(hi[0][mt / 4], x[1]);
-      e2m1x8_to_f16(lo[1][mt / 4], x[2]);
-      e2m1x8_to_f16(hi[1][mt / 4], x[3]);
+    const int by = 2 * (mt & 1);
+    if (by == 0) {
+      e2m1x8_to_f16(c[0][mt / 2], x[0]);
+      e2m1x8_to_f16(c[1][mt / 2], x[1]);
     }
     uint32_t a[4];
-    a[0] = mul2(x[0][mt % 4], s0);
-    a[1] = mul2(x[1][mt % 4], s0);
-    a[2] = mul2(x[2][mt % 4], s1);
-    a[3] = mul2(x[3][mt % 4], s1);
+    a[0] = mul2(x[0][by], s0);
+    a[1] = mul2(x[0][by + 1], s0);
+    a[2] = mul2(x[1][by], s1);
+    a[3] = mul2(x[1][by + 1], s1);
 #pragma unroll
     for (int nh = 0; nh < Cfg::NH; ++nh) mma16816<false>(st.acc[nh][mt], a, pb[nh][0], pb[nh][1]);
   }
@@ -351,116 +388,132 @@ __device__ __forceinline__ void values(Kv4State<Cfg> &st, uint32_t tile, int lan
 
 constexpr float kWeightShift = 15.f;  // the largest weight is 2^15
 
+// NaN into the rows that see a token of `spoiled` (the lane's tokens of NaN scales in a block), in the lane's run of d.
 template <class Cfg>
-__device__ __forceinline__ void stage_step(Kv4State<Cfg> &st, const DecodeParams &p, const Kv4Meta &m, uint32_t tiles,
-                                           int lane) {
-  constexpr int NB = Cfg::NB, NH = Cfg::NH;
-  const int gid = lane >> 2;
-  float s[NB][NH][4];
+__device__ __forceinline__ void spoil(Kv4State<Cfg> &st, const DecodeParams &p, int rem, uint32_t spoiled) {
+  spoiled |= __shfl_xor_sync(kFull, spoiled, 1);  // the group's 16 tokens
+  spoiled |= __shfl_xor_sync(kFull, spoiled, 2);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    if (i < m.nb) {
-      scores<Cfg>(st, tiles + i * Cfg::TILE, lane, (m.bad >> i) & 1, s[i]);
-    } else {
+  for (int nh = 0; nh < Cfg::NH; ++nh)
 #pragma unroll
-      for (int nh = 0; nh < NH; ++nh)
+    for (int c = 0; c < 2; ++c) {
+      const int base = rem - st.back[nh][c] - p.wlen;
+      uint32_t sees = 0;
+#pragma unroll 1
+      for (int tok = 0; tok < kBlock; ++tok) sees |= (uint32_t)(tok - base) < (uint32_t)p.wlen ? 1u << tok : 0u;
+      if (spoiled & sees)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[i][nh][c] = -INFINITY;
+        for (int mt = 0; mt < Cfg::MT; ++mt) st.acc[nh][mt][c] = st.acc[nh][mt][2 + c] = __int_as_float(0x7fc00000);
     }
+}
+
+// The running maximum and sum of one 8-row group over n blocks' raw scores, and the weights as B operands.
+template <class Cfg, int N>
+__device__ __forceinline__ void softmax(Kv4State<Cfg> &st, int nh, const float (&s)[N][Cfg::NH][4],
+                                        uint32_t (&pb)[N][Cfg::NH][2]) {
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    mx0 = fmaxf(mx0, fmaxf(s[i][nh][0], s[i][nh][2]));
+    mx1 = fmaxf(mx1, fmaxf(s[i][nh][1], s[i][nh][3]));
   }
-  // every row of the unit sees every position of the stage
-  const bool edge = m.rem - st.bk_hi < kBlock * m.nb || m.rem - st.bk_lo > p.wlen;
-  const uint32_t wl = (uint32_t)p.wlen;
-  uint32_t pb[NB][NH][2];
+  // exchange and rescale only when some lane holds a larger score
+  if (__any_sync(kFull, (mx0 > st.m[nh][0]) | (mx1 > st.m[nh][1]))) {
 #pragma unroll
-  for (int nh = 0; nh < NH; ++nh) {
-    if (edge) {
-      const int base0 = m.rem - st.back[nh][0] - p.wlen, base1 = m.rem - st.back[nh][1] - p.wlen;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int r = gid + kBlock * i;
-        if ((uint32_t)(r - base0) >= wl) s[i][nh][0] = -INFINITY;
-        if ((uint32_t)(r - base1) >= wl) s[i][nh][1] = -INFINITY;
-        if ((uint32_t)(r + 8 - base0) >= wl) s[i][nh][2] = -INFINITY;
-        if ((uint32_t)(r + 8 - base1) >= wl) s[i][nh][3] = -INFINITY;
-      }
+    for (int off = 4; off < 32; off <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
     }
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    const float mn0 = fmaxf(st.m[nh][0], mx0), mn1 = fmaxf(st.m[nh][1], mx1);
+    const float al0 = st.m[nh][0] == -INFINITY ? 0.f : exp2_fast((st.m[nh][0] - mn0) * st.sc[nh][0]);
+    const float al1 = st.m[nh][1] == -INFINITY ? 0.f : exp2_fast((st.m[nh][1] - mn1) * st.sc[nh][1]);
+    st.l[nh][0] *= al0;
+    st.l[nh][1] *= al1;
+    st.m[nh][0] = mn0;
+    st.m[nh][1] = mn1;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      mx0 = fmaxf(mx0, fmaxf(s[i][nh][0], s[i][nh][2]));
-      mx1 = fmaxf(mx1, fmaxf(s[i][nh][1], s[i][nh][3]));
-    }
-    // exchange and rescale only when some lane holds a larger score
-    if (__any_sync(kFull, (mx0 > st.m[nh][0]) | (mx1 > st.m[nh][1]))) {
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
-      }
-      const float mn0 = fmaxf(st.m[nh][0], mx0), mn1 = fmaxf(st.m[nh][1], mx1);
-      const float al0 = st.m[nh][0] == -INFINITY ? 0.f : exp2_fast((st.m[nh][0] - mn0) * st.sc[nh][0]);
-      const float al1 = st.m[nh][1] == -INFINITY ? 0.f : exp2_fast((st.m[nh][1] - mn1) * st.sc[nh][1]);
-      st.l[nh][0] *= al0;
-      st.l[nh][1] *= al1;
-      st.m[nh][0] = mn0;
-      st.m[nh][1] = mn1;
-#pragma unroll
-      for (int mt = 0; mt < Cfg::MT; ++mt) {
-        st.acc[nh][mt][0] *= al0;
-        st.acc[nh][mt][1] *= al1;
-        st.acc[nh][mt][2] *= al0;
-        st.acc[nh][mt][3] *= al1;
-      }
+    for (int mt = 0; mt < Cfg::MT; ++mt) {
+      st.acc[nh][mt][0] *= al0;
+      st.acc[nh][mt][1] *= al1;
+      st.acc[nh][mt][2] *= al0;
+      st.acc[nh][mt][3] *= al1;
     }
     // (a column that has seen nothing: its scores are -inf, its weights 0)
-    const float o0 = kWeightShift - (st.m[nh][0] == -INFINITY ? 0.f : st.m[nh][0] * st.sc[nh][0]);
-    const float o1 = kWeightShift - (st.m[nh][1] == -INFINITY ? 0.f : st.m[nh][1] * st.sc[nh][1]);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const float p0 = exp2_fast(fmaf(s[i][nh][0], st.sc[nh][0], o0)), p1 = exp2_fast(fmaf(s[i][nh][1], st.sc[nh][1], o1));
-      const float p2 = exp2_fast(fmaf(s[i][nh][2], st.sc[nh][0], o0)), p3 = exp2_fast(fmaf(s[i][nh][3], st.sc[nh][1], o1));
-      st.l[nh][0] += p0 + p2;
-      st.l[nh][1] += p1 + p3;
-      pb[i][nh][0] = movmatrix_trans(pack_f16x2(p0, p1));
-      pb[i][nh][1] = movmatrix_trans(pack_f16x2(p2, p3));
-    }
+    st.off[nh][0] = kWeightShift - (mn0 == -INFINITY ? 0.f : mn0 * st.sc[nh][0]);
+    st.off[nh][1] = kWeightShift - (mn1 == -INFINITY ? 0.f : mn1 * st.sc[nh][1]);
   }
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    if (i < m.nb) {
-      uint32_t w[2], spoiled = 0;
-      v_scales<Cfg>(tiles + i * Cfg::TILE, lane, (m.bad >> i) & 1, edge, m.rem - kBlock * i, w, spoiled);
-      values<Cfg>(st, tiles + i * Cfg::TILE, lane, w, pb[i]);
-      if (edge && __any_sync(kFull, spoiled != 0)) {
-        spoiled |= __shfl_xor_sync(kFull, spoiled, 1);  // the group's 16 tokens
-        spoiled |= __shfl_xor_sync(kFull, spoiled, 2);
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int base = m.rem - kBlock * i - st.back[nh][c] - p.wlen;
-            uint32_t sees = 0;
-#pragma unroll 1
-            for (int tok = 0; tok < kBlock; ++tok) sees |= (uint32_t)(tok - base) < wl ? 1u << tok : 0u;
-            if (spoiled & sees)
-#pragma unroll
-              for (int mt = 0; mt < Cfg::MT; ++mt)
-                st.acc[nh][mt][c] = st.acc[nh][mt][2 + c] = __int_as_float(0x7fc00000);
-          }
-      }
-    }
+  for (int i = 0; i < N; ++i) {
+    const float p0 = exp2_fast(fmaf(s[i][nh][0], st.sc[nh][0], st.off[nh][0]));
+    const float p1 = exp2_fast(fmaf(s[i][nh][1], st.sc[nh][1], st.off[nh][1]));
+    const float p2 = exp2_fast(fmaf(s[i][nh][2], st.sc[nh][0], st.off[nh][0]));
+    const float p3 = exp2_fast(fmaf(s[i][nh][3], st.sc[nh][1], st.off[nh][1]));
+    st.l[nh][0] += p0 + p2;
+    st.l[nh][1] += p1 + p3;
+    pb[i][nh][0] = movmatrix_trans(pack_f16x2(p0, p1));
+    pb[i][nh][1] = movmatrix_trans(pack_f16x2(p2, p3));
   }
 }
 
+// A whole stage, every position of which every row of the unit sees.
 template <class Cfg>
-__device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, const Kv4Meta &m, int w, int lane) {
+__device__ __forceinline__ void full_stage(Kv4State<Cfg> &st, uint32_t tiles, uint32_t step, int lane) {
+  float s[Cfg::NB][Cfg::NH][4];
+  uint32_t pb[Cfg::NB][Cfg::NH][2];
+#pragma unroll
+  for (int i = 0; i < Cfg::NB; ++i) scores<Cfg>(st, tiles + i * step, lane, s[i]);
+#pragma unroll
+  for (int nh = 0; nh < Cfg::NH; ++nh) softmax<Cfg, Cfg::NB>(st, nh, s, pb);
+#pragma unroll
+  for (int i = 0; i < Cfg::NB; ++i) {
+    uint32_t w[2];
+    v_scales<Cfg>(tiles + i * step, lane, w);
+    values<Cfg>(st, tiles + i * step, lane, w, pb[i]);
+  }
+}
+
+// One block of another stage: at a context's or a window's end, of a short range, with a bad id (its values are zeros).
+template <class Cfg>
+__device__ __forceinline__ void edge_block(Kv4State<Cfg> &st, const DecodeParams &p, int rem, bool zero, uint32_t tile,
+                                           int lane) {
+  float s[1][Cfg::NH][4];
+  uint32_t pb[1][Cfg::NH][2];
+  const int gid = lane >> 2;
+  scores<Cfg>(st, tile, lane, s[0]);
+#pragma unroll
+  for (int nh = 0; nh < Cfg::NH; ++nh) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (zero) s[0][nh][c] = 0.f;
+      if ((uint32_t)(gid + 8 * (c >> 1) - (rem - st.back[nh][c & 1] - p.wlen)) >= (uint32_t)p.wlen) s[0][nh][c] = -INFINITY;
+    }
+    softmax<Cfg, 1>(st, nh, s, pb);
+  }
+  uint32_t w[2];
+  v_scales<Cfg>(tile, lane, w);
+  if (zero) w[0] = w[1] = 0;
+  const uint32_t spoiled = clean_scales(w, lane, rem);
+  if (__any_sync(kFull, spoiled != 0)) spoil<Cfg>(st, p, rem, spoiled);
+  values<Cfg>(st, tile, lane, w, pb[0]);
+}
+
+template <class Q>
+__device__ __forceinline__ void store4(void *out, size_t at, float4 v) {
+  *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + at) =
+      make_uint2(pack2(Q{}, v.x, v.y), pack2(Q{}, v.z, v.w));
+}
+
+// Ends a segment: a whole unit's rows go to the output; others leave their sums in part
+// ([GC][D]) and (log2 of the sums' unit, l) in ml.
+template <class Cfg>
+__device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, const Kv4Meta &m, int sub, float *part,
+                                       float2 *ml, int lane) {
   const DecodeParams &p = kp.d;
   const int gid = lane >> 2, tig = lane & 3;
-  const int h = m.hu / p.NC, r0 = (m.hu % p.NC) * Cfg::GC;
+  const int h = m.hu / p.NC * kp.hg + sub, r0 = (m.hu % p.NC) * Cfg::GC;
   const int gc = min(Cfg::GC, p.R - r0);
   constexpr int RUN = Cfg::D / 8;  // a lane's run of d: RUN gid ..
-  const size_t base = ((size_t)w * 2 + ((m.flags & kWFirst) ? 0 : 1)) * Cfg::GC;
+  const bool whole = (m.flags & kOpens) && (m.flags & kCloses);
 #pragma unroll
   for (int nh = 0; nh < Cfg::NH; ++nh)
 #pragma unroll
@@ -469,115 +522,477 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
       const int row = 8 * nh + 2 * tig + c;
-      if (row >= gc) continue;
       // a row that sees nothing gives 0; a sum of NaN gives NaN
-      const float inv = l == 0.f ? 0.f : kp.v_unit / l;
-      float y[RUN];
+      const float f = !whole ? 1.f : l == 0.f ? 0.f : kp.v_unit / l;
+      if (!whole && gid == 0) ml[row] = make_float2(st.m[nh][c] == -INFINITY ? -INFINITY : -st.off[nh][c], l);
+      if (whole && row >= gc) continue;
+      const size_t at = whole ? query_row(p, m.b, h, r0 + row) + RUN * gid : 0;
 #pragma unroll
-      for (int mt = 0; mt < Cfg::MT; ++mt) {
-        y[2 * mt] = st.acc[nh][mt][c] * inv;
-        y[2 * mt + 1] = st.acc[nh][mt][2 + c] * inv;
-      }
-      if (m.flags & kComplete) {
-        uint16_t *o = reinterpret_cast<uint16_t *>(p.out) + query_row(p, m.b, h, r0 + row) + RUN * gid;
-#pragma unroll
-        for (int i = 0; i < RUN / 8; ++i)
-          reinterpret_cast<uint4 *>(o)[i] = make_uint4(
-              pack2(typename Cfg::Q{}, y[8 * i], y[8 * i + 1]), pack2(typename Cfg::Q{}, y[8 * i + 2], y[8 * i + 3]),
-              pack2(typename Cfg::Q{}, y[8 * i + 4], y[8 * i + 5]), pack2(typename Cfg::Q{}, y[8 * i + 6], y[8 * i + 7]));
-      } else {
-        float4 *o = reinterpret_cast<float4 *>(p.part_o + (base + row) * Cfg::D + RUN * gid);
-#pragma unroll
-        for (int i = 0; i < RUN / 4; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        // (a sum of NaN as +inf: the merge then gives NaN)
-        if (gid == 0)
-          p.part_lse[base + row] = l != l ? INFINITY
-                                   : l == 0.f ? -INFINITY : st.m[nh][c] * st.sc[nh][c] - kWeightShift + log2f(l);
+      for (int i = 0; i < RUN / 4; ++i) {
+        const float4 y = make_float4(st.acc[nh][2 * i][c] * f, st.acc[nh][2 * i][2 + c] * f,
+                                     st.acc[nh][2 * i + 1][c] * f, st.acc[nh][2 * i + 1][2 + c] * f);
+        if (whole)
+          store4<typename Cfg::Q>(p.out, at + 4 * i, y);
+        else
+          reinterpret_cast<float4 *>(part + row * Cfg::D + RUN * gid)[i] = y;
       }
     }
 }
 
+// The plan: blocks before each sequence, in a lane's registers (up to 32 sequences: `before` and `items` of
+// sequence `lane`) or in memory.
+struct Kv4Plan {
+  const int32_t *pre;
+  int before, items, total;
+  bool small;
+};
+// Unit and block of item x of the list (a whole warp, the same x).
+struct Kv4Item {
+  int x, b, hu, off, n;  // block off of the unit's n
+};
+__device__ __forceinline__ Kv4Item locate_item(const DecodeParams &p, const Kv4Plan &plan, int x) {
+  const int lane = threadIdx.x & 31;
+  // lo: the largest b with HU * blocks before it <= x (the count of items is within 32 bits)
+  int lo = 0, first, items;
+  if (plan.small) {
+    lo = 31 - __clz(__ballot_sync(kFull, lane < p.B && p.HU * plan.before <= x));
+    first = __shfl_sync(kFull, plan.before, lo);
+    items = __shfl_sync(kFull, plan.items, lo);
+  } else {
+    for (int span = p.B; span > 1;) {
+      const int step = (span + 31) / 32;
+      const bool ok = lane * step < span && p.HU * plan.pre[lo + lane * step] <= x;
+      const int c = 31 - __clz(__ballot_sync(kFull, ok));
+      lo += c * step;
+      span = min(step, span - c * step);
+    }
+    first = plan.pre[lo];
+    items = plan.pre[lo + 1] - first;
+  }
+  Kv4Item r;
+  r.x = x;
+  r.b = lo;
+  r.n = items;
+  const int rr = x - p.HU * first;
+  r.hu = rr / r.n;
+  r.off = rr - r.hu * r.n;
+  return r;
+}
+// The first item of ring r of the CTA range [cs, ce).
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::WARPS * 32, 1) kv4_decode_kernel(const __grid_constant__ Kv4Params kp) {
+__device__ __forceinline__ int ring_cut(const DecodeParams &p, const Kv4Plan &plan, int cs, int ce, int r, int rings) {
+  const int x = cs + (int)((uint64_t)(ce - cs) * (uint32_t)r / (uint32_t)rings);
+  if (r == 0 || r == rings || ce - cs < 2 * Cfg::NB * rings) return x;
+  return x - locate_item(p, plan, x).off % Cfg::NB;  // long ranges: whole stages
+}
+// The first item of CTA range c of `ranges`.
+template <int NB>
+__device__ __forceinline__ int range_cut(const DecodeParams &p, const Kv4Plan &plan, int W, int ranges, int c) {
+  const int q = W / ranges, x = q * c + min(c, W - q * ranges);
+  if (x <= 0 || x >= W) return x;
+  const Kv4Item it = locate_item(p, plan, x);
+  if (it.n <= kKv4Whole) return 2 * it.off < it.n ? x - it.off : x - it.off + it.n;
+  return x - it.off % NB;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __grid_constant__ Kv4Params kp) {
   extern __shared__ __align__(128) uint8_t smem[];
   const DecodeParams &p = kp.d;
-  const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
-  uint8_t *tiles = smem + (size_t)wib * Cfg::STAGES * Cfg::STAGE_BYTES;
-  Kv4Meta *meta = reinterpret_cast<Kv4Meta *>(smem + Cfg::TILES_BYTES) + wib * Cfg::STAGES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES) + wib * Cfg::STAGES;
+  const int tid = threadIdx.x, lane = tid & 31, wib = tid >> 5;
+  constexpr int WARPS = Cfg::WARPS, STAGES = Cfg::STAGES, GC = Cfg::GC, D = Cfg::D;
+  const int hg = kp.hg, rings = WARPS / hg;
+  const int stage_bytes = hg * Cfg::STAGE_BYTES, ring_bytes = STAGES * stage_bytes;
+  Kv4Meta *s_meta = reinterpret_cast<Kv4Meta *>(smem + Cfg::TILES_BYTES);  // [ring][stage]
+  uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES);
+  uint64_t *s_empty = s_full + WARPS * STAGES;
   int32_t *s_prefix = reinterpret_cast<int32_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES + Cfg::BAR_BYTES);
+  __shared__ int2 s_seg[2 * WARPS];           // segments left to join, two a ring, in the list's order: {unit or -1, flags}
+  __shared__ float2 s_ml[2 * WARPS * GC];     // [segment][head][row]
+  __shared__ float s_wt[2 * WARPS * GC];
+  __shared__ int32_t s_ids[WARPS][64];        // table entries ahead, by ring
   __shared__ int32_t s_scan[32];
-  __shared__ int cta_flags;
+  __shared__ int cta_flags, s_abort;          // s_abort: bit r: ring r's consumer gave up
   __shared__ __align__(8) uint64_t dead_bar;  // failure-path test hook: nothing ever arrives on it
-  if (threadIdx.x == 0) cta_flags = 0;
-  if (lane == 0) {
-    for (int s = 0; s < Cfg::STAGES; ++s) mbar_init(&bars[s], 1);
-    fence_barrier_init();
+  if (tid == 0) {
+    cta_flags = s_abort = 0;
+    mbar_init(&dead_bar, 1);
   }
+  if (tid < rings * STAGES) {
+    mbar_init(&s_full[tid], 1);
+    mbar_init(&s_empty[tid], hg);
+  }
+  if (tid < 2 * WARPS) s_seg[tid] = make_int2(-1, 0);
+  fence_barrier_init();
   __syncthreads();
+  grid_dep_launch();  // the merge may take the place of CTAs that have ended; it waits for all of them
   grid_dep_wait();
-  if (p.inline_plan) inline_plan<false>(p, s_prefix, s_scan, &cta_flags);
 
-  const int w = blockIdx.x * Cfg::WARPS + wib;
-  if (w < p.P) {
-    int e;
-    int4 st0;
-    if (p.inline_plan) {
-      st0 = locate<false>(p, s_prefix, w, &e);
-    } else {
-      st0 = p.starts[w];
-      e = p.starts[w + 1].x;
+  // ---- the plan, and the CTA's range [cs, ce) ----
+  Kv4Plan plan;
+  plan.small = p.B <= 32;
+  plan.before = plan.items = 0;
+  if (plan.small) {  // every warp for itself
+    int flags = 0;
+    if (lane < p.B) plan.items = seq_items<false>(p, lane, clamp_len<false>(p, lane, __ldg(p.context_lens + lane), &flags));
+    int x = plan.items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, off);
+      if (lane >= off) x += y;
     }
-    const int total = e - st0.x;
-    const bool stall = p.stall_ns != 0 && st0.x == 0 && total > 0;
-    if (stall) {
-      if (lane == 0) {
-        mbar_init(&dead_bar, 1);
-        fence_barrier_init();
+    plan.before = x - plan.items;
+    plan.total = __shfl_sync(kFull, x, 31);
+    if (wib == 0 && flags) atomicOr(&cta_flags, flags);
+  } else {
+    if (p.inline_plan) inline_plan<false>(p, s_prefix, s_scan, &cta_flags);
+    plan.pre = p.inline_plan ? s_prefix : p.prefix;
+    plan.total = plan.pre[p.B];
+  }
+  const int W = p.HU * plan.total, c = blockIdx.x;
+  const int ranges = min(p.P, max(1, (int)(((int64_t)W * hg + kMinItems - 1) / kMinItems)));
+  const int cs = c < ranges ? range_cut<Cfg::NB>(p, plan, W, ranges, c) : W;
+  const int ce = c < ranges ? range_cut<Cfg::NB>(p, plan, W, ranges, c + 1) : W;
+
+  if (wib >= Cfg::WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_PRODUCER));
+    // ---- producers: a lane fills a ring, rings q, q + 4 .. of warp q ----
+    const int q = wib - WARPS, per = (rings - q + 3) / 4, r = q + 4 * min(lane, max(per, 1) - 1);
+    int nst = 0;
+    Kv4Producer<Cfg::NB> pr;
+    pr.pi = pr.e = pr.s = pr.b = pr.hu = pr.j = pr.n = pr.j0 = pr.ctx = pr.opens = 0;
+    pr.tag_b = pr.tag0 = pr.tag1 = -1;
+    pr.ready = 0;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int x0 = ring_cut<Cfg>(p, plan, cs, ce, q + 4 * i, rings), x1 = ring_cut<Cfg>(p, plan, cs, ce, q + 4 * i + 1, rings);
+      if (x0 >= x1) continue;
+      const Kv4Item it = locate_item(p, plan, x0);
+      if (lane == i) {
+        pr.pi = pr.s = x0;
+        pr.e = x1;
+        pr.b = it.b;
+        pr.hu = it.hu;
+        pr.load_seq(p);
+        pr.j = pr.j0 + it.off;
       }
-      __syncwarp();
     }
-    if (total > 0) {
-      Kv4Producer pr;
-      pr.pi = pr.s = st0.x;
-      pr.e = e;
-      pr.b = st0.y;
-      pr.hu = st0.z;
-      pr.j = st0.w;
-      pr.seg_j0 = pr.seg_wfirst = 0;
-      pr.win_b = -1;
-      pr.win_j0 = pr.win_id = pr.nxt_id = 0;
-      load_seq(pr, p);
-      int issued = 0, nst = 0;
-      for (; nst < Cfg::STAGES && issued < total; ++nst)
-        issued += produce<Cfg>(pr, kp, tiles, meta, bars, nst, lane, &cta_flags);
-      Kv4State<Cfg> state;
-      for (int done = 0, i = 0; done < total; ++i) {
-        const int stage = i % Cfg::STAGES;
-        const uint32_t parity = (uint32_t)(i / Cfg::STAGES) & 1u;
-        if ((stall && i == 0) ? !mbar_wait_bounded(&dead_bar, 0, p.timeout_ns)
-                              : !mbar_wait_bounded(&bars[stage], parity, p.timeout_ns)) {
-          if (lane == 0) atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
-          // let the copies still in flight land before the CTA's memory goes away
-          for (int k = i; k < nst; ++k)
-            mbar_wait_bounded(&bars[k % Cfg::STAGES], (uint32_t)(k / Cfg::STAGES) & 1u, p.timeout_ns);
-          break;
+    uint8_t *tiles = smem + r * ring_bytes;
+    uint64_t *full = s_full + r * STAGES, *empty = s_empty + r * STAGES;
+    // the whole warp fetches window k of the sequence of each of these lanes' rings
+    auto fetch = [&](uint32_t lanes, int k) {
+      for (; lanes; lanes &= lanes - 1) {
+        const int of = __ffs(lanes) - 1;
+        const int fb = __shfl_sync(kFull, pr.b, of), fk = __shfl_sync(kFull, k, of), fn = __shfl_sync(kFull, pr.n, of);
+        const int at = 32 * fk + lane;
+        if (at < fn) cp_async4(smem_u32(&s_ids[q + 4 * of][at & 63]), p.block_table + (size_t)fb * p.max_blocks + at);
+      }
+    };
+    uint64_t idle_since = 0;
+    for (uint32_t idle = 0;;) {
+      const int aborted = *reinterpret_cast<volatile int *>(&s_abort);
+      const bool open = pr.pi < pr.e && !((aborted >> r) & 1);
+      if (!__any_sync(kFull, open)) break;
+      const int stage = nst % STAGES;
+      const bool can = open && (nst < STAGES || mbar_test(&empty[stage], (uint32_t)(nst / STAGES - 1) & 1u));
+      if (__any_sync(kFull, can)) {
+        idle = 0;
+        // the stage's entries lie in windows k0 and k1, at most one further
+        const int k0 = pr.j >> 5, k1 = (pr.j + max(pr.blocks(), 1) - 1) >> 5;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int k = t ? k1 : k0;
+          const bool miss = can && !pr.has(k);
+          const uint32_t missing = __ballot_sync(kFull, miss);
+          if (missing) fetch(missing, k);
+          if (miss) pr.expect(k);
         }
-        const Kv4Meta m = meta[stage];
-        if (m.flags & kFirst) begin<Cfg>(state, p, m, lane);
-        stage_step<Cfg>(state, p, m, smem_u32(tiles + (size_t)stage * Cfg::STAGE_BYTES), lane);
-        if (issued < total) {  // refilled once its fragments are consumed
-          issued += produce<Cfg>(pr, kp, tiles, meta, bars, stage, lane, &cta_flags);
+        const uint32_t need = 1u << (k0 & 1) | 1u << (k1 & 1);
+        if (__any_sync(kFull, can && (pr.ready & need) != need)) {
+          cp_async_wait();
+          pr.ready = 3;
+        }
+        __syncwarp();
+        if (can) {
+          pr.template fill<Cfg>(kp, s_ids[r], tiles + stage * stage_bytes, &s_meta[r * STAGES + stage],
+                                &full[stage], &cta_flags);
           ++nst;
         }
-        if (m.flags & kLast) finish<Cfg>(state, kp, m, w, lane);
-        done += m.nb;
+        __syncwarp();
+        // the window after this one, ahead of its use
+        const int ka = (pr.j >> 5) + 1;
+        const bool ahead = can && pr.pi < pr.e && pr.has(ka - 1) && !pr.has(ka) && 32 * ka < pr.n;
+        const uint32_t more = __ballot_sync(kFull, ahead);
+        if (more) fetch(more, ka);
+        if (ahead) pr.expect(ka);
+      } else {  // every open ring is full: look again shortly, for a limited time
+        __nanosleep(kPollNs);
+        if (idle == 0) idle_since = global_timer_ns();
+        if ((++idle & 255u) == 0 && global_timer_ns() - idle_since > 2 * p.timeout_ns) {
+          if (lane == 0) atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+          break;
+        }
+      }
+    }
+    cp_async_wait();
+    // copies that no consumer waits for any more land before the CTA's memory goes away
+    for (int k = max(0, nst - STAGES); k < nst; ++k)
+      mbar_wait_bounded(&full[k % STAGES], (uint32_t)(k / STAGES) & 1u, p.timeout_ns);
+    return;  // (their registers are fewer than what follows uses)
+  }
+
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_CONSUMER));
+  // ---- consumers: hg warps work through a ring, each on its head's tiles ----
+  const int ring = wib / hg, sub = wib - ring * hg;
+  const int first = ring_cut<Cfg>(p, plan, cs, ce, ring, rings), total = ring_cut<Cfg>(p, plan, cs, ce, ring + 1, rings) - first;
+  if (total > 0) {
+    // failure-path test hook: the worker holding the first work item replaces its first
+    // wait by one on dead_bar, which runs out and takes the timeout path
+    const bool stall = p.stall_ns != 0 && first == 0;
+    uint64_t *full = s_full + ring * STAGES, *empty = s_empty + ring * STAGES;
+    const uint32_t tiles = smem_u32(smem + ring * ring_bytes) + sub * Cfg::TILE, step = hg * Cfg::TILE;
+    Kv4State<Cfg> state;
+    {  // while the first blocks are on their way
+      const Kv4Item it = locate_item(p, plan, first);
+      begin<Cfg>(state, kp, it.b, it.hu, sub, lane);
+    }
+    Kv4Meta m;
+    uint32_t parity = 0;
+    int done = 0;
+    for (int stage = 0; done < total;) {
+      if (stall && done == 0 ? !mbar_wait_bounded(&dead_bar, 0, p.timeout_ns)
+                             : !mbar_wait_bounded(&full[stage], parity, p.timeout_ns)) {
+        if (lane == 0) {
+          atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+          atomicOr(&s_abort, 1 << ring);
+        }
+        break;
+      }
+      m = s_meta[ring * STAGES + stage];
+      const int nb = m.nb();
+      const uint32_t at = tiles + stage * stage_bytes;
+      if ((m.flags & kFirst) && done > 0) begin<Cfg>(state, kp, m.b, m.hu, sub, lane);
+      // every row of the unit sees every position of the stage
+      if (nb == Cfg::NB && m.bad() == 0 && m.rem - state.bk_hi >= kBlock * Cfg::NB && m.rem - state.bk_lo <= p.wlen) {
+        full_stage<Cfg>(state, at, step, lane);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < nb; ++k)
+          edge_block<Cfg>(state, p, m.rem - kBlock * k, (m.bad() >> k) & 1, at + k * step, lane);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);  // (the record is in registers, too)
+      done += nb;
+      if ((m.flags & kLast) && !(m.flags & kEnds)) {
+        // its sums, unless the unit is whole, go to memory: the ring is in use
+        finish<Cfg>(state, kp, m, sub, kp.first_o + (((size_t)blockIdx.x * rings + ring) * hg + sub) * GC * D,
+                    s_ml + (2 * ring * hg + sub) * GC, lane);
+        if (sub == 0 && lane == 0 && (m.flags & (kOpens | kCloses)) != (kOpens | kCloses))
+          s_seg[2 * ring] = make_int2(m.b * p.HU + m.hu, m.flags);
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
+    // the range's last segment stays in the ring, once all its warps are through (or gave up)
+    asm volatile("bar.sync %0, %1;" ::"r"(2 + ring), "r"(hg * 32) : "memory");
+    if (done >= total) {
+      finish<Cfg>(state, kp, m, sub, reinterpret_cast<float *>(smem + ring * ring_bytes) + sub * GC * D,
+                  s_ml + ((2 * ring + 1) * hg + sub) * GC, lane);
+      if (sub == 0 && lane == 0 && (m.flags & (kOpens | kCloses)) != (kOpens | kCloses))
+        s_seg[2 * ring + 1] = make_int2(m.b * p.HU + m.hu, m.flags);
+    }
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");  // the consumers
+
+  // ---- join the segments of each unit; what a unit lacks is in the neighbouring CTAs ----
+  static_assert(2 * WARPS <= 32, "a lane per segment");
+  const int2 seg = lane < 2 * WARPS ? s_seg[lane] : make_int2(-1, 0);
+  const uint32_t valid = __ballot_sync(kFull, seg.x >= 0);
+  const int prev = 31 - __clz(valid & ((1u << lane) - 1));  // the segment before this one, if any
+  const int prev_unit = __shfl_sync(kFull, seg.x, prev & 31);
+  const uint32_t heads = __ballot_sync(kFull, seg.x >= 0 && (prev < 0 || prev_unit != seg.x));  // a unit's first
+  const int rows = hg * GC;  // of a unit
+  for (int t = tid; t < rows; t += WARPS * 32)
+    for (uint32_t todo = heads; todo; todo &= todo - 1) {
+      const int g = __ffs(todo) - 1, next = todo & (todo - 1) ? __ffs(todo & (todo - 1)) - 1 : 32;
+      const uint32_t members = valid & (0xffffffffu << g) & (0xffffffffu >> (32 - next));
+      float M = -INFINITY, l = 0.f;
+#pragma unroll 2
+      for (uint32_t left = members; left; left &= left - 1) M = fmaxf(M, s_ml[(__ffs(left) - 1) * rows + t].x);
+#pragma unroll 2
+      for (uint32_t left = members; left; left &= left - 1) {
+        const int q = __ffs(left) - 1;
+        const float2 ml = s_ml[q * rows + t];
+        // (a row that saw nothing, or NaN alone: its maximum is -inf, its sum 0 or NaN)
+        const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? -1.f : 1.f) : exp2_fast(ml.x - M);
+        s_wt[q * rows + t] = wt;  // -1: nothing to add
+        if (!(wt < 0.f)) l = fmaf(wt, ml.y, l);
+      }
+      s_ml[g * rows + t] = make_float2(M, l);
+    }
+  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+
+  int4 record = make_int4(-1, 0, -1, 0);  // {unit that an earlier CTA began, ends here; unit that goes on}
+  for (uint32_t todo = heads; todo; todo &= todo - 1) {
+    const int g = __ffs(todo) - 1, next = todo & (todo - 1) ? __ffs(todo & (todo - 1)) - 1 : 32;
+    const uint32_t members = valid & (0xffffffffu << g) & (0xffffffffu >> (32 - next));
+    const int unit = __shfl_sync(kFull, seg.x, g);
+    const bool opens = __shfl_sync(kFull, seg.y, g) & kOpens;
+    const bool closes = __shfl_sync(kFull, seg.y, 31 - __clz(members)) & kCloses;
+    if (!opens)
+      record.x = unit, record.y = closes;
+    else if (!closes)
+      record.z = unit;
+    const int b = unit / p.HU, hu = unit - b * p.HU, h0 = hu / p.NC * hg, r0 = (hu % p.NC) * GC;
+    for (int v = tid; v < rows * (D / 4); v += WARPS * 32) {
+      const int row = v / (D / 4), d = 4 * (v % (D / 4)), r = r0 + row % GC;  // row: [head][row]
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t rest = members; rest;) {
+        float4 a[4];
+        float wt[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int q = rest ? __ffs(rest) - 1 : g;
+          wt[t] = rest ? s_wt[q * rows + row] : -1.f;
+          rest &= rest - 1;
+          const float *src = (q & 1) ? reinterpret_cast<const float *>(smem + (q >> 1) * ring_bytes)
+                                     : kp.first_o + ((size_t)blockIdx.x * rings + (q >> 1)) * rows * D;
+          a[t] = *reinterpret_cast<const float4 *>(src + 4 * v);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (!(wt[t] < 0.f)) {
+            acc.x = fmaf(wt[t], a[t].x, acc.x);
+            acc.y = fmaf(wt[t], a[t].y, acc.y);
+            acc.z = fmaf(wt[t], a[t].z, acc.z);
+            acc.w = fmaf(wt[t], a[t].w, acc.w);
+          }
+      }
+      const float2 ml = s_ml[g * rows + row];
+      const float f = ml.y == 0.f ? 0.f : kp.v_unit / ml.y;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      if (opens && closes) {
+        if (r < p.R) store4<typename Cfg::Q>(p.out, query_row(p, b, h0 + row / GC, r) + d, acc);
+      } else {
+        const size_t slot = ((size_t)blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row;
+        *reinterpret_cast<float4 *>(p.part_o + slot * D + d) = acc;
+        // (a sum of NaN as +inf: the merge then gives NaN)
+        if (d == 0) p.part_lse[slot] = ml.y != ml.y ? INFINITY : ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y);
       }
     }
   }
+  // sequences without a block: 0
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (__ldg(p.context_lens + b) <= 0)
+      for (int v = tid; v < p.q_len * p.Hq * (D / 8); v += WARPS * 32)
+        reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (size_t)b * p.q_len * p.Hq * D)[v] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) {
+    kp.records[blockIdx.x] = record;
+    p.hdr->cta_status[blockIdx.x] = (uint8_t)(cta_flags | (p.inline_plan ? 0 : p.hdr->plan_flags));
+    if (blockIdx.x == 0) p.hdr->status = kStatusPerCta | gridDim.x;
+  }
+}
+
+// Joins a unit's partial results: CTA (c, head) does the unit that range c begins and does not end.  A team of
+// threads has a float4 of the head's rows each; teams take the partial results in turn, eight in flight, and
+// are joined through shared memory (a long context's unit has one partial result for each of 76 CTAs).
+constexpr int kMergeThreads = 1024;
+template <class Q>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_constant__ Kv4Params kp) {
+  const DecodeParams &p = kp.d;
+  __shared__ float4 s_acc[kMergeThreads];
+  __shared__ float2 s_ml[kMergeThreads];
+  grid_dep_wait();
+  const int c = blockIdx.x, unit = kp.records[c].z;
+  if (unit < 0) return;
+  // the ranges that continue it: c + 1 .. last
+  int last = c;
+  const int lane = threadIdx.x & 31;
+  for (int at = c + 1; at < p.P; at += 32) {
+    const int4 r = at + lane < p.P ? kp.records[at + lane] : make_int4(-1, 0, -1, 0);
+    const uint32_t goes = __ballot_sync(kFull, r.x == unit), ends = __ballot_sync(kFull, r.x != unit || r.y != 0);
+    const int stop = __ffs(ends);  // 1-based lane of the last (or of one past it)
+    if (stop) {
+      last = at + stop - 1 - ((goes >> (stop - 1)) & 1 ? 0 : 1);
+      break;
+    }
+    last = min(at + 31, p.P - 1);
+  }
+  const int D = p.D, size = p.GC * D / 4, teams = blockDim.x / size, team = threadIdx.x / size;
+  const int v = threadIdx.x - team * size, row = 4 * v / D, d = 4 * v % D;
+  const int b = unit / p.HU, hu = unit % p.HU, r = (hu % p.NC) * p.GC + row, sub = blockIdx.y;
+  constexpr int kBatch = 8;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, den = 0.f;
+  for (int s = c + team; s <= last; s += kBatch * teams) {
+    float4 o[kBatch];
+    float l[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int w = min(s + t * teams, last);
+      const size_t slot = (((size_t)w * 2 + (w == c ? 1 : 0)) * kp.hg + sub) * p.GC + row;
+      l[t] = s + t * teams <= last ? p.part_lse[slot] : -INFINITY;
+      o[t] = *reinterpret_cast<const float4 *>(p.part_o + slot * D + d);
+    }
+    float cm = M;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
+    if (cm == -INFINITY) continue;  // nothing seen yet
+    const float keep = exp2f(M - cm);
+    acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+    den *= keep;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      if (l[t] == -INFINITY) continue;
+      const float wt = exp2f(l[t] - cm);
+      acc.x = fmaf(wt, o[t].x, acc.x);
+      acc.y = fmaf(wt, o[t].y, acc.y);
+      acc.z = fmaf(wt, o[t].z, acc.z);
+      acc.w = fmaf(wt, o[t].w, acc.w);
+      den += wt;
+    }
+    M = cm;
+  }
+  s_acc[threadIdx.x] = acc;
+  s_ml[threadIdx.x] = make_float2(M, den);
   __syncthreads();
-  if (threadIdx.x == 0) p.cta_flags[blockIdx.x] = cta_flags;
-  grid_dep_launch();
+  if (team > 0 || r >= p.R) return;
+  float all = M;
+  for (int t = 1; t < teams; ++t) all = fmaxf(all, s_ml[t * size + v].x);
+  den = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t = 0; t < teams; ++t) {
+    const float2 ml = s_ml[t * size + v];
+    if (ml.x == -INFINITY) continue;
+    const float wt = exp2f(ml.x - all);
+    const float4 a = s_acc[t * size + v];
+    acc.x = fmaf(wt, a.x, acc.x);
+    acc.y = fmaf(wt, a.y, acc.y);
+    acc.z = fmaf(wt, a.z, acc.z);
+    acc.w = fmaf(wt, a.w, acc.w);
+    den = fmaf(wt, ml.y, den);
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  store4<Q>(p.out, query_row(p, b, hu / p.NC * kp.hg + sub, r) + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+}
+
+cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t stream, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.d.n_ctas, p.hg);
+  // a team per eight partial results of a unit
+  const int size = p.d.GC * p.d.D / 4, units = p.d.B * p.d.HU, parts = (p.d.n_ctas + units - 1) / units + 1;
+  int teams = 1;
+  while (teams * size < kMergeThreads && teams * 8 < parts) teams *= 2;
+  cfg.blockDim = dim3(teams * size);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, p.d.out_dtype == PKV_F16 ? kv4_merge_kernel<F16> : kv4_merge_kernel<BF16>, p);
 }
 
 template <class Cfg>
@@ -590,6 +1005,7 @@ static DecodeKernel kv4_entry() {
   k.D = Cfg::D;
   k.GC = Cfg::GC;
   k.warps = Cfg::WARPS;
+  k.threads = Cfg::THREADS;
   k.stages = Cfg::STAGES;
   k.smem_bytes = Cfg::SMEM;
   k.tree = 0;
@@ -602,10 +1018,10 @@ int register_decode_kv4(DecodeKernel *out) {
   out[n++] = kv4_entry<Kv4Cfg<F16, 128, 1, 12, 2, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 1, 12, 4, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<F16, 64, 1, 12, 4, 4>>();
-  out[n++] = kv4_entry<Kv4Cfg<BF16, 128, 2, 12, 4, 2>>();
-  out[n++] = kv4_entry<Kv4Cfg<F16, 128, 2, 12, 4, 2>>();
-  out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 2, 12, 4, 4>>();
-  out[n++] = kv4_entry<Kv4Cfg<F16, 64, 2, 12, 4, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<BF16, 128, 2, 8, 3, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<F16, 128, 2, 8, 3, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 2, 8, 4, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<F16, 64, 2, 8, 4, 4>>();
   return n;
 }
 

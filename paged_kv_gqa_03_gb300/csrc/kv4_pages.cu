@@ -2,10 +2,11 @@
 // append of new tokens, whole pages packed from 16 bits and expanded back, and
 // the copy-on-write copy.
 //
-// One thread quantises or expands a group of 16 elements: the scale needs
-// nothing of another thread, a warp's loads and stores of codes are whole
-// lines, and every output byte is written by one thread.  All are bound by
-// HBM: a token and head read or write 4 D bytes in 16 bits and 18 D / 16 in 4.
+// A thread does 16 elements of K of two neighbouring tokens, or of V, whose codes share
+// bytes: a scale needs nothing of another thread, a warp's loads and stores of codes are whole lines.  A new token
+// whose neighbour is not beside it in the call is stored by an exclusive or into its own
+// nibbles (kv4_store_v1).  All are bound by HBM: a token and head read or write 4 D bytes in 16
+// bits and 18 D / 16 in 4.
 #include "kv4.cuh"
 #include "kv4.h"
 
@@ -43,27 +44,43 @@ __global__ void __launch_bounds__(kThreads)
   const bool v = hv >= Hkv;
   const int64_t slot = slots[t];
   if (slot < 0 || slot / kBlock >= num_blocks) return;
+  const int tok = (int)(slot % kBlock);
+  uint8_t *tile = cache + (size_t)(slot / kBlock * Hkv + h) * Kv4Tile<D>::kBytes;
+  const size_t at = (size_t)h * D + 16 * g;
   float y[16];
-  load16<T>(v ? v_new : k_new, (size_t)(t * (v ? ld_v : ld_k)) + (size_t)h * D + 16 * g, y);
-  const Kv4Group x = kv4_quantise(y, v ? v_unit : k_unit);
-  kv4_store<D>(cache + (size_t)(slot / kBlock * Hkv + h) * Kv4Tile<D>::kBytes, v, (int)(slot % kBlock), g, x);
+  if (!v) {
+    load16<T>(k_new, (size_t)(t * ld_k) + at, y);
+    kv4_store_k<D>(tile, tok, g, kv4_quantise(y, k_unit));
+    return;
+  }
+  // a pair that stands together in the call: its even token's thread stores both
+  if ((tok & 1) && t > 0 && slots[t - 1] == slot - 1) return;
+  const bool two = !(tok & 1) && t + 1 < T_ && slots[t + 1] == slot + 1;
+  load16<T>(v_new, (size_t)(t * ld_v) + at, y);
+  const Kv4Group a = kv4_quantise(y, v_unit);
+  if (two) {
+    load16<T>(v_new, (size_t)((t + 1) * ld_v) + at, y);
+    kv4_store_v2<D>(tile, tok >> 1, g, a, kv4_quantise(y, v_unit));
+  } else {
+    kv4_store_v1<D>(tile, tok, g, a);
+  }
 }
 
-// Thread -> (pair, head, K or V, token, group), the group fastest.
+// Thread -> (pair, head, K or V, tokens 2 u and 2 u + 1, group), the group fastest.
 struct PageThread {
   int64_t pair;
-  int h, tok, g;
+  int h, u, g;
   bool v;
 };
 template <int D>
 __device__ __forceinline__ PageThread page_thread(int Hkv) {
-  constexpr int G = D / 16, kTile = 2 * kBlock * G;
+  constexpr int G = D / 16, kTile = kBlock * G;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int in = (int)(i % kTile);
   const int64_t tile = i / kTile;
   PageThread p;
   p.g = in % G;
-  p.tok = in / G % kBlock;
+  p.u = in / G % (kBlock / 2);
   p.v = in >= kTile / 2;
   p.pair = tile / Hkv;
   p.h = (int)(tile - p.pair * Hkv);
@@ -79,10 +96,18 @@ __global__ void __launch_bounds__(kThreads)
   if (p.pair >= n) return;
   const int src = pairs[2 * p.pair], dst = pairs[2 * p.pair + 1];
   if (src < 0 || src >= num_src || dst < 0 || dst >= num_blocks) return;
-  float y[16];
-  load16<T>(p.v ? vv : k, (((size_t)src * Hkv + p.h) * kBlock + p.tok) * D + 16 * p.g, y);
-  const Kv4Group x = kv4_quantise(y, p.v ? v_unit : k_unit);
-  kv4_store<D>(cache + ((size_t)dst * Hkv + p.h) * Kv4Tile<D>::kBytes, p.v, p.tok, p.g, x);
+  const size_t at = (((size_t)src * Hkv + p.h) * kBlock + 2 * p.u) * D + 16 * p.g;
+  float x[16], y[16];
+  load16<T>(p.v ? vv : k, at, x);
+  load16<T>(p.v ? vv : k, at + D, y);
+  const Kv4Group a = kv4_quantise(x, p.v ? v_unit : k_unit), b = kv4_quantise(y, p.v ? v_unit : k_unit);
+  uint8_t *tile = cache + ((size_t)dst * Hkv + p.h) * Kv4Tile<D>::kBytes;
+  if (p.v) {
+    kv4_store_v2<D>(tile, p.u, p.g, a, b);
+  } else {
+    kv4_store_k<D>(tile, 2 * p.u, p.g, a);
+    kv4_store_k<D>(tile, 2 * p.u + 1, p.g, b);
+  }
 }
 
 template <class T, int D>
@@ -94,11 +119,20 @@ __global__ void __launch_bounds__(kThreads)
   if (p.pair >= n) return;
   const int src = pairs[2 * p.pair], dst = pairs[2 * p.pair + 1];
   if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_dst) return;
-  const Kv4Group x =
-      kv4_load<D>(cache + ((size_t)src * Hkv + p.h) * Kv4Tile<D>::kBytes, p.v, p.tok, p.g);
+  const uint8_t *tile = cache + ((size_t)src * Hkv + p.h) * Kv4Tile<D>::kBytes;
+  Kv4Group a, b;
+  if (p.v) {
+    kv4_load_v2<D>(tile, p.u, p.g, a, b);
+  } else {
+    a = kv4_load_k<D>(tile, 2 * p.u, p.g);
+    b = kv4_load_k<D>(tile, 2 * p.u + 1, p.g);
+  }
+  const size_t at = (((size_t)dst * Hkv + p.h) * kBlock + 2 * p.u) * D + 16 * p.g;
   float y[16];
-  kv4_values(x, p.v ? v_unit : k_unit, y);
-  store16<T>(p.v ? vv : k, (((size_t)dst * Hkv + p.h) * kBlock + p.tok) * D + 16 * p.g, y);
+  kv4_values(a, p.v ? v_unit : k_unit, y);
+  store16<T>(p.v ? vv : k, at, y);
+  kv4_values(b, p.v ? v_unit : k_unit, y);
+  store16<T>(p.v ? vv : k, at + D, y);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -137,7 +171,7 @@ cudaError_t launch_kv4_pack(uint8_t *cache, int64_t num_blocks, const void *k, c
   return dispatch(dtype, D, [&](auto type, auto tile) {
     constexpr int DD = decltype(tile)::kGroups * 16;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * 2 * kBlock * (DD / 16), attr, stream);
+    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * kBlock * (DD / 16), attr, stream);
     return cudaLaunchKernelEx(&cfg, kv4_pack_kernel<decltype(type), DD>, cache, num_blocks, k, v, num_src, pairs, n,
                               Hkv, k_unit, v_unit);
   });
@@ -149,7 +183,7 @@ cudaError_t launch_kv4_expand(void *k, void *v, int dtype, int64_t num_dst, cons
   return dispatch(dtype, D, [&](auto type, auto tile) {
     constexpr int DD = decltype(tile)::kGroups * 16;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * 2 * kBlock * (DD / 16), attr, stream);
+    const cudaLaunchConfig_t cfg = config((int64_t)n * Hkv * kBlock * (DD / 16), attr, stream);
     return cudaLaunchKernelEx(&cfg, kv4_expand_kernel<decltype(type), DD>, k, v, num_dst, cache, num_blocks, pairs, n,
                               Hkv, k_unit, v_unit);
   });

@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
       load16<Type>(s_rows, (size_t)(i / G) * p.D + 16 * g, y);
       const Kv4Group x = kv4_quantise(y, value ? p.v_unit : p.k_unit);
       uint8_t *tile = p.kv4 + (size_t)(slot / kBlock * p.Hkv + h) * (18 * p.D);
+      const int tok = (int)(slot % kBlock);
       if (p.D == 128)
-        kv4_store<128>(tile, value, (int)(slot % kBlock), g, x);
+        value ? kv4_store_v1<128>(tile, tok, g, x) : kv4_store_k<128>(tile, tok, g, x);
       else
-        kv4_store<64>(tile, value, (int)(slot % kBlock), g, x);
+        value ? kv4_store_v1<64>(tile, tok, g, x) : kv4_store_k<64>(tile, tok, g, x);
     }
   }
 }
