@@ -1206,6 +1206,7 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   p.d.inline_plan = B + 1 <= kKv4Prefix ? 1 : 0;
   p.cache = static_cast<const uint8_t *>(cache);
   p.hg = kv4_heads(Hkv);
+  p.hg_log2 = p.hg / 2;  // (of 1, 2 and 4)
   p.d.HU = Hkv / p.hg * c.NC;
   p.records = reinterpret_cast<int4 *>(ws + L.records);
   p.first_o = reinterpret_cast<float *>(ws + L.first_o);

@@ -22,10 +22,11 @@ constexpr int kKv4Whole = 48;
 struct Kv4Params {
   DecodeParams d;  // P: ranges, one per CTA; scale_log2 holds K's unit; k_scale, v_scale, cta_flags unused
   const uint8_t *cache;
-  int hg;          // heads of a unit (d.HU: units of a sequence = Hkv / hg * d.NC)
+  int hg, hg_log2;  // heads of a unit (d.HU: units of a sequence = Hkv / hg * d.NC)
   int4 *records;   // [P]: the units that a CTA's range cuts (kv4_decode.cu)
   float *first_o;  // [P][warps][GC][D]: a ring's first segment, to be joined in its CTA
   float v_unit;
+  int merge_units, merge_rows;  // the merge kernel's CTAs: by unit or by range, and their rows
 };
 struct Kv4WsLayout {
   size_t hdr, prefix, starts, records, part_o, part_lse, first_o, total;
@@ -35,7 +36,7 @@ Kv4WsLayout kv4_ws_layout(int B, int P, int D, int GC, int hg, int warps);
 inline int kv4_heads(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
 int register_decode_kv4(DecodeKernel *out);
 // Joins the units cut between CTAs.
-cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_kv4_merge(Kv4Params p, cudaStream_t stream, bool pdl);
 
 // Rows of new tokens, `ld` elements apart.
 cudaError_t launch_kv4_append(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_v, int new_dtype,

@@ -68,6 +68,24 @@ struct Kv4Cfg {
   static_assert(SMEM + WARPS * (24 * GC + 256) + 512 <= 232448, "shared memory of a CTA");
 };
 
+// Short ranges spend most of their time on instructions that are fetched for the first time (a small call's warps
+// issue for one cycle in six and wait for instructions the others), so what runs once is kept short: one copy of
+// each part, no division where the common shapes need none.
+struct UnitAt {
+  int head, row;  // first kv head and first query row
+};
+__device__ __forceinline__ UnitAt unit_at(const Kv4Params &kp, int hu, int GC) {
+  if (kp.d.NC == 1) return UnitAt{hu << kp.hg_log2, 0};
+  const int g = hu / kp.d.NC;
+  return UnitAt{g << kp.hg_log2, (hu - g * kp.d.NC) * GC};
+}
+// Query row r of kv head h of sequence b, in elements of q / out; positions hidden from it at the end.
+__device__ __forceinline__ size_t row_at(const DecodeParams &p, int b, int h, int r) {
+  const int i = p.q_len == 1 ? 0 : r / p.G;
+  return ((size_t)((b * p.q_len + i) * p.Hq + h * p.G + (r - i * p.G))) * (size_t)p.D;  // (fewer than 2^31 rows)
+}
+__device__ __forceinline__ int hidden_behind(const DecodeParams &p, int r) { return p.q_len == 1 ? 0 : row_back(p, r); }
+
 // (beside kFirst, kLast of decode.cuh)
 constexpr int32_t kOpens = 4;   // the segment begins with the unit's first block
 constexpr int32_t kCloses = 8;  // it ends with its last
@@ -151,9 +169,6 @@ struct Kv4Producer {
                                        uint64_t *full, int *cta_flags) {
     const DecodeParams &p = kp.d;
     const int nb = blocks();
-    int id[NB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) id[i] = i < nb ? ids[(j + i) & 63] : 0;
     int flags = nb << 8;
     if (pi == s || j == j0) {
       flags |= kFirst;
@@ -163,20 +178,19 @@ struct Kv4Producer {
     const int jn = j + nb;
     if (pi + nb == e) flags |= kLast | kEnds;
     if (jn == n) flags |= kLast | kCloses;
-    const int bytes = kp.hg * Cfg::TILE;  // a block's tiles of the unit's heads
-    const uint8_t *head = kp.cache + (size_t)(hu / p.NC) * bytes;
+    const int bytes = Cfg::TILE << kp.hg_log2;  // a block's tiles of the unit's heads
+    const uint8_t *head = kp.cache + (size_t)unit_at(kp, hu, 0).head * Cfg::TILE;
+    // (a bad id: block 0 is read, and its values taken as zeros)
+    auto good = [&](int i) { return (uint64_t)(int64_t)ids[(j + i) & 63] < (uint64_t)p.num_blocks; };
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      if ((uint64_t)(int64_t)id[i] >= (uint64_t)p.num_blocks) {
-        id[i] = 0;  // block 0 is read, and its values taken as zeros
-        flags |= 0x10000 << i;
-      }
+      if (i < nb && !good(i)) flags |= 0x10000 << i;
     if (flags >> 16) atomicOr(cta_flags, PKV_FLAG_BAD_BLOCK);
     *meta = Kv4Meta{b, hu, ctx - j * kBlock, flags};
     mbar_arrive_expect_tx(full, nb * bytes);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      if (i < nb) bulk_load(tiles + i * bytes, head + (size_t)id[i] * p.Hkv * Cfg::TILE, bytes, full);
+#pragma unroll 1
+    for (int i = 0; i < nb; ++i)
+      bulk_load(tiles + i * bytes, head + (size_t)(good(i) ? ids[(j + i) & 63] : 0) * p.Hkv * Cfg::TILE, bytes, full);
     pi += nb;
     j = jn;
     if (pi < e && j == n) {
@@ -206,10 +220,11 @@ template <class Cfg>
 __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, int b, int hu, int sub, int lane) {
   const DecodeParams &p = kp.d;
   const int gid = lane >> 2, tig = lane & 3;
-  const int h = hu / p.NC * kp.hg + sub, r0 = (hu % p.NC) * Cfg::GC;
+  const UnitAt u = unit_at(kp, hu, Cfg::GC);
+  const int h = u.head + sub, r0 = u.row;
   const int gc = min(Cfg::GC, p.R - r0);
-  st.bk_lo = row_back(p, r0 + Cfg::GC - 1);
-  st.bk_hi = row_back(p, r0);
+  st.bk_lo = hidden_behind(p, r0 + Cfg::GC - 1);
+  st.bk_hi = hidden_behind(p, r0);
   // a negative scale is the queries' sign, a scale of 0 a query of zeros
   const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
   const bool none = p.scale_log2 == 0.f;
@@ -217,7 +232,7 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, in
   for (int nh = 0; nh < Cfg::NH; ++nh) {
     const int rq = 8 * nh + gid;
     const bool live = rq < gc && !none;
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + (live ? query_row(p, b, h, r0 + rq) : 0) +
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + (live ? row_at(p, b, h, r0 + rq) : 0) +
                         (Cfg::D / 4) * tig;
     uint2 raw[Cfg::KS];
 #pragma unroll
@@ -250,8 +265,8 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, in
     const float sc = none ? 1.f : fabsf(p.scale_log2);
     st.sc[nh][0] = sc * __shfl_sync(kFull, down, 8 * tig);  // rows 2 tig and 2 tig + 1: lanes of gid 2 tig, 2 tig + 1
     st.sc[nh][1] = sc * __shfl_sync(kFull, down, 8 * tig + 4);
-    st.back[nh][0] = row_back(p, r0 + 8 * nh + 2 * tig);
-    st.back[nh][1] = row_back(p, r0 + 8 * nh + 2 * tig + 1);
+    st.back[nh][0] = hidden_behind(p, r0 + 8 * nh + 2 * tig);
+    st.back[nh][1] = hidden_behind(p, r0 + 8 * nh + 2 * tig + 1);
     st.m[nh][0] = st.m[nh][1] = -INFINITY;
     st.l[nh][0] = st.l[nh][1] = st.off[nh][0] = st.off[nh][1] = 0.f;
 #pragma unroll
@@ -510,8 +525,8 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
                                        float2 *ml, int lane) {
   const DecodeParams &p = kp.d;
   const int gid = lane >> 2, tig = lane & 3;
-  const int h = m.hu / p.NC * kp.hg + sub, r0 = (m.hu % p.NC) * Cfg::GC;
-  const int gc = min(Cfg::GC, p.R - r0);
+  const UnitAt u = unit_at(kp, m.hu, Cfg::GC);
+  const int h = u.head + sub, r0 = u.row, gc = min(Cfg::GC, p.R - r0);
   constexpr int RUN = Cfg::D / 8;  // a lane's run of d: RUN gid ..
   const bool whole = (m.flags & kOpens) && (m.flags & kCloses);
 #pragma unroll
@@ -526,7 +541,7 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
       const float f = !whole ? 1.f : l == 0.f ? 0.f : kp.v_unit / l;
       if (!whole && gid == 0) ml[row] = make_float2(st.m[nh][c] == -INFINITY ? -INFINITY : -st.off[nh][c], l);
       if (whole && row >= gc) continue;
-      const size_t at = whole ? query_row(p, m.b, h, r0 + row) + RUN * gid : 0;
+      const size_t at = whole ? row_at(p, m.b, h, r0 + row) + RUN * gid : 0;
 #pragma unroll
       for (int i = 0; i < RUN / 4; ++i) {
         const float4 y = make_float4(st.acc[nh][2 * i][c] * f, st.acc[nh][2 * i][2 + c] * f,
@@ -578,35 +593,19 @@ __device__ __forceinline__ Kv4Item locate_item(const DecodeParams &p, const Kv4P
   r.off = rr - r.hu * r.n;
   return r;
 }
-// The first item of ring r of the CTA range [cs, ce).
-template <class Cfg>
-__device__ __forceinline__ int ring_cut(const DecodeParams &p, const Kv4Plan &plan, int cs, int ce, int r, int rings) {
-  const int x = cs + (int)((uint64_t)(ce - cs) * (uint32_t)r / (uint32_t)rings);
-  if (r == 0 || r == rings || ce - cs < 2 * Cfg::NB * rings) return x;
-  return x - locate_item(p, plan, x).off % Cfg::NB;  // long ranges: whole stages
-}
-// The first item of CTA range c of `ranges`.
-template <int NB>
-__device__ __forceinline__ int range_cut(const DecodeParams &p, const Kv4Plan &plan, int W, int ranges, int c) {
-  const int q = W / ranges, x = q * c + min(c, W - q * ranges);
-  if (x <= 0 || x >= W) return x;
-  const Kv4Item it = locate_item(p, plan, x);
-  if (it.n <= kKv4Whole) return 2 * it.off < it.n ? x - it.off : x - it.off + it.n;
-  return x - it.off % NB;
-}
-
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __grid_constant__ Kv4Params kp) {
   extern __shared__ __align__(128) uint8_t smem[];
   const DecodeParams &p = kp.d;
   const int tid = threadIdx.x, lane = tid & 31, wib = tid >> 5;
   constexpr int WARPS = Cfg::WARPS, STAGES = Cfg::STAGES, GC = Cfg::GC, D = Cfg::D;
-  const int hg = kp.hg, rings = WARPS / hg;
+  const int hg = kp.hg, rings = WARPS >> kp.hg_log2;
   const int stage_bytes = hg * Cfg::STAGE_BYTES, ring_bytes = STAGES * stage_bytes;
   Kv4Meta *s_meta = reinterpret_cast<Kv4Meta *>(smem + Cfg::TILES_BYTES);  // [ring][stage]
   uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES);
   uint64_t *s_empty = s_full + WARPS * STAGES;
   int32_t *s_prefix = reinterpret_cast<int32_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES + Cfg::BAR_BYTES);
+  __shared__ int4 s_cut[WARPS + 1];           // {item, b, unit, block} at which a ring's range begins
   __shared__ int2 s_seg[2 * WARPS];           // segments left to join, two a ring, in the list's order: {unit or -1, flags}
   __shared__ float2 s_ml[2 * WARPS * GC];     // [segment][head][row]
   __shared__ float s_wt[2 * WARPS * GC];
@@ -649,10 +648,41 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
     plan.pre = p.inline_plan ? s_prefix : p.prefix;
     plan.total = plan.pre[p.B];
   }
-  const int W = p.HU * plan.total, c = blockIdx.x;
-  const int ranges = min(p.P, max(1, (int)(((int64_t)W * hg + kMinItems - 1) / kMinItems)));
-  const int cs = c < ranges ? range_cut<Cfg::NB>(p, plan, W, ranges, c) : W;
-  const int ce = c < ranges ? range_cut<Cfg::NB>(p, plan, W, ranges, c + 1) : W;
+  // Cuts fall on items of equal numbers; one into a unit of few blocks moves to the unit's nearer end, another to
+  // whole stages of its unit.  Warp w finds where ring w begins (ring `rings`: where the last ends).
+  if (wib <= rings) {
+    const int W = p.HU * plan.total, c = blockIdx.x;
+    const int ranges = min(p.P, max(1, (int)((((int64_t)W << kp.hg_log2) + kMinItems - 1) / kMinItems)));
+    const int each = W / ranges, more = W - each * ranges;
+    int cs = W, x = W, n = 0;
+    int4 cut = make_int4(W, p.B, 0, 0);
+#pragma unroll 1
+    for (int t = 0; t < 3 && c < ranges; ++t) {  // the range's beginning, its end, the ring's beginning
+      if (t < 2) {
+        x = each * (c + t) + min(c + t, more);
+      } else {
+        const int ce = x;
+        n = ce - cs;
+        const int q = n / rings;
+        x = cs + q * wib + min(wib, n - q * rings);
+        if (wib == rings) x = ce;
+      }
+      if (x < W) {
+        const Kv4Item it = locate_item(p, plan, x);
+        int back = it.off % Cfg::NB;
+        if (t < 2 && it.n <= kKv4Whole) back = 2 * it.off < it.n ? it.off : it.off - it.n;
+        if (t == 2 && (wib == 0 || wib == rings || n < 2 * Cfg::NB * rings)) back = 0;
+        x -= back;
+        if (t == 2) {
+          const int j0 = p.window > 0 ? first_block<false>(p, it.b, clamped_len(p, __ldg(p.context_lens + it.b))) : 0;
+          cut = make_int4(x, it.b, it.hu, j0 + it.off - back);
+        }
+      }
+      if (t == 0) cs = x;
+    }
+    if (lane == 0) s_cut[wib] = cut;
+  }
+  __syncthreads();
 
   if (wib >= Cfg::WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_PRODUCER));
@@ -663,19 +693,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
     pr.pi = pr.e = pr.s = pr.b = pr.hu = pr.j = pr.n = pr.j0 = pr.ctx = pr.opens = 0;
     pr.tag_b = pr.tag0 = pr.tag1 = -1;
     pr.ready = 0;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-      const int x0 = ring_cut<Cfg>(p, plan, cs, ce, q + 4 * i, rings), x1 = ring_cut<Cfg>(p, plan, cs, ce, q + 4 * i + 1, rings);
-      if (x0 >= x1) continue;
-      const Kv4Item it = locate_item(p, plan, x0);
-      if (lane == i) {
-        pr.pi = pr.s = x0;
-        pr.e = x1;
-        pr.b = it.b;
-        pr.hu = it.hu;
-        pr.load_seq(p);
-        pr.j = pr.j0 + it.off;
-      }
+    if (lane < per && s_cut[r].x < s_cut[r + 1].x) {
+      const int4 from = s_cut[r];
+      pr.pi = pr.s = from.x;
+      pr.e = s_cut[r + 1].x;
+      pr.b = from.y;
+      pr.hu = from.z;
+      pr.j = from.w;
+      pr.load_seq(p);
     }
     uint8_t *tiles = smem + r * ring_bytes;
     uint64_t *full = s_full + r * STAGES, *empty = s_empty + r * STAGES;
@@ -699,7 +724,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
         idle = 0;
         // the stage's entries lie in windows k0 and k1, at most one further
         const int k0 = pr.j >> 5, k1 = (pr.j + max(pr.blocks(), 1) - 1) >> 5;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           const int k = t ? k1 : k0;
           const bool miss = can && !pr.has(k);
@@ -743,35 +768,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
 
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_CONSUMER));
   // ---- consumers: hg warps work through a ring, each on its head's tiles ----
-  const int ring = wib / hg, sub = wib - ring * hg;
-  const int first = ring_cut<Cfg>(p, plan, cs, ce, ring, rings), total = ring_cut<Cfg>(p, plan, cs, ce, ring + 1, rings) - first;
+  const int ring = wib >> kp.hg_log2, sub = wib & (hg - 1);
+  const int4 from = s_cut[ring];
+  const int total = s_cut[ring + 1].x - from.x;
   if (total > 0) {
     // failure-path test hook: the worker holding the first work item replaces its first
     // wait by one on dead_bar, which runs out and takes the timeout path
-    const bool stall = p.stall_ns != 0 && first == 0;
-    uint64_t *full = s_full + ring * STAGES, *empty = s_empty + ring * STAGES;
+    const bool stall = p.stall_ns != 0 && from.x == 0;
     const uint32_t tiles = smem_u32(smem + ring * ring_bytes) + sub * Cfg::TILE, step = hg * Cfg::TILE;
     Kv4State<Cfg> state;
-    {  // while the first blocks are on their way
-      const Kv4Item it = locate_item(p, plan, first);
-      begin<Cfg>(state, kp, it.b, it.hu, sub, lane);
-    }
-    Kv4Meta m;
+    Kv4Meta m = {from.y, from.z, 0, kFirst};
     uint32_t parity = 0;
-    int done = 0;
-    for (int stage = 0; done < total;) {
-      if (stall && done == 0 ? !mbar_wait_bounded(&dead_bar, 0, p.timeout_ns)
-                             : !mbar_wait_bounded(&full[stage], parity, p.timeout_ns)) {
-        if (lane == 0) {
-          atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
-          atomicOr(&s_abort, 1 << ring);
-        }
-        break;
+    for (int done = 0, stage = 0;;) {
+      if (m.flags & kFirst) begin<Cfg>(state, kp, m.b, m.hu, sub, lane);  // (the first: while its blocks are on their way)
+      if (done == 0) {
+        uint64_t *bar = stall ? &dead_bar : &s_full[ring * STAGES];
+        if (!mbar_wait_bounded(bar, 0, p.timeout_ns)) break;
+        m = s_meta[ring * STAGES];
       }
-      m = s_meta[ring * STAGES + stage];
       const int nb = m.nb();
       const uint32_t at = tiles + stage * stage_bytes;
-      if ((m.flags & kFirst) && done > 0) begin<Cfg>(state, kp, m.b, m.hu, sub, lane);
       // every row of the unit sees every position of the stage
       if (nb == Cfg::NB && m.bad() == 0 && m.rem - state.bk_hi >= kBlock * Cfg::NB && m.rem - state.bk_lo <= p.wlen) {
         full_stage<Cfg>(state, at, step, lane);
@@ -781,27 +797,41 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
           edge_block<Cfg>(state, p, m.rem - kBlock * k, (m.bad() >> k) & 1, at + k * step, lane);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);  // (the record is in registers, too)
+      if (lane == 0) mbar_arrive(&s_empty[ring * STAGES + stage]);  // (the record is in registers, too)
       done += nb;
-      if ((m.flags & kLast) && !(m.flags & kEnds)) {
-        // its sums, unless the unit is whole, go to memory: the ring is in use
-        finish<Cfg>(state, kp, m, sub, kp.first_o + (((size_t)blockIdx.x * rings + ring) * hg + sub) * GC * D,
-                    s_ml + (2 * ring * hg + sub) * GC, lane);
+      if (m.flags & kLast) {
+        // The range's last segment leaves its sums in the ring, once all its warps are through; another's, unless
+        // the unit is whole, go to memory.
+        const bool ends = m.flags & kEnds;
+        if (ends) asm volatile("bar.sync %0, %1;" ::"r"(2 + ring), "r"(hg * 32) : "memory");
+        const int seg = 2 * ring + (ends ? 1 : 0);
+        finish<Cfg>(state, kp, m, sub,
+                    ends ? reinterpret_cast<float *>(smem + ring * ring_bytes) + sub * GC * D
+                         : kp.first_o + (((size_t)blockIdx.x * rings + ring) * hg + sub) * GC * D,
+                    s_ml + (seg * hg + sub) * GC, lane);
         if (sub == 0 && lane == 0 && (m.flags & (kOpens | kCloses)) != (kOpens | kCloses))
-          s_seg[2 * ring] = make_int2(m.b * p.HU + m.hu, m.flags);
+          s_seg[seg] = make_int2(m.b * p.HU + m.hu, m.flags);
+        if (ends) {
+          m.flags = 0;
+          break;
+        }
       }
       if (++stage == STAGES) {
         stage = 0;
         parity ^= 1u;
       }
+      if (!mbar_wait_bounded(&s_full[ring * STAGES + stage], parity, p.timeout_ns)) {
+        m.flags = kFirst;
+        break;
+      }
+      m = s_meta[ring * STAGES + stage];
     }
-    // the range's last segment stays in the ring, once all its warps are through (or gave up)
-    asm volatile("bar.sync %0, %1;" ::"r"(2 + ring), "r"(hg * 32) : "memory");
-    if (done >= total) {
-      finish<Cfg>(state, kp, m, sub, reinterpret_cast<float *>(smem + ring * ring_bytes) + sub * GC * D,
-                  s_ml + ((2 * ring + 1) * hg + sub) * GC, lane);
-      if (sub == 0 && lane == 0 && (m.flags & (kOpens | kCloses)) != (kOpens | kCloses))
-        s_seg[2 * ring + 1] = make_int2(m.b * p.HU + m.hu, m.flags);
+    if (m.flags != 0) {  // gave up on a wait
+      if (lane == 0) {
+        atomicOr(&cta_flags, PKV_FLAG_TIMEOUT);
+        atomicOr(&s_abort, 1 << ring);
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(2 + ring), "r"(hg * 32) : "memory");
     }
   }
   asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");  // the consumers
@@ -814,14 +844,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
   const int prev_unit = __shfl_sync(kFull, seg.x, prev & 31);
   const uint32_t heads = __ballot_sync(kFull, seg.x >= 0 && (prev < 0 || prev_unit != seg.x));  // a unit's first
   const int rows = hg * GC;  // of a unit
+#pragma unroll 1
   for (int t = tid; t < rows; t += WARPS * 32)
+#pragma unroll 1
     for (uint32_t todo = heads; todo; todo &= todo - 1) {
       const int g = __ffs(todo) - 1, next = todo & (todo - 1) ? __ffs(todo & (todo - 1)) - 1 : 32;
       const uint32_t members = valid & (0xffffffffu << g) & (0xffffffffu >> (32 - next));
       float M = -INFINITY, l = 0.f;
-#pragma unroll 2
+#pragma unroll 1
       for (uint32_t left = members; left; left &= left - 1) M = fmaxf(M, s_ml[(__ffs(left) - 1) * rows + t].x);
-#pragma unroll 2
+#pragma unroll 1
       for (uint32_t left = members; left; left &= left - 1) {
         const int q = __ffs(left) - 1;
         const float2 ml = s_ml[q * rows + t];
@@ -845,41 +877,46 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
       record.x = unit, record.y = closes;
     else if (!closes)
       record.z = unit;
-    const int b = unit / p.HU, hu = unit - b * p.HU, h0 = hu / p.NC * hg, r0 = (hu % p.NC) * GC;
-    for (int v = tid; v < rows * (D / 4); v += WARPS * 32) {
-      const int row = v / (D / 4), d = 4 * (v % (D / 4)), r = r0 + row % GC;  // row: [head][row]
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t rest = members; rest;) {
-        float4 a[4];
-        float wt[4];
+    const int b = unit / p.HU;
+    const UnitAt u = unit_at(kp, unit - b * p.HU, GC);
+    // four float4 a thread at a time: their loads overlap
+#pragma unroll 1
+    for (int v0 = tid; v0 < rows * (D / 4); v0 += 4 * WARPS * 32) {
+      float4 acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (uint32_t left = members; left; left &= left - 1) {
+        const int q = __ffs(left) - 1;
+        const float *src = (q & 1) ? reinterpret_cast<const float *>(smem + (q >> 1) * ring_bytes)
+                                   : kp.first_o + ((size_t)blockIdx.x * rings + (q >> 1)) * rows * D;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int q = rest ? __ffs(rest) - 1 : g;
-          wt[t] = rest ? s_wt[q * rows + row] : -1.f;
-          rest &= rest - 1;
-          const float *src = (q & 1) ? reinterpret_cast<const float *>(smem + (q >> 1) * ring_bytes)
-                                     : kp.first_o + ((size_t)blockIdx.x * rings + (q >> 1)) * rows * D;
-          a[t] = *reinterpret_cast<const float4 *>(src + 4 * v);
+          const int v = min(v0 + t * WARPS * 32, rows * (D / 4) - 1);
+          const float wt = s_wt[q * rows + v / (D / 4)];
+          const float4 a = *reinterpret_cast<const float4 *>(src + 4 * v);
+          const bool off = wt < 0.f;
+          acc[t].x = off ? acc[t].x : fmaf(wt, a.x, acc[t].x);
+          acc[t].y = off ? acc[t].y : fmaf(wt, a.y, acc[t].y);
+          acc[t].z = off ? acc[t].z : fmaf(wt, a.z, acc[t].z);
+          acc[t].w = off ? acc[t].w : fmaf(wt, a.w, acc[t].w);
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (!(wt[t] < 0.f)) {
-            acc.x = fmaf(wt[t], a[t].x, acc.x);
-            acc.y = fmaf(wt[t], a[t].y, acc.y);
-            acc.z = fmaf(wt[t], a[t].z, acc.z);
-            acc.w = fmaf(wt[t], a[t].w, acc.w);
-          }
       }
-      const float2 ml = s_ml[g * rows + row];
-      const float f = ml.y == 0.f ? 0.f : kp.v_unit / ml.y;
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-      if (opens && closes) {
-        if (r < p.R) store4<typename Cfg::Q>(p.out, query_row(p, b, h0 + row / GC, r) + d, acc);
-      } else {
-        const size_t slot = ((size_t)blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row;
-        *reinterpret_cast<float4 *>(p.part_o + slot * D + d) = acc;
-        // (a sum of NaN as +inf: the merge then gives NaN)
-        if (d == 0) p.part_lse[slot] = ml.y != ml.y ? INFINITY : ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int v = v0 + t * WARPS * 32, row = v / (D / 4), d = 4 * (v % (D / 4)), r = u.row + row % GC;  // row: [head][row]
+        if (v >= rows * (D / 4)) break;
+        const float2 ml = s_ml[g * rows + row];
+        const float f = ml.y == 0.f ? 0.f : __fdividef(kp.v_unit, ml.y);
+        const float4 y = make_float4(acc[t].x * f, acc[t].y * f, acc[t].z * f, acc[t].w * f);
+        if (opens && closes) {
+          if (r < p.R) store4<typename Cfg::Q>(p.out, row_at(p, b, u.head + row / GC, r) + d, y);
+        } else {
+          const int slot = (blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row;
+          *reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + d) = y;
+          // (a sum of NaN as +inf: the merge then gives NaN)
+          if (d == 0) p.part_lse[slot] = ml.y != ml.y ? INFINITY : ml.y == 0.f ? -INFINITY : ml.x + __log2f(ml.y);
+        }
       }
     }
   }
@@ -895,21 +932,32 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
   }
 }
 
-// Joins a unit's partial results: CTA (c, head) does the unit that range c begins and does not end.  A team of
-// threads has a float4 of the head's rows each; teams take the partial results in turn, eight in flight, and
-// are joined through shared memory (a long context's unit has one partial result for each of 76 CTAs).
+// Joins a unit's partial results: CTA (c, part) does the unit that range c begins and does not end, some rows of a
+// head of it.  A team of threads has a float4 of these rows each; teams take the partial results in turn, four
+// in flight, and are joined through shared memory (a long context's unit has one partial result for each of 76 CTAs).
 constexpr int kMergeThreads = 1024;
 template <class Q>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_constant__ Kv4Params kp) {
   const DecodeParams &p = kp.d;
   __shared__ float4 s_acc[kMergeThreads];
   __shared__ float2 s_ml[kMergeThreads];
+  const int lane = threadIdx.x & 31;
   grid_dep_wait();
-  const int c = blockIdx.x, unit = kp.records[c].z;
+  int c = blockIdx.x, unit = -1;
+  if (kp.merge_units) {  // fewer units than ranges: a CTA per unit looks for the range that begins it
+    for (int at = 0; at < p.P && unit < 0; at += 32) {
+      const uint32_t is = __ballot_sync(kFull, at + lane < p.P && kp.records[at + lane].z == (int)blockIdx.x);
+      if (is) {
+        c = at + __ffs(is) - 1;
+        unit = blockIdx.x;
+      }
+    }
+  } else {
+    unit = kp.records[c].z;
+  }
   if (unit < 0) return;
   // the ranges that continue it: c + 1 .. last
   int last = c;
-  const int lane = threadIdx.x & 31;
   for (int at = c + 1; at < p.P; at += 32) {
     const int4 r = at + lane < p.P ? kp.records[at + lane] : make_int4(-1, 0, -1, 0);
     const uint32_t goes = __ballot_sync(kFull, r.x == unit), ends = __ballot_sync(kFull, r.x != unit || r.y != 0);
@@ -920,37 +968,41 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
     }
     last = min(at + 31, p.P - 1);
   }
-  const int D = p.D, size = p.GC * D / 4, teams = blockDim.x / size, team = threadIdx.x / size;
-  const int v = threadIdx.x - team * size, row = 4 * v / D, d = 4 * v % D;
-  const int b = unit / p.HU, hu = unit % p.HU, r = (hu % p.NC) * p.GC + row, sub = blockIdx.y;
-  constexpr int kBatch = 8;
+  const int D = p.D, size = kp.merge_rows * D / 4, team = threadIdx.x / size, teams = blockDim.x / size;
+  const int parts = p.GC / kp.merge_rows, sub = blockIdx.y / parts;
+  const int v = threadIdx.x - team * size, row = blockIdx.y % parts * kp.merge_rows + 4 * v / D, d = 4 * v % D;
+  const int b = unit / p.HU;
+  const UnitAt u = unit_at(kp, unit - b * p.HU, p.GC);
+  const int r = u.row + row;
+  constexpr int kBatch = 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, den = 0.f;
+#pragma unroll 1
   for (int s = c + team; s <= last; s += kBatch * teams) {
     float4 o[kBatch];
     float l[kBatch];
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
       const int w = min(s + t * teams, last);
-      const size_t slot = (((size_t)w * 2 + (w == c ? 1 : 0)) * kp.hg + sub) * p.GC + row;
+      const int slot = ((w * 2 + (w == c ? 1 : 0)) * kp.hg + sub) * p.GC + row;
       l[t] = s + t * teams <= last ? p.part_lse[slot] : -INFINITY;
-      o[t] = *reinterpret_cast<const float4 *>(p.part_o + slot * D + d);
+      o[t] = *reinterpret_cast<const float4 *>(p.part_o + (size_t)slot * D + d);
     }
     float cm = M;
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
     if (cm == -INFINITY) continue;  // nothing seen yet
-    const float keep = exp2f(M - cm);
+    const float keep = exp2_fast(M - cm);
     acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
     den *= keep;
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
-      if (l[t] == -INFINITY) continue;
-      const float wt = exp2f(l[t] - cm);
-      acc.x = fmaf(wt, o[t].x, acc.x);
-      acc.y = fmaf(wt, o[t].y, acc.y);
-      acc.z = fmaf(wt, o[t].z, acc.z);
-      acc.w = fmaf(wt, o[t].w, acc.w);
+      const bool on = l[t] != -INFINITY;
+      const float wt = on ? exp2_fast(l[t] - cm) : 0.f;
+      acc.x = fmaf(wt, on ? o[t].x : 0.f, acc.x);
+      acc.y = fmaf(wt, on ? o[t].y : 0.f, acc.y);
+      acc.z = fmaf(wt, on ? o[t].z : 0.f, acc.z);
+      acc.w = fmaf(wt, on ? o[t].w : 0.f, acc.w);
       den += wt;
     }
     M = cm;
@@ -959,32 +1011,39 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
   s_ml[threadIdx.x] = make_float2(M, den);
   __syncthreads();
   if (team > 0 || r >= p.R) return;
-  float all = M;
-  for (int t = 1; t < teams; ++t) all = fmaxf(all, s_ml[t * size + v].x);
-  den = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int t = 0; t < teams; ++t) {
-    const float2 ml = s_ml[t * size + v];
-    if (ml.x == -INFINITY) continue;
-    const float wt = exp2f(ml.x - all);
-    const float4 a = s_acc[t * size + v];
-    acc.x = fmaf(wt, a.x, acc.x);
-    acc.y = fmaf(wt, a.y, acc.y);
-    acc.z = fmaf(wt, a.z, acc.z);
-    acc.w = fmaf(wt, a.w, acc.w);
-    den = fmaf(wt, ml.y, den);
+  if (teams > 1) {
+    float all = M;
+#pragma unroll 1
+    for (int t = 1; t < teams; ++t) all = fmaxf(all, s_ml[t * size + v].x);
+    den = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int t = 0; t < teams; ++t) {
+      const float2 ml = s_ml[t * size + v];
+      if (ml.x == -INFINITY) continue;
+      const float wt = exp2_fast(ml.x - all);
+      const float4 a = s_acc[t * size + v];
+      acc.x = fmaf(wt, a.x, acc.x);
+      acc.y = fmaf(wt, a.y, acc.y);
+      acc.z = fmaf(wt, a.z, acc.z);
+      acc.w = fmaf(wt, a.w, acc.w);
+      den = fmaf(wt, ml.y, den);
+    }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
-  store4<Q>(p.out, query_row(p, b, hu / p.NC * kp.hg + sub, r) + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  store4<Q>(p.out, row_at(p, b, u.head + sub, r) + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
-cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t stream, bool pdl) {
+cudaError_t launch_kv4_merge(Kv4Params p, cudaStream_t stream, bool pdl) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.d.n_ctas, p.hg);
-  // a team per eight partial results of a unit
-  const int size = p.d.GC * p.d.D / 4, units = p.d.B * p.d.HU, parts = (p.d.n_ctas + units - 1) / units + 1;
+  // many units: a CTA per range and head, one team; few: two rows a CTA and a team per four partial results
+  const int units = p.d.B * p.d.HU, each = (p.d.n_ctas + units - 1) / units + 1;
+  p.merge_units = units < p.d.n_ctas;
+  p.merge_rows = each > 8 ? 2 : p.d.GC;
+  const int size = p.merge_rows * p.d.D / 4;
   int teams = 1;
-  while (teams * size < kMergeThreads && teams * 8 < parts) teams *= 2;
+  while (2 * teams * size <= kMergeThreads && teams * 4 < each) teams *= 2;
+  cfg.gridDim = dim3(p.merge_units ? units : p.d.n_ctas, p.hg * (p.d.GC / p.merge_rows));
   cfg.blockDim = dim3(teams * size);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
