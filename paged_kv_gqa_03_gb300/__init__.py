@@ -636,20 +636,21 @@ def _issue(fn, args, name, prepare, workspace=None):
     return workspace
 
 
-def _token_rows(t, name, shape, dtype, device):
+def _token_rows(t, name, T, heads, D, dtype, device):
     """(pointer, elements from a token to the next) of rows [T, heads, D] whose
     heads lie side by side; a token's row may be a part of a wider one."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is dtype and t.shape == (T, heads, D) and t.get_device() == device:   # one test on the way through
+        ld, sh, sd = t.stride()
+        if sd == 1 and sh == D and T > 1:
+            return t.data_ptr(), ld
+        if t.numel() == 0 or (sd == 1 and (sh == D or heads == 1)):
+            return t.data_ptr(), (ld if T > 1 else heads * D)
+        raise ValueError(f"{name}: the {heads} heads of a token must lie side by side, strides {t.stride()}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-    T, heads, D = shape
-    ld, sh, sd = t.stride()
-    if t.numel() and (sd != 1 or (heads > 1 and sh != D)):
-        raise ValueError(f"{name}: the {heads} heads of a token must lie side by side, strides {t.stride()}")
-    return t.data_ptr(), (ld if T > 1 else heads * D)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _cache4(cache, device):
@@ -666,10 +667,9 @@ def paged_kv4_append(k_new, v_new, cache, slot_mapping, k_unit=1.0, v_unit=1.0, 
     18 * D], at slot_mapping [T] (int64; < 0 skips)."""
     dev = _device_of(cache, "cache")
     ptr, num_blocks, Hkv, D = _cache4(cache, dev)
-    T = k_new.shape[0]
-    shape = (T, Hkv, D)
-    k, ld_k = _token_rows(k_new, "k_new", shape, k_new.dtype, dev)
-    v, ld_v = _token_rows(v_new, "v_new", shape, k_new.dtype, dev)
+    T, dtype = k_new.shape[0], k_new.dtype
+    k, ld_k = _token_rows(k_new, "k_new", T, Hkv, D, dtype, dev)
+    v, ld_v = _token_rows(v_new, "v_new", T, Hkv, D, dtype, dev)
     args = (k, ld_k, v, ld_v, _code(k_new), ptr, _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev),
             T, Hkv, D, num_blocks, float(k_unit), float(v_unit), _stream(stream, dev))
     return _issue(_L.paged_kv4_append, args, "paged_kv4_append", prepare)
@@ -810,13 +810,15 @@ class RopeTable:
         _check(_L.pkv_rope_turns(host.ctypes.data, f.ctypes.data, rot_dim // 2), "pkv_rope_turns")
         self.rot_dim, self.magnitude, self.interleaved, self.frequencies = rot_dim, float(magnitude), bool(interleaved), f
         self.turns = torch.from_numpy(host.view(np.int64)).to("cuda" if device is None else device)
+        self._device = self.turns.get_device()
+        self._args = (self.turns.data_ptr(), rot_dim, 1 if self.interleaved else 0, self.magnitude)
 
 
 def _rope_args(table, positions, T, device):
-    torch = _torch()
-    return (_arg(positions, "positions", torch.int64, (T,), device),
-            _arg(table.turns, "the table's turns", torch.int64, (table.rot_dim // 2,), device),
-            table.rot_dim, 1 if table.interleaved else 0, table.magnitude)
+    """positions .. magnitude of a rope call."""
+    if table._device != device:
+        raise ValueError(f"the table is on {table.turns.device}, expected cuda:{device}")
+    return (_arg(positions, "positions", _torch().int64, (T,), device), *table._args)
 
 
 def paged_rope(q, k, positions, table, q_out=None, k_out=None, stream=None, prepare=False):
@@ -835,21 +837,23 @@ def paged_rope(q, k, positions, table, q_out=None, k_out=None, stream=None, prep
                 raise ValueError(f"{name}_out without {name}")
             side.append((None, 0, None, 0, 0))
             continue
-        shape = (T, x.shape[1], D)
-        p, ld = _token_rows(x, name, shape, dtype, dev)
-        po, ldo = (p, ld) if out is None else _token_rows(out, name + "_out", shape, dtype, dev)
-        side.append((po, ldo, p, ld, shape[1]))
+        heads = x.shape[1]
+        p, ld = _token_rows(x, name, T, heads, D, dtype, dev)
+        po, ldo = (p, ld) if out is None else _token_rows(out, name + "_out", T, heads, D, dtype, dev)
+        side.append((po, ldo, p, ld, heads))
     args = (*side[0][:4], *side[1][:4], _code(first), *_rope_args(table, positions, T, dev), T, side[0][4], side[1][4], D,
             _stream(stream, dev))
     return _issue(_L.paged_rope, args, "paged_rope", prepare)
 
 
 def _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev):
-    T, Hq = q.shape[0], q.shape[1]
-    dtype, kv = q.dtype, (T, Hkv, D)
-    p, ld = _token_rows(q, "q", (T, Hq, D), dtype, dev)
-    po, ldo = (p, ld) if q_out is None else _token_rows(q_out, "q_out", (T, Hq, D), dtype, dev)
-    return (po, ldo, p, ld, *_token_rows(k_new, "k_new", kv, dtype, dev), *_token_rows(v_new, "v_new", kv, dtype, dev), _code(q)), T, Hq
+    """q_out .. dtype of a rope append, T and Hq."""
+    (T, Hq), dtype = q.shape[:2], q.dtype
+    p, ld = _token_rows(q, "q", T, Hq, D, dtype, dev)
+    po, ldo = (p, ld) if q_out is None else _token_rows(q_out, "q_out", T, Hq, D, dtype, dev)
+    k, ld_k = _token_rows(k_new, "k_new", T, Hkv, D, dtype, dev)
+    v, ld_v = _token_rows(v_new, "v_new", T, Hkv, D, dtype, dev)
+    return (po, ldo, p, ld, k, ld_k, v, ld_v, _code(q)), T, Hq
 
 
 def paged_rope_append(q, k_new, v_new, positions, table, k_cache, v_cache, slot_mapping, q_out=None, stream=None,
@@ -858,9 +862,11 @@ def paged_rope_append(q, k_new, v_new, positions, table, k_cache, v_cache, slot_
     by their positions [T] (int64), and writes the rotated keys and v_new into the caches
     [num_blocks, Hkv, 16, D] of the same type at slot_mapping [T] (int64; < 0 skips)."""
     dev = _device_of(q, "q")
-    k, v, _, _, num_blocks, Hkv, D = _cache(k_cache, v_cache, None, None, dev)
-    if k_cache.dtype is not q.dtype:
-        raise TypeError(f"the cache must be {q.dtype}, got {k_cache.dtype}")
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != 16:
+        raise ValueError(f"k_cache must be [num_blocks, Hkv, 16, D], got {tuple(shape)}")
+    num_blocks, Hkv, _, D = shape
+    k, v = _arg(k_cache, "k_cache", q.dtype, shape, dev), _arg(v_cache, "v_cache", q.dtype, shape, dev)
     rows, T, Hq = _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev)
     args = (*rows, *_rope_args(table, positions, T, dev), k, v,
             _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev), T, Hq, Hkv, D, num_blocks, _stream(stream, dev))

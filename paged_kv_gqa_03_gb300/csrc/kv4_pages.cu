@@ -47,20 +47,16 @@ __global__ void __launch_bounds__(kThreads)
   const int tok = (int)(slot % kBlock);
   uint8_t *tile = cache + (size_t)(slot / kBlock * Hkv + h) * Kv4Tile<D>::kBytes;
   const size_t at = (size_t)h * D + 16 * g;
-  float y[16];
   if (!v) {
-    load16<T>(k_new, (size_t)(t * ld_k) + at, y);
-    kv4_store_k<D>(tile, tok, g, kv4_quantise(y, k_unit));
+    kv4_store_k<D>(tile, tok, g, kv4_quantise_at<T>(k_new, (size_t)(t * ld_k) + at, k_unit));
     return;
   }
   // a pair that stands together in the call: its even token's thread stores both
   if ((tok & 1) && t > 0 && slots[t - 1] == slot - 1) return;
   const bool two = !(tok & 1) && t + 1 < T_ && slots[t + 1] == slot + 1;
-  load16<T>(v_new, (size_t)(t * ld_v) + at, y);
-  const Kv4Group a = kv4_quantise(y, v_unit);
+  const Kv4Group a = kv4_quantise_at<T>(v_new, (size_t)(t * ld_v) + at, v_unit);
   if (two) {
-    load16<T>(v_new, (size_t)((t + 1) * ld_v) + at, y);
-    kv4_store_v2<D>(tile, tok >> 1, g, a, kv4_quantise(y, v_unit));
+    kv4_store_v2<D>(tile, tok >> 1, g, a, kv4_quantise_at<T>(v_new, (size_t)((t + 1) * ld_v) + at, v_unit));
   } else {
     kv4_store_v1<D>(tile, tok, g, a);
   }
@@ -97,10 +93,9 @@ __global__ void __launch_bounds__(kThreads)
   const int src = pairs[2 * p.pair], dst = pairs[2 * p.pair + 1];
   if (src < 0 || src >= num_src || dst < 0 || dst >= num_blocks) return;
   const size_t at = (((size_t)src * Hkv + p.h) * kBlock + 2 * p.u) * D + 16 * p.g;
-  float x[16], y[16];
-  load16<T>(p.v ? vv : k, at, x);
-  load16<T>(p.v ? vv : k, at + D, y);
-  const Kv4Group a = kv4_quantise(x, p.v ? v_unit : k_unit), b = kv4_quantise(y, p.v ? v_unit : k_unit);
+  const void *rows = p.v ? vv : k;
+  const float unit = p.v ? v_unit : k_unit;
+  const Kv4Group a = kv4_quantise_at<T>(rows, at, unit), b = kv4_quantise_at<T>(rows, at + D, unit);
   uint8_t *tile = cache + ((size_t)dst * Hkv + p.h) * Kv4Tile<D>::kBytes;
   if (p.v) {
     kv4_store_v2<D>(tile, p.u, p.g, a, b);
@@ -128,11 +123,10 @@ __global__ void __launch_bounds__(kThreads)
     b = kv4_load_k<D>(tile, 2 * p.u + 1, p.g);
   }
   const size_t at = (((size_t)dst * Hkv + p.h) * kBlock + 2 * p.u) * D + 16 * p.g;
-  float y[16];
-  kv4_values(a, p.v ? v_unit : k_unit, y);
-  store16<T>(p.v ? vv : k, at, y);
-  kv4_values(b, p.v ? v_unit : k_unit, y);
-  store16<T>(p.v ? vv : k, at + D, y);
+  void *rows = p.v ? vv : k;
+  const float unit = p.v ? v_unit : k_unit;
+  kv4_values_to<T>(a, unit, rows, at);
+  kv4_values_to<T>(b, unit, rows, at + D);
 }
 
 __global__ void __launch_bounds__(kThreads)

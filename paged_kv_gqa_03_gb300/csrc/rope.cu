@@ -26,7 +26,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxPairs = 64;  // rot / 2, head dim 128
 
 enum Dest { kRows, kCache, kCache4 };
@@ -210,7 +210,7 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
   // few tokens: one item a thread, so that a step's rows are spread over as many CTAs as it
   // has; many: a token's rows in one CTA where three (fp32: five) items a thread hold them
   const bool wide = p.T > 256;
-  constexpr int kWide = T::kBytes == 4 ? 5 : 3;  // (kCache4: at most 40 KiB of rows)
+  constexpr int kWide = 5;  // (kCache4: at most 40 KiB of rows)
   const int cap = kThreads * (wide ? kWide : 1) / items_row;  // heads a CTA holds
   const int parts = (heads + cap - 1) / cap, per = (heads + parts - 1) / parts;
   if ((double)p.T * parts > 2147483000.0) return cudaErrorNotSupported;
