@@ -19,6 +19,12 @@ lengths cross to the device, all from ONE pinned staging buffer with one copy
 (two staging buffers alternate so the host can prepare step n+1 while step n's
 copy is in flight).  Everything is asynchronous on `stream`.
 
+With rope=RopeTable(...) q and k_new come unrotated: a3 turns both by their tokens'
+positions in their sequences and appends the rotated keys (one kernel; FP8
+caches: a rotation in front of the append).
+
+Kv4Step is the same step on a cache held in 4 bits.
+
 TreeStep is the step of speculative decoding with a tree of drafted tokens per
 sequence: the same chain with the tree's masks in the attention, then the
 verification of the drafts, the move of the accepted path's rows in the cache
@@ -28,8 +34,10 @@ import numpy as np
 import torch
 
 from . import (BlockManager, lib, paged_decode_attention, paged_decode_workspace_bytes,
-               paged_kv_append, paged_kv_copy_blocks, paged_tree_attention, paged_tree_commit,
-               paged_tree_verify, paged_tree_workspace_bytes, pkv_copy)
+               paged_kv4_append, paged_kv4_copy_blocks, paged_kv4_decode_attention,
+               paged_kv4_decode_workspace_bytes, paged_kv4_rope_append, paged_kv_append,
+               paged_kv_copy_blocks, paged_rope, paged_rope_append, paged_tree_attention,
+               paged_tree_commit, paged_tree_verify, paged_tree_workspace_bytes, pkv_copy)
 
 _ALIGN = 256
 
@@ -61,18 +69,22 @@ class _Staging:
 
 class DecodeStep:
     def __init__(self, k_cache, v_cache, Hq, q_dtype, max_blocks, k_scale=None, v_scale=None,
-                 num_splits=0, stream=None, scale=None, q_len=1, window=0, calibrated=False):
+                 num_splits=0, stream=None, scale=None, q_len=1, window=0, calibrated=False, rope=None):
         self.k_cache, self.v_cache = k_cache, v_cache
         self.k_scale, self.v_scale = k_scale, v_scale
         self.num_blocks, self.Hkv, _, self.D = k_cache.shape
-        self.Hq, self.q_dtype, self.max_blocks = Hq, q_dtype, max_blocks
         self.new_dtype = q_dtype if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
+        self.calibrated = calibrated
+        self._setup(k_cache.device, Hq, q_dtype, max_blocks, num_splits, stream, scale, q_len, window, rope)
+
+    def _setup(self, device, Hq, q_dtype, max_blocks, num_splits, stream, scale, q_len, window, rope):
+        self.Hq, self.q_dtype, self.max_blocks = Hq, q_dtype, max_blocks
         self.num_splits = num_splits
         self.q_len = q_len
         self.window = window
-        self.calibrated = calibrated
+        self.rope = rope
         self.scale = 1.0 / float(np.sqrt(self.D)) if scale is None else float(scale)
-        self.device = k_cache.device
+        self.device = device
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
         self.bm = BlockManager(self.num_blocks)
         self.seqs = []
@@ -98,7 +110,7 @@ class DecodeStep:
                 ("slots", (B * L,), torch.int64),
                 ("pairs", (2 * B * L,), torch.int32),
                 ("table", (B, self.max_blocks), torch.int32),
-                ("lens", (B,), torch.int32)]
+                ("lens", (B,), torch.int32)] + ([] if self.rope is None else [("positions", (B * L,), torch.int64)])
 
     def _layout(self, B):
         layout, off = {}, 0
@@ -127,6 +139,9 @@ class DecodeStep:
         with torch.cuda.stream(self.stream):
             self._dev = _Staging(layout, total, self.device, False)
             self._ws = torch.empty(self._workspace_bytes(B), dtype=torch.uint8, device=self.device)
+            if self.rope is not None:   # the rotated queries (and, for FP8 caches, keys)
+                self._q_rot = torch.empty((B * self.q_len, self.Hq, self.D), dtype=self.q_dtype, device=self.device)
+                self._k_rot = torch.empty((B * self.q_len, self.Hkv, self.D), dtype=self.new_dtype, device=self.device)
         self.h_seqs = np.empty(B, dtype=np.int64)
         self.h_tok_seqs = np.empty(B * self.q_len, dtype=np.int64)
         self.d_q, self.d_k_new, self.d_v_new = self._dev["q"], self._dev["k_new"], self._dev["v_new"]
@@ -155,6 +170,8 @@ class DecodeStep:
         tables and lengths of q_len new tokens per sequence into it.  Returns
         the number of copy-on-write pairs (raises on OOM)."""
         seqs = self.seqs if seqs is None else seqs
+        if self.rope is not None and len(set(int(s) for s in seqs)) != len(seqs):   # (whose positions would be its last's)
+            raise ValueError("a sequence may appear once in a step with rotary positions")
         self._switch(seqs)
         if self.q_len == 1:
             tok_seqs = self.h_seqs
@@ -162,6 +179,10 @@ class DecodeStep:
             tok_seqs = self.h_tok_seqs
             tok_seqs.reshape(-1, self.q_len)[:] = self.h_seqs[:, None]
         self._reserve(tok_seqs, self.h_slots.numpy(), seqs)
+        if self.rope is not None:
+            L = self.q_len
+            positions = self._host[self._turn]["positions"].numpy().reshape(-1, L)
+            positions[:] = self.h_lens.numpy()[:, None] - L + np.arange(L)
         return self.ncow
 
     def _switch(self, seqs):
@@ -211,21 +232,36 @@ class DecodeStep:
     def launch(self, q, k_new, v_new, out):
         """Runs a2..a8 with device tensors q, k_new, v_new (bookkeeping from
         the last upload())."""
-        s = self.stream
         if self.ncow:
-            paged_kv_copy_blocks(self.k_cache, self.v_cache, self.d_pairs[:2 * self.ncow].view(-1, 2),
-                                 self.k_scale, self.v_scale, stream=s)
-        key = ("append", _buffer(k_new), _buffer(v_new), self.d_slots.data_ptr())
-        call = self._calls.get(key)
-        if call is None:
+            self._copy_blocks(self.d_pairs[:2 * self.ncow].view(-1, 2))
+        key = ("append", None if self.rope is None else _buffer(q), _buffer(k_new), _buffer(v_new), self.d_slots.data_ptr())
+        calls = self._calls.get(key)
+        if calls is None:
             if k_new.dim() == 4:
                 k_new = k_new.view(-1, self.Hkv, self.D)
                 v_new = v_new.view(-1, self.Hkv, self.D)
-            call = self._remember(key, paged_kv_append(
-                k_new, v_new, self.k_cache, self.v_cache, self.d_slots, self.k_scale, self.v_scale,
-                stream=s, calibrated=self.calibrated, prepare=True))
-        call()
-        self.attend(q, out)
+            rows = None if self.rope is None else q.view(-1, self.Hq, self.D)
+            calls = self._remember(key, self._append_calls(rows, k_new, v_new))
+        for call in calls:
+            call()
+        self.attend(q if self.rope is None else self._q_rot.view(q.shape), out)
+
+    def _copy_blocks(self, pairs):
+        paged_kv_copy_blocks(self.k_cache, self.v_cache, pairs, self.k_scale, self.v_scale, stream=self.stream)
+
+    def _append_calls(self, q, k_new, v_new):
+        """a3 of rows [tokens, heads, D] (q: with a rope only): the marshalled calls, in order."""
+        s, calls = self.stream, []
+        if self.rope is not None:
+            positions = self._dev["positions"]
+            if self.k_cache.dtype != torch.float8_e4m3fn:
+                return [paged_rope_append(q, k_new, v_new, positions, self.rope, self.k_cache, self.v_cache, self.d_slots,
+                                          q_out=self._q_rot, stream=s, prepare=True)]
+            calls.append(paged_rope(q, k_new, positions, self.rope, q_out=self._q_rot, k_out=self._k_rot, stream=s,
+                                    prepare=True))
+            k_new = self._k_rot
+        return calls + [paged_kv_append(k_new, v_new, self.k_cache, self.v_cache, self.d_slots, self.k_scale, self.v_scale,
+                                        stream=s, calibrated=self.calibrated, prepare=True)]
 
     def attend(self, q, out):
         """a4-a8 on the current bookkeeping.  The C call's arguments are
@@ -233,11 +269,14 @@ class DecodeStep:
         key = ("attend", _buffer(q), _buffer(out), self.d_table.data_ptr())
         call = self._calls.get(key)
         if call is None:
-            call = self._remember(key, paged_decode_attention(
-                out, q, self.k_cache, self.v_cache, self.d_table, self.d_lens, self.scale,
-                self.k_scale, self.v_scale, num_splits=self.num_splits, workspace=self._ws,
-                stream=self.stream, window=self.window, prepare=True))
+            call = self._remember(key, self._attend_call(q, out))
         call()
+
+    def _attend_call(self, q, out):
+        return paged_decode_attention(
+            out, q, self.k_cache, self.v_cache, self.d_table, self.d_lens, self.scale,
+            self.k_scale, self.v_scale, num_splits=self.num_splits, workspace=self._ws,
+            stream=self.stream, window=self.window, prepare=True)
 
     def _remember(self, key, call):
         if len(self._calls) >= 8:
@@ -334,6 +373,37 @@ class DecodeStep:
     def replay(self):
         with torch.cuda.stream(self.stream):
             self.graph.replay()
+
+
+class Kv4Step(DecodeStep):
+    """DecodeStep on a cache held in 4 bits: cache uint8 [num_blocks, Hkv, 18 * D]
+    (D 64 or 128), k_unit / v_unit the cache's units.  q, k_new and v_new are f16 or bf16
+    (q_dtype)."""
+
+    def __init__(self, cache, Hq, q_dtype, max_blocks, k_unit=1.0, v_unit=1.0, num_splits=0, stream=None,
+                 scale=None, q_len=1, window=0, rope=None):
+        self.cache, self.k_unit, self.v_unit = cache, float(k_unit), float(v_unit)
+        self.num_blocks, self.Hkv, self.D = cache.shape[0], cache.shape[1], cache.shape[2] // 18
+        self.new_dtype = q_dtype
+        self._setup(cache.device, Hq, q_dtype, max_blocks, num_splits, stream, scale, q_len, window, rope)
+
+    def _workspace_bytes(self, B):
+        return paged_kv4_decode_workspace_bytes(B, self.Hq, self.Hkv, self.D, self.q_dtype, self.num_splits, self.q_len)
+
+    def _copy_blocks(self, pairs):
+        paged_kv4_copy_blocks(self.cache, pairs, stream=self.stream)
+
+    def _append_calls(self, q, k_new, v_new):
+        s = self.stream
+        if self.rope is None:
+            return [paged_kv4_append(k_new, v_new, self.cache, self.d_slots, self.k_unit, self.v_unit, stream=s, prepare=True)]
+        return [paged_kv4_rope_append(q, k_new, v_new, self._dev["positions"], self.rope, self.cache, self.d_slots,
+                                      self.k_unit, self.v_unit, q_out=self._q_rot, stream=s, prepare=True)]
+
+    def _attend_call(self, q, out):
+        return paged_kv4_decode_attention(
+            out, q, self.cache, self.d_table, self.d_lens, self.scale, self.k_unit, self.v_unit,
+            num_splits=self.num_splits, workspace=self._ws, stream=self.stream, window=self.window, prepare=True)
 
 
 class TreeStep(DecodeStep):
