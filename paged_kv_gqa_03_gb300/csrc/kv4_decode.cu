@@ -54,18 +54,21 @@ struct Kv4Cfg {
   static constexpr int D = D_, NH = NH_, GC = 8 * NH_, WARPS = WARPS_, STAGES = STAGES_, NB = NB_;
   static constexpr int THREADS = (WARPS + 4) * 32;
   static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_PRODUCER = WARPS == 12 ? 56 : 88;
+  static constexpr int REGS_PRODUCER = 56;
   static constexpr int REGS_CONSUMER = REGS_LAUNCH + (REGS_LAUNCH - REGS_PRODUCER) * 4 / WARPS / 8 * 8;
   static_assert(WARPS % 4 == 0, "warpgroups");
   static_assert(REGS_CONSUMER * WARPS + REGS_PRODUCER * 4 <= REGS_LAUNCH * (WARPS + 4), "registers of the launch");
   static constexpr int TILE = Kv4Tile<D>::kBytes;
   static constexpr int STAGE_BYTES = NB * TILE;
   static constexpr int KS = D / 16, MT = D / 16;
+  // A whole stage at a context's or window's end takes masks in one go (in 16-row units, whose registers that
+  // costs: 16 x 1000-32768, 4 new 92.6 -> 98.5 us, it goes block by block).
+  static constexpr bool kWholeEdges = NH == 1;
   static constexpr size_t TILES_BYTES = (size_t)WARPS * STAGES * STAGE_BYTES;
   static constexpr size_t META_BYTES = (size_t)WARPS * STAGES * 16;
   static constexpr size_t BAR_BYTES = (size_t)WARPS * STAGES * 16;  // full, empty
   static constexpr size_t SMEM = TILES_BYTES + META_BYTES + BAR_BYTES + (size_t)kKv4Prefix * 4;
-  static_assert(SMEM + WARPS * (24 * GC + 256) + 512 <= 232448, "shared memory of a CTA");
+  static_assert(SMEM + WARPS * (16 * GC + 256) + 1024 <= 232448, "shared memory of a CTA");
 };
 
 // Short ranges spend most of their time on instructions that are fetched for the first time (a small call's warps
@@ -470,24 +473,54 @@ __device__ __forceinline__ void softmax(Kv4State<Cfg> &st, int nh, const float (
   }
 }
 
-// A whole stage, every position of which every row of the unit sees.
+// A whole stage.  `edge`: some row of the unit does not see all of it (a context's or a window's end).
 template <class Cfg>
-__device__ __forceinline__ void full_stage(Kv4State<Cfg> &st, uint32_t tiles, uint32_t step, int lane) {
-  float s[Cfg::NB][Cfg::NH][4];
-  uint32_t pb[Cfg::NB][Cfg::NH][2];
+__device__ __forceinline__ void full_stage(Kv4State<Cfg> &st, const DecodeParams &p, int rem, bool edge, uint32_t tiles,
+                                           uint32_t step, int lane) {
+  constexpr int NB = Cfg::NB, NH = Cfg::NH;
+  float s[NB][NH][4];
+  uint32_t pb[NB][NH][2];
 #pragma unroll
-  for (int i = 0; i < Cfg::NB; ++i) scores<Cfg>(st, tiles + i * step, lane, s[i]);
+  for (int i = 0; i < NB; ++i) scores<Cfg>(st, tiles + i * step, lane, s[i]);
+  if (Cfg::kWholeEdges && edge) {
 #pragma unroll
-  for (int nh = 0; nh < Cfg::NH; ++nh) softmax<Cfg, Cfg::NB>(st, nh, s, pb);
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-  for (int i = 0; i < Cfg::NB; ++i) {
-    uint32_t w[2];
-    v_scales<Cfg>(tiles + i * step, lane, w);
-    values<Cfg>(st, tiles + i * step, lane, w, pb[i]);
+      for (int c = 0; c < 2; ++c) {
+        const int r = (lane >> 2) - (rem - st.back[nh][c] - p.wlen);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          if ((uint32_t)(r + kBlock * i) >= (uint32_t)p.wlen) s[i][nh][c] = -INFINITY;
+          if ((uint32_t)(r + kBlock * i + 8) >= (uint32_t)p.wlen) s[i][nh][2 + c] = -INFINITY;
+        }
+      }
+  }
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh) softmax<Cfg, NB>(st, nh, s, pb);
+  if constexpr (Cfg::kWholeEdges) {
+    uint32_t w[NB][2];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) v_scales<Cfg>(tiles + i * step, lane, w[i]);
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t spoiled = clean_scales(w[i], lane, rem - kBlock * i);
+        if (__any_sync(kFull, spoiled != 0)) spoil<Cfg>(st, p, rem - kBlock * i, spoiled);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) values<Cfg>(st, tiles + i * step, lane, w[i], pb[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      uint32_t w[2];
+      v_scales<Cfg>(tiles + i * step, lane, w);
+      values<Cfg>(st, tiles + i * step, lane, w, pb[i]);
+    }
   }
 }
 
-// One block of another stage: at a context's or a window's end, of a short range, with a bad id (its values are zeros).
+// One block of another stage: of fewer blocks, with a bad id (its values are zeros), or see kWholeEdges.
 template <class Cfg>
 __device__ __forceinline__ void edge_block(Kv4State<Cfg> &st, const DecodeParams &p, int rem, bool zero, uint32_t tile,
                                            int lane) {
@@ -539,8 +572,8 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
       const int row = 8 * nh + 2 * tig + c;
       // a row that sees nothing gives 0; a sum of NaN gives NaN
       const float f = !whole ? 1.f : l == 0.f ? 0.f : kp.v_unit / l;
+      if (row >= gc) continue;
       if (!whole && gid == 0) ml[row] = make_float2(st.m[nh][c] == -INFINITY ? -INFINITY : -st.off[nh][c], l);
-      if (whole && row >= gc) continue;
       const size_t at = whole ? row_at(p, m.b, h, r0 + row) + RUN * gid : 0;
 #pragma unroll
       for (int i = 0; i < RUN / 4; ++i) {
@@ -554,11 +587,11 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
     }
 }
 
-// The plan: blocks before each sequence, in a lane's registers (up to 32 sequences: `before` and `items` of
-// sequence `lane`) or in memory.
+// The plan: blocks before each sequence.  Up to 128 sequences it is in a warp's registers: lane l has sequences
+// per l .. per l + per - 1, per = ceil(B / 32), their blocks and those before them; in memory otherwise.
 struct Kv4Plan {
   const int32_t *pre;
-  int before, items, total;
+  int before, items[4], per, total;
   bool small;
 };
 // Unit and block of item x of the list (a whole warp, the same x).
@@ -570,9 +603,19 @@ __device__ __forceinline__ Kv4Item locate_item(const DecodeParams &p, const Kv4P
   // lo: the largest b with HU * blocks before it <= x (the count of items is within 32 bits)
   int lo = 0, first, items;
   if (plan.small) {
-    lo = 31 - __clz(__ballot_sync(kFull, lane < p.B && p.HU * plan.before <= x));
-    first = __shfl_sync(kFull, plan.before, lo);
-    items = __shfl_sync(kFull, plan.items, lo);
+    const int l = 31 - __clz(__ballot_sync(kFull, lane * plan.per < p.B && p.HU * plan.before <= x));
+    first = __shfl_sync(kFull, plan.before, l);
+    items = __shfl_sync(kFull, plan.items[0], l);
+    lo = l * plan.per;
+#pragma unroll
+    for (int i = 1; i < 4 && plan.per > 1; ++i) {
+      const int more = __shfl_sync(kFull, plan.items[i], l);
+      if (i < plan.per && lo + 1 < p.B && p.HU * (first + items) <= x) {
+        ++lo;
+        first += items;
+        items = more;
+      }
+    }
   } else {
     for (int span = p.B; span > 1;) {
       const int step = (span + 31) / 32;
@@ -608,7 +651,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
   __shared__ int4 s_cut[WARPS + 1];           // {item, b, unit, block} at which a ring's range begins
   __shared__ int2 s_seg[2 * WARPS];           // segments left to join, two a ring, in the list's order: {unit or -1, flags}
   __shared__ float2 s_ml[2 * WARPS * GC];     // [segment][head][row]
-  __shared__ float s_wt[2 * WARPS * GC];
   __shared__ int32_t s_ids[WARPS][64];        // table entries ahead, by ring
   __shared__ int32_t s_scan[32];
   __shared__ int cta_flags, s_abort;          // s_abort: bit r: ring r's consumer gave up
@@ -629,18 +671,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
 
   // ---- the plan, and the CTA's range [cs, ce) ----
   Kv4Plan plan;
-  plan.small = p.B <= 32;
-  plan.before = plan.items = 0;
+  plan.small = p.B <= 128;
   if (plan.small) {  // every warp for itself
-    int flags = 0;
-    if (lane < p.B) plan.items = seq_items<false>(p, lane, clamp_len<false>(p, lane, __ldg(p.context_lens + lane), &flags));
-    int x = plan.items;
+    plan.per = (p.B + 31) / 32;
+    int flags = 0, mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = lane * plan.per + i;
+      plan.items[i] = 0;
+      if (i < plan.per && b < p.B)
+        plan.items[i] = seq_items<false>(p, b, clamp_len<false>(p, b, __ldg(p.context_lens + b), &flags));
+      mine += plan.items[i];
+    }
+    int x = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(kFull, x, off);
       if (lane >= off) x += y;
     }
-    plan.before = x - plan.items;
+    plan.before = x - mine;
     plan.total = __shfl_sync(kFull, x, 31);
     if (wib == 0 && flags) atomicOr(&cta_flags, flags);
   } else {
@@ -788,9 +837,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
       }
       const int nb = m.nb();
       const uint32_t at = tiles + stage * stage_bytes;
-      // every row of the unit sees every position of the stage
-      if (nb == Cfg::NB && m.bad() == 0 && m.rem - state.bk_hi >= kBlock * Cfg::NB && m.rem - state.bk_lo <= p.wlen) {
-        full_stage<Cfg>(state, at, step, lane);
+      const bool edge = m.rem - state.bk_hi < kBlock * Cfg::NB || m.rem - state.bk_lo > p.wlen;
+      if (nb == Cfg::NB && m.bad() == 0 && (Cfg::kWholeEdges || !edge)) {
+        full_stage<Cfg>(state, p, m.rem, edge, at, step, lane);
       } else {
 #pragma unroll 1
         for (int k = 0; k < nb; ++k)
@@ -844,28 +893,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
   const int prev_unit = __shfl_sync(kFull, seg.x, prev & 31);
   const uint32_t heads = __ballot_sync(kFull, seg.x >= 0 && (prev < 0 || prev_unit != seg.x));  // a unit's first
   const int rows = hg * GC;  // of a unit
-#pragma unroll 1
-  for (int t = tid; t < rows; t += WARPS * 32)
-#pragma unroll 1
-    for (uint32_t todo = heads; todo; todo &= todo - 1) {
-      const int g = __ffs(todo) - 1, next = todo & (todo - 1) ? __ffs(todo & (todo - 1)) - 1 : 32;
-      const uint32_t members = valid & (0xffffffffu << g) & (0xffffffffu >> (32 - next));
-      float M = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (uint32_t left = members; left; left &= left - 1) M = fmaxf(M, s_ml[(__ffs(left) - 1) * rows + t].x);
-#pragma unroll 1
-      for (uint32_t left = members; left; left &= left - 1) {
-        const int q = __ffs(left) - 1;
-        const float2 ml = s_ml[q * rows + t];
-        // (a row that saw nothing, or NaN alone: its maximum is -inf, its sum 0 or NaN)
-        const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? -1.f : 1.f) : exp2_fast(ml.x - M);
-        s_wt[q * rows + t] = wt;  // -1: nothing to add
-        if (!(wt < 0.f)) l = fmaf(wt, ml.y, l);
-      }
-      s_ml[g * rows + t] = make_float2(M, l);
-    }
-  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-
   int4 record = make_int4(-1, 0, -1, 0);  // {unit that an earlier CTA began, ends here; unit that goes on}
   for (uint32_t todo = heads; todo; todo &= todo - 1) {
     const int g = __ffs(todo) - 1, next = todo & (todo - 1) ? __ffs(todo & (todo - 1)) - 1 : 32;
@@ -879,12 +906,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
       record.z = unit;
     const int b = unit / p.HU;
     const UnitAt u = unit_at(kp, unit - b * p.HU, GC);
-    // four float4 a thread at a time: their loads overlap
+    // four float4 of the rows that exist a thread at a time: their loads overlap
+    const int live = min(GC, p.R - u.row), part = 65536 / live + 1;  // n / live = n * part >> 16 for n < 256
 #pragma unroll 1
-    for (int v0 = tid; v0 < rows * (D / 4); v0 += 4 * WARPS * 32) {
+    for (int v0 = tid; v0 < hg * live * (D / 4); v0 += 4 * WARPS * 32) {
       float4 acc[4];
+      float M[4], l[4];
+      int row[4];  // [head][row]
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < 4; ++t) {
+        const int n = min(v0 + t * WARPS * 32, hg * live * (D / 4) - 1) / (D / 4), sub = n * part >> 16;
+        row[t] = sub * GC + n - sub * live;
+        acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        M[t] = -INFINITY;
+        l[t] = 0.f;
+      }
+      const int d = 4 * (v0 % (D / 4));
+      static_assert(WARPS * 32 % (D / 4) == 0, "a thread keeps its elements");
 #pragma unroll 1
       for (uint32_t left = members; left; left &= left - 1) {
         const int q = __ffs(left) - 1;
@@ -892,30 +930,33 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
                                    : kp.first_o + ((size_t)blockIdx.x * rings + (q >> 1)) * rows * D;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int v = min(v0 + t * WARPS * 32, rows * (D / 4) - 1);
-          const float wt = s_wt[q * rows + v / (D / 4)];
-          const float4 a = *reinterpret_cast<const float4 *>(src + 4 * v);
-          const bool off = wt < 0.f;
-          acc[t].x = off ? acc[t].x : fmaf(wt, a.x, acc[t].x);
-          acc[t].y = off ? acc[t].y : fmaf(wt, a.y, acc[t].y);
-          acc[t].z = off ? acc[t].z : fmaf(wt, a.z, acc[t].z);
-          acc[t].w = off ? acc[t].w : fmaf(wt, a.w, acc[t].w);
+          const float2 ml = s_ml[q * rows + row[t]];
+          const float4 a = *reinterpret_cast<const float4 *>(src + row[t] * D + d);
+          // (of a row that saw nothing, or NaN alone: its maximum is -inf, its sum 0 or NaN)
+          const float m = fmaxf(M[t], ml.x);
+          const float keep = M[t] == -INFINITY ? 1.f : exp2_fast(M[t] - m);
+          const float add = ml.x == -INFINITY ? 1.f : exp2_fast(ml.x - m);
+          if (ml.y == 0.f) continue;
+          M[t] = m;
+          l[t] = fmaf(l[t], keep, ml.y * add);
+          acc[t].x = fmaf(acc[t].x, keep, a.x * add);
+          acc[t].y = fmaf(acc[t].y, keep, a.y * add);
+          acc[t].z = fmaf(acc[t].z, keep, a.z * add);
+          acc[t].w = fmaf(acc[t].w, keep, a.w * add);
         }
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int v = v0 + t * WARPS * 32, row = v / (D / 4), d = 4 * (v % (D / 4)), r = u.row + row % GC;  // row: [head][row]
-        if (v >= rows * (D / 4)) break;
-        const float2 ml = s_ml[g * rows + row];
-        const float f = ml.y == 0.f ? 0.f : __fdividef(kp.v_unit, ml.y);
+        if (v0 + t * WARPS * 32 >= hg * live * (D / 4)) break;
+        const float f = l[t] == 0.f ? 0.f : __fdividef(kp.v_unit, l[t]);
         const float4 y = make_float4(acc[t].x * f, acc[t].y * f, acc[t].z * f, acc[t].w * f);
         if (opens && closes) {
-          if (r < p.R) store4<typename Cfg::Q>(p.out, row_at(p, b, u.head + row / GC, r) + d, y);
+          store4<typename Cfg::Q>(p.out, row_at(p, b, u.head + row[t] / GC, u.row + row[t] % GC) + d, y);
         } else {
-          const int slot = (blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row;
+          const int slot = (blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row[t];
           *reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + d) = y;
           // (a sum of NaN as +inf: the merge then gives NaN)
-          if (d == 0) p.part_lse[slot] = ml.y != ml.y ? INFINITY : ml.y == 0.f ? -INFINITY : ml.x + __log2f(ml.y);
+          if (d == 0) p.part_lse[slot] = l[t] != l[t] ? INFINITY : l[t] == 0.f ? -INFINITY : M[t] + __log2f(l[t]);
         }
       }
     }
@@ -942,6 +983,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
   __shared__ float4 s_acc[kMergeThreads];
   __shared__ float2 s_ml[kMergeThreads];
   const int lane = threadIdx.x & 31;
+  grid_dep_launch();
   grid_dep_wait();
   int c = blockIdx.x, unit = -1;
   if (kp.merge_units) {  // fewer units than ranges: a CTA per unit looks for the range that begins it
@@ -978,7 +1020,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, den = 0.f;
 #pragma unroll 1
-  for (int s = c + team; s <= last; s += kBatch * teams) {
+  for (int s = c + team; s <= last && r < p.R; s += kBatch * teams) {
     float4 o[kBatch];
     float l[kBatch];
 #pragma unroll

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kThreads)
     kv4_append_kernel(const void *__restrict__ k_new, int64_t ld_k, const void *__restrict__ v_new, int64_t ld_v,
                       uint8_t *cache, const int64_t *__restrict__ slots, int T_, int Hkv, int64_t num_blocks,
                       float k_unit, float v_unit) {
+  grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
   grid_dep_wait();
   constexpr int G = D / 16;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -87,6 +88,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_pack_kernel(uint8_t *cache, int64_t num_blocks, const void *__restrict__ k, const void *__restrict__ vv,
                     int64_t num_src, const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
+  grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
   grid_dep_wait();
   const PageThread p = page_thread<D>(Hkv);
   if (p.pair >= n) return;
@@ -109,6 +111,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_expand_kernel(void *k, void *vv, int64_t num_dst, const uint8_t *__restrict__ cache, int64_t num_blocks,
                       const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
+  grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
   grid_dep_wait();
   const PageThread p = page_thread<D>(Hkv);
   if (p.pair >= n) return;
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads)
     kv4_copy_kernel(uint8_t *cache, const int32_t *__restrict__ pairs, size_t block_bytes, int64_t num_blocks) {
+  grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
   grid_dep_wait();
   const int src = pairs[2 * blockIdx.x], dst = pairs[2 * blockIdx.x + 1];
   if (src < 0 || dst < 0 || src >= num_blocks || dst >= num_blocks || src == dst) return;

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   constexpr int VEC = RopeVec<T>::VEC;
   __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
   extern __shared__ __align__(16) uint8_t s_rows[];  // (kCache4) this part's K and V rows
+  grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
   grid_dep_wait();
   const int64_t t = blockIdx.x / parts;
   const int h0 = (int)(blockIdx.x - t * parts) * per_part;

@@ -74,7 +74,8 @@ class Case:
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (8, 1), (6, 2), (14, 2), (32, 2), (21, 1)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (8, 1), (6, 2), (14, 2), (32, 2), (21, 1), (12, 4),
+                                    (9, 3), (24, 12)])
 def test_single_token(pkv, D, dtype, Hq, Hkv):
     c = Case(pkv, [1, 15, 16, 17, 0, 63, 64, 65, 300, 1111], 1, Hq, Hkv, D, dtype, seed=Hq + D)
     c.check()
@@ -100,15 +101,32 @@ def test_split_counts(pkv, splits):
     c.check(num_splits=splits)
 
 
-def test_long_context(pkv):
+@pytest.mark.parametrize("Hq,Hkv,q_len,D", [(8, 1, 1, 128), (16, 4, 1, 128), (4, 2, 2, 64), (32, 8, 3, 128), (8, 8, 1, 64)])
+def test_long_contexts(pkv, Hq, Hkv, q_len, D):
+    """Units cut between many CTAs, of one, two and four heads."""
+    c = Case(pkv, [12000, 3, 4001], q_len, Hq, Hkv, D, BF16, seed=4, keys=2.0)
+    c.check()
+
+
+def test_one_long_context(pkv):
     c = Case(pkv, [40000], 1, 8, 1, 128, BF16, seed=4, keys=2.0)
     c.check()
 
 
-def test_many_sequences(pkv):
-    """More sequences than the kernel plans by itself."""
+@pytest.mark.parametrize("B", [33, 100, 128, 129, 300, 510, 511, 512, 2500])
+def test_many_sequences(pkv, B):
+    """Planned in registers, in shared memory and (511 and more) by a kernel of its own; many are empty."""
     g = torch.Generator().manual_seed(5)
-    c = Case(pkv, torch.randint(0, 70, (2500,), generator=g).tolist(), 1, 4, 2, 64, F16, seed=5)
+    lens = (torch.randint(0, 90, (B,), generator=g) - 20).clamp(min=0).tolist()
+    c = Case(pkv, lens, 1, 4, 2, 64, F16, seed=5)
+    c.check()
+    assert c.status == (0, 0)
+
+
+@pytest.mark.parametrize("lens", [[768] * 9, [769] * 9, [16] * 700, [190, 200] * 40])
+def test_units_whole_or_cut(pkv, lens):
+    """Tables at the border up to which units are not cut between CTAs, and more units than CTAs."""
+    c = Case(pkv, lens, 1, 8, 4, 128, BF16, seed=15)
     c.check()
 
 
