@@ -52,14 +52,31 @@ __device__ __forceinline__ float e4m3_value(uint8_t s) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)));
 }
 
-// The codes of scaled elements, two a byte.
-__device__ __forceinline__ uint2 e2m1_codes(const float (&q)[16]) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i / 4] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_E2M1, cudaRoundNearest)
-                << (8 * (i % 4));
-  return make_uint2(w[0], w[1]);
+// The codes of eight scaled elements, two a byte, the first of a pair in the lower half.
+__device__ __forceinline__ uint32_t e2m1x8(const float *q) {
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+__device__ __forceinline__ uint2 e2m1_codes(const float (&q)[16]) { return make_uint2(e2m1x8(q), e2m1x8(q + 8)); }
+// Packed |a| and the larger of each half, NaN if either is.
+__device__ __forceinline__ uint32_t max_abs2(F16, uint32_t a, uint32_t b) {
+  const uint32_t x = b & 0x7fff7fffu;
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&x));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t max_abs2(BF16, uint32_t a, uint32_t b) {
+  const uint32_t x = b & 0x7fff7fffu;
+  const __nv_bfloat162 r =
+      __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&x));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint8_t e4m3_scale(float most) {
   return __nv_cvt_float_to_fp8(__fdiv_rn(most, 6.f), __NV_SATFINITE, __NV_E4M3);
@@ -86,7 +103,7 @@ __device__ __forceinline__ Kv4Group kv4_quantise(float (&y)[16], float unit) {
   return r;
 }
 
-// The same of 16-bit elements with unit = 1, without divisions (packing 4096 pages: 186 -> 115 us).  An element y has
+// The same of 16-bit elements with unit = 1, without divisions (4096 pages packed and expanded: 186 us with them, 134 without).  An element y has
 // at most 11 significant bits and a border m s between two codes at most 7, so that y / s either is m or
 // is off by 2^-11 m or more, and m >= 1/4: y / s rounded to a multiple of 2^-14 falls on the same side of every border, or
 // on it.  fmaf(y, r, 768) does that rounding (768's unit in the last place is 2^-14; r = 1 / s to 2^-23, |y r| <= 6.4;
@@ -95,8 +112,8 @@ template <class T>
 __device__ __forceinline__ Kv4Group kv4_quantise16(const uint32_t (&w)[8]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-  top = max(top & 0xffffu, top >> 16);  // the largest magnitude's bits
+  for (int i = 0; i < 8; ++i) top = max_abs2(T{}, top, w[i]);
+  top = max(top & 0x7fffu, (top >> 16) & 0x7fffu);  // the largest magnitude's bits (NaN above all)
   Kv4Group r;
   r.codes = make_uint2(0, 0);
   r.scale = 0x7f;

@@ -12,7 +12,11 @@
 
 namespace pkv {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Resident CTAs of the kernels that convert: whole occupancy (32 registers) is worth a few spilled registers (4096
+// pages packed and expanded: 132 us without the bound, 119 with; 16384 tokens appended: 31 and 27), but for fp32 rows.
+template <class T>
+constexpr int kResident = T::kBytes == 4 ? 8 : 16;
 
 static cudaLaunchConfig_t config(int64_t threads, cudaLaunchAttribute *attr, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -28,7 +32,7 @@ static cudaLaunchConfig_t config(int64_t threads, cudaLaunchAttribute *attr, cud
 
 // Thread -> (token, K or V, head, group), the group fastest.
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident<T>)
     kv4_append_kernel(const void *__restrict__ k_new, int64_t ld_k, const void *__restrict__ v_new, int64_t ld_v,
                       uint8_t *cache, const int64_t *__restrict__ slots, int T_, int Hkv, int64_t num_blocks,
                       float k_unit, float v_unit) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ PageThread page_thread(int Hkv) {
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident<T>)
     kv4_pack_kernel(uint8_t *cache, int64_t num_blocks, const void *__restrict__ k, const void *__restrict__ vv,
                     int64_t num_src, const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
   grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident<T>)
     kv4_expand_kernel(void *k, void *vv, int64_t num_dst, const uint8_t *__restrict__ cache, int64_t num_blocks,
                       const int32_t *__restrict__ pairs, int n, int Hkv, float k_unit, float v_unit) {
   grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one

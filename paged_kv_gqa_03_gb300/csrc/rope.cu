@@ -16,7 +16,9 @@
 // Split.  A CTA takes one token, or some heads of it; a thread turns 16 bytes of
 // each half of a pair's run (interleaved: 32 bytes), U of them, and has them in flight
 // before it waits for the sines.  Bound by HBM for prompts (each row read and
-// written once), by latency for a decode step, whose heads are spread over more CTAs.
+// written once: 16384 tokens, 64 + 8 + 8 heads of 128 in bf16, 671 MB in 107 us, 6.3 TB/s of the 6.8 that a
+// copy reaches; 122 us with 256 threads of three items, 118 without the bound on registers), by
+// latency for a decode step, whose heads are spread over more CTAs (64 tokens: 4 us).
 // (4-bit caches: the rows, rounded to their type as a cache of that type would hold
 // them, pass through shared memory to groups of 16.)
 #include "kv4.cuh"
@@ -84,7 +86,7 @@ __device__ __forceinline__ Chunks chunks(const RopeParams &p, int c, bool value)
 }
 
 template <class T, int DEST, int U>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int parts, int per_part) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, int parts, int per_part) {
   using Type = T;
   constexpr int VEC = RopeVec<T>::VEC;
   __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
@@ -209,7 +211,7 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
   const int heads = p.Hq + (DEST == kRows ? 1 : 2) * p.Hkv;
   const int items_row = p.D / (2 * VEC);
   // few tokens: one item a thread, so that a step's rows are spread over as many CTAs as it
-  // has; many: a token's rows in one CTA where three (fp32: five) items a thread hold them
+  // has; many: a token's rows in one CTA where five items a thread hold them
   const bool wide = p.T > 256;
   constexpr int kWide = 5;  // (kCache4: at most 40 KiB of rows)
   const int cap = kThreads * (wide ? kWide : 1) / items_row;  // heads a CTA holds
