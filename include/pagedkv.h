@@ -590,11 +590,11 @@ int paged_kv_copy_blocks(void *k_cache, void *v_cache, int cache_dtype,
  *   s = e4m3(max|y| / 6), saturating at 448;   code = e2m1(y / s), saturating at +-6;
  *   value = code * s * unit
  * both rounded to nearest even, divisions in fp32; E2M1 has the values 0, 0.5, 1, 1.5, 2,
- * 3, 4, 6 and their negatives.  k_unit and v_unit are positive finite numbers that belong
+ * 3, 4, 6 and their negatives.  k_unit and v_unit are numbers within 2^-64 .. 2^64 that belong
  * to the cache (one for all its keys, one for all its values): 1 serves elements whose
  * groups reach 0.1 to 2688; smaller or larger ones want a unit near their typical
- * magnitude (a group whose largest y is below 6 * 2^-10 becomes 0).  A group with an
- * element that is not finite reads as NaN, all 16 of it.  A token's rows do not depend on
+ * magnitude (a group whose largest y is below 6 * 2^-10 becomes 0).  A group with a y
+ * that is not finite reads as NaN, all 16 of it.  A token's rows do not depend on
  * other tokens: there is no order of appends, and nothing is ever re-quantised.
  *
  *   cache   uint8 [num_blocks][Hkv][18 D], 16-byte aligned: K and V of 16 tokens of a
@@ -639,7 +639,8 @@ int paged_kv4_copy_blocks(void *cache, const int32_t *src_dst_pairs, int n_pairs
  *   q, out     [B][q_len][Hq][D], F16 or BF16 (PKV_EUNSUPPORTED for F32), 16-byte aligned
  *   workspace  paged_kv4_decode_workspace_bytes(...) bytes, 256-byte aligned (status:
  *              paged_decode_status)
- * Block tables, lengths, window, scale, num_splits, clamping, flags and errors as there.
+ * Block tables, lengths, window, scale, clamping, flags and errors as there.  num_splits:
+ * contiguous ranges of the blocks, one per CTA (0: one per SM; more than 224 count as 224).
  * A row that sees nothing gives 0.  What a row does not see may hold anything: positions
  * at or past context_lens[b], newer tokens of the step, positions before the window.  A
  * position that reads as NaN gives NaN in the rows that see it (of V: in the group's 16
@@ -674,11 +675,12 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
  *   q, k, v      T rows [Hq or Hkv][D] of dtype F32, F16 or BF16, ld_* elements from a token
  *                to the next, rows 16-byte aligned; D 64 or 128
  *   rot_dim      a multiple of 16, at most D
- *   q_out, k_out may be q, k themselves (same ld), else apart from all that the call reads
+ *   q_out, k_out may be q, k themselves (same ld), else apart from all that the call reads; they
+ *                and the inputs may be columns of one buffer (same ld)
  *
  * paged_rope rotates rows only (Hq or Hkv may be 0).  paged_rope_append writes the
  * rotated keys and the values to their slots of a cache of the same dtype (slots as for
- * paged_kv_append; q_out is written for skipped tokens too), paged_kv4_rope_append those of a
+ * paged_kv_append, distinct; q_out is written for skipped tokens too), paged_kv4_rope_append those of a
  * 4-bit cache: bit for bit what paged_rope and then paged_kv_append / paged_kv4_append give.  FP8 caches:
  * paged_rope, then the append of the cache's scale rule.
  */

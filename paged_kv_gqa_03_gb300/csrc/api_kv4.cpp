@@ -27,14 +27,19 @@ bool aligned(const void *p, int64_t ld, int esize) {  // 16-byte aligned rows
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * esize) % 16 == 0;
 }
 
-// [p, p + rows of n elements, ld apart) and another such range share a byte.
+// Rows of n_a elements, ld_a apart, and rows of n_b share a byte (rows of one buffer's columns, alike in ld, lie
+// between one another and need not).
 bool overlap(const void *a, int64_t ld_a, int64_t n_a, const void *b, int64_t ld_b, int64_t n_b, int64_t rows,
              int esize) {
   if (!a || !b || rows <= 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t ex = x + (uintptr_t)((rows - 1) * ld_a + n_a) * esize;
-  const uintptr_t ey = y + (uintptr_t)((rows - 1) * ld_b + n_b) * esize;
-  return x < ey && y < ex;
+  if (x >= y + (uintptr_t)((rows - 1) * ld_b + n_b) * esize || y >= x + (uintptr_t)((rows - 1) * ld_a + n_a) * esize)
+    return false;
+  if (ld_a != ld_b || rows == 1) return true;
+  // b's row j begins d + (j - i) L bytes behind a's row i, which is r or r - L where they can touch
+  const int64_t L = ld_a * esize, d = (int64_t)(y - x), r = (d % L + L) % L, k = (r - d) / L;
+  auto there = [&](int64_t steps) { return steps > -rows && steps < rows; };
+  return (there(k) && r < n_a * esize) || (there(k - 1) && r - L > -n_b * esize);
 }
 
 // What the calls on 4-bit pages check alike.
@@ -46,7 +51,7 @@ int check_pages(int dtype, int Hkv, int D, int64_t num_blocks, float k_unit, flo
   return PKV_OK;
 }
 
-constexpr double kGrid = 2147483000.0 * 256;  // threads of a grid
+constexpr double kGrid = 2147483000.0 * kKv4PageThreads;  // threads of a grid
 
 int check_rope(const RopeParams &p, int dtype) {
   if (p.T < 0 || p.Hq < 0 || p.Hkv < 0 || p.Hq + p.Hkv == 0 || p.rot <= 0) return PKV_EINVAL;
@@ -154,19 +159,16 @@ int paged_rope(void *q_out, int64_t ld_q_out, const void *q, int64_t ld_q, void 
   if (!rows_ok(q, ld_q, Hq, D, es) || !rows_ok(q_out, ld_q_out, Hq, D, es) || !rows_ok(k, ld_k, Hkv, D, es) ||
       !rows_ok(k_out, ld_k_out, Hkv, D, es))
     return PKV_EINVAL;
-  // in place, or apart from everything the call reads
+  // in place, or apart from everything the call reads and writes
   const int64_t nq = (int64_t)Hq * D, nk = (int64_t)Hkv * D;
   if (Hq > 0) {
-    if (q_out == q && ld_q_out != ld_q) return PKV_EINVAL;
-    if (q_out != q && (overlap(q_out, ld_q_out, nq, q, ld_q, nq, T, es) ||
-                       (Hkv > 0 && overlap(q_out, ld_q_out, nq, k, ld_k, nk, T, es))))
-      return PKV_EINVAL;
+    if (q_out == q ? ld_q_out != ld_q : overlap(q_out, ld_q_out, nq, q, ld_q, nq, T, es)) return PKV_EINVAL;
+    if (Hkv > 0 && overlap(q_out, ld_q_out, nq, k, ld_k, nk, T, es)) return PKV_EINVAL;
   }
   if (Hkv > 0) {
-    if (k_out == k && ld_k_out != ld_k) return PKV_EINVAL;
-    if (k_out != k && (overlap(k_out, ld_k_out, nk, k, ld_k, nk, T, es) ||
-                       (Hq > 0 && (overlap(k_out, ld_k_out, nk, q, ld_q, nq, T, es) ||
-                                   overlap(k_out, ld_k_out, nk, q_out, ld_q_out, nq, T, es)))))
+    if (k_out == k ? ld_k_out != ld_k : overlap(k_out, ld_k_out, nk, k, ld_k, nk, T, es)) return PKV_EINVAL;
+    if (Hq > 0 && (overlap(k_out, ld_k_out, nk, q, ld_q, nq, T, es) ||
+                   overlap(k_out, ld_k_out, nk, q_out, ld_q_out, nq, T, es)))
       return PKV_EINVAL;
   }
   return status_of(launch_rope(p, dtype, reinterpret_cast<cudaStream_t>(stream)));
@@ -184,11 +186,10 @@ static int rope_append(RopeParams &p, int dtype, cudaStream_t stream) {
       !rows_ok(p.k, p.ld_k, p.Hkv, p.D, es) || !rows_ok(p.v, p.ld_v, p.Hkv, p.D, es))
     return PKV_EINVAL;
   const int64_t nq = (int64_t)p.Hq * p.D, nk = (int64_t)p.Hkv * p.D;
-  if (p.q_out == p.q && p.ld_q_out != p.ld_q) return PKV_EINVAL;
-  if (p.q_out != p.q &&
-      (overlap(p.q_out, p.ld_q_out, nq, p.q, p.ld_q, nq, p.T, es) ||
-       overlap(p.q_out, p.ld_q_out, nq, p.k, p.ld_k, nk, p.T, es) ||
-       overlap(p.q_out, p.ld_q_out, nq, p.v, p.ld_v, nk, p.T, es)))
+  if (p.q_out == p.q ? p.ld_q_out != p.ld_q : overlap(p.q_out, p.ld_q_out, nq, p.q, p.ld_q, nq, p.T, es))
+    return PKV_EINVAL;
+  if (overlap(p.q_out, p.ld_q_out, nq, p.k, p.ld_k, nk, p.T, es) ||
+      overlap(p.q_out, p.ld_q_out, nq, p.v, p.ld_v, nk, p.T, es))
     return PKV_EINVAL;
   return status_of(launch_rope(p, dtype, stream));
 }

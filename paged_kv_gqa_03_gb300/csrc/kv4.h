@@ -6,10 +6,13 @@
 
 namespace pkv {
 
-// A tensor's unit: positive and finite.
-inline bool kv4_unit_ok(float u) { return u > 0.f && u <= 3.402823466e38f; }
+// A tensor's unit.  (Within 2^+-64 what is multiplied and divided by it stays within fp32's normal numbers: a
+// unit over a softmax's sum of up to 2^46, code * scale * unit.)
+inline bool kv4_unit_ok(float u) { return u >= 0x1p-64f && u <= 0x1p64f; }
 
 constexpr int kKv4 = 4;  // DecodeKernel::cache_dtype of the 4-bit variants (no public dtype code)
+
+constexpr int kKv4PageThreads = 128;  // a CTA of kv4_pages.cu
 
 constexpr int kKv4MaxRanges = 224;  // WsHeader::cta_status
 

@@ -12,7 +12,7 @@
 
 namespace pkv {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = kKv4PageThreads;
 // Resident CTAs of the kernels that convert: whole occupancy (32 registers) is worth a few spilled registers (4096
 // pages packed and expanded: 132 us without the bound, 119 with; 16384 tokens appended: 31 and 27), but for fp32 rows.
 template <class T>
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, kResident<T>)
   kv4_values_to<T>(b, unit, rows, at + D);
 }
 
+// A CTA a pair, four loads in flight a thread (one after another: a pair of 8 heads 1.6 -> 2.6 us, 256 pairs 3.1 -> 3.6).
 __global__ void __launch_bounds__(kThreads)
     kv4_copy_kernel(uint8_t *cache, const int32_t *__restrict__ pairs, size_t block_bytes, int64_t num_blocks) {
   grid_dep_launch();  // the next kernel of the chain may come up; it waits for this one
@@ -144,7 +145,16 @@ __global__ void __launch_bounds__(kThreads)
   if (src < 0 || dst < 0 || src >= num_blocks || dst >= num_blocks || src == dst) return;
   const uint4 *s = reinterpret_cast<const uint4 *>(cache + (size_t)src * block_bytes);
   uint4 *d = reinterpret_cast<uint4 *>(cache + (size_t)dst * block_bytes);
-  for (size_t i = threadIdx.x; i < block_bytes / 16; i += kThreads) d[i] = s[i];
+  const size_t n = block_bytes / 16;
+  for (size_t i = threadIdx.x; i < n; i += 4 * kThreads) {
+    uint4 x[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (i + t * kThreads < n) x[t] = s[i + t * kThreads];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (i + t * kThreads < n) d[i + t * kThreads] = x[t];
+  }
 }
 
 // f(T{}, integral_constant<int, D>) of a (dtype, head dim).

@@ -18,7 +18,7 @@
 // before it waits for the sines.  Bound by HBM for prompts (each row read and
 // written once: 16384 tokens, 64 + 8 + 8 heads of 128 in bf16, 671 MB in 107 us, 6.3 TB/s of the 6.8 that a
 // copy reaches; 122 us with 256 threads of three items, 118 without the bound on registers), by
-// latency for a decode step, whose heads are spread over more CTAs (64 tokens: 4 us).
+// latency for a decode step, whose heads are spread over more CTAs (64 tokens: 7 us).
 // (4-bit caches: the rows, rounded to their type as a cache of that type would hold
 // them, pass through shared memory to groups of 16.)
 #include "kv4.cuh"
@@ -213,7 +213,7 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
   // few tokens: one item a thread, so that a step's rows are spread over as many CTAs as it
   // has; many: a token's rows in one CTA where five items a thread hold them
   const bool wide = p.T > 256;
-  constexpr int kWide = 5;  // (kCache4: at most 40 KiB of rows)
+  constexpr int kWide = 5;  // (kCache4: at most 20 KiB of rows)
   const int cap = kThreads * (wide ? kWide : 1) / items_row;  // heads a CTA holds
   const int parts = (heads + cap - 1) / cap, per = (heads + parts - 1) / parts;
   if ((double)p.T * parts > 2147483000.0) return cudaErrorNotSupported;

@@ -130,7 +130,7 @@ def test_units_whole_or_cut(pkv, lens):
     c.check()
 
 
-@pytest.mark.parametrize("unit", [(1e-6, 3e-5), (1e6, 2e3), (0.37, 5.0)])
+@pytest.mark.parametrize("unit", [(1e-6, 3e-5), (1e6, 2e3), (0.37, 5.0), (2.0 ** -64, 2.0 ** 64), (2.0 ** 64, 2.0 ** -64)])
 def test_units(pkv, unit):
     """Keys and values far from 1, held by their units."""
     c = Case(pkv, [100, 31, 500], 2, 8, 2, 128, BF16, seed=6, unit=unit)

@@ -157,6 +157,23 @@ def test_blocks_beyond_32_bit_offsets(pkv):
         same(got[0], want[1])
 
 
+def test_neighbours_appended_at_once(pkv):
+    """Even tokens on one stream, their odd neighbours, whose values share bytes, on another."""
+    n, Hkv, D = 4096, 4, 128
+    k, v = rows((n, Hkv, D), BF16, 12), rows((n, Hkv, D), BF16, 13)
+    slots = torch.arange(n, device="cuda")
+    want = torch.zeros(n // 16, Hkv, 18 * D, dtype=torch.uint8, device="cuda")
+    pkv.paged_kv4_append(k, v, want, slots)
+    parts = [(k[i::2].contiguous(), v[i::2].contiguous(), slots[i::2].contiguous()) for i in range(2)]
+    got, streams = torch.zeros_like(want), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (a, b, s), stream in zip(parts, streams):
+            pkv.paged_kv4_append(a, b, got, s, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_nothing_to_do(pkv):
     cache = torch.full((1, 1, 18 * 64), 3, dtype=torch.uint8, device="cuda")
     e = torch.empty(0, 1, 64, dtype=F16, device="cuda")

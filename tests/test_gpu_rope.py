@@ -140,6 +140,23 @@ def test_stream_and_graph(pkv):
         assert torch.equal(out, want) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
 
 
+def test_columns_of_one_buffer(pkv):
+    """Outputs side by side in one buffer, and both turned in place in the projection that holds them."""
+    T, Hq, Hkv, D = 70, 6, 2, 64
+    qkv, q, k, v = projection(T, Hq, Hkv, D, F16, 4)
+    pos, table = torch.arange(T, device="cuda") * 1000, pkv.RopeTable(D, interleaved=True)
+    apart = [torch.empty(T, h, D, dtype=F16, device="cuda") for h in (Hq, Hkv)]
+    pkv.paged_rope(q, k, pos, table, q_out=apart[0], k_out=apart[1])
+    both = torch.zeros(T, Hq + Hkv, D, dtype=F16, device="cuda")
+    pkv.paged_rope(q, k, pos, table, q_out=both[:, Hkv:], k_out=both[:, :Hkv])
+    assert torch.equal(both[:, Hkv:], apart[0]) and torch.equal(both[:, :Hkv], apart[1])
+    values = v.clone()
+    pkv.paged_rope(q, k, pos, table)
+    assert torch.equal(q, apart[0]) and torch.equal(k, apart[1]) and torch.equal(v, values)
+    with pytest.raises(pkv.PagedKVError):
+        pkv.paged_rope(q, qkv[:, 1:1 + Hkv], pos, table)
+
+
 def test_no_tokens(pkv):
     e = torch.empty(0, 2, 64, dtype=F16, device="cuda")
     i = torch.empty(0, dtype=torch.int64, device="cuda")

@@ -129,6 +129,24 @@ def test_rope_refusals(pkv, which):
         assert rope(L, which, c2=None) == bad
 
 
+@pytest.mark.parametrize("which", ["rope", "append", "kv4"])
+def test_rope_in_place_over_other_inputs(pkv, which):
+    """Queries that are turned in place must not be the keys (or the values), not even in part."""
+    for kw in (dict(qo=P, ldqo=512, k=P, ldk=512), dict(qo=P, ldqo=512, k=P + 1008, ldk=512),
+               dict(qo=P, ldqo=512, k=P - 512 + 16, ldk=512), dict(qo=P, ldqo=512, k=P + 16 * 1024, ldk=256, T=40)):
+        assert rope(L := pkv.lib(), which, **kw) == pkv.PKV_EINVAL, kw
+    if which == "rope":
+        assert rope(L, which, ko=2 * P, q=2 * P + 512, ldq=512, ldk=512, ldko=512) == pkv.PKV_EINVAL
+    else:
+        assert rope(L, which, qo=P, ldqo=512, v=P + 16, ldv=512) == pkv.PKV_EINVAL
+
+
+def test_units_range(pkv):
+    L = pkv.lib()
+    for unit, rc in ((2.0 ** -64, pkv.PKV_OK), (2.0 ** 64, pkv.PKV_OK), (2.0 ** -65, pkv.PKV_EINVAL), (2.0 ** 65, pkv.PKV_EINVAL)):
+        assert append(L, ku=unit, T=0) == rc and append(L, vu=unit, T=0) == rc
+
+
 def test_turns(pkv):
     """The fraction of a turn a position, in 2^-64, to the frequency's own 53 bits."""
     f = np.array([1.0, 0.5, 2 * math.pi, 3e-9, 0.0, 100.0, 2 * math.pi * 0.999999])
