@@ -1205,11 +1205,14 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   p.d.n_ctas = P;
   p.d.inline_plan = B + 1 <= kKv4Prefix ? 1 : 0;
   p.cache = static_cast<const uint8_t *>(cache);
+  // the most blocks that a unit reads
+  const int64_t most = window > 0 ? std::min((int64_t)max_blocks_per_seq, ((int64_t)window + q_len + 14) / kBlock + 1)
+                                  : max_blocks_per_seq;
   // Heads a unit takes together.  Short tables' units are not cut between CTAs: two heads where that spreads few units
   // over more rings (us a call, 4 / 2 heads: 1 x 333 12.3 / 11.0, 1 x 700 17.0 / 13.3, 1 x 333 with 4 new tokens
   // 16.8 / 13.1; but for a few blocks, 1 x 100 9.6 / 11.5).
   p.hg = kv4_heads(Hkv);
-  if (p.hg == 4 && max_blocks_per_seq > 12 && max_blocks_per_seq <= kKv4Whole && (int64_t)B * (Hkv / 4) * c.NC < P) p.hg = 2;
+  if (p.hg == 4 && most > 12 && most <= kv4_whole(D) && (int64_t)B * (Hkv / 4) * c.NC < P) p.hg = 2;
   p.hg_log2 = p.hg / 2;  // (of 1, 2 and 4)
   p.d.HU = Hkv / p.hg * c.NC;
   p.records = reinterpret_cast<int4 *>(ws + L.records);
@@ -1218,8 +1221,8 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   void *args[1] = {&p};
   cudaError_t e = launch_units(k, p.d, args, st);
-  // a table of no more blocks: no unit is cut between CTAs
-  if (e == cudaSuccess && max_blocks_per_seq > kKv4Whole && P > 1) e = launch_kv4_merge(p, st, st != nullptr);
+  // units of no more blocks: none is cut between CTAs
+  if (e == cudaSuccess && most > kv4_whole(D) && P > 1) e = launch_kv4_merge(p, st, st != nullptr);
   return cuda_status(e);
 }
 

@@ -20,7 +20,9 @@ constexpr int kKv4MaxRanges = 224;  // WsHeader::cta_status
 constexpr int kKv4Prefix = 512;
 
 // Units of at most this many blocks are not cut between CTAs (kv4_decode.cu).
-constexpr int kKv4Whole = 48;
+template <int D>
+constexpr int kKv4Whole = D == 64 ? 96 : 48;
+inline int kv4_whole(int D) { return D == 64 ? kKv4Whole<64> : kKv4Whole<128>; }
 
 struct Kv4Params {
   DecodeParams d;  // P: ranges, one per CTA; scale_log2 holds K's unit; k_scale, v_scale, cta_flags unused

@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
       if (x < W) {
         const Kv4Item it = locate_item(p, plan, x);
         int back = it.off % Cfg::NB;
-        if (t < 2 && it.n <= kKv4Whole) back = 2 * it.off < it.n ? it.off : it.off - it.n;
+        if (t < 2 && it.n <= kKv4Whole<D>) back = 2 * it.off < it.n ? it.off : it.off - it.n;
         if (t == 2 && (wib == 0 || wib == rings || n < 2 * Cfg::NB * rings)) back = 0;
         x -= back;
         if (t == 2) {
