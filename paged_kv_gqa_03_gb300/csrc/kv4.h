@@ -19,7 +19,8 @@ constexpr int kKv4MaxRanges = 224;  // WsHeader::cta_status
 // Batches of fewer sequences are planned inside the decode kernel.
 constexpr int kKv4Prefix = 512;
 
-// Units of at most this many blocks are not cut between CTAs (kv4_decode.cu).
+// Units of at most this many blocks (alike in bytes) are not cut between CTAs (kv4_decode.cu): 128 x 385-1409 in a step
+// 57.5 us, 59.9 with 64; D = 64, 32 x 512-4096 with a window of 1024 (65 blocks) 33.3 us, 36.2 with 48.
 template <int D>
 constexpr int kKv4Whole = D == 64 ? 96 : 48;
 inline int kv4_whole(int D) { return D == 64 ? kKv4Whole<64> : kKv4Whole<128>; }
