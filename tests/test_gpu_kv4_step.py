@@ -43,7 +43,9 @@ class Mirror:
         rq = self.rotated(q, len(k) - n).to(q.dtype)
         want = ref.attention(rq, k, v, scale, window)
         tol = ref.tolerance(want, rq, k, v, scale, out.dtype)
-        # a rotated element may round the other way: one rounding of q, and of a key (in the cache's steps: its group)
+        # A rotated element may round the other way: a step of 2^-8 (bf16) of one element of q or of a key moves a score by
+        # less than 2^-8 of one of its D terms; where a key's element stands on a border between two codes the term moves by a
+        # third of itself.  A weight then is off by the few such elements' share of its score: 2^-7 of the largest value.
         turn = 0.0 if self.table is None else 0.5
         err = (out.cpu().double() - want).abs()
         assert (err <= tol + turn * float(v.abs().max()) * 2.0 ** -6).all(), (seq, float((err - tol).max()))
