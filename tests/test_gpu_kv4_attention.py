@@ -130,6 +130,22 @@ def test_units_whole_or_cut(pkv, lens):
     c.check()
 
 
+@pytest.mark.parametrize("D,whole", [(64, 96), (128, 48)])
+@pytest.mark.parametrize("q_len", [1, 3])
+@pytest.mark.parametrize("over", [0, 1])
+def test_windows_whole_or_cut(pkv, D, whole, q_len, over):
+    """Windows that reach into `whole` blocks at most, and one position more, at every offset within a block."""
+    lens = [4096 + i for i in range(17)] + [whole * 16, 20, 0]
+    c = Case(pkv, lens, q_len, 4, 4, D, BF16, seed=16)
+    c.check(window=16 * whole - 15 - q_len + over)
+
+
+@pytest.mark.parametrize("lens", [[1536] * 9, [1537] * 9, [700, 1500] * 10])
+def test_units_whole_or_cut_64(pkv, lens):
+    c = Case(pkv, lens, 1, 8, 4, 64, F16, seed=17)
+    c.check()
+
+
 @pytest.mark.parametrize("unit", [(1e-6, 3e-5), (1e6, 2e3), (0.37, 5.0), (2.0 ** -64, 2.0 ** 64), (2.0 ** 64, 2.0 ** -64)])
 def test_units(pkv, unit):
     """Keys and values far from 1, held by their units."""
