@@ -636,18 +636,19 @@ def _issue(fn, args, name, prepare, workspace=None):
     return workspace
 
 
-def _token_rows(t, name, T, heads, D, dtype, device):
+def _token_rows(t, name, shape, dtype, device):
     """(pointer, elements from a token to the next) of rows [T, heads, D] whose
     heads lie side by side; a token's row may be a part of a wider one."""
-    if t.dtype is dtype and t.shape == (T, heads, D) and t.get_device() == device:   # one test on the way through
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:   # one test on the way through
         ld, sh, sd = t.stride()
-        if sd == 1 and sh == D and T > 1:
+        T, heads, D = shape
+        if T > 1 and sh == D and sd == 1:
             return t.data_ptr(), ld
         if t.numel() == 0 or (sd == 1 and (sh == D or heads == 1)):
             return t.data_ptr(), (ld if T > 1 else heads * D)
         raise ValueError(f"{name}: the {heads} heads of a token must lie side by side, strides {t.stride()}")
-    if t.shape != (T, heads, D):
-        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
@@ -656,9 +657,11 @@ def _token_rows(t, name, T, heads, D, dtype, device):
 def _cache4(cache, device):
     """(pointer, num_blocks, Hkv, D) of a 4-bit cache, uint8 [num_blocks, Hkv, 18 D]."""
     shape = cache.shape
-    if len(shape) != 3 or shape[2] not in (18 * 64, 18 * 128):
-        raise ValueError(f"a 4-bit cache must be [num_blocks, Hkv, 18 * D], D 64 or 128, got {tuple(shape)}")
-    return _arg(cache, "cache", _torch().uint8, shape, device), shape[0], shape[1], shape[2] // 18
+    if len(shape) == 3:
+        num_blocks, Hkv, tile = shape
+        if tile == 18 * 128 or tile == 18 * 64:
+            return _arg(cache, "cache", _torch().uint8, shape, device), num_blocks, Hkv, tile // 18
+    raise ValueError(f"a 4-bit cache must be [num_blocks, Hkv, 18 * D], D 64 or 128, got {tuple(shape)}")
 
 
 def paged_kv4_append(k_new, v_new, cache, slot_mapping, k_unit=1.0, v_unit=1.0, stream=None, prepare=False):
@@ -668,8 +671,9 @@ def paged_kv4_append(k_new, v_new, cache, slot_mapping, k_unit=1.0, v_unit=1.0, 
     dev = _device_of(cache, "cache")
     ptr, num_blocks, Hkv, D = _cache4(cache, dev)
     T, dtype = k_new.shape[0], k_new.dtype
-    k, ld_k = _token_rows(k_new, "k_new", T, Hkv, D, dtype, dev)
-    v, ld_v = _token_rows(v_new, "v_new", T, Hkv, D, dtype, dev)
+    shape = (T, Hkv, D)
+    k, ld_k = _token_rows(k_new, "k_new", shape, dtype, dev)
+    v, ld_v = _token_rows(v_new, "v_new", shape, dtype, dev)
     args = (k, ld_k, v, ld_v, _code(k_new), ptr, _arg(slot_mapping, "slot_mapping", _torch().int64, (T,), dev),
             T, Hkv, D, num_blocks, float(k_unit), float(v_unit), _stream(stream, dev))
     return _issue(_L.paged_kv4_append, args, "paged_kv4_append", prepare)
@@ -678,11 +682,10 @@ def paged_kv4_append(k_new, v_new, cache, slot_mapping, k_unit=1.0, v_unit=1.0, 
 def _pages(cache, k_cache, v_cache, pairs):
     dev = _device_of(cache, "cache")
     ptr, num_blocks, Hkv, D = _cache4(cache, dev)
-    shape = (k_cache.shape[0], Hkv, 16, D)
-    k = _arg(k_cache, "k_cache", k_cache.dtype, shape, dev)
-    v = _arg(v_cache, "v_cache", k_cache.dtype, shape, dev)
-    n = pairs.shape[0]
-    return dev, ptr, num_blocks, k, v, shape[0], _arg(pairs, "src_dst_pairs", _torch().int32, (n, 2), dev), n, Hkv, D
+    others, n, dtype = k_cache.shape[0], pairs.shape[0], k_cache.dtype
+    shape = (others, Hkv, 16, D)
+    k, v = _arg(k_cache, "k_cache", dtype, shape, dev), _arg(v_cache, "v_cache", dtype, shape, dev)
+    return dev, ptr, num_blocks, k, v, others, _arg(pairs, "src_dst_pairs", _torch().int32, (n, 2), dev), n, Hkv, D
 
 
 def paged_kv4_pack_blocks(cache, k_cache, v_cache, src_dst_pairs, k_unit=1.0, v_unit=1.0, stream=None,
@@ -735,27 +738,29 @@ def paged_kv4_decode_attention(out, q, cache, block_table, context_lens, scale, 
     workspace: a uint8 CUDA tensor of paged_kv4_decode_workspace_bytes(...) bytes, allocated
     here (by torch) when None; returned for paged_decode_status.  prepare=True
     returns the call as a Prepared object, which holds the workspace."""
-    torch = _torch()
-    dev, shape = _device_of(q, "q"), q.shape
-    if len(shape) not in (3, 4):
+    dev, shape, dtype = _device_of(q, "q"), q.shape, q.dtype
+    if len(shape) == 3:
+        (B, Hq, D), q_len = shape, 1
+    elif len(shape) == 4:
+        B, q_len, Hq, D = shape
+    else:
         raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(shape)}")
-    if out.shape != shape or out.dtype is not q.dtype:
-        raise ValueError(f"out must be {tuple(shape)} of {q.dtype}, got {tuple(out.shape)} of {out.dtype}")
-    if out.is_cuda and out.get_device() != dev:
+    if out.shape != shape or out.dtype is not dtype:
+        raise ValueError(f"out must be {tuple(shape)} of {dtype}, got {tuple(out.shape)} of {out.dtype}")
+    out_dev = out.get_device()
+    if out_dev >= 0 and out_dev != dev:
         raise ValueError(f"out is on {out.device}, expected cuda:{dev}")
-    B, Hq, D = shape[0], shape[-2], shape[-1]
-    q_len = shape[1] if len(shape) == 4 else 1
     ptr, num_blocks, Hkv, cD = _cache4(cache, dev)
     if cD != D:
         raise ValueError(f"the cache's head dim is {cD}, q's {D}")
     table, max_blocks = _table(block_table, B, dev)
-    lens = _arg(context_lens, "context_lens", torch.int32, (B,), dev)
+    lens = _arg(context_lens, "context_lens", _torch().int32, (B,), dev)
+    code = _code(q)
     if workspace is None:
-        workspace = _workspace(paged_kv4_decode_workspace_bytes(B, Hq, Hkv, D, _code(q), num_splits, q_len),
-                               q.device, stream)
-    args = (_out(out), _arg(q, "q", q.dtype, shape, dev), _code(q), ptr, table, max_blocks, lens, B, q_len,
-            int(window), Hq, Hkv, D, num_blocks, float(scale), float(k_unit), float(v_unit), num_splits,
-            _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream, dev))
+        workspace = _workspace(paged_kv4_decode_workspace_bytes(B, Hq, Hkv, D, code, num_splits, q_len), q.device, stream)
+    args = (_out(out), _arg(q, "q", dtype, shape, dev), code, ptr, table, max_blocks, lens, B, q_len, int(window), Hq, Hkv, D,
+            num_blocks, float(scale), float(k_unit), float(v_unit), num_splits, _dev(workspace, "workspace"),
+            workspace.nbytes, _stream(stream, dev))
     return _issue(_L.paged_kv4_decode_attention, args, "paged_kv4_decode_attention", prepare, workspace)
 
 
@@ -838,8 +843,8 @@ def paged_rope(q, k, positions, table, q_out=None, k_out=None, stream=None, prep
             side.append((None, 0, None, 0, 0))
             continue
         heads = x.shape[1]
-        p, ld = _token_rows(x, name, T, heads, D, dtype, dev)
-        po, ldo = (p, ld) if out is None else _token_rows(out, name + "_out", T, heads, D, dtype, dev)
+        p, ld = _token_rows(x, name, (T, heads, D), dtype, dev)
+        po, ldo = (p, ld) if out is None else _token_rows(out, name + "_out", (T, heads, D), dtype, dev)
         side.append((po, ldo, p, ld, heads))
     args = (*side[0][:4], *side[1][:4], _code(first), *_rope_args(table, positions, T, dev), T, side[0][4], side[1][4], D,
             _stream(stream, dev))
@@ -848,11 +853,13 @@ def paged_rope(q, k, positions, table, q_out=None, k_out=None, stream=None, prep
 
 def _rope_rows(q, k_new, v_new, q_out, Hkv, D, dev):
     """q_out .. dtype of a rope append, T and Hq."""
-    (T, Hq), dtype = q.shape[:2], q.dtype
-    p, ld = _token_rows(q, "q", T, Hq, D, dtype, dev)
-    po, ldo = (p, ld) if q_out is None else _token_rows(q_out, "q_out", T, Hq, D, dtype, dev)
-    k, ld_k = _token_rows(k_new, "k_new", T, Hkv, D, dtype, dev)
-    v, ld_v = _token_rows(v_new, "v_new", T, Hkv, D, dtype, dev)
+    dtype = q.dtype
+    T, Hq, _ = q.shape
+    rows, kv = (T, Hq, D), (T, Hkv, D)
+    p, ld = _token_rows(q, "q", rows, dtype, dev)
+    po, ldo = (p, ld) if q_out is None else _token_rows(q_out, "q_out", rows, dtype, dev)
+    k, ld_k = _token_rows(k_new, "k_new", kv, dtype, dev)
+    v, ld_v = _token_rows(v_new, "v_new", kv, dtype, dev)
     return (po, ldo, p, ld, k, ld_k, v, ld_v, _code(q)), T, Hq
 
 
