@@ -1119,6 +1119,8 @@ static DecodeKernel kv4_entry() {
   return k;
 }
 
+// Warps: as many as the registers of a unit's sums and queries leave without spills (16-row units, 16 x 1000-32768,
+// 4 new, 32 / 8 heads: of D = 64 12 warps 62 us, 8 70; of D = 128 12 warps 101 to 132, 8 93).
 int register_decode_kv4(DecodeKernel *out) {
   int n = 0;
   out[n++] = kv4_entry<Kv4Cfg<BF16, 128, 1, 12, 2, 4>>();
@@ -1127,8 +1129,8 @@ int register_decode_kv4(DecodeKernel *out) {
   out[n++] = kv4_entry<Kv4Cfg<F16, 64, 1, 12, 4, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<BF16, 128, 2, 8, 3, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<F16, 128, 2, 8, 3, 4>>();
-  out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 2, 8, 4, 4>>();
-  out[n++] = kv4_entry<Kv4Cfg<F16, 64, 2, 8, 4, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 2, 12, 4, 4>>();
+  out[n++] = kv4_entry<Kv4Cfg<F16, 64, 2, 12, 4, 4>>();
   return n;
 }
 
