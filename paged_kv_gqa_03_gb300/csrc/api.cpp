@@ -67,8 +67,8 @@ Kv4WsLayout kv4_ws_layout(int B, int P, int D, int GC, int hg, int warps) {
   o = align_up(o + sizeof(int4) * (size_t)P, 256);
   L.part_o = o;  // [P][2][hg][GC][D]
   o = align_up(o + sizeof(float) * (size_t)P * 2 * hg * GC * D, 256);
-  L.part_lse = o;
-  o = align_up(o + sizeof(float) * (size_t)P * 2 * hg * GC, 256);
+  L.part_lse = o;  // [P][2][hg][GC] {largest raw score, sum of weights, the scores' factor}
+  o = align_up(o + sizeof(float4) * (size_t)P * 2 * hg * GC, 256);
   L.first_o = o;
   o = align_up(o + sizeof(float) * (size_t)P * warps * GC * D, 256);
   L.total = o;

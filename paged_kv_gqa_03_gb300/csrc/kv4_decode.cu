@@ -38,7 +38,9 @@
 // 4 new tokens, 16 x 1000-32768: 90 us.  D = 64 costs the instructions of a softmax on half the bytes: 64 x 8192,
 // 32 / 8 heads (303 MB) 84 us (16 warps of 96 registers: 80, and short calls no faster).
 //
-// Weights.  exp2(x - m + 15): f16 then holds a weight to 11 bits down to 2^-29 of
+// Weights.  exp2((s - m) * c + 15), s a raw score, m the largest, c its factor (scale and units): the difference comes
+// first, so that the largest weight is 2^15 exactly, however large the scores; what is joined goes by the same
+// differences of raw maxima, next to sums that are not turned into logarithms.  f16 then holds a weight to 11 bits down to 2^-29 of
 // the largest and to 2^-39 at all; l sums the same numbers in 32 bits.  bf16 queries
 // enter f16 scaled by a power of two per row (their largest element in [2^14, 2^15)).
 //
@@ -220,7 +222,7 @@ struct Kv4State {
   uint32_t qb[Cfg::NH][Cfg::KS][2];
   float acc[Cfg::NH][Cfg::MT][4];
   float m[Cfg::NH][2], l[Cfg::NH][2];  // of score columns 8 nh + 2 tig, + 1; m: largest raw score
-  float sc[Cfg::NH][2], off[Cfg::NH][2];  // weight = 2^(raw score * sc + off)
+  float sc[Cfg::NH][2], at[Cfg::NH][2];  // weight = 2^((raw score - at) * sc + kWeightShift); at: m, or 0 while it is -inf
   int back[Cfg::NH][2];
   int bk_lo, bk_hi;
 };
@@ -277,7 +279,7 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, in
     st.back[nh][0] = hidden_behind(p, r0 + 8 * nh + 2 * tig);
     st.back[nh][1] = hidden_behind(p, r0 + 8 * nh + 2 * tig + 1);
     st.m[nh][0] = st.m[nh][1] = -INFINITY;
-    st.l[nh][0] = st.l[nh][1] = st.off[nh][0] = st.off[nh][1] = 0.f;
+    st.l[nh][0] = st.l[nh][1] = st.at[nh][0] = st.at[nh][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < Cfg::MT; ++mt)
 #pragma unroll
@@ -463,15 +465,15 @@ __device__ __forceinline__ void softmax(Kv4State<Cfg> &st, int nh, const float (
       st.acc[nh][mt][3] *= al1;
     }
     // (a column that has seen nothing: its scores are -inf, its weights 0)
-    st.off[nh][0] = kWeightShift - (mn0 == -INFINITY ? 0.f : mn0 * st.sc[nh][0]);
-    st.off[nh][1] = kWeightShift - (mn1 == -INFINITY ? 0.f : mn1 * st.sc[nh][1]);
+    st.at[nh][0] = mn0 == -INFINITY ? 0.f : mn0;
+    st.at[nh][1] = mn1 == -INFINITY ? 0.f : mn1;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float p0 = exp2_fast(fmaf(s[i][nh][0], st.sc[nh][0], st.off[nh][0]));
-    const float p1 = exp2_fast(fmaf(s[i][nh][1], st.sc[nh][1], st.off[nh][1]));
-    const float p2 = exp2_fast(fmaf(s[i][nh][2], st.sc[nh][0], st.off[nh][0]));
-    const float p3 = exp2_fast(fmaf(s[i][nh][3], st.sc[nh][1], st.off[nh][1]));
+    const float p0 = exp2_fast(fmaf(s[i][nh][0] - st.at[nh][0], st.sc[nh][0], kWeightShift));
+    const float p1 = exp2_fast(fmaf(s[i][nh][1] - st.at[nh][1], st.sc[nh][1], kWeightShift));
+    const float p2 = exp2_fast(fmaf(s[i][nh][2] - st.at[nh][0], st.sc[nh][0], kWeightShift));
+    const float p3 = exp2_fast(fmaf(s[i][nh][3] - st.at[nh][1], st.sc[nh][1], kWeightShift));
     st.l[nh][0] += p0 + p2;
     st.l[nh][1] += p1 + p3;
     pb[i][nh][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -558,10 +560,10 @@ __device__ __forceinline__ void store4(void *out, size_t at, float4 v) {
 }
 
 // Ends a segment: a whole unit's rows go to the output; others leave their sums in part
-// ([GC][D]) and (log2 of the sums' unit, l) in ml.
+// ([GC][D]), (largest raw score, l) in ml and the scores' factor in scs.
 template <class Cfg>
 __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, const Kv4Meta &m, int sub, float *part,
-                                       float2 *ml, int lane) {
+                                       float2 *ml, float *scs, int lane) {
   const DecodeParams &p = kp.d;
   const int gid = lane >> 2, tig = lane & 3;
   const UnitAt u = unit_at(kp, m.hu, Cfg::GC);
@@ -579,7 +581,10 @@ __device__ __forceinline__ void finish(Kv4State<Cfg> &st, const Kv4Params &kp, c
       // a row that sees nothing gives 0; a sum of NaN gives NaN
       const float f = !whole ? 1.f : l == 0.f ? 0.f : kp.v_unit / l;
       if (row >= gc) continue;
-      if (!whole && gid == 0) ml[row] = make_float2(st.m[nh][c] == -INFINITY ? -INFINITY : -st.off[nh][c], l);
+      if (!whole && gid == 0) {
+        ml[row] = make_float2(st.m[nh][c], l);
+        scs[row] = st.sc[nh][c];
+      }
       const size_t at = whole ? row_at(p, m.b, h, r0 + row) + RUN * gid : 0;
 #pragma unroll
       for (int i = 0; i < RUN / 4; ++i) {
@@ -654,6 +659,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
   uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES);
   uint64_t *s_empty = s_full + WARPS * STAGES;
   int32_t *s_prefix = reinterpret_cast<int32_t *>(smem + Cfg::TILES_BYTES + Cfg::META_BYTES + Cfg::BAR_BYTES);
+  float *s_sc = reinterpret_cast<float *>(s_prefix);  // [segment][head][row], once the plan is done
+  static_assert(2 * WARPS * GC <= kKv4Prefix, "factors in the plan's place");
   __shared__ int4 s_cut[WARPS + 1];           // {item, b, unit, block} at which a ring's range begins
   __shared__ int2 s_seg[2 * WARPS];           // segments left to join, two a ring, in the list's order: {unit or -1, flags}
   __shared__ float2 s_ml[2 * WARPS * GC];     // [segment][head][row]
@@ -863,7 +870,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
         finish<Cfg>(state, kp, m, sub,
                     ends ? reinterpret_cast<float *>(smem + ring * ring_bytes) + sub * GC * D
                          : kp.first_o + (((size_t)blockIdx.x * rings + ring) * hg + sub) * GC * D,
-                    s_ml + (seg * hg + sub) * GC, lane);
+                    s_ml + (seg * hg + sub) * GC, s_sc + (seg * hg + sub) * GC, lane);
         if (sub == 0 && lane == 0 && (m.flags & (kOpens | kCloses)) != (kOpens | kCloses))
           s_seg[seg] = make_int2(m.b * p.HU + m.hu, m.flags);
         if (ends) {
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
 #pragma unroll 1
     for (int v0 = tid; v0 < hg * live * (D / 4); v0 += 4 * WARPS * 32) {
       float4 acc[4];
-      float M[4], l[4];
+      float M[4], l[4], sc[4];
       int row[4];  // [head][row]
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -926,6 +933,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
         acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
         M[t] = -INFINITY;
         l[t] = 0.f;
+        sc[t] = s_sc[g * rows + row[t]];  // (the same in all segments of a unit)
       }
       const int d = 4 * (v0 % (D / 4));
       static_assert(WARPS * 32 % (D / 4) == 0, "a thread keeps its elements");
@@ -940,8 +948,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
           const float4 a = *reinterpret_cast<const float4 *>(src + row[t] * D + d);
           // (of a row that saw nothing, or NaN alone: its maximum is -inf, its sum 0 or NaN)
           const float m = fmaxf(M[t], ml.x);
-          const float keep = M[t] == -INFINITY ? 1.f : exp2_fast(M[t] - m);
-          const float add = ml.x == -INFINITY ? 1.f : exp2_fast(ml.x - m);
+          const float keep = M[t] == -INFINITY ? 1.f : exp2_fast((M[t] - m) * sc[t]);
+          const float add = ml.x == -INFINITY ? 1.f : exp2_fast((ml.x - m) * sc[t]);
           if (ml.y == 0.f) continue;
           M[t] = m;
           l[t] = fmaf(l[t], keep, ml.y * add);
@@ -961,8 +969,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) kv4_decode_kernel(const __gri
         } else {
           const int slot = (blockIdx.x * 2 + (opens ? 1 : 0)) * rows + row[t];
           *reinterpret_cast<float4 *>(p.part_o + (size_t)slot * D + d) = y;
-          // (a sum of NaN as +inf: the merge then gives NaN)
-          if (d == 0) p.part_lse[slot] = l[t] != l[t] ? INFINITY : l[t] == 0.f ? -INFINITY : M[t] + __log2f(l[t]);
+          // {largest raw score, l, factor} (a sum of NaN as a score of +inf: the merge then gives NaN)
+          if (d == 0)
+            reinterpret_cast<float4 *>(p.part_lse)[slot] =
+                make_float4(l[t] != l[t] ? INFINITY : l[t] == 0.f ? -INFINITY : M[t], l[t] != l[t] ? 1.f : l[t], sc[t], 0.f);
         }
       }
     }
@@ -1025,28 +1035,32 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
   constexpr int kBatch = 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, den = 0.f;
+  const float4 *ml = reinterpret_cast<const float4 *>(p.part_lse);
+  const float sc = ml[((c * 2 + 1) * kp.hg + sub) * p.GC + row].z;  // (the same in all of them)
 #pragma unroll 1
   for (int s = c + team; s <= last && r < p.R; s += kBatch * teams) {
     float4 o[kBatch];
-    float l[kBatch];
+    float m[kBatch], l[kBatch];
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
       const int w = min(s + t * teams, last);
       const int slot = ((w * 2 + (w == c ? 1 : 0)) * kp.hg + sub) * p.GC + row;
-      l[t] = s + t * teams <= last ? p.part_lse[slot] : -INFINITY;
+      const float4 x = ml[slot];
+      m[t] = s + t * teams <= last ? x.x : -INFINITY;
+      l[t] = x.y;
       o[t] = *reinterpret_cast<const float4 *>(p.part_o + (size_t)slot * D + d);
     }
     float cm = M;
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, l[t]);
+    for (int t = 0; t < kBatch; ++t) cm = fmaxf(cm, m[t]);
     if (cm == -INFINITY) continue;  // nothing seen yet
-    const float keep = exp2_fast(M - cm);
+    const float keep = M == -INFINITY ? 0.f : exp2_fast((M - cm) * sc);
     acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
     den *= keep;
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
-      const bool on = l[t] != -INFINITY;
-      const float wt = on ? exp2_fast(l[t] - cm) : 0.f;
+      const bool on = m[t] != -INFINITY;
+      const float wt = on ? l[t] * exp2_fast((m[t] - cm) * sc) : 0.f;
       acc.x = fmaf(wt, on ? o[t].x : 0.f, acc.x);
       acc.y = fmaf(wt, on ? o[t].y : 0.f, acc.y);
       acc.z = fmaf(wt, on ? o[t].z : 0.f, acc.z);
@@ -1069,7 +1083,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
     for (int t = 0; t < teams; ++t) {
       const float2 ml = s_ml[t * size + v];
       if (ml.x == -INFINITY) continue;
-      const float wt = exp2_fast(ml.x - all);
+      const float wt = exp2_fast((ml.x - all) * sc);
       const float4 a = s_acc[t * size + v];
       acc.x = fmaf(wt, a.x, acc.x);
       acc.y = fmaf(wt, a.y, acc.y);
