@@ -7,7 +7,8 @@
 namespace pkv {
 
 // A tensor's unit.  (Within 2^+-64 what is multiplied and divided by it stays within fp32's normal numbers: a
-// unit over a softmax's sum of up to 2^46, code * scale * unit.)
+// unit over a softmax's sum of up to 2^46, code * scale * unit.  The scores' factor, k_unit times the softmax scale times a
+// query row's power of two, may leave them: the decode kernel bounds it.)
 inline bool kv4_unit_ok(float u) { return u >= 0x1p-64f && u <= 0x1p64f; }
 
 constexpr int kKv4 = 4;  // DecodeKernel::cache_dtype of the 4-bit variants (no public dtype code)

@@ -48,6 +48,8 @@
 // of the rows that see the position, as the formula does, and of no others: hidden
 // scores are selected away; in blocks that some row does not see whole, V scales of
 // NaN are set to 0 and NaN is added to the rows that see them.
+#include <cfloat>
+
 #include "decode.cuh"
 #include "kv4.cuh"
 #include "kv4.h"
@@ -274,8 +276,10 @@ __device__ __forceinline__ void begin(Kv4State<Cfg> &st, const Kv4Params &kp, in
       st.qb[nh][ks][1] = raw[ks].y ^ flip;
     }
     const float sc = none ? 1.f : fabsf(p.scale_log2);
-    st.sc[nh][0] = sc * __shfl_sync(kFull, down, 8 * tig);  // rows 2 tig and 2 tig + 1: lanes of gid 2 tig, 2 tig + 1
-    st.sc[nh][1] = sc * __shfl_sync(kFull, down, 8 * tig + 4);
+    // Within the normal numbers: a product of 0 would make NaN of a hidden score's -inf, one of inf of a difference of 0.
+    // (Raw scores differ by less than 2^36 and, where they do, by 2^-34 or more: the weights are those of the product.)
+    st.sc[nh][0] = fminf(fmaxf(sc * __shfl_sync(kFull, down, 8 * tig), FLT_MIN), FLT_MAX);  // rows 2 tig and 2 tig + 1:
+    st.sc[nh][1] = fminf(fmaxf(sc * __shfl_sync(kFull, down, 8 * tig + 4), FLT_MIN), FLT_MAX);  // lanes of gid 2 tig, ..
     st.back[nh][0] = hidden_behind(p, r0 + 8 * nh + 2 * tig);
     st.back[nh][1] = hidden_behind(p, r0 + 8 * nh + 2 * tig + 1);
     st.m[nh][0] = st.m[nh][1] = -INFINITY;
