@@ -251,25 +251,13 @@ __device__ __forceinline__ void store_half16(void *p, const Half16 &r) {
   }
 }
 
-// 16 consecutive elements (16-byte aligned) <-> floats.
-template <class T>
+// 16 consecutive floats (16-byte aligned).
 __device__ __forceinline__ void load16(const void *p, size_t i, float (&y)[16]) {
-  if constexpr (T::kBytes == 4) {
-    const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+  const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = f[j];
-      y[4 * j] = v.x; y[4 * j + 1] = v.y; y[4 * j + 2] = v.z; y[4 * j + 3] = v.w;
-    }
-  } else {
-    const uint4 *u = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-    const uint4 a = u[0], b = u[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = unpack2(T{}, w[j]);
-      y[2 * j] = v.x; y[2 * j + 1] = v.y;
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = f[j];
+    y[4 * j] = v.x; y[4 * j + 1] = v.y; y[4 * j + 2] = v.z; y[4 * j + 3] = v.w;
   }
 }
 
@@ -291,22 +279,40 @@ __device__ __forceinline__ void store16(void *p, size_t i, const float (&y)[16])
   }
 }
 
-// 16 elements at p[i ..] as the format holds them.
+// 16 elements of a 16-bit type as the format holds them: the one way for whole pages, appended rows and rotated rows, whose
+// bytes are the same.  (Of an element that comes to 0 the sign depends on the unit: the divisions keep it.)
+template <class T>
+__device__ __forceinline__ Kv4Group kv4_quantise_half(const uint32_t (&w)[8], float unit) {
+  if (unit == 1.f) return kv4_quantise16<T>(w);
+  float y[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 v = unpack2(T{}, w[j]);
+    y[2 * j] = v.x; y[2 * j + 1] = v.y;
+  }
+  return kv4_quantise(y, unit);
+}
+// 16 elements at p[i ..] of global memory.
 template <class T>
 __device__ __forceinline__ Kv4Group kv4_quantise_at(const void *p, size_t i, float unit) {
   if constexpr (T::kBytes == 2) {
-    const Half16 h = load_half16(static_cast<const uint16_t *>(p) + i);
-    if (unit == 1.f) return kv4_quantise16<T>(h.w);
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = unpack2(T{}, h.w[j]);
-      y[2 * j] = v.x; y[2 * j + 1] = v.y;
-    }
-    return kv4_quantise(y, unit);
+    return kv4_quantise_half<T>(load_half16(static_cast<const uint16_t *>(p) + i).w, unit);
   } else {
     float y[16];
-    load16<T>(p, i, y);
+    load16(p, i, y);
+    return kv4_quantise(y, unit);
+  }
+}
+// The same of shared memory.
+template <class T>
+__device__ __forceinline__ Kv4Group kv4_quantise_shared(const void *p, size_t i, float unit) {
+  if constexpr (T::kBytes == 2) {
+    const uint4 *u = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    const uint4 a = u[0], b = u[1];
+    return kv4_quantise_half<T>({a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, unit);
+  } else {
+    float y[16];
+    load16(p, i, y);
     return kv4_quantise(y, unit);
   }
 }

@@ -192,9 +192,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, i
       const int hh = first + i / G, g = i % G;
       const bool value = hh >= p.Hq + p.Hkv;
       const int h = value ? hh - p.Hq - p.Hkv : hh - p.Hq;
-      float y[16];
-      load16<Type>(s_rows, (size_t)(i / G) * p.D + 16 * g, y);
-      const Kv4Group x = kv4_quantise(y, value ? p.v_unit : p.k_unit);
+      const Kv4Group x = kv4_quantise_shared<Type>(s_rows, (size_t)(i / G) * p.D + 16 * g, value ? p.v_unit : p.k_unit);
       uint8_t *tile = p.kv4 + (size_t)(slot / kBlock * p.Hkv + h) * (18 * p.D);
       const int tok = (int)(slot % kBlock);
       if (p.D == 128)
