@@ -86,6 +86,7 @@ constexpr int kMaxDevices = 64;
 struct Registry {
   DecodeKernel k[kMaxKernels];
   int n = 0;
+  Kv4Kernel kv4[kKv4Kernels];
 };
 
 Registry &registry() {
@@ -98,7 +99,7 @@ Registry &registry() {
     r.n += register_decode_f32(r.k + r.n);
     r.n += register_decode_tree(r.k + r.n);
     r.n += register_decode_tree_fp8(r.k + r.n);
-    r.n += register_decode_kv4(r.k + r.n);
+    register_decode_kv4(r.kv4);
   });
   return r;
 }
@@ -125,14 +126,14 @@ void take_stall(Params &p, int which) {
 
 struct DeviceFacts {
   int sm_count = 0;
-  int ctas_per_sm[kMaxKernels] = {};  // 0 = not yet configured
+  int ctas_per_sm[kMaxKernels + kKv4Kernels] = {};  // 0 = not yet configured (the 4-bit kernels' at the end)
 };
 std::mutex g_dev_mu;
 DeviceFacts g_dev[kMaxDevices];
 
-// Configures kernel `ki` on the current device (opt-in shared memory) and
-// returns its resident CTAs per SM and the SM count.
-int kernel_occupancy(int ki, int *ctas_per_sm, int *sm_count) {
+// Configures a kernel on the current device (opt-in shared memory) and
+// returns its resident CTAs per SM, kept at `at`, and the SM count.
+int occupancy(int at, const void *fn, int threads, size_t smem_bytes, int *ctas_per_sm, int *sm_count) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_status(e);
@@ -143,19 +144,22 @@ int kernel_occupancy(int ki, int *ctas_per_sm, int *sm_count) {
     e = cudaDeviceGetAttribute(&f.sm_count, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_status(e);
   }
-  if (f.ctas_per_sm[ki] == 0) {
-    const DecodeKernel &k = registry().k[ki];
-    e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem_bytes);
+  if (f.ctas_per_sm[at] == 0) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes);
     if (e != cudaSuccess) return cuda_status(e);
     int nb = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, k.fn, k.threads, k.smem_bytes);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, threads, smem_bytes);
     if (e != cudaSuccess) return cuda_status(e);
     if (nb <= 0) return PKV_EUNSUPPORTED;
-    f.ctas_per_sm[ki] = nb;
+    f.ctas_per_sm[at] = nb;
   }
-  *ctas_per_sm = f.ctas_per_sm[ki];
+  *ctas_per_sm = f.ctas_per_sm[at];
   *sm_count = f.sm_count;
   return PKV_OK;
+}
+int kernel_occupancy(int ki, int *ctas_per_sm, int *sm_count) {
+  const DecodeKernel &k = registry().k[ki];
+  return occupancy(ki, k.fn, k.warps * 32, k.smem_bytes, ctas_per_sm, sm_count);
 }
 
 // The current device's SM count (cached).
@@ -293,7 +297,7 @@ struct Choice {
 };
 
 // Picks the kernel for a shape: tensor cores (8-row units, unused columns
-// padded; 16-row units on fp8 and 4-bit caches past 8 rows) for every group size on
+// padded; 16-row units on fp8 caches past 8 rows) for every group size on
 // 16-bit and fp8 caches — even for
 // MHA the mma.sync block step measured faster on GB300 than the CUDA-core one
 // (5.83 vs 5.56 TB/s, fp16 MHA layer) — and CUDA cores for fp32 caches.  The
@@ -331,7 +335,7 @@ int choose_kernel(int cache_dtype, int q_dtype, int D, int R, Choice *c, bool tr
   // 32K fp8 layer at 16 rows, one 16-row unit per kv head against two 8-row
   // units streaming the same blocks)
   int GC = mma ? 8 : (R >= 2 ? 2 : 1);
-  if (mma && (cache_dtype == PKV_FP8_E4M3 || cache_dtype == kKv4) && R > 8 && want_gc != 8) GC = 16;
+  if (mma && cache_dtype == PKV_FP8_E4M3 && R > 8 && want_gc != 8) GC = 16;
   Registry &r = registry();
   int first = -1;
   for (int pass = 0; pass < 2 && first < 0; ++pass) {
@@ -402,6 +406,26 @@ int plan_call(int cache_dtype, int q_dtype, int B, int q_len, int Hq, int Hkv, i
   }
   if (*P > (1 << 24)) return PKV_EINVAL;
   (void)B;
+  return PKV_OK;
+}
+
+// The same of the 4-bit attention: units of 8 rows, 16 past 8 rows a kv head; P ranges, one per CTA: num_splits, or one
+// per SM.
+int plan_kv4(int q_dtype, int q_len, int Hq, int Hkv, int D, int num_splits, Choice *c, int *P) {
+  const int R = q_len * (Hq / Hkv), GC = R > 8 ? 16 : 8;
+  const Kv4Kernel *k = registry().kv4;
+  for (c->ki = 0; c->ki < kKv4Kernels; ++c->ki)
+    if (k[c->ki].q_dtype == q_dtype && k[c->ki].D == D && k[c->ki].GC == GC) break;
+  if (c->ki == kKv4Kernels) return PKV_EUNSUPPORTED;
+  c->GC = GC;
+  c->NC = (R + GC - 1) / GC;
+  if (num_splits < 0 || num_splits > (1 << 24)) return PKV_EINVAL;
+  *P = num_splits;
+  if (num_splits == 0) {
+    const int rc = device_sm_count(P);
+    if (rc != PKV_OK) return rc;
+  }
+  *P = std::min(*P, kKv4MaxRanges);
   return PKV_OK;
 }
 
@@ -597,18 +621,13 @@ static DecodeParams unit_params(const Choice &c, int P, void *out, const void *q
   p.out_dtype = q_dtype;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.inline_plan = B + 1 <= kInlinePrefix ? 1 : 0;
-  p.n_ctas = (P + registry().k[c.ki].warps - 1) / registry().k[c.ki].warps;
   take_stall(p, PKV_STALL_DECODE);
   return p;
 }
 
-// Ranges of the 4-bit attention, one per CTA: num_splits, or one per SM.
-static int kv4_ranges(int P, int ki, int num_splits) {
-  return std::min(num_splits > 0 ? num_splits : P / registry().k[ki].warps, kKv4MaxRanges);
-}
-
 // Plan (large batches) and decode kernel.
-static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, void **args, cudaStream_t s) {
+static cudaError_t launch_units(const void *fn, int threads, size_t smem_bytes, const DecodeParams &p, void **args,
+                                cudaStream_t s) {
   const bool pdl = s != nullptr;  // programmatic launch on explicit streams only
   cudaError_t e = cudaSuccess;
   if (!p.inline_plan) {
@@ -618,15 +637,15 @@ static cudaError_t launch_units(const DecodeKernel &k, const DecodeParams &p, vo
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_ctas);
-  cfg.blockDim = dim3(k.threads);
-  cfg.dynamicSmemBytes = k.smem_bytes;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelExC(&cfg, k.fn, args);
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 // The decode kernel (8- or 16-row units, one partition per warp) and its
@@ -654,6 +673,8 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
 
   DecodeParams p = unit_params(c, P, out, q, q_dtype, k_scale, v_scale, block_table, max_blocks_per_seq, context_lens, B,
                                q_len, window, Hq, Hkv, D, num_blocks, scale, workspace);
+  const DecodeKernel &k = registry().k[c.ki];
+  p.n_ctas = (P + k.warps - 1) / k.warps;
   if (tree) {
     p.tree_mask = tree->mask;
     p.tree_lens = tree->lens;
@@ -662,7 +683,7 @@ static int run_units(const Choice &c, int P, void *out, const void *q, int q_dty
   }
   void *args[3] = {&p, &tmK, &tmV};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_units(registry().k[c.ki], p, args, s);
+  cudaError_t e = launch_units(k.fn, k.warps * 32, k.smem_bytes, p, args, s);
   if (e == cudaSuccess) e = launch_splitk_merge(p, s, s != nullptr);
   return cuda_status(e);
 }
@@ -1161,9 +1182,9 @@ int paged_kv4_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, i
   if (rc != PKV_OK) return rc;
   Choice c;
   int P = 0;
-  rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
+  rc = plan_kv4(q_dtype, q_len, Hq, Hkv, D, num_splits, &c, &P);
   if (rc != PKV_OK) return rc;
-  *bytes_out = kv4_ws_layout(B, kv4_ranges(P, c.ki, num_splits), D, c.GC, kv4_heads(Hkv), registry().k[c.ki].warps).total;
+  *bytes_out = kv4_ws_layout(B, P, D, c.GC, kv4_heads(Hkv), registry().kv4[c.ki].warps).total;
   return PKV_OK;
 }
 
@@ -1182,15 +1203,14 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   if (!aligned16(out) || !aligned16(q) || !aligned16(cache)) return PKV_EINVAL;
   Choice c;
   int P = 0;
-  rc = plan_call(kKv4, q_dtype, B, q_len, Hq, Hkv, D, num_splits, &c, &P);
+  rc = plan_kv4(q_dtype, q_len, Hq, Hkv, D, num_splits, &c, &P);
   if (rc != PKV_OK) return rc;
-  P = kv4_ranges(P, c.ki, num_splits);
-  const DecodeKernel &k = registry().k[c.ki];
+  const Kv4Kernel &k = registry().kv4[c.ki];
   const Kv4WsLayout L = kv4_ws_layout(B, P, D, c.GC, kv4_heads(Hkv), k.warps);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < L.total)
     return PKV_EWORKSPACE;
   int ctas = 0, sms = 0;
-  rc = kernel_occupancy(c.ki, &ctas, &sms);  // also opts the kernel into its shared memory
+  rc = occupancy(kMaxKernels + c.ki, k.fn, k.threads, k.smem_bytes, &ctas, &sms);  // opts into its shared memory
   if (rc != PKV_OK) return rc;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   Kv4Params p;
@@ -1220,7 +1240,7 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
   p.v_unit = v_unit;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   void *args[1] = {&p};
-  cudaError_t e = launch_units(k, p.d, args, st);
+  cudaError_t e = launch_units(k.fn, k.threads, k.smem_bytes, p.d, args, st);
   // units of no more blocks: none is cut between CTAs
   if (e == cudaSuccess && most > kv4_whole(D) && P > 1) e = launch_kv4_merge(p, st, st != nullptr);
   return cuda_status(e);

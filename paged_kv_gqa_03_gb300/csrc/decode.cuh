@@ -1373,7 +1373,6 @@ DecodeKernel decode_entry() {
   k.D = Cfg::D;
   k.GC = Cfg::GC;
   k.warps = Cfg::WARPS;
-  k.threads = Cfg::WARPS * 32;
   k.stages = Cfg::STAGES;
   k.smem_bytes = Cfg::SMEM;
   k.tree = Cfg::TREE ? 1 : 0;

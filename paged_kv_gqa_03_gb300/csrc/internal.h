@@ -146,8 +146,7 @@ struct DecodeKernel {
   const void *fn;       // __global__ void (DecodeParams, CUtensorMap, CUtensorMap)
   int mma;              // 1 = tensor-core (mma.sync) path, 0 = CUDA-core path
   int cache_dtype, q_dtype, D, GC;
-  int warps, stages;    // warps that work through a partition each
-  int threads;          // of a CTA
+  int warps, stages;
   size_t smem_bytes;
   int tree;             // 1 = masks from a tree of drafted tokens
 };

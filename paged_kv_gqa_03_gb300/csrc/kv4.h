@@ -11,8 +11,6 @@ namespace pkv {
 // query row's power of two, may leave them: the decode kernel bounds it.)
 inline bool kv4_unit_ok(float u) { return u >= 0x1p-64f && u <= 0x1p64f; }
 
-constexpr int kKv4 = 4;  // DecodeKernel::cache_dtype of the 4-bit variants (no public dtype code)
-
 constexpr int kKv4PageThreads = 128;  // a CTA of kv4_pages.cu
 
 constexpr int kKv4MaxRanges = 224;  // WsHeader::cta_status
@@ -41,7 +39,16 @@ struct Kv4WsLayout {
 Kv4WsLayout kv4_ws_layout(int B, int P, int D, int GC, int hg, int warps);
 // Heads that a unit takes together: neighbours in the cache, read by one copy.
 inline int kv4_heads(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
-int register_decode_kv4(DecodeKernel *out);
+// One compiled variant of the decode kernel.
+struct Kv4Kernel {
+  const void *fn;  // __global__ void (Kv4Params)
+  int q_dtype, D, GC;
+  int warps;    // consumers
+  int threads;  // of a CTA: consumers and producers
+  size_t smem_bytes;
+};
+constexpr int kKv4Kernels = 8;
+void register_decode_kv4(Kv4Kernel (&out)[kKv4Kernels]);
 // Joins the units cut between CTAs.
 cudaError_t launch_kv4_merge(Kv4Params p, cudaStream_t stream, bool pdl);
 

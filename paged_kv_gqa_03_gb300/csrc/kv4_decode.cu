@@ -1121,25 +1121,14 @@ cudaError_t launch_kv4_merge(Kv4Params p, cudaStream_t stream, bool pdl) {
 }
 
 template <class Cfg>
-static DecodeKernel kv4_entry() {
-  DecodeKernel k;
-  k.fn = reinterpret_cast<const void *>(&kv4_decode_kernel<Cfg>);
-  k.mma = 1;
-  k.cache_dtype = kKv4;
-  k.q_dtype = Cfg::Q::kCode;
-  k.D = Cfg::D;
-  k.GC = Cfg::GC;
-  k.warps = Cfg::WARPS;
-  k.threads = Cfg::THREADS;
-  k.stages = Cfg::STAGES;
-  k.smem_bytes = Cfg::SMEM;
-  k.tree = 0;
-  return k;
+static Kv4Kernel kv4_entry() {
+  return Kv4Kernel{reinterpret_cast<const void *>(&kv4_decode_kernel<Cfg>), Cfg::Q::kCode, Cfg::D, Cfg::GC, Cfg::WARPS,
+                   Cfg::THREADS, Cfg::SMEM};
 }
 
 // Warps: as many as the registers of a unit's sums and queries leave without spills (16-row units, 16 x 1000-32768,
 // 4 new, 32 / 8 heads: of D = 64 12 warps 62 us, 8 70; of D = 128 12 warps 101 to 132, 8 93).
-int register_decode_kv4(DecodeKernel *out) {
+void register_decode_kv4(Kv4Kernel (&out)[kKv4Kernels]) {
   int n = 0;
   out[n++] = kv4_entry<Kv4Cfg<BF16, 128, 1, 12, 2, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<F16, 128, 1, 12, 2, 4>>();
@@ -1149,7 +1138,6 @@ int register_decode_kv4(DecodeKernel *out) {
   out[n++] = kv4_entry<Kv4Cfg<F16, 128, 2, 8, 3, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<BF16, 64, 2, 12, 4, 4>>();
   out[n++] = kv4_entry<Kv4Cfg<F16, 64, 2, 12, 4, 4>>();
-  return n;
 }
 
 }  // namespace pkv
