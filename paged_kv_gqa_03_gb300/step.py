@@ -68,11 +68,14 @@ class _Staging:
 
 
 class DecodeStep:
+    rotates_apart = False   # FP8 caches: the keys are rotated in a call of its own, in front of the append
+
     def __init__(self, k_cache, v_cache, Hq, q_dtype, max_blocks, k_scale=None, v_scale=None,
                  num_splits=0, stream=None, scale=None, q_len=1, window=0, calibrated=False, rope=None):
         self.k_cache, self.v_cache = k_cache, v_cache
         self.k_scale, self.v_scale = k_scale, v_scale
         self.num_blocks, self.Hkv, _, self.D = k_cache.shape
+        self.rotates_apart = k_cache.dtype == torch.float8_e4m3fn
         self.new_dtype = q_dtype if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
         self.calibrated = calibrated
         self._setup(k_cache.device, Hq, q_dtype, max_blocks, num_splits, stream, scale, q_len, window, rope)
@@ -139,9 +142,10 @@ class DecodeStep:
         with torch.cuda.stream(self.stream):
             self._dev = _Staging(layout, total, self.device, False)
             self._ws = torch.empty(self._workspace_bytes(B), dtype=torch.uint8, device=self.device)
-            if self.rope is not None:   # the rotated queries (and, for FP8 caches, keys)
+            if self.rope is not None:
                 self._q_rot = torch.empty((B * self.q_len, self.Hq, self.D), dtype=self.q_dtype, device=self.device)
-                self._k_rot = torch.empty((B * self.q_len, self.Hkv, self.D), dtype=self.new_dtype, device=self.device)
+                if self.rotates_apart:
+                    self._k_rot = torch.empty((B * self.q_len, self.Hkv, self.D), dtype=self.new_dtype, device=self.device)
         self.h_seqs = np.empty(B, dtype=np.int64)
         self.h_tok_seqs = np.empty(B * self.q_len, dtype=np.int64)
         self.d_q, self.d_k_new, self.d_v_new = self._dev["q"], self._dev["k_new"], self._dev["v_new"]
@@ -254,7 +258,7 @@ class DecodeStep:
         s, calls = self.stream, []
         if self.rope is not None:
             positions = self._dev["positions"]
-            if self.k_cache.dtype != torch.float8_e4m3fn:
+            if not self.rotates_apart:
                 return [paged_rope_append(q, k_new, v_new, positions, self.rope, self.k_cache, self.v_cache, self.d_slots,
                                           q_out=self._q_rot, stream=s, prepare=True)]
             calls.append(paged_rope(q, k_new, positions, self.rope, q_out=self._q_rot, k_out=self._k_rot, stream=s,
