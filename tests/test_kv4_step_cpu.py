@@ -14,6 +14,29 @@ class Rope:     # (a RopeTable, as far as a step looks at it)
     rot_dim = 64
 
 
+@pytest.mark.parametrize("shape", [(8, 2, 18 * 96), (8, 2, 18 * 64 + 1), (8, 2, 64), (8, 2, 0), (8, 2 * 18 * 64), (8, 2, 16, 64)])
+def test_a_cache_of_another_shape_is_refused(monkeypatch, shape):
+    _pkv()
+    from paged_kv_gqa_03_gb300.step import Kv4Step
+    with pytest.raises(ValueError, match="4-bit cache"):
+        Kv4Step(_gpu(torch.zeros(shape, dtype=torch.uint8)), 4, BF16, 8, stream=object())
+
+
+def test_a_cache_of_another_type_is_refused(monkeypatch):
+    _pkv()
+    from paged_kv_gqa_03_gb300.step import Kv4Step
+    with pytest.raises(TypeError, match="uint8"):
+        Kv4Step(_gpu(torch.zeros(8, 2, 18 * 64, dtype=torch.int8)), 4, BF16, 8, stream=object())
+
+
+def test_a_cache_of_its_shape(monkeypatch):
+    _pkv()
+    from paged_kv_gqa_03_gb300.step import Kv4Step
+    for D in (64, 128):
+        s = Kv4Step(_gpu(torch.zeros(8, 2, 18 * D, dtype=torch.uint8)), 4, BF16, 8, stream=object())
+        assert (s.num_blocks, s.Hkv, s.D) == (8, 2, D)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "kv4"])
 def test_rotated_keys_have_a_buffer_only_where_they_are_appended_apart(monkeypatch, kind):
     """FP8 caches: the rotation is a call of its own.  The fused appends write rotated keys to the cache."""
