@@ -667,8 +667,10 @@ int paged_kv4_decode_attention(void *out, const void *q, int q_dtype, const void
  * elements is turned by the angle position * f_i and scaled by `magnitude`:
  *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin),
  * a pair being elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1; the
- * head's other elements stay.  Angles are exact at any position; the rotation is fp32,
- * rounded once to the rows' type.
+ * head's other elements stay.  A table entry is f_i / 2 pi as a double has it, in 64 bits of a
+ * turn, and position * entry is exact: an angle is off by at most
+ * |position| * (2^-52 f_i + 2^-61) radians (at position 2^20 and below 2^-32 f_i, at 2^40 2^-12 f_i)
+ * and the rounding of the turn's fraction to fp32; the rotation is fp32, rounded once to the rows' type.
  *   turns        [rot_dim / 2] uint64, device: f_i / 2 pi in 2^-64, from pkv_rope_turns
  *                (a host call: frequencies are radians a position, >= 0 and finite; any scaling
  *                for long contexts is in the frequencies and the magnitude)

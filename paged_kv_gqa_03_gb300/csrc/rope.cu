@@ -8,9 +8,10 @@
 // a pair being elements (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved.
 //
 // The angle.  f_i comes as turns a position in 2^-64 (uint64): position * turns
-// mod 2^64 is then the exact fraction of a turn, whatever the position, with one
-// integer product; as a float in half turns it goes to sincospi.  (A 32-bit
-// product position * f_i is off by 0.06 radians at position 10^6.)  A token's
+// mod 2^64 is then the fraction of a turn without a further rounding, whatever the position, with one
+// integer product; as a float in half turns it goes to sincospi.  What is off is the table's entry,
+// f_i / 2 pi in double: |position| (2^-52 f_i + 2^-61) radians, 2^-32 at 10^6.  (A 32-bit
+// product position * f_i is off by 0.06 radians there.)  A token's
 // rot / 2 sines are computed once a CTA and read by all heads.
 //
 // Split.  A CTA takes one token, or some heads of it; a thread turns 16 bytes of
