@@ -5,17 +5,21 @@
 // A thread does 16 elements of K of two neighbouring tokens, or of V, whose codes share
 // bytes: a scale needs nothing of another thread, a warp's loads and stores of codes are whole lines.  A new token
 // whose neighbour is not beside it in the call is stored by an exclusive or into its own
-// nibbles (kv4_store_v1).  All are bound by HBM: a token and head read or write 4 D bytes in 16
-// bits and 18 D / 16 in 4.  4096 pages of 8 heads of 128 in bf16 (344 MB): packed in 59 us (5.8 TB/s, three
-// issue slots of four taken: the conversions), expanded in 52 (6.5 TB/s); 16384 tokens appended in 27 us (6.3 TB/s).
+// nibbles (kv4_store_v1).  A token and head read or write 4 D bytes in 16 bits and 18 D / 16 in 4.  4096 pages of 8
+// heads of 128 in bf16 (344 MB): expanded in 55 us (6.2 TB/s: HBM), packed in 60 (5.7 TB/s, three issue slots of four
+// taken: the conversions).  16384 tokens (86 MB) appended in 21 us: 4.1 TB/s, 0.6 of a copy's rate, DRAM busy for 39 %;
+// issue slots again (0.73 a clock) and waits for the slots and rows, one load of a row in flight a thread, half of V's
+// threads leaving at once.  Divisions (fp32 rows, units other than 1) cost more: packed in 111 us (fp32, 612 MB) and
+// 136 (bf16, unit 2^-4), appended in 38 and 44.
 #include "kv4.cuh"
 #include "kv4.h"
 
 namespace pkv {
 
 constexpr int kThreads = kKv4PageThreads;
-// Resident CTAs of the kernels that convert: whole occupancy (32 registers) is worth a few spilled registers (4096
-// pages packed and expanded: 132 us without the bound, 119 with; 16384 tokens appended: 31 and 27), but for fp32 rows.
+// Resident CTAs of the kernels that convert: whole occupancy (32 registers) is worth a few spilled registers, but for
+// fp32 rows (bf16, 8 heads of 128 and of 64, with a bound of 8 and with this one: 4096 pages packed 69.9 -> 60.1 us and
+// 37.8 -> 33.4, expanded 58.8 -> 55.1 and 31.7 -> 29.5; 16384 tokens appended 25.8 -> 21.1 and 14.7 -> 12.3).
 template <class T>
 constexpr int kResident = T::kBytes == 4 ? 8 : 16;
 
