@@ -40,9 +40,10 @@
 //
 // Weights.  exp2((s - m) * c + 15), s a raw score, m the largest, c its factor (scale and units): the difference comes
 // first, so that the largest weight is 2^15 exactly, however large the scores; what is joined goes by the same
-// differences of raw maxima, next to sums that are not turned into logarithms.  f16 then holds a weight to 11 bits down to 2^-29 of
-// the largest and to 2^-39 at all; l sums the same numbers in 32 bits.  bf16 queries
-// enter f16 scaled by a power of two per row (their largest element in [2^14, 2^15)).
+// differences of raw maxima, next to sums that are not turned into logarithms.  f16 then holds a weight to 11 bits
+// down to 2^-29 of the largest and to 2^-39 at all.  l sums the weights in 32 bits before they are rounded to f16: a
+// weight counts by up to 2^-11 of itself differently above and below.  bf16 queries enter f16 scaled by a power of two
+// per row (their largest element in [2^14, 2^15)).
 //
 // Not finite.  A group's NaN scale makes NaN of the scores, or of the output elements,
 // of the rows that see the position, as the formula does, and of no others: hidden
