@@ -264,19 +264,10 @@ __device__ __forceinline__ void load16(const void *p, size_t i, float (&y)[16]) 
 __device__ __forceinline__ uint32_t pack2(F16, float lo, float hi) { return pack_f16x2(lo, hi); }
 __device__ __forceinline__ uint32_t pack2(BF16, float lo, float hi) { return pack_bf16x2(lo, hi); }
 
-template <class T>
 __device__ __forceinline__ void store16(void *p, size_t i, const float (&y)[16]) {
-  if constexpr (T::kBytes == 4) {
-    float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+  float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-  } else {
-    uint4 *u = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      u[j] = make_uint4(pack2(T{}, y[8 * j], y[8 * j + 1]), pack2(T{}, y[8 * j + 2], y[8 * j + 3]),
-                        pack2(T{}, y[8 * j + 4], y[8 * j + 5]), pack2(T{}, y[8 * j + 6], y[8 * j + 7]));
-  }
+  for (int j = 0; j < 4; ++j) f[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
 }
 
 // 16 elements of a 16-bit type as the format holds them: the one way for whole pages, appended rows and rotated rows, whose
@@ -326,7 +317,7 @@ __device__ __forceinline__ void kv4_values_to(const Kv4Group &g, float unit, voi
     for (int j = 0; j < 8; ++j) h.w[j] = pack2(T{}, y[2 * j], y[2 * j + 1]);
     store_half16(static_cast<uint16_t *>(p) + i, h);
   } else {
-    store16<T>(p, i, y);
+    store16(p, i, y);
   }
 }
 
