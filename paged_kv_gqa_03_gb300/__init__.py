@@ -897,6 +897,7 @@ class BlockManager:
     adopt / fork / free and per-token slot mapping with copy-on-write."""
 
     def __init__(self, num_blocks):
+        self._destroy = _L.pkv_bm_destroy   # (of the library that makes the handle, whatever _L is in the end)
         self._h = _L.pkv_bm_create(num_blocks)
         if not self._h:
             raise MemoryError("pkv_bm_create failed")
@@ -905,7 +906,7 @@ class BlockManager:
     def __del__(self):
         h = getattr(self, "_h", None)
         if h:
-            _L.pkv_bm_destroy(h)
+            self._destroy(h)
             self._h = None
 
     def allocate(self, seq, num_tokens):
