@@ -776,7 +776,8 @@ class RopeTable:
                 pair is interpolated by the factor and the fastest stays;
       "parts"   by the turns r_i = original_positions * f_i / 2 pi that a pair makes over the
                 original context: f_i where r_i >= fast, f_i / factor where r_i <= slow, and
-                linear in r_i between.
+                linear in r_i between.  (Models that go from one to the other linearly in the
+                pair's index i: pass their f_i as `frequencies`.)
     frequencies: f_i themselves (float64 [rot_dim / 2]), instead of base and scaling.
     magnitude scales the rotated elements (0.1 ln(factor) + 1 goes with "parts" where the
     model was trained so; 1 leaves them).  interleaved: pairs are elements

@@ -32,11 +32,14 @@
 //    register of the fragment.
 //  * Blocks that every row of the unit sees whole take no mask.
 //
-// Measured, cold inputs, 64 / 8 heads of 128, bf16: 64 x 8192 (606 MB) 118 us, 5.15 TB/s; another 64 sequences cost
+// Measured, cold inputs, 64 / 8 heads of 128, bf16: 64 x 8192 (604 MB) 118 us, 5.1 TB/s; another 64 sequences cost
 // 91 us, 6.6 TB/s; the rest is the launch and first fills (~10 us), the last units' imbalance and the merge (~9).
-// 1 x 131072 47 us; 1 x 333 14 us, of which 8 until the first tile has landed.  16-row units, 32 / 8 heads,
-// 4 new tokens, 16 x 1000-32768: 90 us.  D = 64 costs the instructions of a softmax on half the bytes: 64 x 8192,
-// 32 / 8 heads (303 MB) 84 us (16 warps of 96 registers: 80, and short calls no faster).
+// 1 x 131072 48 us; 1 x 333 14 us, of which 8 until the first tile has landed.  16-row units, 32 / 8 heads,
+// 4 new tokens, 16 x 1000-32768: 90 us; more rows widen the codes again, 16 rows at a time: 16 x 8192, 64 / 8 heads,
+// 1, 2, 4, 8 new tokens (8 to 64 rows a kv head) 43, 55, 85, 144 us.  16-row units of D = 128 issue 0.44 instructions a
+// clock from two warps a scheduler, the tensor pipe active for a third of the time: bound by waits, of dependent
+// instructions first.  D = 64 costs the instructions of a softmax on half the bytes: 64 x 8192, 32 / 8 heads (302 MB)
+// 79 us.
 //
 // Weights.  exp2((s - m) * c + 15), s a raw score, m the largest, c its factor (scale and units): the difference comes
 // first, so that the largest weight is 2^15 exactly, however large the scores; what is joined goes by the same

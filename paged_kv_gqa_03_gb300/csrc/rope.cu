@@ -20,8 +20,9 @@
 // written once: 16384 tokens, 64 + 8 + 8 heads of 128 in bf16, 671 MB in 107 us, 6.3 TB/s of the 6.8 that a
 // copy reaches; 122 us with 256 threads of three items, 118 without the bound on registers), by
 // latency for a decode step, whose heads are spread over more CTAs (64 tokens: 7 us).
-// (4-bit caches: the rows, rounded to their type as a cache of that type would hold
-// them, pass through shared memory to groups of 16.)
+// 4-bit caches: the rows, rounded to their type as a cache of that type would hold
+// them, pass through shared memory to groups of 16; V's codes go out by exclusive ors, token by token.  16384
+// tokens as above (623 MB) 116 us, 5.4 TB/s; 2048 21 us, 64 5 us; with a unit of 2^-4, by divisions, 131, 23 and 6.
 #include "kv4.cuh"
 #include "kv4.h"
 
