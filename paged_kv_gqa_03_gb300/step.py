@@ -33,7 +33,7 @@ and, on the host, the release of the rejected positions.
 import numpy as np
 import torch
 
-from . import (BlockManager, _cache4, lib, paged_decode_attention, paged_decode_workspace_bytes,
+from . import (BlockManager, _cache4, _dev, lib, paged_decode_attention, paged_decode_workspace_bytes,
                paged_kv4_append, paged_kv4_copy_blocks, paged_kv4_decode_attention,
                paged_kv4_decode_workspace_bytes, paged_kv4_rope_append, paged_kv_append,
                paged_kv_copy_blocks, paged_rope, paged_rope_append, paged_tree_attention,
@@ -387,6 +387,7 @@ class Kv4Step(DecodeStep):
     def __init__(self, cache, Hq, q_dtype, max_blocks, k_unit=1.0, v_unit=1.0, num_splits=0, stream=None,
                  scale=None, q_len=1, window=0, rope=None):
         self.cache, self.k_unit, self.v_unit = cache, float(k_unit), float(v_unit)
+        _dev(cache, "cache")
         _, self.num_blocks, self.Hkv, self.D = _cache4(cache, cache.get_device())
         self.new_dtype = q_dtype
         self._setup(cache.device, Hq, q_dtype, max_blocks, num_splits, stream, scale, q_len, window, rope)

@@ -15,21 +15,28 @@ class Rope:     # (a RopeTable, as far as a step looks at it)
 
 
 @pytest.mark.parametrize("shape", [(8, 2, 18 * 96), (8, 2, 18 * 64 + 1), (8, 2, 64), (8, 2, 0), (8, 2 * 18 * 64), (8, 2, 16, 64)])
-def test_a_cache_of_another_shape_is_refused(monkeypatch, shape):
+def test_a_cache_of_another_shape_is_refused(shape):
     _pkv()
     from paged_kv_gqa_03_gb300.step import Kv4Step
     with pytest.raises(ValueError, match="4-bit cache"):
         Kv4Step(_gpu(torch.zeros(shape, dtype=torch.uint8)), 4, BF16, 8, stream=object())
 
 
-def test_a_cache_of_another_type_is_refused(monkeypatch):
+def test_a_cache_of_another_type_is_refused():
     _pkv()
     from paged_kv_gqa_03_gb300.step import Kv4Step
     with pytest.raises(TypeError, match="uint8"):
         Kv4Step(_gpu(torch.zeros(8, 2, 18 * 64, dtype=torch.int8)), 4, BF16, 8, stream=object())
 
 
-def test_a_cache_of_its_shape(monkeypatch):
+def test_a_cache_in_host_memory_is_refused():
+    _pkv()
+    from paged_kv_gqa_03_gb300.step import Kv4Step
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        Kv4Step(torch.zeros(8, 2, 18 * 64, dtype=torch.uint8), 4, BF16, 8, stream=object())
+
+
+def test_a_cache_of_its_shape():
     _pkv()
     from paged_kv_gqa_03_gb300.step import Kv4Step
     for D in (64, 128):
